@@ -76,16 +76,16 @@ INSTRUCTION = {
 _CSRC = os.path.join("block_scaled_matrix_amd", "csrc")
 KERNEL_SOURCES = {
     "box_copy": ["k_tile.hip", "bsm_device.hpp"],
-    "gemm_bf16": ["k_gemm_dense.hip", "gemm_common.hpp", "bsm_device.hpp"],
-    "gemm_mxfp8": ["k_gemm_mx_any.hip", "gemm_mx_any.hpp", "gemm_common.hpp", "bsm_device.hpp"],
-    "gemm_mxfp8_fastacc": ["k_gemm_mx.hip", "gemm_common.hpp", "bsm_device.hpp"],
-    "gemm_mxfp4": ["k_gemm_mx.hip", "gemm_common.hpp", "bsm_device.hpp"],
+    "gemm_bf16": ["k_gemm_dense.hip", "gemm_dense_tile.hpp", "gemm_common.hpp", "bsm_device.hpp"],
+    "gemm_mxfp8": ["k_gemm_mx_any.hip", "gemm_mx_any.hpp", "store16.hpp", "gemm_common.hpp", "bsm_device.hpp"],
+    "gemm_mxfp8_fastacc": ["k_gemm_mx.hip", "gemm_mx_tile.hpp", "store16.hpp", "gemm_common.hpp", "bsm_device.hpp"],
+    "gemm_mxfp4": ["k_gemm_mx.hip", "gemm_mx_tile.hpp", "store16.hpp", "gemm_common.hpp", "bsm_device.hpp"],
     "add_one": ["k_tile.hip", "bsm_device.hpp"],
     "gather4": ["k_tile.hip", "bsm_device.hpp"],
     "scatter4": ["k_tile.hip", "bsm_device.hpp"],
     "box_load_rank3": ["k_tile.hip", "bsm_device.hpp"],
-    "gemm_e4m3_e2m1": ["k_gemm_mx_any.hip", "gemm_mx_any.hpp", "gemm_common.hpp", "bsm_device.hpp"],
-    "gemm_e2m3_e2m3": ["k_gemm_mx_any.hip", "gemm_mx_any.hpp", "gemm_common.hpp", "bsm_device.hpp"],
+    "gemm_e4m3_e2m1": ["k_gemm_mx_any.hip", "gemm_mx_any.hpp", "store16.hpp", "gemm_common.hpp", "bsm_device.hpp"],
+    "gemm_e2m3_e2m3": ["k_gemm_mx_any.hip", "gemm_mx_any.hpp", "store16.hpp", "gemm_common.hpp", "bsm_device.hpp"],
     "box_copy_only": ["k_tile.hip", "bsm_device.hpp"],
     "box_reduce_only": ["k_tile.hip", "bsm_device.hpp"],
 }
@@ -556,11 +556,11 @@ def host_cpu():
 # unragged 16256-row view.
 NAME_RULES = [
     (r"k_gemm_dense<4, true, false, true>", "gemm_bf16"),
-    (r"k_gemm_mx_any<0, 0, false, false, true>", "gemm_mxfp8"),
-    (r"k_gemm_mx<0, 0, 0, false>", "gemm_mxfp8_fastacc"),
-    (r"k_gemm_mx<4, 4, 4, false>", "gemm_mxfp4"),
-    (r"k_gemm_mx_any<0, 4, false, false, true>", "gemm_e4m3_e2m1"),
-    (r"k_gemm_mx_any<2, 2, false, false, false>", "gemm_e2m3_e2m3"),
+    (r"k_gemm_mx_any<0, 0, false, false, true(>|, bsm::gemm::WholeProduct)", "gemm_mxfp8"),
+    (r"k_gemm_mx<0, 0, 0, false(>|, bsm::gemm::WholeProduct)", "gemm_mxfp8_fastacc"),
+    (r"k_gemm_mx<4, 4, 4, false(>|, bsm::gemm::WholeProduct)", "gemm_mxfp4"),
+    (r"k_gemm_mx_any<0, 4, false, false, true(>|, bsm::gemm::WholeProduct)", "gemm_e4m3_e2m1"),
+    (r"k_gemm_mx_any<2, 2, false, false, false(>|, bsm::gemm::WholeProduct)", "gemm_e2m3_e2m3"),
     (r"k_row4<false>", "gather4"),
     (r"k_row4<true>", "scatter4"),
     (r"k_box_load\(", "box_load_rank3"),

@@ -63,7 +63,7 @@
 // distinct (row parity, chunk) pairs), so no two lanes of a half-wave share a bank.
 #pragma once
 #include <type_traits>
-#include "gemm_common.hpp"
+#include "store16.hpp"
 #include "../../include/bsm.h"
 
 namespace bsm {
@@ -531,15 +531,15 @@ __device__ __forceinline__ void mfma16(const i32x8 (&fa)[4], const i32x8 (&fb)[4
   }
 }
 
-template <int CA, int CB, bool AMN, bool BMN, bool BF>
-__global__ __launch_bounds__(256, 1) void k_gemm_mx_any(GemmArgs a, int tiles_m, int tiles_n) {
+template <int CA, int CB, bool AMN, bool BMN, bool BF, class WHERE, int OUT>
+__global__ __launch_bounds__(256, 1) void k_gemm_mx_any(GemmArgs a, WHERE where) {
   typedef Op<CA, AMN> PA;
   typedef Op<CB, BMN> PB;
   typedef Lay<CA, CB> L;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[L::BYTES];
   const int q = threadIdx.x, lane = q & 63, w = __builtin_amdgcn_readfirstlane(q >> 6);
   int tm, tn;
-  gemm::tile_coords(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  if (!where.locate(a, lane, tm, tn)) return;
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
   const int wa = 128 * (w >> 1), wb = 128 * (w & 1);
   const float sgn = a.negate ? -1.0f : 1.0f;
@@ -773,12 +773,8 @@ __global__ __launch_bounds__(256, 1) void k_gemm_mx_any(GemmArgs a, int tiles_m,
   __syncthreads();
   // (accumulation as a constant in each branch: the fresh-D path then holds no registers for
   // D's values, which made the compiler spill accumulators here)
-  if (a.accum)
-    gemm::store_tile_lines(a.D, a.ldd, a.M, a.N, m0 + wa, n0 + wb, lane, sgn, acc, lds + 32768 * w, true, a.ew_op,
-                           a.ew_scale, a.ew_bias);
-  else
-    gemm::store_tile_lines(a.D, a.ldd, a.M, a.N, m0 + wa, n0 + wb, lane, sgn, acc, lds + 32768 * w, false, a.ew_op,
-                           a.ew_scale, a.ew_bias);
+  if (a.accum) gemm::store_tile_as<OUT>(a, m0 + wa, n0 + wb, lane, sgn, acc, lds + 32768 * w, true);
+  else gemm::store_tile_as<OUT>(a, m0 + wa, n0 + wb, lane, sgn, acc, lds + 32768 * w, false);
 }
 
 // Launch of one (A format, B format, major orders) instance on the route the call asks for:
@@ -794,8 +790,8 @@ hipError_t launch_route(const GemmArgs& a, int tiles_m, int tiles_n, hipStream_t
   if constexpr (tuned || fp6_mn) {
     return hipErrorInvalidValue;
   } else {
-    hipLaunchKernelGGL((k_gemm_mx_any<CA, CB, AMN, BMN, BF>), dim3(tiles_m * tiles_n), dim3(256), 0, st, a, tiles_m,
-                       tiles_n);
+    hipLaunchKernelGGL((k_gemm_mx_any<CA, CB, AMN, BMN, BF, gemm::WholeProduct, BSM_F32>), dim3(tiles_m * tiles_n),
+                       dim3(256), 0, st, a, gemm::WholeProduct{tiles_m, tiles_n});
     return hipGetLastError();
   }
 }

@@ -24,7 +24,8 @@ EWISE = {"none": 0, "silu_affine": 1}
 EXPORTS = ("bsm_image_stride", "bsm_tile_box_load", "bsm_tile_box_store", "bsm_tile_box_copy",
            "bsm_tile_box_load_steps", "bsm_tile_box_store_steps", "bsm_tile_gather4", "bsm_tile_scatter4", "bsm_gemm",
            "bsm_gemm_block_scale", "bsm_gemm_ewise", "bsm_gemm_block_scale_ewise", "bsm_gemm_block_scale_major",
-           "bsm_gemm_block_scale_fastacc", "bsm_debug_stream_mix_bf16", "bsm_debug_mfma_loop", "bsm_tile_add_scalar_f32", "bsm_debug_fragments", "bsm_debug_fragment_shape", "bsm_last_error")
+           "bsm_gemm_block_scale_fastacc", "bsm_gemm_grouped", "bsm_gemm_grouped_wgrad",
+           "bsm_debug_stream_mix_bf16", "bsm_debug_mfma_loop", "bsm_tile_add_scalar_f32", "bsm_debug_fragments", "bsm_debug_fragment_shape", "bsm_last_error")
 
 
 class BsmError(RuntimeError):
@@ -80,6 +81,9 @@ def lib():
         L.bsm_gemm_block_scale_major.argtypes = [I64, I64, I64, I32, P, I64, C.c_char, P, I64, I32, P, I64, C.c_char,
                                                  P, I64, P, I64, C.c_int, C.c_int, C.c_int, C.POINTER(bsm_ewise), P]
         L.bsm_gemm_block_scale_fastacc.argtypes = L.bsm_gemm_block_scale_ewise.argtypes
+        L.bsm_gemm_grouped.argtypes = [I64, I64, I64, I32, P, I32, P, I64, P, I64, C.c_char, I64, I32, P, I64, C.c_int,
+                                       C.POINTER(bsm_ewise), P]
+        L.bsm_gemm_grouped_wgrad.argtypes = [I64, I64, I64, I32, P, I32, P, I64, P, I64, I32, P, I64, I64, C.c_int, P]
         L.bsm_tile_add_scalar_f32.argtypes = [P, P, I64, C.c_float, P]
         L.bsm_debug_stream_mix_bf16.argtypes = [P, P, P, I64, P]
         L.bsm_debug_mfma_loop.argtypes = [I32, I64, I32, P, P]
@@ -90,7 +94,8 @@ def lib():
                       "bsm_tile_box_store_steps", "bsm_tile_gather4",
                       "bsm_tile_scatter4", "bsm_gemm",
                       "bsm_gemm_block_scale", "bsm_gemm_ewise", "bsm_gemm_block_scale_ewise",
-                      "bsm_gemm_block_scale_major", "bsm_gemm_block_scale_fastacc", "bsm_tile_add_scalar_f32",
+                      "bsm_gemm_block_scale_major", "bsm_gemm_block_scale_fastacc", "bsm_gemm_grouped",
+                      "bsm_gemm_grouped_wgrad", "bsm_tile_add_scalar_f32",
                       "bsm_debug_fragments", "bsm_debug_stream_mix_bf16", "bsm_debug_mfma_loop"):
             getattr(L, rc_fn).restype = C.c_int
         _lib = L
@@ -252,6 +257,50 @@ def bsm_gemm_block_scale_fastacc(M, N, K, a_fmt: str, A, lda, SFA, ld_sfa, b_fmt
     _check(lib().bsm_gemm_block_scale_fastacc(M, N, K, DTYPE[a_fmt], _ptr(A), lda, _ptr(SFA), ld_sfa, DTYPE[b_fmt],
                                               _ptr(B), ldb, _ptr(SFB), ld_sfb, _ptr(D), ldd, neg_a, neg_b, accum,
                                               C.byref(ew) if ew is not None else None, _stream(stream)))
+
+
+def _here(stream, *tensors):
+    """The stream's handle, once every torch tensor given is known to live on the current device: the kernels
+    take addresses, and one of the host or of another device would fault them. Work on another device goes
+    under torch.cuda.device of that device."""
+    at = None
+    for t in tensors:
+        if t is None or isinstance(t, int):
+            continue
+        if not t.is_cuda:
+            raise BsmError(-13, f"a tensor on {t.device}: the library takes device memory")
+        if at is None:
+            import torch
+            at = torch.cuda.current_device()
+        if t.device.index != at:
+            raise BsmError(-13, f"a tensor on {t.device} while the current device is cuda:{at}")
+    return _stream(stream)
+
+
+def _ints(t, what):
+    """Address of a DEVICE array of int32, checked where it is a torch tensor."""
+    if t is not None and not isinstance(t, int):
+        import torch
+        if t.dtype != torch.int32:
+            raise BsmError(-8, f"{what} must be int32, not {t.dtype}")
+        if not t.is_contiguous():
+            raise BsmError(-5, f"{what} must be contiguous")
+    return _ptr(t)
+
+
+def bsm_gemm_grouped(rows, N, K, n_groups, offsets, ab: str, A, lda, B, ldb, b_major: str, stride_b, d_fmt: str, D, ldd,
+                     accum=0, ew: bsm_ewise | None = None, stream=None):
+    s = _here(stream, offsets, A, B, D)
+    _check(lib().bsm_gemm_grouped(rows, N, K, n_groups, _ints(offsets, "offsets"), DTYPE[ab], _ptr(A), lda, _ptr(B), ldb,
+                                  b_major.encode(), stride_b, DTYPE[d_fmt], _ptr(D), ldd, accum,
+                                  C.byref(ew) if ew is not None else None, s))
+
+
+def bsm_gemm_grouped_wgrad(rows, M, N, n_groups, offsets, ab: str, A, lda, B, ldb, d_fmt: str, D, ldd, stride_d, accum=0,
+                           stream=None):
+    s = _here(stream, offsets, A, B, D)
+    _check(lib().bsm_gemm_grouped_wgrad(rows, M, N, n_groups, _ints(offsets, "offsets"), DTYPE[ab], _ptr(A), lda, _ptr(B), ldb,
+                                        DTYPE[d_fmt], _ptr(D), ldd, stride_d, accum, s))
 
 
 def bsm_tile_add_scalar_f32(src, dst, n: int, s: float, stream=None):

@@ -516,6 +516,118 @@ int bsm_gemm_block_scale_fastacc(int64_t M, int64_t N, int64_t K, int32_t a_fmt,
                           "bsm_gemm_block_scale_fastacc", 1);
 }
 
+// Rules shared by the grouped calls: the groups and their offsets, and a D of a chosen format.
+static int check_groups(int64_t rows, int32_t n_groups, const int32_t* offsets) {
+  if (rows < 0 || rows > 0x7FFFFFFF) return fail(BSM_E_SHAPE, "rows = %lld out of range", (long long)rows);
+  if (n_groups < 0 || n_groups > 65536) return fail(BSM_E_SHAPE, "n_groups = %d not in 0 .. 65536", n_groups);
+  if (n_groups == 0) return BSM_OK;
+  if (!offsets) return fail(BSM_E_NULL, "offsets is NULL");
+  if ((uintptr_t)offsets % 4) return fail(BSM_E_ALIGN, "offsets not 4-byte aligned");
+  return BSM_OK;
+}
+
+static int check_out(const void* D, int64_t N, int64_t ldd, int32_t d_fmt) {
+  const int64_t q = d_fmt == BSM_F32 ? 4 : 8;
+  if (!D) return fail(BSM_E_NULL, "D is NULL");
+  if ((uintptr_t)D % 16) return fail(BSM_E_ALIGN, "D not 16-byte aligned");
+  if (ldd < N || ldd % q) return fail(BSM_E_ALIGN, "ldd = %lld must be >= N and a multiple of %d", (long long)ldd, (int)q);
+  if (ldd > (int64_t(1) << 31)) return fail(BSM_E_SHAPE, "ldd = %lld out of range", (long long)ldd);
+  return BSM_OK;
+}
+
+static int check_ewise(const bsm_ewise* ew);
+
+// Half-open range of `n` blocks, `stride` elements apart, of `rows` rows of ld elements, the last
+// row `len` elements long, of `bits` bits each.
+static Range block_range(const void* p, int64_t n, int64_t stride, int64_t rows, int64_t ld, int64_t len, int bits) {
+  const __int128 elems = (__int128)(n - 1) * stride + (__int128)(rows - 1) * ld + len;
+  return Range{(uintptr_t)p, (uintptr_t)p + (uintptr_t)(elems * bits / 8)};
+}
+
+int bsm_gemm_grouped(int64_t rows, int64_t N, int64_t K, int32_t n_groups, const int32_t* offsets, int32_t ab,
+                     const void* A, int64_t lda, const void* B, int64_t ldb, char b_major, int64_t stride_b,
+                     int32_t d_fmt, void* D, int64_t ldd, int accum, const bsm_ewise* ew, void* stream) {
+  int rc;
+  if ((rc = check_flag(accum, "accum"))) return rc;
+  if (ew && (rc = check_ewise(ew))) return rc;
+  if (ab != BSM_F16 && ab != BSM_BF16) return fail(BSM_E_DTYPE, "ab = %d: grouped GEMM takes F16 or BF16", ab);
+  if (d_fmt != BSM_F32 && d_fmt != ab) return fail(BSM_E_DTYPE, "d_fmt = %d is neither F32 nor the operands' format", d_fmt);
+  if (N < 0 || K < 0 || N > 0x7FFFFFFF || K > 0x7FFFFFFF)
+    return fail(BSM_E_SHAPE, "N, K = %lld, %lld out of range", (long long)N, (long long)K);
+  if (b_major != 'k' && b_major != 'n') return fail(BSM_E_MAJOR, "b_major '%c' is not 'k' or 'n'", b_major);
+  if ((rc = check_groups(rows, n_groups, offsets))) return rc;
+  if (rows == 0 || N == 0 || n_groups == 0) return ok();
+  if ((rc = check_out(D, N, ldd, d_fmt))) return rc;
+  const Range rd = block_range(D, 1, 0, rows, ldd, N, d_fmt == BSM_F32 ? 32 : 16);
+  if (overlap(rd, block_range(offsets, 1, 0, 1, 0, n_groups + int64_t(1), 32))) return fail(BSM_E_ALIAS, "offsets overlap D");
+  if (K > 0) {
+    if (!A || !B) return fail(BSM_E_NULL, "A or B is NULL");
+    if ((uintptr_t)A % 16 || (uintptr_t)B % 16) return fail(BSM_E_ALIGN, "A and B must be 16-byte aligned");
+    const int64_t blen = b_major == 'k' ? K : N, brows = b_major == 'k' ? N : K;
+    if (lda < K || lda % 8) return fail(BSM_E_ALIGN, "lda = %lld must be >= K and a multiple of 8", (long long)lda);
+    if (ldb < blen || ldb % 8) return fail(BSM_E_ALIGN, "ldb = %lld must be >= %lld and a multiple of 8", (long long)ldb, (long long)blen);
+    if (lda > (int64_t(1) << 22) || ldb > (int64_t(1) << 22))
+      return fail(BSM_E_SHAPE, "lda, ldb must be at most 2^22 elements (32-bit in-tile offsets)");
+    if (stride_b < 0 || stride_b > (int64_t(1) << 44)) return fail(BSM_E_SHAPE, "stride_b = %lld out of range", (long long)stride_b);
+    if (stride_b % 8) return fail(BSM_E_ALIGN, "stride_b = %lld is not a multiple of 8", (long long)stride_b);
+    if (overlap(rd, block_range(A, 1, 0, rows, lda, K, 16)) || overlap(rd, block_range(B, n_groups, stride_b, brows, ldb, blen, 16)))
+      return fail(BSM_E_ALIAS, "A or B overlaps D");
+  }
+  bsm::GemmArgs g{};
+  g.N = N; g.K = K; g.dtype = ab;
+  g.A = A; g.lda = lda; g.a_kmajor = 1;
+  g.B = B; g.ldb = ldb; g.b_kmajor = b_major == 'k';
+  g.D = (float*)D; g.ldd = ldd; g.d_fmt = d_fmt; g.accum = accum;
+  if (ew) { g.ew_op = ew->op; g.ew_scale = ew->scale; g.ew_bias = ew->bias; }
+  bsm::GroupArgs gr{};
+  gr.offsets = offsets; gr.n = n_groups; gr.rows = (int32_t)rows; gr.stride_b = stride_b;
+  hipError_t e = bsm::launch_gemm_grouped(g, gr, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "bsm_gemm_grouped");
+  return ok();
+}
+
+int bsm_gemm_grouped_wgrad(int64_t rows, int64_t M, int64_t N, int32_t n_groups, const int32_t* offsets, int32_t ab,
+                           const void* A, int64_t lda, const void* B, int64_t ldb, int32_t d_fmt, void* D, int64_t ldd,
+                           int64_t stride_d, int accum, void* stream) {
+  int rc;
+  if ((rc = check_flag(accum, "accum"))) return rc;
+  if (ab != BSM_F16 && ab != BSM_BF16) return fail(BSM_E_DTYPE, "ab = %d: grouped GEMM takes F16 or BF16", ab);
+  if (d_fmt != BSM_F32 && d_fmt != ab) return fail(BSM_E_DTYPE, "d_fmt = %d is neither F32 nor the operands' format", d_fmt);
+  if (M < 0 || N < 0 || M > 0x7FFFFFFF || N > 0x7FFFFFFF)
+    return fail(BSM_E_SHAPE, "M, N = %lld, %lld out of range", (long long)M, (long long)N);
+  if ((rc = check_groups(rows, n_groups, offsets))) return rc;
+  if (M == 0 || N == 0 || n_groups == 0) return ok();
+  if ((rc = check_out(D, N, ldd, d_fmt))) return rc;
+  if (n_groups > 1) {
+    if (stride_d < 0 || stride_d > (int64_t(1) << 44)) return fail(BSM_E_SHAPE, "stride_d = %lld out of range", (long long)stride_d);
+    if (stride_d % (d_fmt == BSM_F32 ? 4 : 8)) return fail(BSM_E_ALIGN, "stride_d = %lld: outputs must start 16-byte aligned", (long long)stride_d);
+    if (stride_d < (M - 1) * ldd + N) return fail(BSM_E_ALIAS, "stride_d = %lld: the groups' outputs overlap", (long long)stride_d);
+  } else {
+    stride_d = 0;
+  }
+  const Range rd = block_range(D, n_groups, stride_d, M, ldd, N, d_fmt == BSM_F32 ? 32 : 16);
+  if (overlap(rd, block_range(offsets, 1, 0, 1, 0, n_groups + int64_t(1), 32))) return fail(BSM_E_ALIAS, "offsets overlap D");
+  if (rows > 0) {
+    if (!A || !B) return fail(BSM_E_NULL, "A or B is NULL");
+    if ((uintptr_t)A % 16 || (uintptr_t)B % 16) return fail(BSM_E_ALIGN, "A and B must be 16-byte aligned");
+    if (lda < M || lda % 8) return fail(BSM_E_ALIGN, "lda = %lld must be >= M and a multiple of 8", (long long)lda);
+    if (ldb < N || ldb % 8) return fail(BSM_E_ALIGN, "ldb = %lld must be >= N and a multiple of 8", (long long)ldb);
+    if (lda > (int64_t(1) << 22) || ldb > (int64_t(1) << 22))
+      return fail(BSM_E_SHAPE, "lda, ldb must be at most 2^22 elements (32-bit in-tile offsets)");
+    if (overlap(rd, block_range(A, 1, 0, rows, lda, M, 16)) || overlap(rd, block_range(B, 1, 0, rows, ldb, N, 16)))
+      return fail(BSM_E_ALIAS, "A or B overlaps D");
+  }
+  bsm::GemmArgs g{};
+  g.M = M; g.N = N; g.dtype = ab;
+  g.A = A; g.lda = lda; g.B = B; g.ldb = ldb;
+  g.D = (float*)D; g.ldd = ldd; g.d_fmt = d_fmt; g.accum = accum;
+  bsm::GroupArgs gr{};
+  gr.offsets = offsets; gr.n = n_groups; gr.rows = (int32_t)rows; gr.stride_d = stride_d;
+  hipError_t e = bsm::launch_gemm_grouped_wgrad(g, gr, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "bsm_gemm_grouped_wgrad");
+  return ok();
+}
+
 int bsm_tile_add_scalar_f32(const float* src, float* dst, int64_t n, float s, void* stream) {
   if (n < 0) return fail(BSM_E_SHAPE, "n = %lld is negative", (long long)n);
   if (n == 0) return ok();

@@ -71,6 +71,7 @@ struct GemmArgs {
   int32_t accum;
   int32_t ew_op;        // bsm_ewise_op applied to each output before its store (0: none)
   float ew_scale, ew_bias;
+  int32_t d_fmt;        // D's format where a call lets it be chosen: BSM_F32, BSM_F16, BSM_BF16 (else unused: F32)
   int32_t mx_window;    // block scaled: 1 = every pairing on the scaled f8f6f4 MFMA (its 2^-13 block
                         // window), 0 = exact products (bf16 MFMA) for the pairings that need them
 };
@@ -85,6 +86,20 @@ hipError_t launch_gemm_mx_any(const GemmArgs& a, hipStream_t st);
 hipError_t launch_gemm_mx_mn_a(const GemmArgs& a, hipStream_t st);
 hipError_t launch_gemm_mx_mn_b(const GemmArgs& a, hipStream_t st);
 hipError_t launch_gemm_mx_mn_ab(const GemmArgs& a, hipStream_t st);
+
+// Rows in groups (grouped.hpp): group g is rows offsets[g] .. offsets[g + 1] - 1 of `rows` rows.
+struct GroupArgs {
+  const int32_t* offsets;  // DEVICE, n + 1 values
+  int32_t n;
+  int32_t rows;
+  int64_t stride_b;        // elements between the groups' B operands (grouped products)
+  int64_t stride_sfb;      // bytes between their scale tensors (block scaled)
+  int64_t stride_d;        // elements between the groups' outputs (weight gradient)
+};
+// a.M unused; rows, N, K > 0, n > 0.
+hipError_t launch_gemm_grouped(const GemmArgs& a, const GroupArgs& gr, hipStream_t st);
+// a.K unused; M, N > 0, n > 0; A and B MN-major (rows of M and N elements).
+hipError_t launch_gemm_grouped_wgrad(const GemmArgs& a, const GroupArgs& gr, hipStream_t st);
 
 // Diagnostics (k_diag.hip): the box copy's traffic mix on flat bf16 buffers of n elements
 // (n a multiple of 8, 16-byte aligned), and workgroups x 256 lanes of back-to-back MFMAs of

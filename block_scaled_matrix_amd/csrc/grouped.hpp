@@ -1,0 +1,84 @@
+// grouped.hpp - rows in groups: the offsets a grouped product reads on the device, and which tile
+// of which group a workgroup works on.
+//
+// offsets holds n + 1 row numbers; group g is rows offsets[g] .. offsets[g + 1] - 1. The host does
+// not see them (a router writes them on the device), so the grid covers the most tiles any split
+// can have, ceil(rows / BM) summed over the groups <= rows / BM + min(n, rows), and every
+// workgroup finds its own tile from the offsets: one load and one 64-lane scan per 64 groups, made
+// by each wave for itself (no LDS, no barrier). Offsets are clamped to 0 .. rows and a decreasing
+// pair is an empty group, so no offset leads outside the buffers.
+#pragma once
+#include "bsm_device.hpp"
+#include "bsm_internal.hpp"
+
+namespace bsm {
+namespace grouped {
+
+// First row and end of group i < n.
+__device__ __forceinline__ void group_range(const GroupArgs& gr, int i, int& lo, int& hi) {
+  lo = min(max(gr.offsets[i], 0), gr.rows);
+  hi = max(min(max(gr.offsets[i + 1], 0), gr.rows), lo);
+}
+
+__device__ __forceinline__ int wave_inclusive_scan(int v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int u = __shfl_up(v, d);
+    if (lane >= d) v += u;
+  }
+  return v;
+}
+
+struct Spot {
+  int g, row0, rows;  // the group, its first row and its row count
+  int tm, tn;         // the tile within the group
+};
+
+// Tile `pid` of the launch (wave-uniform result; false: no such tile). Tiles are numbered group by
+// group, inside a group in bands of GROUP_M tile rows walked column by column, and the numbers are
+// dealt to the XCDs (workgroup p runs on XCD p % 8) in eight contiguous ranges, so that the
+// workgroups of one XCD share a group's weight panels in its L2.
+template <int BM, int GROUP_M>
+__device__ __forceinline__ bool find_tile(const GroupArgs& gr, int pid, int tiles_n, int lane, Spot& s) {
+  auto tiles_of = [&](int i, int& lo, int& hi) {
+    if (i < gr.n) group_range(gr, i, lo, hi);
+    else lo = hi = 0;
+    return (int)(((int64_t)(hi - lo) + BM - 1) / BM);
+  };
+  int lo, hi, all = 0;
+  for (int i0 = 0; i0 < gr.n; i0 += 64)
+    all += __builtin_amdgcn_readlane(wave_inclusive_scan(tiles_of(i0 + lane, lo, hi), lane), 63);
+  const int total = all * tiles_n, chunk = (total + 7) >> 3;
+  const int lid = (pid & 7) * chunk + (pid >> 3);
+  if ((pid >> 3) >= chunk || lid >= total) return false;
+  const int rt = lid / tiles_n;
+  int before = 0;
+  for (int i0 = 0; i0 < gr.n; i0 += 64) {
+    const int t = tiles_of(i0 + lane, lo, hi);
+    const int incl = wave_inclusive_scan(t, lane);
+    const uint64_t past = __ballot(before + incl > rt);
+    if (past) {
+      const int at = __builtin_ctzll(past);
+      s.g = i0 + at;
+      s.row0 = __builtin_amdgcn_readlane(lo, at);
+      s.rows = __builtin_amdgcn_readlane(hi, at) - s.row0;
+      const int tiles_m = __builtin_amdgcn_readlane(t, at);
+      const int first_tile = before + __builtin_amdgcn_readlane(incl, at) - tiles_m;
+      const int li = lid - first_tile * tiles_n;
+      if (li < 0 || li >= tiles_m * tiles_n) return false;  // (offsets that overlap beyond all counting)
+      const int per_band = GROUP_M * tiles_n, band = li / per_band, first = band * GROUP_M;
+      const int size = min(tiles_m - first, GROUP_M), in = li - band * per_band;
+      s.tm = first + in % size;
+      s.tn = in / size;
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(incl, 63);
+  }
+  return false;
+}
+
+// Row tiles that `rows` rows in n groups can need at most.
+inline int64_t most_row_tiles(int64_t rows, int64_t n, int64_t bm) { return rows / bm + (n < rows ? n : rows); }
+
+}  // namespace grouped
+}  // namespace bsm

@@ -1,0 +1,101 @@
+// k_gemm_grouped.hip - fp16/bf16 products with a weight per group of rows, and their weight gradient.
+//
+//   grouped:  D[r, n] = f((D[r, n] +) sum_k A[r, k] B_g(n, k))      r in group g
+//   wgrad:    D_g[m, n] = (D_g[m, n] +) sum_{r in group g} A[r, m] B[r, n]
+//
+// Large groups run the dense GEMM's 256 x 256 tile (gemm_dense_tile.hpp) on the group's rows: the
+// operands' bases move to the group's first row and its weight, M (grouped) or K (wgrad) is the
+// group's row count. Rows past a group's end are other groups' rows: they are clamped away on the
+// load (grouped) or zeroed (wgrad, the partial last K tile) and never stored.
+#include "gemm_dense_tile.hpp"
+#include "store16.hpp"
+#include "grouped.hpp"
+
+namespace bsm {
+namespace {
+
+using namespace dense;
+
+template <int DT>
+__device__ __forceinline__ void store_out(const GemmArgs& a, void* D, int64_t M, int64_t row0, int64_t col0, int lane,
+                                          const f32x4 (&acc)[8][8], uint8_t* region) {
+  if (a.d_fmt == BSM_F32) {
+    if (a.accum) store_tile16((float*)D, a.ldd, M, a.N, row0, col0, lane, 1.0f, acc, region, true, a.ew_op, a.ew_scale, a.ew_bias);
+    else store_tile16((float*)D, a.ldd, M, a.N, row0, col0, lane, 1.0f, acc, region, false, a.ew_op, a.ew_scale, a.ew_bias);
+  } else {
+    if (a.accum) gemm::store_tile16_bits<DT>((uint16_t*)D, a.ldd, M, a.N, row0, col0, lane, acc, region, true, a.ew_op, a.ew_scale, a.ew_bias);
+    else gemm::store_tile16_bits<DT>((uint16_t*)D, a.ldd, M, a.N, row0, col0, lane, acc, region, false, a.ew_op, a.ew_scale, a.ew_bias);
+  }
+}
+
+__device__ __forceinline__ void* row_ptr(const GemmArgs& a, int64_t elements) {
+  return (uint8_t*)a.D + elements * (a.d_fmt == BSM_F32 ? 4 : 2);
+}
+
+template <int DT, bool BKM>
+__global__ __launch_bounds__(256, 1) void k_grouped(GemmArgs a, GroupArgs gr, int tiles_n) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * STAGE_BYTES];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  grouped::Spot s;
+  if (!grouped::find_tile<BM, 4>(gr, blockIdx.x, tiles_n, lane, s)) return;
+  GemmArgs t = a;
+  t.M = s.rows;
+  t.A = (const uint16_t*)a.A + (int64_t)s.row0 * a.lda;
+  t.B = (const uint16_t*)a.B + (int64_t)s.g * gr.stride_b;
+  f32x4 acc[8][8];
+  tile_product<DT, true, BKM>(t, s.tm, s.tn, lds, lane, w, acc);
+  store_out<DT>(a, row_ptr(a, (int64_t)s.row0 * a.ldd), s.rows, (int64_t)s.tm * BM + 128 * (w >> 1),
+                (int64_t)s.tn * BN + 128 * (w & 1), lane, acc, lds + 32768 * w);
+}
+
+// Workgroup p: tile of group (p's number) / (tiles_m * tiles_n), dealt to the XCDs in contiguous
+// ranges when their number divides by eight.
+template <int DT>
+__global__ __launch_bounds__(256, 1) void k_grouped_wgrad(GemmArgs a, GroupArgs gr, int tiles_m, int tiles_n) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * STAGE_BYTES];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int per = tiles_m * tiles_n, total = per * gr.n, pid = blockIdx.x;
+  const int lid = (total & 7) == 0 ? (pid & 7) * (total >> 3) + (pid >> 3) : pid;
+  const int g = lid / per, in = lid - g * per;
+  const int band = in / (4 * tiles_n), size = min(tiles_m - 4 * band, 4), li = in - band * 4 * tiles_n;
+  const int tm = 4 * band + li % size, tn = li / size;
+  int lo, hi;
+  grouped::group_range(gr, g, lo, hi);
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  hi = __builtin_amdgcn_readfirstlane(hi);
+  GemmArgs t = a;
+  t.K = hi - lo;
+  t.A = (const uint16_t*)a.A + (int64_t)lo * a.lda;
+  t.B = (const uint16_t*)a.B + (int64_t)lo * a.ldb;
+  f32x4 acc[8][8];
+  tile_product<DT, false, false>(t, tm, tn, lds, lane, w, acc);
+  store_out<DT>(a, row_ptr(a, (int64_t)g * gr.stride_d), a.M, (int64_t)tm * BM + 128 * (w >> 1),
+                (int64_t)tn * BN + 128 * (w & 1), lane, acc, lds + 32768 * w);
+}
+
+template <int DT>
+hipError_t launch_grouped_dt(const GemmArgs& a, const GroupArgs& gr, hipStream_t st) {
+  const int64_t tn = (a.N + BN - 1) / BN, n = (grouped::most_row_tiles(gr.rows, gr.n, BM) * tn + 7) / 8 * 8;
+  if (n > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const dim3 grid((uint32_t)n);
+  if (a.b_kmajor) hipLaunchKernelGGL((k_grouped<DT, true>), grid, dim3(256), 0, st, a, gr, (int)tn);
+  else hipLaunchKernelGGL((k_grouped<DT, false>), grid, dim3(256), 0, st, a, gr, (int)tn);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_gemm_grouped(const GemmArgs& a, const GroupArgs& gr, hipStream_t st) {
+  return a.dtype == BSM_BF16 ? launch_grouped_dt<BSM_BF16>(a, gr, st) : launch_grouped_dt<BSM_F16>(a, gr, st);
+}
+
+hipError_t launch_gemm_grouped_wgrad(const GemmArgs& a, const GroupArgs& gr, hipStream_t st) {
+  const int64_t tm = (a.M + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
+  if (tm * tn * gr.n > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const dim3 grid((uint32_t)(tm * tn * gr.n));
+  if (a.dtype == BSM_BF16) hipLaunchKernelGGL(k_grouped_wgrad<BSM_BF16>, grid, dim3(256), 0, st, a, gr, (int)tm, (int)tn);
+  else hipLaunchKernelGGL(k_grouped_wgrad<BSM_F16>, grid, dim3(256), 0, st, a, gr, (int)tm, (int)tn);
+  return hipGetLastError();
+}
+
+}  // namespace bsm

@@ -320,6 +320,48 @@ int bsm_gemm_block_scale_fastacc(int64_t M, int64_t N, int64_t K,
                                  float* D, int64_t ldd, int neg_a, int neg_b, int accum,
                                  const bsm_ewise* ew, void* stream);
 
+/* Products with a weight per group of rows (the rows of one expert, one request, one
+ * segment; [MMA] "Call parameters" for each group's product): group g of n_groups is the
+ * rows offsets[g] .. offsets[g+1] - 1 of A and D, and for every such row r
+ *   D[r,n] = f(x),  x = (accum ? D[r,n] : 0) + sum_k A(r,k) * B_g(n,k),
+ * products and sums in float32, rounded once to D's format.
+ *   rows:      rows of A and D, 0 .. 2^31 - 1;
+ *   offsets:   DEVICE array of n_groups + 1 int32, non-decreasing, in 0 .. rows, 4-byte
+ *              aligned; read by the kernels, so a router may have written it on the same
+ *              stream. A group may be empty. Rows before offsets[0] and from
+ *              offsets[n_groups] on belong to no group: their D is neither read nor
+ *              written and their A has no effect. (Offsets outside 0 .. rows are clamped to
+ *              it and a decreasing pair is an empty group, so no offset leads outside the
+ *              buffers; groups that overlap race on the rows they share.)
+ *   n_groups:  0 .. 65536 (0: no-op);
+ *   ab:        BSM_F16 or BSM_BF16 (both operands);
+ *   A:         A(r,k) = A[r*lda + k];
+ *   B, b_major, stride_b: group g's weight starts at B + g * stride_b elements;
+ *              'k': B_g(n,k) = [n*ldb + k] (ldb >= K), the forward product of weights kept
+ *              (N,K); 'n': B_g(n,k) = [k*ldb + n] (ldb >= N), e.g. the input gradient
+ *              dX = dY * W with W kept (N_out,K_in) and called with N = K_in, K = N_out.
+ *              stride_b >= 0, a multiple of 8; 0 gives every group the same weight;
+ *   d_fmt:     BSM_F32, or the operands' own format (anything else -> BSM_E_DTYPE);
+ *   D:         16-byte aligned, ldd >= N and a multiple of 4 (F32) or 8 (16-bit);
+ *   accum:     0 or 1 (with 0, D is never read); ew as for bsm_gemm_ewise, or NULL.
+ * Alignment, whole-row buffers and the limit on lda and ldb as for bsm_gemm. K == 0 gives
+ * D = f(accum ? D : 0) on the groups' rows. A, B and offsets must not overlap D. */
+int bsm_gemm_grouped(int64_t rows, int64_t N, int64_t K, int32_t n_groups, const int32_t* offsets, int32_t ab,
+                     const void* A, int64_t lda, const void* B, int64_t ldb, char b_major, int64_t stride_b,
+                     int32_t d_fmt, void* D, int64_t ldd, int accum, const bsm_ewise* ew, void* stream);
+
+/* The weight gradient of bsm_gemm_grouped: one (M,N) output per group,
+ *   D_g[m,n] = (accum ? D_g[m,n] : 0) + sum_{r in group g} A(r,m) * B(r,n),
+ * sums in float32, rounded once to D's format. A(r,m) = A[r*lda + m] (lda >= M, e.g. dY),
+ * B(r,n) = B[r*ldb + n] (ldb >= N, e.g. X); D_g starts at D + g * stride_d elements. A group
+ * without rows gives D_g = accum ? D_g : 0. rows, offsets, n_groups, ab, d_fmt, D, ldd and
+ * accum as for bsm_gemm_grouped; rows in no group have no effect. stride_d a multiple of 4
+ * (F32) or 8 (16-bit), and with more than one group at least (M-1)*ldd + N (groups' outputs
+ * must not overlap; BSM_E_ALIAS). The same inputs give the same bits on every call. */
+int bsm_gemm_grouped_wgrad(int64_t rows, int64_t M, int64_t N, int32_t n_groups, const int32_t* offsets, int32_t ab,
+                           const void* A, int64_t lda, const void* B, int64_t ldb, int32_t d_fmt, void* D, int64_t ldd,
+                           int64_t stride_d, int accum, void* stream);
+
 /* Element-wise scalar add on float32 ([TOE] "A Load, Compute, and Store Example"
  * adds one to a (2,32,3,4) tile; [TP] "Scalar compositions"): dst[i] = src[i] + s,
  * i < n, each lane moving 16-byte vectors. src, dst 16-byte aligned; they may be

@@ -180,23 +180,12 @@ def audit(text: str) -> list:
                 rd = {r for r in _reads((op, ops)) if r[0] in "va"}
                 if not rd:
                     continue
-                hit = lambda x: x[0].startswith("v_mfma") and bool(_writes(x) & rd)
-                w = _min_since(f, i, hit, 19)
-                if w < 19:
-                    # the nearest MFMA writing what this reads: its shape sets the requirement
-                    need = _min_need(f, i, rd)
+                # each shape's own requirement, along every path on which an MFMA of it wrote what this reads
+                for need in (7, 11, 19):
+                    hit = lambda x: x[0].startswith("v_mfma") and _passes(x) + 3 == need and bool(_writes(x) & rd)
+                    w = _min_since(f, i, hit, need)
                     if w < need:
                         out.append(f"{f['name']}: {op} #{i}: {w} wait states after an MFMA wrote what it reads "
                                    f"(needs {need})")
     return out
 
-
-def _min_need(f, i: int, rd: set) -> int:
-    """passes + 3 of the MFMA that last wrote any of rd on the fall-through path before i
-    (the largest such requirement among the nearest writers, 19 if none is found nearby)."""
-    ins = f["ins"]
-    for j in range(i - 1, max(i - 200, -1), -1):
-        op = ins[j][0]
-        if op.startswith("v_mfma") and _writes(ins[j]) & rd:
-            return _passes(ins[j]) + 3
-    return 19

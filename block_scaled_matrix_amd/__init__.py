@@ -25,6 +25,7 @@ EXPORTS = ("bsm_image_stride", "bsm_tile_box_load", "bsm_tile_box_store", "bsm_t
            "bsm_tile_box_load_steps", "bsm_tile_box_store_steps", "bsm_tile_gather4", "bsm_tile_scatter4", "bsm_gemm",
            "bsm_gemm_block_scale", "bsm_gemm_ewise", "bsm_gemm_block_scale_ewise", "bsm_gemm_block_scale_major",
            "bsm_gemm_block_scale_fastacc", "bsm_gemm_grouped", "bsm_gemm_grouped_wgrad",
+           "bsm_gemm_grouped_block_scale", "bsm_gemm_lora", "bsm_gemm_lora_workspace",
            "bsm_debug_stream_mix_bf16", "bsm_debug_mfma_loop", "bsm_tile_add_scalar_f32", "bsm_debug_fragments", "bsm_debug_fragment_shape", "bsm_last_error")
 
 
@@ -84,6 +85,12 @@ def lib():
         L.bsm_gemm_grouped.argtypes = [I64, I64, I64, I32, P, I32, P, I64, P, I64, C.c_char, I64, I32, P, I64, C.c_int,
                                        C.POINTER(bsm_ewise), P]
         L.bsm_gemm_grouped_wgrad.argtypes = [I64, I64, I64, I32, P, I32, P, I64, P, I64, I32, P, I64, I64, C.c_int, P]
+        L.bsm_gemm_grouped_block_scale.argtypes = [I64, I64, I64, I32, P, I32, P, I64, P, I64, I32, P, I64, I64, P, I64, I64,
+                                                   C.c_int, I32, P, I64, C.c_int, C.POINTER(bsm_ewise), P]
+        L.bsm_gemm_lora_workspace.restype = I64
+        L.bsm_gemm_lora_workspace.argtypes = [I64, I64]
+        L.bsm_gemm_lora.argtypes = [I64, I64, I64, I64, I32, P, I32, P, I64, P, I64, P, I64, I64, P, I64, I64, P, P, I32, P,
+                                    I64, C.c_int, C.POINTER(bsm_ewise), P]
         L.bsm_tile_add_scalar_f32.argtypes = [P, P, I64, C.c_float, P]
         L.bsm_debug_stream_mix_bf16.argtypes = [P, P, P, I64, P]
         L.bsm_debug_mfma_loop.argtypes = [I32, I64, I32, P, P]
@@ -95,7 +102,7 @@ def lib():
                       "bsm_tile_scatter4", "bsm_gemm",
                       "bsm_gemm_block_scale", "bsm_gemm_ewise", "bsm_gemm_block_scale_ewise",
                       "bsm_gemm_block_scale_major", "bsm_gemm_block_scale_fastacc", "bsm_gemm_grouped",
-                      "bsm_gemm_grouped_wgrad", "bsm_tile_add_scalar_f32",
+                      "bsm_gemm_grouped_wgrad", "bsm_gemm_grouped_block_scale", "bsm_gemm_lora", "bsm_tile_add_scalar_f32",
                       "bsm_debug_fragments", "bsm_debug_stream_mix_bf16", "bsm_debug_mfma_loop"):
             getattr(L, rc_fn).restype = C.c_int
         _lib = L
@@ -301,6 +308,28 @@ def bsm_gemm_grouped_wgrad(rows, M, N, n_groups, offsets, ab: str, A, lda, B, ld
     s = _here(stream, offsets, A, B, D)
     _check(lib().bsm_gemm_grouped_wgrad(rows, M, N, n_groups, _ints(offsets, "offsets"), DTYPE[ab], _ptr(A), lda, _ptr(B), ldb,
                                         DTYPE[d_fmt], _ptr(D), ldd, stride_d, accum, s))
+
+
+def bsm_gemm_grouped_block_scale(rows, N, K, n_groups, offsets, a_fmt: str, A, lda, SFA, ld_sfa, b_fmt: str, B, ldb, stride_b,
+                                 SFB, ld_sfb, stride_sfb, fast, d_fmt: str, D, ldd, accum=0, ew: bsm_ewise | None = None,
+                                 stream=None):
+    s = _here(stream, offsets, A, SFA, B, SFB, D)
+    _check(lib().bsm_gemm_grouped_block_scale(rows, N, K, n_groups, _ints(offsets, "offsets"), DTYPE[a_fmt], _ptr(A), lda,
+                                              _ptr(SFA), ld_sfa, DTYPE[b_fmt], _ptr(B), ldb, stride_b, _ptr(SFB), ld_sfb,
+                                              stride_sfb, fast, DTYPE[d_fmt], _ptr(D), ldd, accum,
+                                              C.byref(ew) if ew is not None else None, s))
+
+
+def bsm_gemm_lora_workspace(rows, R) -> int:
+    return _check(lib().bsm_gemm_lora_workspace(rows, R))
+
+
+def bsm_gemm_lora(rows, N, K, R, n_adapters, adapter, ab: str, X, ldx, W, ldw, LA, ld_la, stride_la, LB, ld_lb, stride_lb, scale,
+                  workspace, d_fmt: str, D, ldd, accum=0, ew: bsm_ewise | None = None, stream=None):
+    s = _here(stream, adapter, X, W, LA, LB, scale, workspace, D)
+    _check(lib().bsm_gemm_lora(rows, N, K, R, n_adapters, _ints(adapter, "adapter"), DTYPE[ab], _ptr(X), ldx, _ptr(W), ldw,
+                               _ptr(LA), ld_la, stride_la, _ptr(LB), ld_lb, stride_lb, _ptr(scale), _ptr(workspace),
+                               DTYPE[d_fmt], _ptr(D), ldd, accum, C.byref(ew) if ew is not None else None, s))
 
 
 def bsm_tile_add_scalar_f32(src, dst, n: int, s: float, stream=None):

@@ -628,6 +628,134 @@ int bsm_gemm_grouped_wgrad(int64_t rows, int64_t M, int64_t N, int32_t n_groups,
   return ok();
 }
 
+int bsm_gemm_grouped_block_scale(int64_t rows, int64_t N, int64_t K, int32_t n_groups, const int32_t* offsets,
+                                 int32_t a_fmt, const void* A, int64_t lda, const uint8_t* SFA, int64_t ld_sfa,
+                                 int32_t b_fmt, const void* B, int64_t ldb, int64_t stride_b, const uint8_t* SFB,
+                                 int64_t ld_sfb, int64_t stride_sfb, int fast, int32_t d_fmt, void* D, int64_t ldd,
+                                 int accum, const bsm_ewise* ew, void* stream) {
+  int rc;
+  if ((rc = check_flag(fast, "fast")) || (rc = check_flag(accum, "accum"))) return rc;
+  if (ew && (rc = check_ewise(ew))) return rc;
+  const bool known = (a_fmt == BSM_E4M3 && (b_fmt == BSM_E4M3 || b_fmt == BSM_E2M1)) || (a_fmt == BSM_E2M1 && b_fmt == BSM_E2M1);
+  if (!known)
+    return fail(BSM_E_DTYPE, "a_fmt %d x b_fmt %d: grouped block-scaled GEMM takes E4M3 x E4M3, E4M3 x E2M1 or E2M1 x E2M1", a_fmt, b_fmt);
+  if (d_fmt != BSM_F32 && d_fmt != BSM_BF16) return fail(BSM_E_DTYPE, "d_fmt = %d is neither F32 nor BF16", d_fmt);
+  if (N < 0 || K < 0 || N > 0x7FFFFFFF || K > 0x7FFFFFFF)
+    return fail(BSM_E_SHAPE, "N, K = %lld, %lld out of range", (long long)N, (long long)K);
+  if (K % 32) return fail(BSM_E_SHAPE, "K = %lld is not a multiple of the 32-element scale block", (long long)K);
+  if ((rc = check_groups(rows, n_groups, offsets))) return rc;
+  if (rows == 0 || N == 0 || n_groups == 0) return ok();
+  if ((rc = check_out(D, N, ldd, d_fmt))) return rc;
+  const Range rd = block_range(D, 1, 0, rows, ldd, N, d_fmt == BSM_F32 ? 32 : 16);
+  if (overlap(rd, block_range(offsets, 1, 0, 1, 0, n_groups + int64_t(1), 32))) return fail(BSM_E_ALIAS, "offsets overlap D");
+  if (K > 0) {
+    const int ba = a_fmt == BSM_E2M1 ? 4 : 8, bb = b_fmt == BSM_E2M1 ? 4 : 8;
+    if (!A || !B || !SFA || !SFB) return fail(BSM_E_NULL, "A, B, SFA or SFB is NULL");
+    if ((uintptr_t)A % 16 || (uintptr_t)B % 16) return fail(BSM_E_ALIGN, "A and B must be 16-byte aligned");
+    if (lda < K || ldb < K) return fail(BSM_E_ALIGN, "lda = %lld, ldb = %lld must be >= K", (long long)lda, (long long)ldb);
+    if (lda > (int64_t(1) << 24) || ldb > (int64_t(1) << 24) || lda * ba / 8 > (int64_t(1) << 23) ||
+        ldb * bb / 8 > (int64_t(1) << 23) || ld_sfa > (int64_t(1) << 24) || ld_sfb > (int64_t(1) << 24))
+      return fail(BSM_E_SHAPE, "leading dimensions too large for 32-bit in-tile offsets");
+    if ((lda * ba) % 128 || (ldb * bb) % 128)
+      return fail(BSM_E_ALIGN, "lda = %lld, ldb = %lld: rows must start 16-byte aligned", (long long)lda, (long long)ldb);
+    if (ld_sfa < K / 32 || ld_sfb < K / 32) return fail(BSM_E_ALIGN, "ld_sfa, ld_sfb must be >= K/32");
+    if (ld_sfa % 4 || ld_sfb % 4 || (uintptr_t)SFA % 4 || (uintptr_t)SFB % 4)
+      return fail(BSM_E_ALIGN, "scale rows must start 4-byte aligned (SFA, SFB 4-byte aligned, ld_sfa, ld_sfb multiples of 4)");
+    if (stride_b < 0 || stride_b > (int64_t(1) << 44) || stride_sfb < 0 || stride_sfb > (int64_t(1) << 44))
+      return fail(BSM_E_SHAPE, "stride_b = %lld or stride_sfb = %lld out of range", (long long)stride_b, (long long)stride_sfb);
+    if ((stride_b * bb) % 128 || stride_sfb % 4)
+      return fail(BSM_E_ALIGN, "stride_b = %lld must be whole 16 bytes and stride_sfb = %lld a multiple of 4", (long long)stride_b, (long long)stride_sfb);
+    if (overlap(rd, block_range(A, 1, 0, rows, lda, K, ba)) || overlap(rd, block_range(B, n_groups, stride_b, N, ldb, K, bb)) ||
+        overlap(rd, block_range(SFA, 1, 0, rows, ld_sfa, ld_sfa, 8)) ||
+        overlap(rd, block_range(SFB, n_groups, stride_sfb, N, ld_sfb, ld_sfb, 8)))
+      return fail(BSM_E_ALIAS, "an operand or scale tensor overlaps D");
+  }
+  bsm::GemmArgs g{};
+  g.N = N; g.K = K; g.dtype = a_fmt; g.dtype_b = b_fmt;
+  g.A = A; g.lda = lda; g.a_kmajor = 1;
+  g.B = B; g.ldb = ldb; g.b_kmajor = 1;
+  g.SFA = SFA; g.ld_sfa = ld_sfa; g.SFB = SFB; g.ld_sfb = ld_sfb;
+  g.D = (float*)D; g.ldd = ldd; g.d_fmt = d_fmt; g.accum = accum; g.mx_window = fast;
+  if (ew) { g.ew_op = ew->op; g.ew_scale = ew->scale; g.ew_bias = ew->bias; }
+  bsm::GroupArgs gr{};
+  gr.offsets = offsets; gr.n = n_groups; gr.rows = (int32_t)rows; gr.stride_b = stride_b; gr.stride_sfb = stride_sfb;
+  hipError_t e = bsm::launch_gemm_grouped_mx(g, gr, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "bsm_gemm_grouped_block_scale");
+  return ok();
+}
+
+int64_t bsm_gemm_lora_workspace(int64_t rows, int64_t R) {
+  if (rows < 0 || rows > 0x7FFFFFFF) return fail(BSM_E_SHAPE, "rows = %lld out of range", (long long)rows);
+  if (R < 0 || R > 256) return fail(BSM_E_SHAPE, "R = %lld not in 0 .. 256", (long long)R);
+  ok();
+  return rows * ((R + 31) / 32 * 32) * 4;
+}
+
+int bsm_gemm_lora(int64_t rows, int64_t N, int64_t K, int64_t R, int32_t n_adapters, const int32_t* adapter, int32_t ab,
+                  const void* X, int64_t ldx, const void* W, int64_t ldw, const void* LA, int64_t ld_la,
+                  int64_t stride_la, const void* LB, int64_t ld_lb, int64_t stride_lb, const float* scale,
+                  void* workspace, int32_t d_fmt, void* D, int64_t ldd, int accum, const bsm_ewise* ew, void* stream) {
+  int rc;
+  if ((rc = check_flag(accum, "accum"))) return rc;
+  if (ew && (rc = check_ewise(ew))) return rc;
+  if (ab != BSM_F16 && ab != BSM_BF16) return fail(BSM_E_DTYPE, "ab = %d: bsm_gemm_lora takes F16 or BF16", ab);
+  if (d_fmt != BSM_F32 && d_fmt != ab) return fail(BSM_E_DTYPE, "d_fmt = %d is neither F32 nor the operands' format", d_fmt);
+  if (rows < 0 || N < 0 || K < 0 || rows > 0x7FFFFFFF || N > 0x7FFFFFFF || K > 0x7FFFFFFF)
+    return fail(BSM_E_SHAPE, "rows, N, K = %lld, %lld, %lld out of range", (long long)rows, (long long)N, (long long)K);
+  const int64_t wsb = bsm_gemm_lora_workspace(rows, R);
+  if (wsb < 0) return (int)wsb;
+  if (n_adapters < 0) return fail(BSM_E_SHAPE, "n_adapters = %d is negative", n_adapters);
+  if (rows == 0 || N == 0) return ok();
+  if ((rc = check_out(D, N, ldd, d_fmt))) return rc;
+  const Range rd = block_range(D, 1, 0, rows, ldd, N, d_fmt == BSM_F32 ? 32 : 16);
+  const bool adapters = K > 0 && R > 0 && n_adapters > 0;
+  if (K > 0) {
+    if (!X || !W) return fail(BSM_E_NULL, "X or W is NULL");
+    if ((uintptr_t)X % 16 || (uintptr_t)W % 16) return fail(BSM_E_ALIGN, "X and W must be 16-byte aligned");
+    if (ldx < K || ldx % 8) return fail(BSM_E_ALIGN, "ldx = %lld must be >= K and a multiple of 8", (long long)ldx);
+    if (ldw < K || ldw % 8) return fail(BSM_E_ALIGN, "ldw = %lld must be >= K and a multiple of 8", (long long)ldw);
+    if (ldx > (int64_t(1) << 22) || ldw > (int64_t(1) << 22))
+      return fail(BSM_E_SHAPE, "ldx, ldw must be at most 2^22 elements (32-bit in-tile offsets)");
+    if (overlap(rd, block_range(X, 1, 0, rows, ldx, K, 16)) || overlap(rd, block_range(W, 1, 0, N, ldw, K, 16)))
+      return fail(BSM_E_ALIAS, "X or W overlaps D");
+  }
+  if (adapters) {
+    if (!adapter || !LA || !LB || !scale || !workspace) return fail(BSM_E_NULL, "adapter, LA, LB, scale or workspace is NULL");
+    if ((uintptr_t)LA % 16 || (uintptr_t)LB % 16 || (uintptr_t)workspace % 16)
+      return fail(BSM_E_ALIGN, "LA, LB and workspace must be 16-byte aligned");
+    if ((uintptr_t)adapter % 4 || (uintptr_t)scale % 4) return fail(BSM_E_ALIGN, "adapter and scale must be 4-byte aligned");
+    if (ld_la < K || ld_la % 8) return fail(BSM_E_ALIGN, "ld_la = %lld must be >= K and a multiple of 8", (long long)ld_la);
+    if (ld_lb < R || ld_lb % 8) return fail(BSM_E_ALIGN, "ld_lb = %lld must be >= R and a multiple of 8", (long long)ld_lb);
+    if (ld_la > (int64_t(1) << 22) || ld_lb > (int64_t(1) << 22))
+      return fail(BSM_E_SHAPE, "ld_la, ld_lb must be at most 2^22 elements");
+    if (stride_la < 0 || stride_lb < 0 || stride_la > (int64_t(1) << 44) || stride_lb > (int64_t(1) << 44))
+      return fail(BSM_E_SHAPE, "stride_la = %lld or stride_lb = %lld out of range", (long long)stride_la, (long long)stride_lb);
+    if (stride_la % 8 || stride_lb % 8) return fail(BSM_E_ALIGN, "stride_la and stride_lb must be multiples of 8");
+    const Range rw{(uintptr_t)workspace, (uintptr_t)workspace + (uintptr_t)wsb};
+    const Range in[] = {block_range(LA, n_adapters, stride_la, R, ld_la, K, 16), block_range(LB, n_adapters, stride_lb, N, ld_lb, R, 16),
+                        block_range(adapter, 1, 0, 1, 0, rows, 32), block_range(scale, 1, 0, 1, 0, n_adapters, 32),
+                        block_range(X, 1, 0, rows, ldx, K, 16), block_range(W, 1, 0, N, ldw, K, 16)};
+    for (const Range& r : in)
+      if (overlap(rd, r) || overlap(rw, r)) return fail(BSM_E_ALIAS, "an input overlaps D or the workspace");
+    if (overlap(rd, rw)) return fail(BSM_E_ALIAS, "the workspace overlaps D");
+  }
+  bsm::GemmArgs g{};
+  g.M = rows; g.N = N; g.K = K; g.dtype = ab;
+  g.A = X; g.lda = ldx; g.a_kmajor = 1;
+  g.B = W; g.ldb = ldw; g.b_kmajor = 1;
+  g.D = (float*)D; g.ldd = ldd; g.d_fmt = d_fmt; g.accum = accum;
+  if (ew) { g.ew_op = ew->op; g.ew_scale = ew->scale; g.ew_bias = ew->bias; }
+  bsm::LoraArgs lo{};
+  if (adapters) {
+    lo.n = n_adapters; lo.R = (int32_t)R; lo.adapter = adapter; lo.scale = scale; lo.U = (float*)workspace;
+    lo.LA = LA; lo.ld_la = ld_la; lo.stride_la = stride_la;
+    lo.LB = LB; lo.ld_lb = ld_lb; lo.stride_lb = stride_lb;
+  }
+  hipError_t e = bsm::launch_gemm_lora(g, lo, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "bsm_gemm_lora");
+  return ok();
+}
+
 int bsm_tile_add_scalar_f32(const float* src, float* dst, int64_t n, float s, void* stream) {
   if (n < 0) return fail(BSM_E_SHAPE, "n = %lld is negative", (long long)n);
   if (n == 0) return ok();

@@ -101,6 +101,23 @@ hipError_t launch_gemm_grouped(const GemmArgs& a, const GroupArgs& gr, hipStream
 // a.K unused; M, N > 0, n > 0; A and B MN-major (rows of M and N elements).
 hipError_t launch_gemm_grouped_wgrad(const GemmArgs& a, const GroupArgs& gr, hipStream_t st);
 
+// Block scaled: E4M3 x E4M3 (mx_window chooses the route), E4M3 x E2M1 (likewise), E2M1 x E2M1; d_fmt F32
+// or BF16. The second launches the pairings and routes that the general kernel serves.
+hipError_t launch_gemm_grouped_mx(const GemmArgs& a, const GroupArgs& gr, hipStream_t st);
+hipError_t launch_gemm_grouped_mx_any(const GemmArgs& a, const GroupArgs& gr, hipStream_t st);
+
+// Low-rank adapters chosen per row (lora.hpp): row t adds U[t] LB_a^T, U[t] = scale_a X[t] LA_a^T.
+struct LoraArgs {
+  int32_t n, R;                              // adapters, rank (either 0: the projection alone)
+  const int32_t* adapter;                    // DEVICE, one per row; outside 0 .. n - 1: none
+  const void* LA; int64_t ld_la, stride_la;  // (R, K) per adapter
+  const void* LB; int64_t ld_lb, stride_lb;  // (N, R) per adapter
+  const float* scale;                        // DEVICE, n values
+  float* U;                                  // workspace, M rows of R rounded up to 32
+};
+// a.A K-major (M, K), a.B K-major (N, K); M, N > 0.
+hipError_t launch_gemm_lora(const GemmArgs& a, const LoraArgs& lo, hipStream_t st);
+
 // Diagnostics (k_diag.hip): the box copy's traffic mix on flat bf16 buffers of n elements
 // (n a multiple of 8, 16-byte aligned), and workgroups x 256 lanes of back-to-back MFMAs of
 // `kind` (BSM_BF16, BSM_E4M3, BSM_E2M1), iters x 16 per wave, one float per lane to out.

@@ -1,0 +1,136 @@
+// lora.hpp - low-rank adapters chosen per row: what the shrink and the expand share.
+//
+//   D[t, n] = f((D[t, n] +) sum_k X[t, k] W[n, k] + sum_r U[t, r] LB_a[n, r]),
+//   U[t, r] = scale_a * sum_k X[t, k] LA_a[r, k],      a = adapter[t] (outside 0 .. n - 1: none)
+//
+// U is kept in float32 in the caller's workspace, rows of Rp = R rounded up to 32 values, those past
+// R zero; rows without an adapter are not written and never read.
+//
+// A 16-row block of the matrix instruction may hold rows of up to 16 adapters. The block is worked
+// off adapter by adapter with the other rows' operand zeroed, so a row's sum only ever sees its own
+// adapter's weights: requests in any order need no sorting, and long requests cost one pass.
+#pragma once
+#include "bsm_device.hpp"
+#include "bsm_internal.hpp"
+#include "../../include/bsm.h"
+
+namespace bsm {
+namespace lora {
+
+__host__ __device__ inline int64_t padded_rank(int64_t R) { return (R + 31) / 32 * 32; }
+
+// The adapter of row t (lane-wise), -1 for none and for rows past the last.
+__device__ __forceinline__ int adapter_of(const LoraArgs& lo, int64_t t, int64_t rows) {
+  const int a = lo.n > 0 && t < rows ? lo.adapter[t] : -1;
+  return a < lo.n ? a : -1;
+}
+
+// id: lane l's value is row l%16's adapter. Bit i of the result (i < 16): row i has an adapter that
+// no earlier row of the block has.
+__device__ __forceinline__ uint32_t first_rows(int id, int lane) {
+  bool first = id >= 0;
+#pragma unroll
+  for (int j = 0; j < 15; j++) {
+    const int v = __builtin_amdgcn_readlane(id, j);
+    if ((lane & 15) > j && v == id) first = false;
+  }
+  return (uint32_t)__ballot(first) & 0xFFFFu;
+}
+
+// 8 consecutive elements (16 bytes) of a 16-bit row, those at or past `left` elements zero.
+__device__ __forceinline__ uint4 load8(const uint16_t* p, int64_t left) {
+  if (left <= 0) return make_uint4(0, 0, 0, 0);
+  uint4 v = *(const uint4*)p;
+  if (left < 8) {
+    uint32_t wd[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int d = 0; d < 4; d++) {
+      const int64_t n = left - 2 * d;
+      wd[d] &= n >= 2 ? 0xFFFFFFFFu : (n == 1 ? 0xFFFFu : 0u);
+    }
+    v = make_uint4(wd[0], wd[1], wd[2], wd[3]);
+  }
+  return v;
+}
+
+template <int DT>
+__device__ __forceinline__ f32x4 mfma16(uint4 b, uint4 a, f32x4 c) {
+  if constexpr (DT == BSM_BF16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, b), __builtin_bit_cast(f16x8, a), c, 0, 0, 0);
+}
+
+// One 32-value step of a row's U: what the lane (row l%16, r 8(l/16) .. +7) holds.
+struct UPart { float v[8]; };
+
+__device__ __forceinline__ UPart load_u(const float* U, int64_t Rp, int64_t t, int r0, int lane, bool mine) {
+  UPart u;
+  if (mine) {
+    const float4* p = (const float4*)(U + t * Rp + r0 + 8 * (lane >> 4));
+    const float4 x = p[0], y = p[1];
+    u.v[0] = x.x; u.v[1] = x.y; u.v[2] = x.z; u.v[3] = x.w;
+    u.v[4] = y.x; u.v[5] = y.y; u.v[6] = y.z; u.v[7] = y.w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; e++) u.v[e] = 0.f;
+  }
+  return u;
+}
+
+// A float32 as a sum of bf16 terms cut off from the top (8 significant bits each, so three hold all
+// 24 and nothing rounds or overflows): the upper half of the word, then the rest. An infinity has no
+// rest; a NaN's rest is NaN.
+__device__ __forceinline__ uint32_t top_bits(float v) { return __float_as_uint(v) & 0xFFFF0000u; }
+__device__ __forceinline__ float rest_of(float v) {
+  const float t = __uint_as_float(top_bits(v));
+  return v == t ? 0.f : v - t;
+}
+// The top terms of eight values as an operand of the bf16 matrix instruction; v becomes the rests.
+__device__ __forceinline__ uint4 cut_top(float (&v)[8]) {
+  uint32_t o[4];
+#pragma unroll
+  for (int e = 0; e < 4; e++) {
+    o[e] = (top_bits(v[2 * e]) >> 16) | top_bits(v[2 * e + 1]);
+    v[2 * e] = rest_of(v[2 * e]);
+    v[2 * e + 1] = rest_of(v[2 * e + 1]);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// One 32-value step of U as three bf16 operands, U = t[0] + t[1] + t[2] (to float32's last bit, values
+// near its subnormals aside).
+struct USplit { uint4 t[3]; };
+__device__ __forceinline__ USplit split_u(UPart u) {
+  USplit s;
+#pragma unroll
+  for (int q = 0; q < 3; q++) s.t[q] = cut_top(u.v);
+  return s;
+}
+
+// U (16 rows x 32) LB^T (32 x 16 columns) with U at float32 precision on the bf16 matrix instruction:
+// three products with bf16 weights, six with f16 ones (11 bits: two bf16 terms), the small terms
+// first. U rounded to 16 bits instead would cost one, and an error of 2^-9 (2^-12) of the adapter's
+// part; the float32 matrix instruction takes 8 for the same 32 values at an eighth of the rate.
+template <int DT>
+__device__ __forceinline__ f32x4 expand_step(const USplit& u, uint4 b) {
+  f32x4 d = {0.f, 0.f, 0.f, 0.f};
+  if constexpr (DT == BSM_BF16) {
+#pragma unroll
+    for (int q = 2; q >= 0; q--) d = mfma16<BSM_BF16>(b, u.t[q], d);
+  } else {
+    const uint32_t wd[4] = {b.x, b.y, b.z, b.w};
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; e++) v[e] = f16_bits_to_f32((uint16_t)(wd[e >> 1] >> (16 * (e & 1))));
+    const uint4 hi = cut_top(v), lo = cut_top(v);
+#pragma unroll
+    for (int q = 2; q >= 0; q--) d = mfma16<BSM_BF16>(lo, u.t[q], d);
+#pragma unroll
+    for (int q = 2; q >= 0; q--) d = mfma16<BSM_BF16>(hi, u.t[q], d);
+  }
+  return d;
+}
+
+}  // namespace lora
+}  // namespace bsm

@@ -362,6 +362,55 @@ int bsm_gemm_grouped_wgrad(int64_t rows, int64_t M, int64_t N, int32_t n_groups,
                            const void* A, int64_t lda, const void* B, int64_t ldb, int32_t d_fmt, void* D, int64_t ldd,
                            int64_t stride_d, int accum, void* stream);
 
+/* bsm_gemm_grouped with block-scaled operands, both K-major, e.g. the experts of a served
+ * model: for the rows r of group g
+ *   D[r,n] = f(x),  x = (accum ? D[r,n] : 0) + sum_k A(r,k) * B_g(n,k),
+ *   A(r,k) = dec(A[r*lda + k]) * 2^(SFA[r*ld_sfa + k/32] - 127),
+ *   B_g(n,k) = dec(B[g*stride_b + n*ldb + k]) * 2^(SFB[g*stride_sfb + n*ld_sfb + k/32] - 127).
+ *   a_fmt x b_fmt: E4M3 x E4M3, E4M3 x E2M1 or E2M1 x E2M1 (else BSM_E_DTYPE);
+ *   fast:       0: the precision of bsm_gemm_block_scale (products summed exactly, 1e-5 *
+ *               sum_k |a b|); 1: that of bsm_gemm_block_scale_fastacc is accepted (a block's
+ *               products summed on a grid of 2^-13 of its largest), which runs large groups at the
+ *               full 8-bit rate;
+ *   stride_b:   elements between the groups' weights, >= 0, a multiple of 16 bytes (0: one weight);
+ *   stride_sfb: bytes between their scales, >= 0, a multiple of 4;
+ *   d_fmt:      BSM_F32 or BSM_BF16.
+ * rows, offsets, n_groups, D, ldd, accum and ew as for bsm_gemm_grouped; element formats,
+ * alignment, leading dimensions and K (a multiple of 32) as for bsm_gemm_block_scale. A, B, SFA,
+ * SFB and offsets must not overlap D. */
+int bsm_gemm_grouped_block_scale(int64_t rows, int64_t N, int64_t K, int32_t n_groups, const int32_t* offsets,
+                                 int32_t a_fmt, const void* A, int64_t lda, const uint8_t* SFA, int64_t ld_sfa,
+                                 int32_t b_fmt, const void* B, int64_t ldb, int64_t stride_b, const uint8_t* SFB,
+                                 int64_t ld_sfb, int64_t stride_sfb, int fast, int32_t d_fmt, void* D, int64_t ldd,
+                                 int accum, const bsm_ewise* ew, void* stream);
+
+/* A shared projection with a low-rank adapter chosen per row, for many requests at once:
+ *   D[t,n] = f(x),  x = (accum ? D[t,n] : 0) + sum_k X(t,k) * W(n,k)
+ *                       + sum_r U(t,r) * LB_a(n,r),   U(t,r) = scale[a] * sum_k X(t,k) * LA_a(r,k),
+ * a = adapter[t]; a row whose adapter lies outside 0 .. n_adapters - 1 (say -1) has none. Products
+ * and sums in float32, U kept in float32 (both call and caller may rely on it: the adapter's part
+ * is not rounded to the operands' format), D rounded once.
+ *   rows, N, K, R: R is the adapters' rank, 0 .. 256 (0: the projection alone; adapters of a smaller
+ *              rank are padded with zero rows of LA or zero columns of LB);
+ *   adapter:   DEVICE array of `rows` int32, 4-byte aligned, any order and repetition;
+ *   ab:        BSM_F16 or BSM_BF16 (X, W, LA and LB);
+ *   X, W:      X(t,k) = X[t*ldx + k], W(n,k) = W[n*ldw + k];
+ *   LA, LB:    adapter a's at LA + a*stride_la, LB + a*stride_lb elements: LA_a(r,k) = [r*ld_la + k]
+ *              (ld_la >= K), LB_a(n,r) = [n*ld_lb + r] (ld_lb >= R); strides >= 0, multiples of 8;
+ *   scale:     DEVICE array of n_adapters float32, 4-byte aligned;
+ *   workspace: DEVICE, 16-byte aligned, bsm_gemm_lora_workspace(rows, R) bytes; holds U between
+ *              the call's kernels and nothing from one call to the next. Calls that may run at the
+ *              same time (other streams, other graphs) need one each;
+ *   d_fmt, D, ldd, accum, ew as for bsm_gemm_grouped; alignment, whole-row buffers and leading
+ *              dimensions (at most 2^22) as for bsm_gemm.
+ * K == 0 gives D = f(accum ? D : 0). No input may overlap D or the workspace. */
+int bsm_gemm_lora(int64_t rows, int64_t N, int64_t K, int64_t R, int32_t n_adapters, const int32_t* adapter, int32_t ab,
+                  const void* X, int64_t ldx, const void* W, int64_t ldw, const void* LA, int64_t ld_la,
+                  int64_t stride_la, const void* LB, int64_t ld_lb, int64_t stride_lb, const float* scale,
+                  void* workspace, int32_t d_fmt, void* D, int64_t ldd, int accum, const bsm_ewise* ew, void* stream);
+/* Bytes of that workspace, or a negative status for rows or R out of range. */
+int64_t bsm_gemm_lora_workspace(int64_t rows, int64_t R);
+
 /* Element-wise scalar add on float32 ([TOE] "A Load, Compute, and Store Example"
  * adds one to a (2,32,3,4) tile; [TP] "Scalar compositions"): dst[i] = src[i] + s,
  * i < n, each lane moving 16-byte vectors. src, dst 16-byte aligned; they may be

@@ -85,3 +85,64 @@ def test_tensors_of_the_host_are_refused():
         expect("BSM_E_ARG", fn, a=t)
         expect("BSM_E_ARG", fn, offsets=off)
         expect("BSM_E_ARG", fn, d=t)
+
+
+SA, SB = FAKE + (4 << 36), FAKE + (5 << 36)
+
+
+def mx(rows=100, N=64, K=128, n_groups=4, offsets=OFF, a_fmt="e4m3", a=A, lda=128, sa=SA, ld_sfa=4, b_fmt="e4m3", b=B, ldb=128,
+       stride_b=8192, sb=SB, ld_sfb=4, stride_sfb=256, fast=0, d_fmt="bf16", d=D, ldd=64, accum=0, ew=None):
+    bsm.bsm_gemm_grouped_block_scale(rows, N, K, n_groups, offsets, a_fmt, a, lda, sa, ld_sfa, b_fmt, b, ldb, stride_b, sb, ld_sfb,
+                                     stride_sfb, fast, d_fmt, d, ldd, accum, ew, 0)
+
+
+def test_block_scaled_refusals():
+    for name, bad in (("BSM_E_NULL", dict(offsets=0)), ("BSM_E_NULL", dict(a=0)), ("BSM_E_NULL", dict(sa=0)),
+                      ("BSM_E_NULL", dict(sb=0)), ("BSM_E_NULL", dict(d=0)), ("BSM_E_ALIGN", dict(a=A + 8)),
+                      ("BSM_E_ALIGN", dict(sa=SA + 2)), ("BSM_E_ALIGN", dict(sb=SB + 1)), ("BSM_E_ALIGN", dict(lda=112)),
+                      ("BSM_E_ALIGN", dict(lda=136)), ("BSM_E_ALIGN", dict(ldb=130)), ("BSM_E_ALIGN", dict(ld_sfa=6)),
+                      ("BSM_E_ALIGN", dict(K=256, lda=256, ldb=256, ld_sfb=4)), ("BSM_E_ALIGN", dict(stride_b=8200)),
+                      ("BSM_E_ALIGN", dict(stride_sfb=258)), ("BSM_E_SHAPE", dict(stride_b=-128)),
+                      ("BSM_E_SHAPE", dict(stride_sfb=-4)), ("BSM_E_SHAPE", dict(K=100)), ("BSM_E_SHAPE", dict(rows=1 << 31)),
+                      ("BSM_E_SHAPE", dict(n_groups=65537)), ("BSM_E_SHAPE", dict(lda=1 << 24)),
+                      ("BSM_E_DTYPE", dict(a_fmt="e2m1")), ("BSM_E_DTYPE", dict(b_fmt="e5m2")), ("BSM_E_DTYPE", dict(a_fmt="bf16")),
+                      ("BSM_E_DTYPE", dict(d_fmt="f16")), ("BSM_E_ARG", dict(fast=2)), ("BSM_E_ARG", dict(accum=-1)),
+                      ("BSM_E_ALIAS", dict(a=D + 1024)), ("BSM_E_ALIAS", dict(sa=D + 64)), ("BSM_E_ALIAS", dict(b=D - 8192)),
+                      ("BSM_E_ALIAS", dict(sb=D - 512)), ("BSM_E_ALIAS", dict(offsets=D + 4))):
+        expect(name, mx, **bad)
+    mx(rows=0, a=0, sa=0, b=0, sb=0, d=0)
+    mx(N=0, a=0, sa=0, b=0, sb=0, d=0)
+    mx(n_groups=0, offsets=0, a=0, d=0)
+    expect("BSM_E_ARG", mx, a=torch.zeros(64, dtype=torch.uint8))
+
+
+WS, AD, SC = FAKE + (6 << 36), FAKE + (7 << 36), FAKE + (8 << 36)
+
+
+def lora(rows=100, N=64, K=64, R=16, n=4, adapter=AD, ab="bf16", x=A, ldx=64, w=B, ldw=64, la=SA, ld_la=64, stride_la=1024, lb=SB,
+         ld_lb=16, stride_lb=1024, scale=SC, ws=WS, d_fmt="bf16", d=D, ldd=64, accum=0, ew=None):
+    bsm.bsm_gemm_lora(rows, N, K, R, n, adapter, ab, x, ldx, w, ldw, la, ld_la, stride_la, lb, ld_lb, stride_lb, scale, ws, d_fmt, d,
+                      ldd, accum, ew, 0)
+
+
+def test_adapter_refusals():
+    for name, bad in (("BSM_E_NULL", dict(x=0)), ("BSM_E_NULL", dict(w=0)), ("BSM_E_NULL", dict(la=0)), ("BSM_E_NULL", dict(lb=0)),
+                      ("BSM_E_NULL", dict(adapter=0)), ("BSM_E_NULL", dict(scale=0)), ("BSM_E_NULL", dict(ws=0)),
+                      ("BSM_E_NULL", dict(d=0)), ("BSM_E_ALIGN", dict(x=A + 2)), ("BSM_E_ALIGN", dict(la=SA + 8)),
+                      ("BSM_E_ALIGN", dict(ws=WS + 4)), ("BSM_E_ALIGN", dict(adapter=AD + 1)), ("BSM_E_ALIGN", dict(scale=SC + 2)),
+                      ("BSM_E_ALIGN", dict(ldx=60)), ("BSM_E_ALIGN", dict(ldw=56)), ("BSM_E_ALIGN", dict(ld_la=56)),
+                      ("BSM_E_ALIGN", dict(ld_lb=8)), ("BSM_E_ALIGN", dict(ld_lb=20)), ("BSM_E_ALIGN", dict(stride_la=1028)),
+                      ("BSM_E_ALIGN", dict(stride_lb=1020)), ("BSM_E_ALIGN", dict(ldd=60)), ("BSM_E_SHAPE", dict(R=257)),
+                      ("BSM_E_SHAPE", dict(R=-1)), ("BSM_E_SHAPE", dict(rows=-1)), ("BSM_E_SHAPE", dict(n=-1)),
+                      ("BSM_E_SHAPE", dict(stride_la=-8)), ("BSM_E_SHAPE", dict(ld_la=1 << 23)), ("BSM_E_DTYPE", dict(ab="e4m3")),
+                      ("BSM_E_DTYPE", dict(d_fmt="f16")), ("BSM_E_ARG", dict(accum=2)), ("BSM_E_ARG", dict(ew=bsm.ewise_desc(9))),
+                      ("BSM_E_ALIAS", dict(x=D + 64)), ("BSM_E_ALIAS", dict(ws=D + 64)), ("BSM_E_ALIAS", dict(ws=B)),
+                      ("BSM_E_ALIAS", dict(adapter=WS + 4)), ("BSM_E_ALIAS", dict(lb=D - 2 * 3 * 1024))):
+        expect(name, lora, **bad)
+    lora(rows=0, x=0, w=0, d=0)
+    lora(N=0, x=0, w=0, d=0)
+    assert bsm.bsm_gemm_lora_workspace(100, 16) == 100 * 32 * 4
+    assert bsm.bsm_gemm_lora_workspace(0, 16) == 0 == bsm.bsm_gemm_lora_workspace(7, 0)
+    for rows, R in ((-1, 8), (8, 300), (1 << 31, 8)):
+        expect("BSM_E_SHAPE", bsm.bsm_gemm_lora_workspace, rows=rows, R=R)
+    expect("BSM_E_ARG", lora, scale=torch.ones(4))

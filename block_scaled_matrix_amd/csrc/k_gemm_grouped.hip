@@ -8,6 +8,7 @@
 // group's row count. Rows past a group's end are other groups' rows: they are clamped away on the
 // load (grouped) or zeroed (wgrad, the partial last K tile) and never stored.
 #include "gemm_dense_tile.hpp"
+#include "gemm_mid_tile.hpp"
 #include "store16.hpp"
 #include "grouped.hpp"
 
@@ -73,12 +74,42 @@ __global__ __launch_bounds__(256, 1) void k_grouped_wgrad(GemmArgs a, GroupArgs 
                 (int64_t)tn * BN + 128 * (w & 1), lane, acc, lds + 32768 * w);
 }
 
+// The product of one group of rows out of the call's: operands and output moved to it.
+__device__ __forceinline__ GemmArgs group_product(const GemmArgs& a, const GroupArgs& gr, int g, int row0, int rows) {
+  GemmArgs t = a;
+  t.M = rows;
+  t.A = (const uint16_t*)a.A + (int64_t)row0 * a.lda;
+  t.B = (const uint16_t*)a.B + (int64_t)g * gr.stride_b;
+  t.D = (float*)row_ptr(a, (int64_t)row0 * a.ldd);
+  return t;
+}
+
+// Groups of few rows: tiles of 128 rows, a group's last one of as few as hold its rows.
+template <int DT, bool BKM>
+__global__ __launch_bounds__(256, 2) void k_grouped_mid(GemmArgs a, GroupArgs gr, int tiles_n) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[mid::LDS_BYTES];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  grouped::Spot s;
+  if (!grouped::find_tile<128, 4>(gr, blockIdx.x, tiles_n, lane, s)) return;
+  const GemmArgs t = group_product(a, gr, s.g, s.row0, s.rows);
+  const int64_t m0 = 128 * (int64_t)s.tm, n0 = mid::BN * (int64_t)s.tn;
+  const int left = s.rows - 128 * s.tm;
+  if (left <= 32) mid::tile<DT, 32, true, BKM>(t, m0, n0, lds, lane, w);
+  else if (left <= 64) mid::tile<DT, 64, true, BKM>(t, m0, n0, lds, lane, w);
+  else mid::tile<DT, 128, true, BKM>(t, m0, n0, lds, lane, w);
+}
+
 template <int DT>
 hipError_t launch_grouped_dt(const GemmArgs& a, const GroupArgs& gr, hipStream_t st) {
-  const int64_t tn = (a.N + BN - 1) / BN, n = (grouped::most_row_tiles(gr.rows, gr.n, BM) * tn + 7) / 8 * 8;
+  const bool big = gr.rows / gr.n >= 192;
+  const int bm = big ? BM : 128, bn = big ? BN : mid::BN;
+  const int64_t tn = (a.N + bn - 1) / bn, n = (grouped::most_row_tiles(gr.rows, gr.n, bm) * tn + 7) / 8 * 8;
   if (n > 0x7FFFFFFF) return hipErrorInvalidValue;
   const dim3 grid((uint32_t)n);
-  if (a.b_kmajor) hipLaunchKernelGGL((k_grouped<DT, true>), grid, dim3(256), 0, st, a, gr, (int)tn);
+  if (!big) {
+    if (a.b_kmajor) hipLaunchKernelGGL((k_grouped_mid<DT, true>), grid, dim3(256), 0, st, a, gr, (int)tn);
+    else hipLaunchKernelGGL((k_grouped_mid<DT, false>), grid, dim3(256), 0, st, a, gr, (int)tn);
+  } else if (a.b_kmajor) hipLaunchKernelGGL((k_grouped<DT, true>), grid, dim3(256), 0, st, a, gr, (int)tn);
   else hipLaunchKernelGGL((k_grouped<DT, false>), grid, dim3(256), 0, st, a, gr, (int)tn);
   return hipGetLastError();
 }

@@ -3,10 +3,11 @@
 //   grouped:  D[r, n] = f((D[r, n] +) sum_k A[r, k] B_g(n, k))      r in group g
 //   wgrad:    D_g[m, n] = (D_g[m, n] +) sum_{r in group g} A[r, m] B[r, n]
 //
-// Large groups run the dense GEMM's 256 x 256 tile (gemm_dense_tile.hpp) on the group's rows: the
-// operands' bases move to the group's first row and its weight, M (grouped) or K (wgrad) is the
-// group's row count. Rows past a group's end are other groups' rows: they are clamped away on the
-// load (grouped) or zeroed (wgrad, the partial last K tile) and never stored.
+// A tile works on one group's product: the operands' bases move to the group's first row and its
+// weight, M (grouped) or K (wgrad) is the group's row count. Rows past a group's end are other groups'
+// rows: they are clamped away on the load (grouped) or zeroed (wgrad, the partial last K tile) and
+// never stored. Two tiles: the dense GEMM's 256 x 256 (gemm_dense_tile.hpp) and 32 / 64 / 128 x 128
+// (gemm_mid_tile.hpp).
 #include "gemm_dense_tile.hpp"
 #include "gemm_mid_tile.hpp"
 #include "store16.hpp"
@@ -49,17 +50,24 @@ __global__ __launch_bounds__(256, 1) void k_grouped(GemmArgs a, GroupArgs gr, in
                 (int64_t)s.tn * BN + 128 * (w & 1), lane, acc, lds + 32768 * w);
 }
 
-// Workgroup p: tile of group (p's number) / (tiles_m * tiles_n), dealt to the XCDs in contiguous
-// ranges when their number divides by eight.
-template <int DT>
-__global__ __launch_bounds__(256, 1) void k_grouped_wgrad(GemmArgs a, GroupArgs gr, int tiles_m, int tiles_n) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * STAGE_BYTES];
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int per = tiles_m * tiles_n, total = per * gr.n, pid = blockIdx.x;
-  const int lid = (total & 7) == 0 ? (pid & 7) * (total >> 3) + (pid >> 3) : pid;
-  const int g = lid / per, in = lid - g * per;
+// Workgroup p runs on XCD p % 8. Every XCD gets a contiguous eighth of each group's tiles (groups in
+// turn), so that the groups' row counts, which are the tiles' lengths here, do not unbalance the XCDs,
+// while the tiles that share a group's panels still meet in one L2.
+struct WgradSpot { int g, tm, tn; };
+__device__ __forceinline__ bool wgrad_tile(int pid, int n, int tiles_m, int tiles_n, WgradSpot& s) {
+  const int per = tiles_m * tiles_n, share = (per + 7) >> 3;
+  const int x = pid & 7, q = pid >> 3;
+  s.g = q / share;
+  const int in = x * share + (q - s.g * share);
+  if (in >= per) return false;
   const int band = in / (4 * tiles_n), size = min(tiles_m - 4 * band, 4), li = in - band * 4 * tiles_n;
-  const int tm = 4 * band + li % size, tn = li / size;
+  s.tm = 4 * band + li % size;
+  s.tn = li / size;
+  return true;
+}
+
+// One group's weight gradient out of the call's: K is its row count.
+__device__ __forceinline__ GemmArgs wgrad_product(const GemmArgs& a, const GroupArgs& gr, int g) {
   int lo, hi;
   grouped::group_range(gr, g, lo, hi);
   lo = __builtin_amdgcn_readfirstlane(lo);
@@ -68,10 +76,17 @@ __global__ __launch_bounds__(256, 1) void k_grouped_wgrad(GemmArgs a, GroupArgs 
   t.K = hi - lo;
   t.A = (const uint16_t*)a.A + (int64_t)lo * a.lda;
   t.B = (const uint16_t*)a.B + (int64_t)lo * a.ldb;
-  f32x4 acc[8][8];
-  tile_product<DT, false, false>(t, tm, tn, lds, lane, w, acc);
-  store_out<DT>(a, row_ptr(a, (int64_t)g * gr.stride_d), a.M, (int64_t)tm * BM + 128 * (w >> 1),
-                (int64_t)tn * BN + 128 * (w & 1), lane, acc, lds + 32768 * w);
+  t.D = (float*)row_ptr(a, (int64_t)g * gr.stride_d);
+  return t;
+}
+
+template <int DT>
+__global__ __launch_bounds__(256, 2) void k_grouped_wgrad(GemmArgs a, GroupArgs gr, int tiles_m, int tiles_n) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[mid::LDS_BYTES];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  WgradSpot s;
+  if (!wgrad_tile(blockIdx.x, gr.n, tiles_m, tiles_n, s)) return;
+  mid::tile<DT, 128, false, false>(wgrad_product(a, gr, s.g), 128 * (int64_t)s.tm, 128 * (int64_t)s.tn, lds, lane, w);
 }
 
 // The product of one group of rows out of the call's: operands and output moved to it.
@@ -101,7 +116,12 @@ __global__ __launch_bounds__(256, 2) void k_grouped_mid(GemmArgs a, GroupArgs gr
 
 template <int DT>
 hipError_t launch_grouped_dt(const GemmArgs& a, const GroupArgs& gr, hipStream_t st) {
-  const bool big = gr.rows / gr.n >= 192;
+  // The 256 x 256 tile only where groups fill it and there are four rounds of it over the 256 CUs:
+  // 16381 rows over 16 groups, N 4096, K 8192 (1152 tiles) 1155 us against 1180 us on 128 x 128
+  // tiles; 8190 rows over 8 groups, N 2048, K 8192 (288 tiles, the second round nearly empty) 400 us
+  // against 364 us.
+  const int64_t tiles = (gr.rows + BM - 1) / BM * ((a.N + BN - 1) / BN);
+  const bool big = gr.rows / gr.n >= 192 && tiles >= 1024;
   const int bm = big ? BM : 128, bn = big ? BN : mid::BN;
   const int64_t tn = (a.N + bn - 1) / bn, n = (grouped::most_row_tiles(gr.rows, gr.n, bm) * tn + 7) / 8 * 8;
   if (n > 0x7FFFFFFF) return hipErrorInvalidValue;
@@ -120,13 +140,18 @@ hipError_t launch_gemm_grouped(const GemmArgs& a, const GroupArgs& gr, hipStream
   return a.dtype == BSM_BF16 ? launch_grouped_dt<BSM_BF16>(a, gr, st) : launch_grouped_dt<BSM_F16>(a, gr, st);
 }
 
-hipError_t launch_gemm_grouped_wgrad(const GemmArgs& a, const GroupArgs& gr, hipStream_t st) {
-  const int64_t tm = (a.M + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
-  if (tm * tn * gr.n > 0x7FFFFFFF) return hipErrorInvalidValue;
-  const dim3 grid((uint32_t)(tm * tn * gr.n));
-  if (a.dtype == BSM_BF16) hipLaunchKernelGGL(k_grouped_wgrad<BSM_BF16>, grid, dim3(256), 0, st, a, gr, (int)tm, (int)tn);
-  else hipLaunchKernelGGL(k_grouped_wgrad<BSM_F16>, grid, dim3(256), 0, st, a, gr, (int)tm, (int)tn);
+template <int DT>
+static hipError_t launch_wgrad_dt(const GemmArgs& a, const GroupArgs& gr, hipStream_t st) {
+  // 128 x 128 tiles always: on 256 x 256 ones 8 groups of 16381 rows (M 4096, N 2048) took 350 us
+  // against 331 us, and 32 groups of 1021 rows (M 1000, N 520) 40 us against 18.5 us.
+  const int64_t tm = (a.M + 127) / 128, tn = (a.N + 127) / 128, share = (tm * tn + 7) / 8;
+  if (share > 0x7FFFFFFF / 8 / gr.n) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(k_grouped_wgrad<DT>, dim3((uint32_t)(share * 8 * gr.n)), dim3(256), 0, st, a, gr, (int)tm, (int)tn);
   return hipGetLastError();
+}
+
+hipError_t launch_gemm_grouped_wgrad(const GemmArgs& a, const GroupArgs& gr, hipStream_t st) {
+  return a.dtype == BSM_BF16 ? launch_wgrad_dt<BSM_BF16>(a, gr, st) : launch_wgrad_dt<BSM_F16>(a, gr, st);
 }
 
 }  // namespace bsm

@@ -102,9 +102,11 @@ hipError_t launch_gemm_grouped(const GemmArgs& a, const GroupArgs& gr, hipStream
 hipError_t launch_gemm_grouped_wgrad(const GemmArgs& a, const GroupArgs& gr, hipStream_t st);
 
 // Block scaled: E4M3 x E4M3 (mx_window chooses the route), E4M3 x E2M1 (likewise), E2M1 x E2M1; d_fmt F32
-// or BF16. The second launches the pairings and routes that the general kernel serves.
+// or BF16. The second launches the pairings and routes that the general kernel serves, the third
+// the tiles for groups of few rows.
 hipError_t launch_gemm_grouped_mx(const GemmArgs& a, const GroupArgs& gr, hipStream_t st);
 hipError_t launch_gemm_grouped_mx_any(const GemmArgs& a, const GroupArgs& gr, hipStream_t st);
+hipError_t launch_gemm_grouped_mx_mid(const GemmArgs& a, const GroupArgs& gr, hipStream_t st);
 
 // Low-rank adapters chosen per row (lora.hpp): row t adds U[t] LB_a^T, U[t] = scale_a X[t] LA_a^T.
 struct LoraArgs {

@@ -1,0 +1,228 @@
+// gemm_mid_mx_tile.hpp - block-scaled output tiles of 32, 64 or 128 rows x 128 columns on gfx950 MFMA, the
+// counterpart of gemm_mid_tile.hpp (ring of direct copies, two workgroups a CU, one barrier per K tile)
+// for products with few rows.
+//
+//  - K tiles of 128 elements (128 or 64 bytes of a row) with their scale words (one 32-bit word per
+//    row: the tile's four 32-K blocks) in the same stage; operand layouts, fragment reads and
+//    conversions are the general kernel's (gemm_mx_any.hpp);
+//  - 32x32 accumulators with the operands swapped, waves 2 x 2 of BM/2 x 64 (BM 32: 1 x 4 of 32 x 32);
+//  - BF: exact products on the bf16 MFMA (elements times their scale converted in registers), else the
+//    scaled f8f6f4 MFMA. Which one a call takes is gemm_mx_any.hpp's rule;
+//  - the scale copies move 4 bytes a lane over 64 rows, the slowest shape of a copy (four times a
+//    1 KiB operand copy's time), one a wave and K tile: 12 KiB of an E4M3 x E2M1 tile with 32 rows then
+//    pass at about 27 bytes a clock and CU, twice what HBM delivers, so the weights' stream still
+//    bounds the tile. (The ring that spares those copies in the 256 x 256 kernels needs a buffer of
+//    four K tiles per copy in flight, more than half a CU's LDS here.)
+#pragma once
+#include "gemm_mx_any.hpp"
+
+namespace bsm {
+namespace midmx {
+
+constexpr int BN = 128, KT = 128;
+constexpr int LDS_BYTES = 80 * 1024;
+
+// An operand tile of ROWS rows x 128 elements of format code C.
+template <int C, int ROWS>
+struct Tile {
+  typedef mxany::Op<C, false> P;
+  static constexpr int BYTES = ROWS * P::ROW;
+  static constexpr int ALL = BYTES / 1024;                  // 1 KiB copies
+  static constexpr int COPIES = ALL < 4 ? 1 : ALL / 4;      // per wave (fewer than four: repeated)
+  __device__ static int copy_of(int w, int j) { return (w + 4 * j) % ALL; }
+  __device__ static void offsets(int64_t ld_bytes, int64_t rows, int w, int lane, uint32_t (&off)[COPIES]) {
+#pragma unroll
+    for (int j = 0; j < COPIES; j++) {
+      const int p = 64 * copy_of(w, j) + lane, r = p / P::CPR, c = P::logical(p % P::CPR, r);
+      off[j] = (uint32_t)(min((int64_t)r, rows - 1) * ld_bytes + 16 * c);
+    }
+  }
+  // The partial last K tile, `left` bytes of each row (whole chunks), zero past them.
+  __device__ static void fill(const uint8_t* base, const uint32_t (&off)[COPIES], int left, uint8_t* tile, int w, int lane) {
+#pragma unroll
+    for (int j = 0; j < COPIES; j++) {
+      const int p = 64 * copy_of(w, j) + lane, r = p / P::CPR, c = P::logical(p % P::CPR, r);
+      lds_write_b128(tile + 16 * p, 16 * c < left ? *(const uint4*)(base + off[j]) : make_uint4(0, 0, 0, 0));
+    }
+  }
+};
+
+// A BM x 128 tile staged in LDS as float32 (rows of 512 bytes, chunk c of row r at c ^ (r & 15)) to D
+// in its format, D = round(f(x (+ D))), whole row pieces, masked at D's edges: wave w of four takes rows
+// w BM/4 ...
+template <int BM>
+__device__ __forceinline__ void store_rows(const GemmArgs& a, int64_t m0, int64_t n0, const uint8_t* lds, int lane, int w) {
+  if (a.d_fmt == BSM_F32) {
+#pragma unroll 4
+    for (int j = 0; j < BM / 8; j++) {
+      const int r = w * (BM / 4) + 2 * j + (lane >> 5), c = lane & 31;
+      const uint4 x = lds_read_b128(lds + 512 * r + 16 * (c ^ (r & 15)));
+      float v[4] = {__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w)};
+      const int64_t row = m0 + r, col = n0 + 4 * c;
+      if (row >= a.M || col >= a.N) continue;
+      gemm::global_f32* p = (gemm::global_f32*)(a.D + row * a.ldd + col);
+      const bool whole = col + 4 <= a.N;
+#pragma unroll
+      for (int e = 0; e < 4; e++)
+        if (whole || col + e < a.N) {
+          if (a.accum) v[e] += p[e];
+          if (a.ew_op) v[e] = silu_affine(v[e], a.ew_scale, a.ew_bias);
+          if (!whole) p[e] = v[e];
+        }
+      if (whole) *(gemm::global_u32x4*)p = u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+    }
+    return;
+  }
+#pragma unroll 2
+  for (int j = 0; j < BM / 16; j++) {
+    const int r = w * (BM / 4) + 4 * j + (lane >> 4), c = 2 * (lane & 15);
+    const uint4 x0 = lds_read_b128(lds + 512 * r + 16 * (c ^ (r & 15)));
+    const uint4 x1 = lds_read_b128(lds + 512 * r + 16 * ((c + 1) ^ (r & 15)));
+    float v[8] = {__uint_as_float(x0.x), __uint_as_float(x0.y), __uint_as_float(x0.z), __uint_as_float(x0.w),
+                  __uint_as_float(x1.x), __uint_as_float(x1.y), __uint_as_float(x1.z), __uint_as_float(x1.w)};
+    const int64_t row = m0 + r, col = n0 + 4 * c;
+    if (row >= a.M || col >= a.N) continue;
+    uint16_t* p = (uint16_t*)a.D + row * a.ldd + col;
+    const bool whole = col + 8 <= a.N;
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+      if (whole || col + e < a.N) {
+        if (a.accum) v[e] += bf16_bits_to_f32(p[e]);
+        if (a.ew_op) v[e] = silu_affine(v[e], a.ew_scale, a.ew_bias);
+        if (!whole) p[e] = f32_to_bf16_bits(v[e]);
+      }
+    if (whole) {
+      u32x4 o;
+#pragma unroll
+      for (int e = 0; e < 4; e++) o[e] = (uint32_t)f32_to_bf16_bits(v[2 * e]) | ((uint32_t)f32_to_bf16_bits(v[2 * e + 1]) << 16);
+      *(gemm::global_u32x4*)p = o;
+    }
+  }
+}
+
+// One BM x 128 tile at (m0, n0) of the product that `a` describes, by four waves with LDS_BYTES of LDS.
+template <int CA, int CB, bool BF, int BM>
+__device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, uint8_t* lds, int lane, int w) {
+  typedef Tile<CA, BM> TA;
+  typedef Tile<CB, BN> TB;
+  constexpr int SCALES = TA::BYTES + TB::BYTES, STAGE = SCALES + 1024;
+  constexpr int NST = LDS_BYTES / STAGE < 6 ? LDS_BYTES / STAGE : 6, PER = TA::COPIES + TB::COPIES + 1;
+  constexpr int MI = BM == 128 ? 2 : 1, NI = BM == 32 ? 1 : 2;
+  static_assert(NST >= 2 && BM * 512 <= LDS_BYTES, "stages");
+  const int wa = BM == 32 ? 0 : (BM / 2) * (w >> 1), wb = BM == 32 ? 32 * w : 64 * (w & 1);
+  const int sh = 8 * (lane >> 5);
+  const int64_t lda = a.lda * TA::P::BITS / 8, ldb = a.ldb * TB::P::BITS / 8;
+  const uint8_t* A = (const uint8_t*)a.A + m0 * lda;
+  const uint8_t* B = (const uint8_t*)a.B + n0 * ldb;
+  uint32_t ao[TA::COPIES], bo[TB::COPIES];
+  TA::offsets(lda, a.M - m0, w, lane, ao);
+  TB::offsets(ldb, a.N - n0, w, lane, bo);
+  // This wave's scale words: waves 0, 1 A's rows 64w .. (BM 32 and 64: wave 1 repeats wave 0's), waves
+  // 2, 3 B's rows 64 (w - 2) ...; words at SCALES + 256 w + 4 l.
+  const int srow = (w < 2 ? (BM == 128 ? 64 * w : 0) : 64 * (w - 2)) + lane;
+  const uint8_t* sf = w < 2 ? a.SFA + m0 * a.ld_sfa : a.SFB + n0 * a.ld_sfb;
+  const int64_t soff = w < 2 ? min((int64_t)srow, a.M - 1 - m0) * a.ld_sfa : min((int64_t)srow, a.N - 1 - n0) * a.ld_sfb;
+  const uint8_t* const scale_a = lds + SCALES + 4 * wa;         // (BM 32, 64: rows in wave 0's words)
+  const uint8_t* const scale_b = lds + SCALES + 512 + 4 * wb;
+  f32x16 acc[MI][NI];
+#pragma unroll
+  for (int m = 0; m < MI; m++)
+#pragma unroll
+    for (int n = 0; n < NI; n++)
+#pragma unroll
+      for (int e = 0; e < 16; e++) acc[m][n][e] = 0.f;
+  const int nfull = (int)(a.K / KT), tail = (int)(a.K % KT);
+  const uint32_t lds0 = gemm::lds_addr(lds);
+  auto issue = [&](int kt, int stage) {
+    const int64_t k = min(kt, nfull - 1);
+    uint64_t ga, gb;
+    gemm::sgpr_base2(A + k * TA::P::ROW, B + k * TB::P::ROW, ga, gb);
+    const uint64_t gs = gemm::sgpr_base(sf + 4 * k);
+    const uint32_t at = lds0 + stage * STAGE;
+    gemm::dma4u(gs, (uint32_t)soff, at + SCALES + 256 * w);
+#pragma unroll
+    for (int j = 0; j < TA::COPIES; j++) gemm::dma16u(ga, ao[j], at + 1024 * TA::copy_of(w, j));
+#pragma unroll
+    for (int j = 0; j < TB::COPIES; j++) gemm::dma16u(gb, bo[j], at + TA::BYTES + 1024 * TB::copy_of(w, j));
+  };
+  auto multiply = [&](int st) {
+    const uint8_t* ta = lds + st * STAGE;
+    const uint8_t* tb = ta + TA::BYTES;
+    uint32_t sa[MI], sb[NI];
+#pragma unroll
+    for (int m = 0; m < MI; m++) sa[m] = *(const BSM_LDS uint32_t*)(scale_a + st * STAGE + 4 * (32 * m + (lane & 31)));
+#pragma unroll
+    for (int n = 0; n < NI; n++) sb[n] = *(const BSM_LDS uint32_t*)(scale_b + st * STAGE + 4 * (32 * n + (lane & 31)));
+    auto step = [&](auto sc) {
+      constexpr int S = decltype(sc)::value;
+      i32x8 fa[MI], fb[NI];
+#pragma unroll
+      for (int n = 0; n < NI; n++) fb[n] = mxany::read_frag<CB, false, BF>(tb, wb, n, S, lane);
+#pragma unroll
+      for (int m = 0; m < MI; m++) fa[m] = mxany::read_frag<CA, false, BF>(ta, wa, m, S, lane);
+      if constexpr (BF) {
+        const uint32_t rot = (uint32_t)(16 * S + 9 + sh) & 31u;
+        uint4 pb[NI][4];
+#pragma unroll
+        for (int n = 0; n < NI; n++) mxany::cvt_whole<CB>(fb[n], __builtin_amdgcn_alignbit(sb[n], sb[n], rot), pb[n]);
+#pragma unroll
+        for (int m = 0; m < MI; m++) {
+          uint4 pa[4];
+          mxany::cvt_whole<CA>(fa[m], __builtin_amdgcn_alignbit(sa[m], sa[m], rot), pa);
+#pragma unroll
+          for (int j = 0; j < 4; j++)
+#pragma unroll
+            for (int n = 0; n < NI; n++) acc[m][n] = mxany::mfma_bf16(pb[n][j], pa[j], acc[m][n]);
+        }
+      } else {
+#pragma unroll
+        for (int m = 0; m < MI; m++)
+#pragma unroll
+          for (int n = 0; n < NI; n++)
+            acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[n], fa[m], acc[m][n], CB, CA, 2 * S,
+                                                                        (int)(sb[n] >> sh), 2 * S, (int)(sa[m] >> sh));
+      }
+    };
+    step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
+  };
+  if (nfull > 0) {
+#pragma unroll
+    for (int i = 0; i < NST - 1; i++) issue(i, i);
+    int cur = 0;
+    for (int kt = 0; kt < nfull; kt++) {
+      gemm::stage_barrier<(NST - 2) * PER>();
+      issue(kt + NST - 1, cur == 0 ? NST - 1 : cur - 1);
+      multiply(cur);
+      cur = cur + 1 == NST ? 0 : cur + 1;
+    }
+  }
+  gemm::stage_barrier<0>();
+  if (tail) {
+    TA::fill(A + (int64_t)nfull * TA::P::ROW, ao, tail * TA::P::BITS / 8, lds, w, lane);
+    TB::fill(B + (int64_t)nfull * TB::P::ROW, bo, tail * TB::P::BITS / 8, lds + TA::BYTES, w, lane);
+    const uint32_t x = *(const uint32_t*)(sf + soff + 4 * (int64_t)nfull);
+    *(BSM_LDS uint32_t*)(lds + SCALES + 256 * w + 4 * lane) = mxany::mask_scale_word(x, nfull, a.K / 32);
+    __syncthreads();
+    multiply(0);
+    __syncthreads();
+  }
+  // register 4q + e of a block is row l%32, column 8q + 4(l/32) + e
+#pragma unroll
+  for (int m = 0; m < MI; m++)
+#pragma unroll
+    for (int n = 0; n < NI; n++)
+#pragma unroll
+      for (int q = 0; q < 4; q++) {
+        const int r = wa + 32 * m + (lane & 31), c = wb / 4 + 8 * n + 2 * q + (lane >> 5);
+        const f32x16& v = acc[m][n];
+        lds_write_b128(lds + 512 * r + 16 * (c ^ (r & 15)),
+                       make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
+                                  __float_as_uint(v[4 * q + 3])));
+      }
+  __syncthreads();
+  store_rows<BM>(a, m0, n0, lds, lane, w);
+}
+
+}  // namespace midmx
+}  // namespace bsm

@@ -77,9 +77,10 @@ def _writes(ins) -> set:
     return _regs(ops[0])
 
 
-def _min_since(f, i: int, hit, need: int) -> int:
+def _min_since(f, i: int, hit, need: int, stop=None) -> int:
     """Fewest wait states on any path from the last instruction satisfying hit(ins) to
-    instruction i (need or more if none is closer than need)."""
+    instruction i (need or more if none is closer than need). A path ends at an instruction
+    satisfying stop(ins)."""
     ins, labels = f["ins"], f["labels"]
     preds = f.setdefault("_preds", None)
     if preds is None:
@@ -115,6 +116,8 @@ def _min_since(f, i: int, hit, need: int) -> int:
             seen[j] = ws
             if hit(ins[j]):
                 best = min(best, ws)
+                break
+            if stop is not None and stop(ins[j]):
                 break
             ws += _waits(ins[j])
     return best
@@ -184,6 +187,10 @@ def audit(text: str) -> list:
                 for need in (7, 11, 19):
                     hit = lambda x: x[0].startswith("v_mfma") and _passes(x) + 3 == need and bool(_writes(x) & rd)
                     w = _min_since(f, i, hit, need)
+                    if w < need:
+                        # register by register: one that something else has written since holds no MFMA result
+                        w = min(_min_since(f, i, lambda x: hit(x) and r in _writes(x), need,
+                                           lambda x: not x[0].startswith("v_mfma") and r in _writes(x)) for r in rd)
                     if w < need:
                         out.append(f"{f['name']}: {op} #{i}: {w} wait states after an MFMA wrote what it reads "
                                    f"(needs {need})")

@@ -184,10 +184,17 @@ __device__ __forceinline__ void store(const GemmArgs& a, int64_t row0, int64_t c
   }
 }
 
+// Nothing to add to a tile's sums before they are stored.
+struct NoMore {
+  template <int MI>
+  __device__ __forceinline__ void operator()(int64_t, int64_t, f32x4 (&)[MI][4]) const {}
+};
+
 // One BM x 128 tile at (m0, n0) of the product that `a` describes (M, N, K, A, B, D its own), by four
-// waves with LDS_BYTES of LDS.
-template <int DT, int BM, bool AK, bool BKM>
-__device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, uint8_t* lds, int lane, int w) {
+// waves with LDS_BYTES of LDS. more(row0, col0, acc) may add to a wave's sums before the store.
+template <int DT, int BM, bool AK, bool BKM, class MORE = NoMore>
+__device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, uint8_t* lds, int lane, int w,
+                                     const MORE& more = MORE()) {
   typedef Tile<BM, AK> TA;
   typedef Tile<BN, BKM> TB;
   constexpr int MI = BM / 32, STAGE = TA::BYTES + TB::BYTES, NST = LDS_BYTES / STAGE, PER = TA::COPIES + TB::COPIES;
@@ -264,6 +271,7 @@ __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, 
     multiply(lds, (tail + 31) / 32);
     __syncthreads();
   }
+  more(m0 + wa, n0 + wb, acc);
   store<DT, MI>(a, m0 + wa, n0 + wb, lane, acc, lds + MI * 4096 * w);
 }
 

@@ -1,14 +1,14 @@
 // k_gemm_lora.hip - a shared projection with a low-rank adapter chosen per row (lora.hpp has the
 // formula). Two launches: the shrink writes U, the projection adds U LB^T to its accumulators before
-// its only store, so D is written once and never read back.
-#include "gemm_dense_tile.hpp"
+// its only store, so D is written once and never read back. Up to 64 rows (a decode batch) both work
+// row by row on the vector units, beside the weights' stream; beyond, on the matrix units.
+#include "gemm_mid_tile.hpp"
 #include "lora.hpp"
+#include "skinny.hpp"
 #include "store16.hpp"
 
 namespace bsm {
 namespace {
-
-using namespace dense;
 
 // Shrink: workgroup (b, z, j) computes U[16b .. 16b + 15][16z .. 16z + 15] for the rows of the j-th
 // distinct adapter of those 16 rows (none: it ends). Its four waves split K in interleaved pieces of
@@ -46,60 +46,178 @@ __global__ __launch_bounds__(256) void k_lora_shrink(GemmArgs a, LoraArgs lo, in
     f32x4 s = part[0][lane];
 #pragma unroll
     for (int q = 1; q < 4; q++) s += part[q][lane];
-    s *= lo.scale[ad];
+#pragma unroll
+    for (int e = 0; e < 4; e++) s[e] = 16 * (int)blockIdx.y + 4 * G + e < lo.R ? s[e] * lo.scale[ad] : 0.f;
     *(f32x4*)(lo.U + t * Rp + 16 * blockIdx.y + 4 * G) = s;
   }
 }
 
+// Projection and expand on tiles of 32, 64 or 128 x 128 (the last rows take the smallest that holds
+// them), two workgroups a CU. (On the 256 x 256 tile, whose accumulators leave the expand few
+// registers, 8190 rows with rank 64, N 8192, K 4096 took 714 us.)
 template <int DT>
-__global__ __launch_bounds__(256, 1) void k_lora(GemmArgs a, LoraArgs args, int64_t Rp, int tiles_m, int tiles_n) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * STAGE_BYTES];
-  // The adapters' arguments wait in LDS until the projection's K loop is over: held in SGPRs
-  // through it they made the compiler spill some.
-  __shared__ LoraArgs late;
-  if (threadIdx.x == 0) late = args;
+struct Expand {
+  const LoraArgs& lo;
+  int64_t Rp, M, N;
+  int lane;
+  template <int MI>
+  __device__ __forceinline__ void operator()(int64_t row0, int64_t col0, f32x4 (&acc)[MI][4]) const {
+    lora::expand<DT>(lo, Rp, M, N, row0, col0, lane, acc);
+  }
+};
+
+template <int DT>
+__global__ __launch_bounds__(256, 2) void k_lora(GemmArgs a, LoraArgs lo, int64_t Rp, int tiles_m, int tiles_n) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[mid::LDS_BYTES];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int tm, tn;
   gemm::tile_coords(blockIdx.x, tiles_m, tiles_n, tm, tn);
-  f32x4 acc[8][8];
-  tile_product<DT, true, true>(a, tm, tn, lds, lane, w, acc);
-  const int64_t row0 = (int64_t)tm * BM + 128 * (w >> 1), col0 = (int64_t)tn * BN + 128 * (w & 1);
-  const int i = lane & 15, G = lane >> 4;
-  const LoraArgs lo = late;
-  const int R = __builtin_amdgcn_readfirstlane(lo.R);
+  const Expand<DT> expand{lo, Rp, a.M, a.N, lane};
+  const int64_t m0 = 128 * (int64_t)tm, n0 = mid::BN * (int64_t)tn;
+  const int64_t left = a.M - m0;
+  if (left <= 32) mid::tile<DT, 32, true, true>(a, m0, n0, lds, lane, w, expand);
+  else if (left <= 64) mid::tile<DT, 64, true, true>(a, m0, n0, lds, lane, w, expand);
+  else mid::tile<DT, 128, true, true>(a, m0, n0, lds, lane, w, expand);
+}
+
+// Eight consecutive 16-bit values as float32.
+template <int DT>
+__device__ __forceinline__ void widen8(uint4 x, float (&v)[8]) {
+  const uint32_t wd[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-  for (int mt = 0; mt < 8; mt++) {
-    const int64_t t = row0 + 16 * mt + i;
-    const int id = lora::adapter_of(lo, t, a.M);
-    for (uint32_t firsts = lora::first_rows(id, lane); firsts; firsts &= firsts - 1) {
-      const int ad = __builtin_amdgcn_readlane(id, __builtin_ctz(firsts));
-      const bool mine = id == ad;
-      const uint16_t* lb = (const uint16_t*)lo.LB + (int64_t)ad * lo.stride_lb + 8 * G;
-      for (int r0 = 0; r0 < R; r0 += 32) {
-        const lora::USplit u = lora::split_u(lora::load_u(lo.U, Rp, t, r0, lane, mine));
+  for (int e = 0; e < 8; e++) {
+    const uint16_t h = (uint16_t)(wd[e >> 1] >> (16 * (e & 1)));
+    v[e] = DT == BSM_BF16 ? bf16_bits_to_f32(h) : f16_bits_to_f32(h);
+  }
+}
+
+// Shrink of few rows: workgroup (t, z) computes U[t][32z .. 32z + 31], wave w of sixteen its values
+// 32z + w and + 16: lane l sums the products of k 8l .. 8l + 7 of every 512 (one line of each operand
+// per eight lanes, eight pieces of 512 asked for at once), the lanes in a fixed tree. Values past R
+// are zero.
+template <int DT>
+__global__ __launch_bounds__(1024) void k_lora_shrink_rows(GemmArgs a, LoraArgs lo, int64_t Rp) {
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t = blockIdx.x;
+  const int id = __builtin_amdgcn_readfirstlane(lora::adapter_of(lo, t, a.M));
+  if (id < 0) return;
+  const uint16_t* x = (const uint16_t*)a.A + t * a.lda + 8 * lane;
+  for (int r = 32 * blockIdx.y + w; r < 32 * (int)blockIdx.y + 32; r += 16) {
+    float s = 0.f;
+    if (r < lo.R) {
+      const uint16_t* la = (const uint16_t*)lo.LA + (int64_t)id * lo.stride_la + (int64_t)r * lo.ld_la + 8 * lane;
+      auto dot = [&](uint4 p, uint4 q) {
+        float pf[8], qf[8];
+        widen8<DT>(p, pf);
+        widen8<DT>(q, qf);
 #pragma unroll
-        for (int nt = 0; nt < 8; nt++) {
-          const int64_t n = min(col0 + 16 * nt + i, a.N - 1);
-          const uint4 b = lora::load8(lb + n * lo.ld_lb + r0, R - r0 - 8 * G);
-          // (a sum of its own: another row's zeros times an infinity of this adapter are not zero)
-          const f32x4 d = lora::expand_step<DT>(u, b);
-          if (mine) acc[mt][nt] += d;
+        for (int e = 0; e < 8; e++) s = __builtin_fmaf(pf[e], qf[e], s);
+      };
+      int64_t k = 0;
+      for (; k + 8 * 512 <= a.K; k += 8 * 512) {
+        uint4 xv[8], v[8];
+#pragma unroll
+        for (int q = 0; q < 8; q++) {
+          xv[q] = *(const uint4*)(x + k + 512 * q);
+          v[q] = *(const uint4*)(la + k + 512 * q);
         }
+#pragma unroll
+        for (int q = 0; q < 8; q++) dot(xv[q], v[q]);
+      }
+#pragma unroll 2
+      for (; k < a.K; k += 512) {
+        const int64_t left = a.K - k - 8 * lane;
+        dot(lora::load8(x + k, left), lora::load8(la + k, left));
+      }
+#pragma unroll
+      for (int d = 32; d; d >>= 1) s += __shfl_xor(s, d);
+      s *= lo.scale[id];
+    }
+    if (lane == 0) lo.U[t * Rp + r] = s;
+  }
+}
+
+// Projection and expand of few rows: skinny.hpp's product for 16 MT rows and, while its weights are on
+// their way, the adapters' part, row by row: wave w takes rows w, w + 8, ..; lane l sums r 8(l/16) .. +7 of every 32 for column l%16, in
+// float32, the four lanes of a column in a fixed tree. A row reads its own adapter only.
+template <int DT, int MT>
+__global__ __launch_bounds__(skinny::THREADS) void k_lora_skinny(GemmArgs a, LoraArgs lo, int64_t Rp, int tiles_n) {
+  __shared__ f32x4 part[skinny::WAVES][MT][64];
+  __shared__ float adapted[16 * MT][17];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15, G = lane >> 4;
+  const int64_t m0 = 16 * MT * (int64_t)(blockIdx.x / tiles_n), n0 = skinny::BN * (int64_t)(blockIdx.x % tiles_n);
+  f32x4 acc[MT];
+  skinny::product<DT, MT>(a, m0, n0, lane, w, acc, [&]() {
+    // (no branch on a row's adapter: every row's loads go out together; a row without one reads
+    // adapter 0's weights and its own unwritten U, and its sum is dropped)
+    constexpr int ROWS = 2 * MT;
+    int64_t t[ROWS];
+    int id[ROWS];
+    const uint16_t* lb[ROWS];
+    float s[ROWS];
+#pragma unroll
+    for (int j = 0; j < ROWS; j++) {
+      t[j] = min(m0 + w + 8 * j, a.M - 1);
+      id[j] = __builtin_amdgcn_readfirstlane(lora::adapter_of(lo, m0 + w + 8 * j, a.M));
+      lb[j] = (const uint16_t*)lo.LB + (int64_t)max(id[j], 0) * lo.stride_lb + min(n0 + i, a.N - 1) * lo.ld_lb + 8 * G;
+      s[j] = 0.f;
+    }
+    for (int r = 0; r < lo.R; r += 32) {
+      lora::UPart u[ROWS];
+      uint4 b[ROWS];
+#pragma unroll
+      for (int j = 0; j < ROWS; j++) {
+        b[j] = lora::load8(lb[j] + r, lo.R - r - 8 * G);
+        u[j] = lora::load_u(lo.U, Rp, t[j], r, lane, true);
+      }
+#pragma unroll
+      for (int j = 0; j < ROWS; j++) {
+        float v[8];
+        widen8<DT>(b[j], v);
+#pragma unroll
+        for (int e = 0; e < 8; e++) s[j] = __builtin_fmaf(u[j].v[e], v[e], s[j]);
       }
     }
+#pragma unroll
+    for (int j = 0; j < ROWS; j++) {
+      s[j] += __shfl_xor(s[j], 16);
+      s[j] += __shfl_xor(s[j], 32);
+      if (G == 0) adapted[w + 8 * j][i] = id[j] >= 0 ? s[j] : 0.f;
+    }
+  });
+#pragma unroll
+  for (int m = 0; m < MT; m++) part[w][m][lane] = acc[m];
+  __syncthreads();
+  if (w < MT) {
+    f32x4 s = part[0][w][lane];
+#pragma unroll
+    for (int q = 1; q < skinny::WAVES; q++) s += part[q][w][lane];
+#pragma unroll
+    for (int e = 0; e < 4; e++) s[e] += adapted[16 * w + i][4 * G + e];
+    skinny::store4<DT>(a, m0 + 16 * w + i, n0 + 4 * G, s);
   }
-  uint8_t* region = lds + 32768 * w;
-  if (a.d_fmt == BSM_F32)
-    store_tile16(a.D, a.ldd, a.M, a.N, row0, col0, lane, 1.0f, acc, region, a.accum, a.ew_op, a.ew_scale, a.ew_bias);
-  else
-    gemm::store_tile16_bits<DT>((uint16_t*)a.D, a.ldd, a.M, a.N, row0, col0, lane, acc, region, a.accum, a.ew_op,
-                                a.ew_scale, a.ew_bias);
+}
+
+template <int DT, int MT>
+hipError_t launch_skinny(const GemmArgs& a, const LoraArgs& lo, int64_t Rp, hipStream_t st) {
+  const int64_t tn = (a.N + skinny::BN - 1) / skinny::BN, n = (a.M + 16 * MT - 1) / (16 * MT) * tn;
+  if (n > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (lo.n > 0) {
+    hipLaunchKernelGGL(k_lora_shrink_rows<DT>, dim3((uint32_t)a.M, (uint32_t)(Rp / 32)), dim3(1024), 0, st, a, lo, Rp);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((k_lora_skinny<DT, MT>), dim3((uint32_t)n), dim3(skinny::THREADS), 0, st, a, lo, Rp, (int)tn);
+  return hipGetLastError();
 }
 
 template <int DT>
 hipError_t launch(const GemmArgs& a, const LoraArgs& lo, hipStream_t st) {
   const int64_t Rp = lora::padded_rank(lo.R);
-  const int64_t tm = (a.M + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
+  if (a.M <= 16) return launch_skinny<DT, 1>(a, lo, Rp, st);
+  if (a.M <= 32) return launch_skinny<DT, 2>(a, lo, Rp, st);
+  if (a.M <= 64) return launch_skinny<DT, 4>(a, lo, Rp, st);
+  const int64_t tm = (a.M + 127) / 128, tn = (a.N + mid::BN - 1) / mid::BN;
   if (tm * tn > 0x7FFFFFFF) return hipErrorInvalidValue;
   if (lo.R > 0 && lo.n > 0) {
     const dim3 grid((uint32_t)((a.M + 15) / 16), (uint32_t)(Rp / 16), (uint32_t)(lo.n < 16 ? lo.n : 16));

@@ -10,6 +10,7 @@
 // off adapter by adapter with the other rows' operand zeroed, so a row's sum only ever sees its own
 // adapter's weights: requests in any order need no sorting, and long requests cost one pass.
 #pragma once
+#include <type_traits>
 #include "bsm_device.hpp"
 #include "bsm_internal.hpp"
 #include "../../include/bsm.h"
@@ -108,13 +109,12 @@ __device__ __forceinline__ USplit split_u(UPart u) {
   return s;
 }
 
-// U (16 rows x 32) LB^T (32 x 16 columns) with U at float32 precision on the bf16 matrix instruction:
+// d + U (16 rows x 32) LB^T (32 x 16 columns) with U at float32 precision on the bf16 matrix instruction:
 // three products with bf16 weights, six with f16 ones (11 bits: two bf16 terms), the small terms
 // first. U rounded to 16 bits instead would cost one, and an error of 2^-9 (2^-12) of the adapter's
 // part; the float32 matrix instruction takes 8 for the same 32 values at an eighth of the rate.
 template <int DT>
-__device__ __forceinline__ f32x4 expand_step(const USplit& u, uint4 b) {
-  f32x4 d = {0.f, 0.f, 0.f, 0.f};
+__device__ __forceinline__ f32x4 expand_step(const USplit& u, uint4 b, f32x4 d) {
   if constexpr (DT == BSM_BF16) {
 #pragma unroll
     for (int q = 2; q >= 0; q--) d = mfma16<BSM_BF16>(b, u.t[q], d);
@@ -130,6 +130,60 @@ __device__ __forceinline__ f32x4 expand_step(const USplit& u, uint4 b) {
     for (int q = 2; q >= 0; q--) d = mfma16<BSM_BF16>(hi, u.t[q], d);
   }
   return d;
+}
+
+// Smallest adapter above `after` among the rows whose adapters the lanes hold in id[] (lane l: row
+// l%16 of each 16-row block), INT_MAX if there is none. Wave-uniform.
+template <int MI>
+__device__ __forceinline__ int next_adapter(const int (&id)[MI], int after) {
+  int v = 0x7FFFFFFF;
+#pragma unroll
+  for (int m = 0; m < MI; m++) v = id[m] > after ? min(v, id[m]) : v;
+#pragma unroll
+  for (int d = 8; d; d >>= 1) v = min(v, __shfl_xor(v, d));
+  return __builtin_amdgcn_readfirstlane(v);
+}
+
+// Adds the adapters' part U LB^T to a wave's MI x NI blocks of 16x16 accumulators (operands swapped:
+// lane l holds row row0 + 16 m + l%16, columns col0 + 16 n + 4(l/16) .. +3), adapter by adapter in
+// ascending order, 32 of the rank at a time: all of U's and LB's loads of a step go out together, and LB
+// is read once for all the rows. A block whose 16 rows are all the adapter's accumulates in place; in
+// a mixed one the product is a sum of its own, added where the row is the adapter's (another row's
+// zeros times an infinity of this adapter are not zero).
+template <int DT, int MI, int NI>
+__device__ __forceinline__ void expand(const LoraArgs& lo, int64_t Rp, int64_t M, int64_t N, int64_t row0, int64_t col0,
+                                       int lane, f32x4 (&acc)[MI][NI]) {
+  const int i = lane & 15, G = lane >> 4, R = __builtin_amdgcn_readfirstlane(lo.R);
+  int id[MI];
+#pragma unroll
+  for (int m = 0; m < MI; m++) id[m] = adapter_of(lo, row0 + 16 * m + i, M);
+  for (int ad = next_adapter(id, -1); ad != 0x7FFFFFFF; ad = next_adapter(id, ad)) {
+    const uint16_t* lb = (const uint16_t*)lo.LB + (int64_t)ad * lo.stride_lb + 8 * G;
+    for (int r0 = 0; r0 < R; r0 += 32) {
+      UPart u[MI];
+      uint4 b[NI];
+#pragma unroll
+      for (int n = 0; n < NI; n++) b[n] = load8(lb + min(col0 + 16 * n + i, N - 1) * lo.ld_lb + r0, R - r0 - 8 * G);
+#pragma unroll
+      for (int m = 0; m < MI; m++) u[m] = load_u(lo.U, Rp, row0 + 16 * m + i, r0, lane, id[m] == ad);
+#pragma unroll
+      for (int m = 0; m < MI; m++) {
+        const uint32_t rows = (uint32_t)__ballot(id[m] == ad) & 0xFFFFu;
+        if (!rows) continue;
+        const USplit us = split_u(u[m]);
+        if (rows == 0xFFFFu) {
+#pragma unroll
+          for (int n = 0; n < NI; n++) acc[m][n] = expand_step<DT>(us, b[n], acc[m][n]);
+        } else {
+#pragma unroll
+          for (int n = 0; n < NI; n++) {
+            const f32x4 d = expand_step<DT>(us, b[n], f32x4{0.f, 0.f, 0.f, 0.f});
+            if (id[m] == ad) acc[m][n] += d;
+          }
+        }
+      }
+    }
+  }
 }
 
 }  // namespace lora

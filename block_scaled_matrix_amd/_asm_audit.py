@@ -95,31 +95,34 @@ def _min_since(f, i: int, hit, need: int, stop=None) -> int:
         f["_preds"] = preds
         f["_starts"] = starts
     starts = f["_starts"]
+
+    def before(j):
+        """Instructions that may run right before instruction j."""
+        if j in starts:
+            yield from preds.get(j, [])
+        if j > 0 and not (j in starts and ins[j - 1][0] in ("s_branch", "s_endpgm", "s_setpc_b64")):
+            yield j - 1
+
     best = need
-    stack = [(i, 0)]
+    stack = [(b, 0) for b in before(i)]
     seen = {}
     while stack:
         j, ws = stack.pop()
         while ws < best:
-            if j in starts or j == 0:
-                for b in preds.get(j, []):
-                    if seen.get(b, 1 << 30) > ws:
-                        stack.append((b + 1, ws))
-                if j == 0:
-                    break
-                prev = ins[j - 1][0]
-                if j in starts and prev in ("s_branch", "s_endpgm", "s_setpc_b64"):
-                    break
-            j -= 1
             if seen.get(j, 1 << 30) <= ws:
                 break
             seen[j] = ws
             if hit(ins[j]):
-                best = min(best, ws)
+                best = ws
                 break
             if stop is not None and stop(ins[j]):
                 break
             ws += _waits(ins[j])
+            prev = list(before(j))
+            if not prev:
+                break
+            stack += [(b, ws) for b in prev[1:]]
+            j = prev[0]
     return best
 
 

@@ -20,12 +20,15 @@ __device__ __forceinline__ void group_range(const GroupArgs& gr, int i, int& lo,
   hi = max(min(max(gr.offsets[i + 1], 0), gr.rows), lo);
 }
 
-__device__ __forceinline__ int wave_inclusive_scan(int v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int u = __shfl_up(v, d);
-    if (lane >= d) v += u;
-  }
+// Inclusive sum over the 64 lanes, in the vector unit's own lane shifts: within rows of 16, then the
+// last lane of each row into the rows behind it.
+__device__ __forceinline__ int wave_inclusive_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);   // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);   // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);   // row_shr:8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // row_bcast:15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // row_bcast:31 into rows 2 and 3
   return v;
 }
 
@@ -45,17 +48,23 @@ __device__ __forceinline__ bool find_tile(const GroupArgs& gr, int pid, int tile
     else lo = hi = 0;
     return (int)(((int64_t)(hi - lo) + BM - 1) / BM);
   };
-  int lo, hi, all = 0;
-  for (int i0 = 0; i0 < gr.n; i0 += 64)
-    all += __builtin_amdgcn_readlane(wave_inclusive_scan(tiles_of(i0 + lane, lo, hi), lane), 63);
+  int lo, hi;
+  int t = tiles_of(lane, lo, hi), incl = wave_inclusive_scan(t);
+  int all = __builtin_amdgcn_readlane(incl, 63);
+  for (int i0 = 64; i0 < gr.n; i0 += 64) {
+    int l, h;
+    all += __builtin_amdgcn_readlane(wave_inclusive_scan(tiles_of(i0 + lane, l, h)), 63);
+  }
   const int total = all * tiles_n, chunk = (total + 7) >> 3;
   const int lid = (pid & 7) * chunk + (pid >> 3);
   if ((pid >> 3) >= chunk || lid >= total) return false;
   const int rt = lid / tiles_n;
   int before = 0;
   for (int i0 = 0; i0 < gr.n; i0 += 64) {
-    const int t = tiles_of(i0 + lane, lo, hi);
-    const int incl = wave_inclusive_scan(t, lane);
+    if (i0 > 0) {
+      t = tiles_of(i0 + lane, lo, hi);
+      incl = wave_inclusive_scan(t);
+    }
     const uint64_t past = __ballot(before + incl > rt);
     if (past) {
       const int at = __builtin_ctzll(past);

@@ -10,6 +10,7 @@
 // (gemm_mid_tile.hpp).
 #include "gemm_dense_tile.hpp"
 #include "gemm_mid_tile.hpp"
+#include "skinny.hpp"
 #include "store16.hpp"
 #include "grouped.hpp"
 
@@ -114,6 +115,21 @@ __global__ __launch_bounds__(256, 2) void k_grouped_mid(GemmArgs a, GroupArgs gr
   else mid::tile<DT, 128, true, BKM>(t, m0, n0, lds, lane, w);
 }
 
+// Few tiles: 16 MT rows x 16 columns a workgroup, its eight waves splitting K (skinny.hpp).
+template <int DT, int MT>
+__global__ __launch_bounds__(skinny::THREADS) void k_grouped_skinny(GemmArgs a, GroupArgs gr, int tiles_n) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[skinny::lds_bytes<MT>()];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  grouped::Spot s;
+  if (!grouped::find_tile<16 * MT, 4>(gr, blockIdx.x, tiles_n, lane, s)) return;
+  const GemmArgs t = group_product(a, gr, s.g, s.row0, s.rows);
+  const int64_t m0 = 16 * MT * (int64_t)s.tm, n0 = skinny::BN * (int64_t)s.tn;
+  f32x4 acc[MT];
+  skinny::product<DT, MT>(t, m0, n0, lane, w, lds + w * (1 + MT) * 2048, acc, []() {});
+  skinny::join<MT>(lds, lane, w, acc);
+  if (w < MT) skinny::store4<DT>(t, m0 + 16 * w + (lane & 15), n0 + 4 * (lane >> 4), acc[0]);
+}
+
 template <int DT>
 hipError_t launch_grouped_dt(const GemmArgs& a, const GroupArgs& gr, hipStream_t st) {
   // The 256 x 256 tile only where groups fill it and there are four rounds of it over the 256 CUs:
@@ -122,11 +138,22 @@ hipError_t launch_grouped_dt(const GemmArgs& a, const GroupArgs& gr, hipStream_t
   // against 364 us.
   const int64_t tiles = (gr.rows + BM - 1) / BM * ((a.N + BN - 1) / BN);
   const bool big = gr.rows / gr.n >= 192 && tiles >= 1024;
-  const int bm = big ? BM : 128, bn = big ? BN : mid::BN;
+  // Sixteen columns a workgroup where 128-column tiles would leave half the CUs without one: 16 rows of
+  // one group, N = K = 4096 (32 such tiles) 21.8 -> 11.0 us, 64 rows 29.9 -> 15.2 us, 8 rows over 8 groups,
+  // N 1024, K 2048 (64) 12.4 -> 9.3 us; even at 128 of them (32 rows over 8 groups, N = K = 2048: 18.0
+  // and 18.2 us) and behind for more rows a group (500 rows, N = K = 2048: 21.8 and 27.1 us).
+  const int64_t used = gr.n < gr.rows ? gr.n : gr.rows, each = (gr.rows + used - 1) / used;
+  const bool few = a.b_kmajor && each <= 64 && used * ((a.N + mid::BN - 1) / mid::BN) < 128;
+  const int mt = !few ? 0 : each <= 16 ? 1 : each <= 32 ? 2 : 4;
+  const int bm = few ? 16 * mt : (big ? BM : 128), bn = few ? skinny::BN : (big ? BN : mid::BN);
   const int64_t tn = (a.N + bn - 1) / bn, n = (grouped::most_row_tiles(gr.rows, gr.n, bm) * tn + 7) / 8 * 8;
   if (n > 0x7FFFFFFF) return hipErrorInvalidValue;
   const dim3 grid((uint32_t)n);
-  if (!big) {
+  if (few) {
+    if (mt == 1) hipLaunchKernelGGL((k_grouped_skinny<DT, 1>), grid, dim3(skinny::THREADS), 0, st, a, gr, (int)tn);
+    else if (mt == 2) hipLaunchKernelGGL((k_grouped_skinny<DT, 2>), grid, dim3(skinny::THREADS), 0, st, a, gr, (int)tn);
+    else hipLaunchKernelGGL((k_grouped_skinny<DT, 4>), grid, dim3(skinny::THREADS), 0, st, a, gr, (int)tn);
+  } else if (!big) {
     if (a.b_kmajor) hipLaunchKernelGGL((k_grouped_mid<DT, true>), grid, dim3(256), 0, st, a, gr, (int)tn);
     else hipLaunchKernelGGL((k_grouped_mid<DT, false>), grid, dim3(256), 0, st, a, gr, (int)tn);
   } else if (a.b_kmajor) hipLaunchKernelGGL((k_grouped<DT, true>), grid, dim3(256), 0, st, a, gr, (int)tn);

@@ -142,12 +142,12 @@ __global__ __launch_bounds__(1024) void k_lora_shrink_rows(GemmArgs a, LoraArgs 
 // float32, the four lanes of a column in a fixed tree. A row reads its own adapter only.
 template <int DT, int MT>
 __global__ __launch_bounds__(skinny::THREADS) void k_lora_skinny(GemmArgs a, LoraArgs lo, int64_t Rp, int tiles_n) {
-  __shared__ f32x4 part[skinny::WAVES][MT][64];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[skinny::lds_bytes<MT>()];
   __shared__ float adapted[16 * MT][17];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15, G = lane >> 4;
   const int64_t m0 = 16 * MT * (int64_t)(blockIdx.x / tiles_n), n0 = skinny::BN * (int64_t)(blockIdx.x % tiles_n);
   f32x4 acc[MT];
-  skinny::product<DT, MT>(a, m0, n0, lane, w, acc, [&]() {
+  skinny::product<DT, MT>(a, m0, n0, lane, w, lds + w * (1 + MT) * 2048, acc, [&]() {
     // (no branch on a row's adapter: every row's loads go out together; a row without one reads
     // adapter 0's weights and its own unwritten U, and its sum is dropped)
     constexpr int ROWS = 2 * MT;
@@ -185,16 +185,11 @@ __global__ __launch_bounds__(skinny::THREADS) void k_lora_skinny(GemmArgs a, Lor
       if (G == 0) adapted[w + 8 * j][i] = id[j] >= 0 ? s[j] : 0.f;
     }
   });
-#pragma unroll
-  for (int m = 0; m < MT; m++) part[w][m][lane] = acc[m];
-  __syncthreads();
+  skinny::join<MT>(lds, lane, w, acc);
   if (w < MT) {
-    f32x4 s = part[0][w][lane];
 #pragma unroll
-    for (int q = 1; q < skinny::WAVES; q++) s += part[q][w][lane];
-#pragma unroll
-    for (int e = 0; e < 4; e++) s[e] += adapted[16 * w + i][4 * G + e];
-    skinny::store4<DT>(a, m0 + 16 * w + i, n0 + 4 * G, s);
+    for (int e = 0; e < 4; e++) acc[0][e] += adapted[16 * w + i][4 * G + e];
+    skinny::store4<DT>(a, m0 + 16 * w + i, n0 + 4 * G, acc[0]);
   }
 }
 
@@ -216,6 +211,7 @@ hipError_t launch(const GemmArgs& a, const LoraArgs& lo, hipStream_t st) {
   const int64_t Rp = lora::padded_rank(lo.R);
   if (a.M <= 16) return launch_skinny<DT, 1>(a, lo, Rp, st);
   if (a.M <= 32) return launch_skinny<DT, 2>(a, lo, Rp, st);
+  if (a.M <= 48) return launch_skinny<DT, 3>(a, lo, Rp, st);
   if (a.M <= 64) return launch_skinny<DT, 4>(a, lo, Rp, st);
   const int64_t tm = (a.M + 127) / 128, tn = (a.N + mid::BN - 1) / mid::BN;
   if (tm * tn > 0x7FFFFFFF) return hipErrorInvalidValue;

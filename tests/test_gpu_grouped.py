@@ -204,3 +204,12 @@ def test_gradients_against_differences():
         m[e, n, k] -= 0.5
         assert abs(loss(x, p) - loss(x, m) - float(dw[e, n, k])) <= 1e-3
     assert not dw[1].any()
+
+
+@pytest.mark.parametrize("sizes", [[1], [16], [17], [1] * 8, [64], [33, 0, 20], [90, 2, 3], [0, 150, 1, 2]])
+@pytest.mark.parametrize("ab,d", [("bf16", "bf16"), ("f16", "f32")])
+@pytest.mark.parametrize("K", [64, 72, 500, 512, 1099, 4160])
+def test_few_rows_and_long_k(sizes, ab, d, K):
+    """Few tiles and a long sum (the waves split K), with groups far above the average among them."""
+    run(sizes, 50, K, ab, "k", d, seed=K, first=1, behind=1, extra=8)
+    run(sizes, 50, K, ab, "k", d, 1, bsm.ewise_desc("silu_affine", 0.5, 0.25), seed=K)

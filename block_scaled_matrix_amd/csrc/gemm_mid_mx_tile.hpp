@@ -2,17 +2,16 @@
 // counterpart of gemm_mid_tile.hpp (ring of direct copies, two workgroups a CU, one barrier per K tile)
 // for products with few rows.
 //
-//  - K tiles of 128 elements (128 or 64 bytes of a row) with their scale words (one 32-bit word per
-//    row: the tile's four 32-K blocks) in the same stage; operand layouts, fragment reads and
-//    conversions are the general kernel's (gemm_mx_any.hpp);
+//  - K tiles of 128 elements (128 or 64 bytes of a row; one 32-bit scale word per row: the tile's four
+//    32-K blocks); operand layouts, fragment reads and conversions are the general kernel's
+//    (gemm_mx_any.hpp);
 //  - 32x32 accumulators with the operands swapped, waves 2 x 2 of BM/2 x 64 (BM 32: 1 x 4 of 32 x 32);
 //  - BF: exact products on the bf16 MFMA (elements times their scale converted in registers), else the
 //    scaled f8f6f4 MFMA. Which one a call takes is gemm_mx_any.hpp's rule;
-//  - the scale copies move 4 bytes a lane over 64 rows, the slowest shape of a copy (four times a
-//    1 KiB operand copy's time), one a wave and K tile: 12 KiB of an E4M3 x E2M1 tile with 32 rows then
-//    pass at about 27 bytes a clock and CU, twice what HBM delivers, so the weights' stream still
-//    bounds the tile. (The ring that spares those copies in the 256 x 256 kernels needs a buffer of
-//    four K tiles per copy in flight, more than half a CU's LDS here.)
+//  - scale words come through a ring of three groups of four K tiles (16 bytes of a row), a quarter of a
+//    group with every K tile's operands, 16 rows a copy: copies of 64 rows, one word of each per K tile,
+//    held the copy path for longer than the operands did (E4M3 x E2M1, 64 rows over 32 groups,
+//    N = K = 4096: 65 us).
 #pragma once
 #include "gemm_mx_any.hpp"
 
@@ -105,10 +104,11 @@ template <int CA, int CB, bool BF, int BM>
 __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, uint8_t* lds, int lane, int w) {
   typedef Tile<CA, BM> TA;
   typedef Tile<CB, BN> TB;
-  constexpr int SCALES = TA::BYTES + TB::BYTES, STAGE = SCALES + 1024;
-  constexpr int NST = LDS_BYTES / STAGE < 6 ? LDS_BYTES / STAGE : 6, PER = TA::COPIES + TB::COPIES + 1;
+  // three scale buffers of A's 128 rows and B's 128, 16 bytes a row, then the stages
+  constexpr int GROUP = 4096, RING = 3 * GROUP, STAGE = TA::BYTES + TB::BYTES;
+  constexpr int FIT = (LDS_BYTES - RING) / STAGE, NST = FIT < 6 ? FIT : 6, PER = TA::COPIES + TB::COPIES + 1;
   constexpr int MI = BM == 128 ? 2 : 1, NI = BM == 32 ? 1 : 2;
-  static_assert(NST >= 2 && BM * 512 <= LDS_BYTES, "stages");
+  static_assert(NST >= 2 && NST <= 6 && BM * 512 <= LDS_BYTES, "stages");
   const int wa = BM == 32 ? 0 : (BM / 2) * (w >> 1), wb = BM == 32 ? 32 * w : 64 * (w & 1);
   const int sh = 8 * (lane >> 5);
   const int64_t lda = a.lda * TA::P::BITS / 8, ldb = a.ldb * TB::P::BITS / 8;
@@ -117,13 +117,8 @@ __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, 
   uint32_t ao[TA::COPIES], bo[TB::COPIES];
   TA::offsets(lda, a.M - m0, w, lane, ao);
   TB::offsets(ldb, a.N - n0, w, lane, bo);
-  // This wave's scale words: waves 0, 1 A's rows 64w .. (BM 32 and 64: wave 1 repeats wave 0's), waves
-  // 2, 3 B's rows 64 (w - 2) ...; words at SCALES + 256 w + 4 l.
-  const int srow = (w < 2 ? (BM == 128 ? 64 * w : 0) : 64 * (w - 2)) + lane;
-  const uint8_t* sf = w < 2 ? a.SFA + m0 * a.ld_sfa : a.SFB + n0 * a.ld_sfb;
-  const int64_t soff = w < 2 ? min((int64_t)srow, a.M - 1 - m0) * a.ld_sfa : min((int64_t)srow, a.N - 1 - n0) * a.ld_sfb;
-  const uint8_t* const scale_a = lds + SCALES + 4 * wa;         // (BM 32, 64: rows in wave 0's words)
-  const uint8_t* const scale_b = lds + SCALES + 512 + 4 * wb;
+  uint64_t sfa, sfb;
+  gemm::sgpr_base2(a.SFA + m0 * a.ld_sfa, a.SFB + n0 * a.ld_sfb, sfa, sfb);
   f32x16 acc[MI][NI];
 #pragma unroll
   for (int m = 0; m < MI; m++)
@@ -133,26 +128,35 @@ __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, 
       for (int e = 0; e < 16; e++) acc[m][n][e] = 0.f;
   const int nfull = (int)(a.K / KT), tail = (int)(a.K % KT);
   const uint32_t lds0 = gemm::lds_addr(lds);
+  // Quarter q of scale group g (K tiles 4g ..), this wave's 16 rows of its 64: rows 64q + 16w .. of A's
+  // 128 and B's 128, lane l moving the word at place l%4 of row l/4 (mxany::ring_word_offset). Words
+  // past the last whole tile and rows past the operand repeat the last ones (unused values).
+  auto quarter = [&](int g, int q) {
+    const int op = q >> 1, R = 64 * (q & 1) + 16 * w + (lane >> 2);
+    const int word = (lane & 3) ^ ((R >> 4) & 3) ^ ((R >> 6) & 1) ^ (op ? 2 : 0);
+    const int64_t rows = op ? a.N - n0 : a.M - m0;
+    const uint32_t off = (uint32_t)(min((int64_t)R, rows - 1) * (op ? a.ld_sfb : a.ld_sfa)) + 4u * (uint32_t)min(4 * g + word, nfull - 1);
+    gemm::dma4u(op ? sfb : sfa, off, lds0 + (g % 3) * GROUP + 2048 * op + 16 * (64 * (q & 1) + 16 * w));
+  };
+  // Tile kt's copies, and with them quarter (kt + 3) % 4 of scale group (kt + 3) / 4: group g comes with
+  // tiles 4g - 3 .. 4g, so waiting for tile 4g's operands waits for it; its buffer was last read for tile
+  // 4g - 9, before the copies of tile 4g - 3 go out (at tile 4g - 2 - NST or later, NST <= 6).
+  // Past the last tile the copies repeat the last one's into a stage that nobody reads again, so
+  // that the counts waited for stay fixed.
   auto issue = [&](int kt, int stage) {
     const int64_t k = min(kt, nfull - 1);
     uint64_t ga, gb;
     gemm::sgpr_base2(A + k * TA::P::ROW, B + k * TB::P::ROW, ga, gb);
-    const uint64_t gs = gemm::sgpr_base(sf + 4 * k);
-    const uint32_t at = lds0 + stage * STAGE;
-    gemm::dma4u(gs, (uint32_t)soff, at + SCALES + 256 * w);
+    const uint32_t at = lds0 + RING + stage * STAGE;
+    quarter((kt + 3) >> 2, (kt + 3) & 3);
 #pragma unroll
     for (int j = 0; j < TA::COPIES; j++) gemm::dma16u(ga, ao[j], at + 1024 * TA::copy_of(w, j));
 #pragma unroll
     for (int j = 0; j < TB::COPIES; j++) gemm::dma16u(gb, bo[j], at + TA::BYTES + 1024 * TB::copy_of(w, j));
   };
-  auto multiply = [&](int st) {
-    const uint8_t* ta = lds + st * STAGE;
+  auto multiply = [&](int st, const uint32_t (&sa)[MI], const uint32_t (&sb)[NI]) {
+    const uint8_t* ta = lds + RING + st * STAGE;
     const uint8_t* tb = ta + TA::BYTES;
-    uint32_t sa[MI], sb[NI];
-#pragma unroll
-    for (int m = 0; m < MI; m++) sa[m] = *(const BSM_LDS uint32_t*)(scale_a + st * STAGE + 4 * (32 * m + (lane & 31)));
-#pragma unroll
-    for (int n = 0; n < NI; n++) sb[n] = *(const BSM_LDS uint32_t*)(scale_b + st * STAGE + 4 * (32 * n + (lane & 31)));
     auto step = [&](auto sc) {
       constexpr int S = decltype(sc)::value;
       i32x8 fa[MI], fb[NI];
@@ -186,25 +190,38 @@ __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, 
     step(std::integral_constant<int, 0>{});
     step(std::integral_constant<int, 1>{});
   };
+  uint32_t sa[MI], sb[NI];
   if (nfull > 0) {
+#pragma unroll
+    for (int q = 0; q < 3; q++) quarter(0, q);
 #pragma unroll
     for (int i = 0; i < NST - 1; i++) issue(i, i);
     int cur = 0;
     for (int kt = 0; kt < nfull; kt++) {
       gemm::stage_barrier<(NST - 2) * PER>();
       issue(kt + NST - 1, cur == 0 ? NST - 1 : cur - 1);
-      multiply(cur);
+      const uint8_t* sc = lds + ((kt >> 2) % 3) * GROUP;
+#pragma unroll
+      for (int m = 0; m < MI; m++) sa[m] = *(const BSM_LDS uint32_t*)(sc + mxany::ring_word_offset(0, wa + 32 * m + (lane & 31), kt & 3));
+#pragma unroll
+      for (int n = 0; n < NI; n++) sb[n] = *(const BSM_LDS uint32_t*)(sc + 2048 + mxany::ring_word_offset(1, wb + 32 * n + (lane & 31), kt & 3));
+      multiply(cur, sa, sb);
       cur = cur + 1 == NST ? 0 : cur + 1;
     }
   }
   gemm::stage_barrier<0>();
   if (tail) {
-    TA::fill(A + (int64_t)nfull * TA::P::ROW, ao, tail * TA::P::BITS / 8, lds, w, lane);
-    TB::fill(B + (int64_t)nfull * TB::P::ROW, bo, tail * TB::P::BITS / 8, lds + TA::BYTES, w, lane);
-    const uint32_t x = *(const uint32_t*)(sf + soff + 4 * (int64_t)nfull);
-    *(BSM_LDS uint32_t*)(lds + SCALES + 256 * w + 4 * lane) = mxany::mask_scale_word(x, nfull, a.K / 32);
+    TA::fill(A + (int64_t)nfull * TA::P::ROW, ao, tail * TA::P::BITS / 8, lds + RING, w, lane);
+    TB::fill(B + (int64_t)nfull * TB::P::ROW, bo, tail * TB::P::BITS / 8, lds + RING + TA::BYTES, w, lane);
+    // (each lane reads its rows' words itself: once per tile)
+#pragma unroll
+    for (int m = 0; m < MI; m++)
+      sa[m] = mxany::mask_scale_word(mxany::load_scale_word(a.SFA, a.ld_sfa, m0, a.M, wa + 32 * m + (lane & 31), nfull), nfull, a.K / 32);
+#pragma unroll
+    for (int n = 0; n < NI; n++)
+      sb[n] = mxany::mask_scale_word(mxany::load_scale_word(a.SFB, a.ld_sfb, n0, a.N, wb + 32 * n + (lane & 31), nfull), nfull, a.K / 32);
     __syncthreads();
-    multiply(0);
+    multiply(0, sa, sb);
     __syncthreads();
   }
   // register 4q + e of a block is row l%32, column 8q + 4(l/32) + e

@@ -1,37 +1,46 @@
-// gemm_mid_tile.hpp - fp16/bf16 output tiles of 32, 64 or 128 rows x 128 columns on gfx950 MFMA, for products
-// with too few rows for the 256 x 256 tile of gemm_dense_tile.hpp: they stream the weights rather than wait
-// for the matrix pipe.
+// gemm_mid_tile.hpp - fp16/bf16 output tiles of 32, 64, 128 or 256 rows x 128 columns on gfx950 MFMA, for
+// products with too few rows, or too few tiles, for the 256 x 256 tile of gemm_dense_tile.hpp.
 //
 //  - four waves in a 2 x 2 grid, each BM/2 x 64 of the tile as 16x16x32 blocks (operands swapped, so a
 //    lane holds four consecutive columns of one row);
-//  - K tiles of 64 (128-byte rows, or 64 k-rows of 256 bytes where N is the contiguous axis) stream
+//  - K tiles of BK 64 (128-byte rows, or k-rows of 256 bytes where M or N is the contiguous axis) stream
 //    HBM -> LDS by direct copies into a ring of NST stages sized so that two workgroups share a CU
 //    (at most 80 KiB each): the copies of NST - 1 tiles are in flight while one is multiplied, and
 //    one workgroup multiplies while the other waits;
 //  - one barrier per K tile: it tells that the tile's copies have landed for every wave and that every
 //    wave is done with the stage that the next copies overwrite;
+//  - 256 rows need BK 32 to fit: fewer bytes through LDS and copy path per product, but K-major rows then
+//    move in half lines, which cost more than that saves (16381 rows over 16 groups, N 4096, K 8192:
+//    1259 us against 1188 us on 128 rows); with both operands MN-major it pays (the weight gradient of
+//    16381 rows over 8 groups, M 4096, N 2048: 306 against 343 us). Raising the waves' priority
+//    around the matrix instructions, or issuing the copies after the first fragment reads, was 2-6%
+//    slower;
 //  - LDS layouts: K-major as in gemm_common.hpp; MN-major rows of 256 bytes with chunk c of k-row kr
 //    at c ^ 4(kr & 3) ^ 2((kr >> 3) & 1): the eight 32-byte pieces that a half-wave's transposing read
 //    touches lie in the eight different eighths of a row, all 64 banks.
 #pragma once
+#include <type_traits>
 #include "store16.hpp"
 #include "../../include/bsm.h"
 
 namespace bsm {
 namespace mid {
 
-constexpr int BN = 128, BK = 64;
+constexpr int BN = 128;
 constexpr int LDS_BYTES = 80 * 1024;
 
-// An operand tile of ROWS rows (M or N) x 64 K elements.
-template <int ROWS, bool KMAJ>
+// An operand tile of ROWS rows (M or N) x BK K elements (64 or 32).
+template <int ROWS, bool KMAJ, int BK>
 struct Tile {
   static constexpr int BYTES = ROWS * BK * 2;
+  static constexpr int CPR = BK / 8;            // 16-byte chunks of a row (K-major)
   static constexpr int COPIES = BYTES / 4096;   // per wave
   static constexpr int KROW = ROWS * 2;         // bytes of a k-row (MN-major)
   static constexpr int CPK = KROW / 16;         // its chunks
-  static_assert(KMAJ || ROWS == 128, "MN-major tiles are 128 wide");
+  static_assert(KMAJ || ROWS >= 128, "MN-major tiles are at least 128 wide");
 
+  // chunk c of K-major row r sits at c ^ rswz(r): the 16 rows that one 16-lane group reads lie in all banks
+  __device__ static int rswz(int r) { return CPR == 8 ? (r >> 1) & 7 : (r >> 2) & 3; }
   __device__ static uint32_t swz(int kr) { return (uint32_t)(4 * (kr & 3) ^ 2 * ((kr >> 3) & 1)); }
 
   // Per-lane byte offsets of this wave's copies from the tile's base; rows (K-major) or chunks
@@ -41,7 +50,7 @@ struct Tile {
     for (int j = 0; j < COPIES; j++) {
       const int p = 64 * (w + 4 * j) + lane;    // 16-byte chunk of the tile
       if (KMAJ) {
-        const int r = p >> 3, c = (p & 7) ^ ((r >> 1) & 7);
+        const int r = p / CPR, c = (p % CPR) ^ rswz(r);
         off[j] = (uint32_t)((min(row0 + r, rows - 1) - row0) * ld * 2 + 16 * c);
       } else {
         const int kr = p / CPK, c = (p % CPK) ^ (int)swz(kr);
@@ -59,7 +68,7 @@ struct Tile {
       const int p = 64 * (w + 4 * j) + lane;
       uint4 v = make_uint4(0, 0, 0, 0);
       if (KMAJ) {
-        const int r = p >> 3, c = (p & 7) ^ ((r >> 1) & 7), n = left - 8 * c;
+        const int r = p / CPR, c = (p % CPR) ^ rswz(r), n = left - 8 * c;
         if (n > 0) {
           v = *(const uint4*)((const uint8_t*)b + off[j]);
           if (n < 8) {
@@ -80,7 +89,7 @@ struct Tile {
     const int G = lane >> 4, i = lane & 15;
     if (KMAJ) {
       const int r = r0 + i, c = 4 * s + G;
-      return lds_read_b128(tile + r * 128 + ((c ^ ((r >> 1) & 7)) << 4));
+      return lds_read_b128(tile + r * 2 * BK + ((c ^ rswz(r)) << 4));
     }
     uint2 h[2];
 #pragma unroll
@@ -103,8 +112,8 @@ __device__ __forceinline__ f32x4 mfma(uint4 b, uint4 a, f32x4 c) {
 // Stores one wave's MI x 4 blocks (rows row0 .. + 16 MI - 1, columns col0 .. + 63 of D) in D's format,
 // through `region` (MI * 4 KiB of LDS): rows of 256 bytes, chunk c of row r at c ^ (r & 15), then
 // whole row pieces: D = round(f(acc (+ D))), masked at D's edges. A is GemmArgs with M, N, D the product's.
-template <int DT, int MI>
-__device__ __forceinline__ void store(const GemmArgs& a, int64_t row0, int64_t col0, int lane, const f32x4 (&acc)[MI][4],
+template <int DT, int ALL, int M0, int MI>
+__device__ __forceinline__ void store(const GemmArgs& a, int64_t row0, int64_t col0, int lane, const f32x4 (&acc)[ALL][4],
                                       uint8_t* region) {
   const int i = lane & 15, G = lane >> 4;
 #pragma unroll
@@ -112,7 +121,7 @@ __device__ __forceinline__ void store(const GemmArgs& a, int64_t row0, int64_t c
 #pragma unroll
     for (int n = 0; n < 4; n++) {
       const int r = 16 * m + i, c = 4 * n + G;
-      const f32x4& v = acc[m][n];
+      const f32x4& v = acc[M0 + m][n];
       lds_write_b128(region + 256 * r + 16 * (c ^ (r & 15)),
                      make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
     }
@@ -184,21 +193,22 @@ __device__ __forceinline__ void store(const GemmArgs& a, int64_t row0, int64_t c
   }
 }
 
-// Nothing to add to a tile's sums before they are stored.
+// Nothing to add to a tile's sums before they are stored. (kStores: `more` stores them itself.)
 struct NoMore {
+  static constexpr bool kStores = false;
   template <int MI>
   __device__ __forceinline__ void operator()(int64_t, int64_t, f32x4 (&)[MI][4]) const {}
 };
 
 // One BM x 128 tile at (m0, n0) of the product that `a` describes (M, N, K, A, B, D its own), by four
-// waves with LDS_BYTES of LDS. more(row0, col0, acc) may add to a wave's sums before the store.
-template <int DT, int BM, bool AK, bool BKM, class MORE = NoMore>
+// waves with LDS bytes of LDS. more(row0, col0, acc) may add to a wave's sums before the store.
+template <int DT, int BM, bool AK, bool BKM, int BK = 64, class MORE = NoMore, int LDS = LDS_BYTES>
 __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, uint8_t* lds, int lane, int w,
                                      const MORE& more = MORE()) {
-  typedef Tile<BM, AK> TA;
-  typedef Tile<BN, BKM> TB;
-  constexpr int MI = BM / 32, STAGE = TA::BYTES + TB::BYTES, NST = LDS_BYTES / STAGE, PER = TA::COPIES + TB::COPIES;
-  static_assert(NST >= 2 && MI * 16384 <= NST * STAGE, "stages");
+  typedef Tile<BM, AK, BK> TA;
+  typedef Tile<BN, BKM, BK> TB;
+  constexpr int MI = BM / 32, STAGE = TA::BYTES + TB::BYTES, NST = LDS / STAGE, PER = TA::COPIES + TB::COPIES;
+  static_assert(NST >= 2 && (MI < 4 ? MI : 4) * 16384 <= LDS, "stages");
   const int wa = (BM / 2) * (w >> 1), wb = 64 * (w & 1);
   const uint16_t* A = (const uint16_t*)a.A;
   const uint16_t* B = (const uint16_t*)a.B;
@@ -224,8 +234,9 @@ __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, 
 #pragma unroll
     for (int j = 0; j < TB::COPIES; j++) gemm::dma16u(gb, bo[j], at + TA::BYTES + 1024 * (w + 4 * j));
   };
-  auto multiply = [&](const uint8_t* st, int steps) {
-    for (int s = 0; s < steps; s++) {
+  auto multiply = [&](const uint8_t* st, auto steps) {
+#pragma unroll
+    for (int s = 0; s < decltype(steps)::value; s++) {
       uint4 fa[MI], fb[4];
 #pragma unroll
       for (int n = 0; n < 4; n++) fb[n] = TB::frag(st + TA::BYTES, lane, wb + 16 * n, s);
@@ -244,19 +255,7 @@ __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, 
     for (int kt = 0; kt < nfull; kt++) {
       gemm::stage_barrier<(NST - 2) * PER>();
       issue(kt + NST - 1, cur == 0 ? NST - 1 : cur - 1);
-      const uint8_t* st = lds + cur * STAGE;
-#pragma unroll
-      for (int s = 0; s < 2; s++) {
-        uint4 fa[MI], fb[4];
-#pragma unroll
-        for (int n = 0; n < 4; n++) fb[n] = TB::frag(st + TA::BYTES, lane, wb + 16 * n, s);
-#pragma unroll
-        for (int m = 0; m < MI; m++) fa[m] = TA::frag(st, lane, wa + 16 * m, s);
-#pragma unroll
-        for (int m = 0; m < MI; m++)
-#pragma unroll
-          for (int n = 0; n < 4; n++) acc[m][n] = mfma<DT>(fb[n], fa[m], acc[m][n]);
-      }
+      multiply(lds + cur * STAGE, std::integral_constant<int, BK / 32>{});
       cur = cur + 1 == NST ? 0 : cur + 1;
     }
   }
@@ -268,11 +267,18 @@ __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, 
     TA::fill(TA::base(A, a.lda, m0, k0), ao, tail, lds, w, lane);
     TB::fill(TB::base(B, a.ldb, n0, k0), bo, tail, lds + TA::BYTES, w, lane);
     __syncthreads();
-    multiply(lds, (tail + 31) / 32);
+    if (BK == 32 || tail <= 32) multiply(lds, std::integral_constant<int, 1>{});
+    else multiply(lds, std::integral_constant<int, 2>{});
     __syncthreads();
   }
   more(m0 + wa, n0 + wb, acc);
-  store<DT, MI>(a, m0 + wa, n0 + wb, lane, acc, lds + MI * 4096 * w);
+  if constexpr (MORE::kStores) {
+  } else if constexpr (MI <= 4) {
+    store<DT, MI, 0, MI>(a, m0 + wa, n0 + wb, lane, acc, lds + MI * 4096 * w);
+  } else {
+    store<DT, MI, 0, 4>(a, m0 + wa, n0 + wb, lane, acc, lds + 16384 * w);
+    store<DT, MI, 4, 4>(a, m0 + wa + 64, n0 + wb, lane, acc, lds + 16384 * w);
+  }
 }
 
 }  // namespace mid

@@ -81,13 +81,13 @@ __device__ __forceinline__ GemmArgs wgrad_product(const GemmArgs& a, const Group
   return t;
 }
 
-template <int DT>
+template <int DT, int BM, int BK>
 __global__ __launch_bounds__(256, 2) void k_grouped_wgrad(GemmArgs a, GroupArgs gr, int tiles_m, int tiles_n) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[mid::LDS_BYTES];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   WgradSpot s;
   if (!wgrad_tile(blockIdx.x, gr.n, tiles_m, tiles_n, s)) return;
-  mid::tile<DT, 128, false, false>(wgrad_product(a, gr, s.g), 128 * (int64_t)s.tm, 128 * (int64_t)s.tn, lds, lane, w);
+  mid::tile<DT, BM, false, false, BK>(wgrad_product(a, gr, s.g), BM * (int64_t)s.tm, mid::BN * (int64_t)s.tn, lds, lane, w);
 }
 
 // The product of one group of rows out of the call's: operands and output moved to it.
@@ -169,11 +169,16 @@ hipError_t launch_gemm_grouped(const GemmArgs& a, const GroupArgs& gr, hipStream
 
 template <int DT>
 static hipError_t launch_wgrad_dt(const GemmArgs& a, const GroupArgs& gr, hipStream_t st) {
-  // 128 x 128 tiles always: on 256 x 256 ones 8 groups of 16381 rows (M 4096, N 2048) took 350 us
-  // against 331 us, and 32 groups of 1021 rows (M 1000, N 520) 40 us against 18.5 us.
-  const int64_t tm = (a.M + 127) / 128, tn = (a.N + 127) / 128, share = (tm * tn + 7) / 8;
+  // Tiles of 256 rows where groups have rows enough for a long loop and the tiles fill the CUs: 16381
+  // rows over 8 groups (M 4096, N 2048) 306 us against 343 us on 128; 1021 over 32 (M 1000, N 520) 21.1
+  // against 19.8 us. (The dense GEMM's 256 x 256 tile: 350 and 40 us.)
+  const int64_t tn = (a.N + mid::BN - 1) / mid::BN;
+  const bool tall = gr.rows / gr.n >= 192 && (a.M + 255) / 256 * tn * gr.n >= 512;
+  const int64_t tm = tall ? (a.M + 255) / 256 : (a.M + 127) / 128, share = (tm * tn + 7) / 8;
   if (share > 0x7FFFFFFF / 8 / gr.n) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(k_grouped_wgrad<DT>, dim3((uint32_t)(share * 8 * gr.n)), dim3(256), 0, st, a, gr, (int)tm, (int)tn);
+  const dim3 grid((uint32_t)(share * 8 * gr.n));
+  if (tall) hipLaunchKernelGGL((k_grouped_wgrad<DT, 256, 32>), grid, dim3(256), 0, st, a, gr, (int)tm, (int)tn);
+  else hipLaunchKernelGGL((k_grouped_wgrad<DT, 128, 64>), grid, dim3(256), 0, st, a, gr, (int)tm, (int)tn);
   return hipGetLastError();
 }
 

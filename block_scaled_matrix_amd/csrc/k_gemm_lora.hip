@@ -10,45 +10,63 @@
 namespace bsm {
 namespace {
 
-// Shrink: workgroup (b, z, j) computes U[16b .. 16b + 15][16z .. 16z + 15] for the rows of the j-th
-// distinct adapter of those 16 rows (none: it ends). Its four waves split K in interleaved pieces of
-// 64 and are summed through LDS in a fixed order. Lane group G of a wave holds the contiguous k
-// 16G .. 16G + 15 of a piece on both sides (two matrix instructions of 32), so a row's piece is one
-// whole 128-byte line.
+// Shrink: workgroup (b, y, z) computes U[32b .. 32b + 31][128y .. 128y + 127] for the z-th, (z + Z)-th, ..
+// distinct adapter of those 32 rows in ascending order, on gemm_mid_tile.hpp's 32 x 128 tile with the
+// adapter's LA as the weights. Rows of other adapters are multiplied along and not stored; values past R
+// are zero. Bound by the copies into LDS (LA again for every 32 rows).
 template <int DT>
-__global__ __launch_bounds__(256) void k_lora_shrink(GemmArgs a, LoraArgs lo, int64_t Rp) {
-  __shared__ f32x4 part[4][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, i = lane & 15, G = lane >> 4;
-  const int64_t t = 16 * (int64_t)blockIdx.x + i;
-  const int id = lora::adapter_of(lo, t, a.M);
-  uint32_t firsts = lora::first_rows(id, lane);
-  for (int j = blockIdx.z; j > 0 && firsts; j--) firsts &= firsts - 1;
-  if (!firsts) return;
-  const int ad = __builtin_amdgcn_readlane(id, __builtin_ctz(firsts));
-  const bool mine = id == ad;
-  const int r = 16 * blockIdx.y + i;
-  const uint16_t* x = (const uint16_t*)a.A + t * a.lda + 16 * G;
-  const uint16_t* la = (const uint16_t*)lo.LA + (int64_t)ad * lo.stride_la + (int64_t)r * lo.ld_la + 16 * G;
-  const bool row = r < lo.R;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int64_t k0 = 64 * w; k0 < a.K; k0 += 256) {
+struct StoreU {
+  static constexpr bool kStores = true;
+  const LoraArgs* late;
+  int64_t Rp, M;
+  int ad, lane;
+  template <int MI>
+  __device__ __forceinline__ void operator()(int64_t row0, int64_t col0, f32x4 (&acc)[MI][4]) const {
+    const LoraArgs lo = *late;
+    const int i = lane & 15, G = lane >> 4;
+    const float scale = lo.scale[ad];
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
-      const int64_t left = a.K - k0 - 16 * G - 8 * h;
-      const uint4 av = lora::load8(x + k0 + 8 * h, mine ? left : 0);
-      const uint4 bv = lora::load8(la + k0 + 8 * h, row ? left : 0);
-      acc = lora::mfma16<DT>(bv, av, acc);
+    for (int m = 0; m < MI; m++) {
+      const int64_t t = row0 + 16 * m + i;
+      if (lora::adapter_of(lo, t, M) != ad) continue;
+#pragma unroll
+      for (int n = 0; n < 4; n++) {
+        const int r = (int)col0 + 16 * n + 4 * G;
+        if (r >= Rp) continue;
+        f32x4 u;
+#pragma unroll
+        for (int e = 0; e < 4; e++) u[e] = r + e < lo.R ? acc[m][n][e] * scale : 0.f;
+        *(f32x4*)(lo.U + t * Rp + r) = u;
+      }
     }
   }
-  part[w][lane] = acc;
+};
+
+template <int DT>
+__global__ __launch_bounds__(256, 2) void k_lora_shrink(GemmArgs a, LoraArgs lo, int64_t Rp) {
+  // The arguments that only the store needs wait in LDS, beside the tile's three stages (two
+  // workgroups a CU still fit): held in SGPRs through the tile's loop they made the compiler spill some.
+  constexpr int TILE = 60 * 1024;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[TILE];
+  __shared__ LoraArgs late;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t m0 = 32 * (int64_t)blockIdx.x;
+  int id[2];
+#pragma unroll
+  for (int m = 0; m < 2; m++) id[m] = lora::adapter_of(lo, m0 + 16 * m + (lane & 15), a.M);
+  int ad = lora::next_adapter(id, -1);
+  for (int z = 0; z < (int)blockIdx.z && ad != 0x7FFFFFFF; z++) ad = lora::next_adapter(id, ad);
+  if (threadIdx.x == 0) late = lo;
   __syncthreads();
-  if (w == 0 && mine) {
-    f32x4 s = part[0][lane];
-#pragma unroll
-    for (int q = 1; q < 4; q++) s += part[q][lane];
-#pragma unroll
-    for (int e = 0; e < 4; e++) s[e] = 16 * (int)blockIdx.y + 4 * G + e < lo.R ? s[e] * lo.scale[ad] : 0.f;
-    *(f32x4*)(lo.U + t * Rp + 16 * blockIdx.y + 4 * G) = s;
+  while (ad != 0x7FFFFFFF) {
+    GemmArgs p = a;
+    p.B = (const uint16_t*)lo.LA + (int64_t)ad * lo.stride_la;
+    p.ldb = lo.ld_la;
+    p.N = lo.R;
+    mid::tile<DT, 32, true, true, 64, StoreU<DT>, TILE>(p, m0, 128 * (int64_t)blockIdx.y, lds, lane, w,
+                                                        StoreU<DT>{&late, Rp, a.M, ad, lane});
+    for (int z = 0; z < (int)gridDim.z && ad != 0x7FFFFFFF; z++) ad = lora::next_adapter(id, ad);
+    __syncthreads();   // every wave is done with LDS
   }
 }
 
@@ -57,6 +75,7 @@ __global__ __launch_bounds__(256) void k_lora_shrink(GemmArgs a, LoraArgs lo, in
 // registers, 8190 rows with rank 64, N 8192, K 4096 took 714 us.)
 template <int DT>
 struct Expand {
+  static constexpr bool kStores = false;
   const LoraArgs& lo;
   int64_t Rp, M, N;
   int lane;
@@ -75,9 +94,9 @@ __global__ __launch_bounds__(256, 2) void k_lora(GemmArgs a, LoraArgs lo, int64_
   const Expand<DT> expand{lo, Rp, a.M, a.N, lane};
   const int64_t m0 = 128 * (int64_t)tm, n0 = mid::BN * (int64_t)tn;
   const int64_t left = a.M - m0;
-  if (left <= 32) mid::tile<DT, 32, true, true>(a, m0, n0, lds, lane, w, expand);
-  else if (left <= 64) mid::tile<DT, 64, true, true>(a, m0, n0, lds, lane, w, expand);
-  else mid::tile<DT, 128, true, true>(a, m0, n0, lds, lane, w, expand);
+  if (left <= 32) mid::tile<DT, 32, true, true, 64>(a, m0, n0, lds, lane, w, expand);
+  else if (left <= 64) mid::tile<DT, 64, true, true, 64>(a, m0, n0, lds, lane, w, expand);
+  else mid::tile<DT, 128, true, true, 64>(a, m0, n0, lds, lane, w, expand);
 }
 
 // Eight consecutive 16-bit values as float32.
@@ -216,7 +235,7 @@ hipError_t launch(const GemmArgs& a, const LoraArgs& lo, hipStream_t st) {
   const int64_t tm = (a.M + 127) / 128, tn = (a.N + mid::BN - 1) / mid::BN;
   if (tm * tn > 0x7FFFFFFF) return hipErrorInvalidValue;
   if (lo.R > 0 && lo.n > 0) {
-    const dim3 grid((uint32_t)((a.M + 15) / 16), (uint32_t)(Rp / 16), (uint32_t)(lo.n < 16 ? lo.n : 16));
+    const dim3 grid((uint32_t)((a.M + 31) / 32), (uint32_t)((lo.R + 127) / 128), (uint32_t)(lo.n < 4 ? lo.n : 4));
     hipLaunchKernelGGL(k_lora_shrink<DT>, grid, dim3(256), 0, st, a, lo, Rp);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

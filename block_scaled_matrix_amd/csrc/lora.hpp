@@ -26,18 +26,6 @@ __device__ __forceinline__ int adapter_of(const LoraArgs& lo, int64_t t, int64_t
   return a < lo.n ? a : -1;
 }
 
-// id: lane l's value is row l%16's adapter. Bit i of the result (i < 16): row i has an adapter that
-// no earlier row of the block has.
-__device__ __forceinline__ uint32_t first_rows(int id, int lane) {
-  bool first = id >= 0;
-#pragma unroll
-  for (int j = 0; j < 15; j++) {
-    const int v = __builtin_amdgcn_readlane(id, j);
-    if ((lane & 15) > j && v == id) first = false;
-  }
-  return (uint32_t)__ballot(first) & 0xFFFFu;
-}
-
 // 8 consecutive elements (16 bytes) of a 16-bit row, those at or past `left` elements zero.
 __device__ __forceinline__ uint4 load8(const uint16_t* p, int64_t left) {
   if (left <= 0) return make_uint4(0, 0, 0, 0);

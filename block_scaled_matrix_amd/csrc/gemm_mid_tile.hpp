@@ -208,7 +208,7 @@ __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, 
   typedef Tile<BM, AK, BK> TA;
   typedef Tile<BN, BKM, BK> TB;
   constexpr int MI = BM / 32, STAGE = TA::BYTES + TB::BYTES, NST = LDS / STAGE, PER = TA::COPIES + TB::COPIES;
-  static_assert(NST >= 2 && (MI < 4 ? MI : 4) * 16384 <= LDS, "stages");
+  static_assert(NST >= 2, "stages");
   const int wa = (BM / 2) * (w >> 1), wb = 64 * (w & 1);
   const uint16_t* A = (const uint16_t*)a.A;
   const uint16_t* B = (const uint16_t*)a.B;
@@ -272,12 +272,16 @@ __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, 
     __syncthreads();
   }
   more(m0 + wa, n0 + wb, acc);
-  if constexpr (MORE::kStores) {
-  } else if constexpr (MI <= 4) {
-    store<DT, MI, 0, MI>(a, m0 + wa, n0 + wb, lane, acc, lds + MI * 4096 * w);
-  } else {
-    store<DT, MI, 0, 4>(a, m0 + wa, n0 + wb, lane, acc, lds + 16384 * w);
-    store<DT, MI, 4, 4>(a, m0 + wa + 64, n0 + wb, lane, acc, lds + 16384 * w);
+  // the sums leave through LDS in parts of MC blocks of 16 rows a wave
+  if constexpr (!MORE::kStores) {
+    constexpr int FIT = LDS / 16384, MC = MI < FIT ? MI : (FIT >= 4 ? 4 : 2);
+    static_assert(MI % MC == 0 && MC * 16384 <= LDS, "store parts");
+    auto part = [&](auto m) {
+      constexpr int M0 = decltype(m)::value * MC;
+      if constexpr (M0 < MI) store<DT, MI, M0, MC>(a, m0 + wa + 16 * M0, n0 + wb, lane, acc, lds + MC * 4096 * w);
+    };
+    part(std::integral_constant<int, 0>{});
+    part(std::integral_constant<int, 1>{});
   }
 }
 

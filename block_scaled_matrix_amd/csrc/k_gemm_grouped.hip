@@ -81,13 +81,15 @@ __device__ __forceinline__ GemmArgs wgrad_product(const GemmArgs& a, const Group
   return t;
 }
 
-template <int DT, int BM, int BK>
-__global__ __launch_bounds__(256, 2) void k_grouped_wgrad(GemmArgs a, GroupArgs gr, int tiles_m, int tiles_n) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[mid::LDS_BYTES];
+template <int DT, int BM, int BK, int PER_CU>
+__global__ __launch_bounds__(256, PER_CU) void k_grouped_wgrad(GemmArgs a, GroupArgs gr, int tiles_m, int tiles_n) {
+  constexpr int LDS = 160 * 1024 / PER_CU;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[LDS];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   WgradSpot s;
   if (!wgrad_tile(blockIdx.x, gr.n, tiles_m, tiles_n, s)) return;
-  mid::tile<DT, BM, false, false, BK>(wgrad_product(a, gr, s.g), BM * (int64_t)s.tm, mid::BN * (int64_t)s.tn, lds, lane, w);
+  mid::tile<DT, BM, false, false, BK, mid::NoMore, LDS>(wgrad_product(a, gr, s.g), BM * (int64_t)s.tm,
+                                                        mid::BN * (int64_t)s.tn, lds, lane, w);
 }
 
 // The product of one group of rows out of the call's: operands and output moved to it.
@@ -169,7 +171,9 @@ hipError_t launch_gemm_grouped(const GemmArgs& a, const GroupArgs& gr, hipStream
 
 template <int DT>
 static hipError_t launch_wgrad_dt(const GemmArgs& a, const GroupArgs& gr, hipStream_t st) {
-  // Tiles of 256 rows where groups have rows enough for a long loop and the tiles fill the CUs: 16381
+  // Few rows a group: the loop is a step or two and loads, sums and stores of different tiles overlap, so
+  // four workgroups share a CU (K tiles of 32, 40 KiB of LDS each): 1021 rows over 32 groups (M 1000,
+  // N 520) 15.0 us against 18.5 us on two. Tiles of 256 rows where groups have rows enough for a long loop and the tiles fill the CUs: 16381
   // rows over 8 groups (M 4096, N 2048) 306 us against 343 us on 128; 1021 over 32 (M 1000, N 520) 21.1
   // against 19.8 us. (The dense GEMM's 256 x 256 tile: 350 and 40 us.)
   const int64_t tn = (a.N + mid::BN - 1) / mid::BN;
@@ -177,8 +181,9 @@ static hipError_t launch_wgrad_dt(const GemmArgs& a, const GroupArgs& gr, hipStr
   const int64_t tm = tall ? (a.M + 255) / 256 : (a.M + 127) / 128, share = (tm * tn + 7) / 8;
   if (share > 0x7FFFFFFF / 8 / gr.n) return hipErrorInvalidValue;
   const dim3 grid((uint32_t)(share * 8 * gr.n));
-  if (tall) hipLaunchKernelGGL((k_grouped_wgrad<DT, 256, 32>), grid, dim3(256), 0, st, a, gr, (int)tm, (int)tn);
-  else hipLaunchKernelGGL((k_grouped_wgrad<DT, 128, 64>), grid, dim3(256), 0, st, a, gr, (int)tm, (int)tn);
+  if (tall) hipLaunchKernelGGL((k_grouped_wgrad<DT, 256, 32, 2>), grid, dim3(256), 0, st, a, gr, (int)tm, (int)tn);
+  else if (gr.rows / gr.n < 64) hipLaunchKernelGGL((k_grouped_wgrad<DT, 128, 32, 4>), grid, dim3(256), 0, st, a, gr, (int)tm, (int)tn);
+  else hipLaunchKernelGGL((k_grouped_wgrad<DT, 128, 64, 2>), grid, dim3(256), 0, st, a, gr, (int)tm, (int)tn);
   return hipGetLastError();
 }
 

@@ -37,6 +37,15 @@ struct Spot {
   int tm, tn;         // the tile within the group
 };
 
+// Tile `li` of tiles_m x tiles_n in bands of GROUP_M tile rows walked column by column.
+template <int GROUP_M>
+__device__ __forceinline__ void band_tile(int li, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int per_band = GROUP_M * tiles_n, band = li / per_band, first = band * GROUP_M;
+  const int size = min(tiles_m - first, GROUP_M), in = li - band * per_band;
+  tm = first + in % size;
+  tn = in / size;
+}
+
 // Tile `pid` of the launch (wave-uniform result; false: no such tile). Tiles are numbered group by
 // group, inside a group in bands of GROUP_M tile rows walked column by column, and the numbers are
 // dealt to the XCDs (workgroup p runs on XCD p % 8) in eight contiguous ranges, so that the
@@ -75,10 +84,7 @@ __device__ __forceinline__ bool find_tile(const GroupArgs& gr, int pid, int tile
       const int first_tile = before + __builtin_amdgcn_readlane(incl, at) - tiles_m;
       const int li = lid - first_tile * tiles_n;
       if (li < 0 || li >= tiles_m * tiles_n) return false;  // (offsets that overlap beyond all counting)
-      const int per_band = GROUP_M * tiles_n, band = li / per_band, first = band * GROUP_M;
-      const int size = min(tiles_m - first, GROUP_M), in = li - band * per_band;
-      s.tm = first + in % size;
-      s.tn = in / size;
+      band_tile<GROUP_M>(li, tiles_m, tiles_n, s.tm, s.tn);
       return true;
     }
     before += __builtin_amdgcn_readlane(incl, 63);

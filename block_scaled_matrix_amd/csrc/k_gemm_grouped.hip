@@ -61,9 +61,7 @@ __device__ __forceinline__ bool wgrad_tile(int pid, int n, int tiles_m, int tile
   s.g = q / share;
   const int in = x * share + (q - s.g * share);
   if (in >= per) return false;
-  const int band = in / (4 * tiles_n), size = min(tiles_m - 4 * band, 4), li = in - band * 4 * tiles_n;
-  s.tm = 4 * band + li % size;
-  s.tn = li / size;
+  grouped::band_tile<4>(in, tiles_m, tiles_n, s.tm, s.tn);
   return true;
 }
 
@@ -102,13 +100,15 @@ __device__ __forceinline__ GemmArgs group_product(const GemmArgs& a, const Group
   return t;
 }
 
-// Groups of few rows: tiles of 128 rows, a group's last one of as few as hold its rows.
+// Tiles of 128 rows, a group's last one of as few as hold its rows. Bands of eight tile rows: an XCD's 64
+// tiles at work then read 16 panels of A and B, not 20 as in bands of four (8192 rows over 8 groups,
+// N 4096, K 8192: 545 against 567 us).
 template <int DT, bool BKM>
 __global__ __launch_bounds__(256, 2) void k_grouped_mid(GemmArgs a, GroupArgs gr, int tiles_n) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[mid::LDS_BYTES];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   grouped::Spot s;
-  if (!grouped::find_tile<128, 4>(gr, blockIdx.x, tiles_n, lane, s)) return;
+  if (!grouped::find_tile<128, 8>(gr, blockIdx.x, tiles_n, lane, s)) return;
   const GemmArgs t = group_product(a, gr, s.g, s.row0, s.rows);
   const int64_t m0 = 128 * (int64_t)s.tm, n0 = mid::BN * (int64_t)s.tn;
   const int left = s.rows - 128 * s.tm;
@@ -134,12 +134,15 @@ __global__ __launch_bounds__(skinny::THREADS) void k_grouped_skinny(GemmArgs a, 
 
 template <int DT>
 hipError_t launch_grouped_dt(const GemmArgs& a, const GroupArgs& gr, hipStream_t st) {
-  // The 256 x 256 tile only where groups fill it and there are four rounds of it over the 256 CUs:
-  // 16381 rows over 16 groups, N 4096, K 8192 (1152 tiles) 1155 us against 1180 us on 128 x 128
-  // tiles; 8190 rows over 8 groups, N 2048, K 8192 (288 tiles, the second round nearly empty) 400 us
-  // against 364 us.
-  const int64_t tiles = (gr.rows + BM - 1) / BM * ((a.N + BN - 1) / BN);
-  const bool big = gr.rows / gr.n >= 192 && tiles >= 1024;
+  // 256 x 256 or 128 x 128 tiles: what each would take, in rounds over the 256 CUs (512 slots) and at the
+  // rates that each reaches on even groups (1.15 and 0.97 PFLOP/s), with half a tile lost per group
+  // and, on the small tiles, half a round at the end. 16381 rows over 16 groups, N 4096, K 8192: 1155
+  // and 1180 us; 8190 rows over 8 groups, N 2048 (288 large tiles, the second round nearly empty): 400
+  // and 357 us.
+  auto row_tiles = [&](double bm) { return gr.n == 1 ? (double)((gr.rows + (int64_t)bm - 1) / (int64_t)bm) : gr.rows / bm + 0.5 * gr.n; };
+  const double large = (double)(((int64_t)(row_tiles(BM) * ((a.N + BN - 1) / BN)) + 255) / 256) * 256 * BM * BN / 1.15;
+  const double small = (row_tiles(128) * ((a.N + mid::BN - 1) / mid::BN) + 256) * 128 * mid::BN / 0.97;
+  const bool big = gr.rows / gr.n >= 192 && large < small;
   // Sixteen columns a workgroup where 128-column tiles would leave half the CUs without one: 16 rows of
   // one group, N = K = 4096 (32 such tiles) 21.8 -> 11.0 us, 64 rows 29.9 -> 15.2 us, 8 rows over 8 groups,
   // N 1024, K 2048 (64) 12.4 -> 9.3 us; even at 128 of them (32 rows over 8 groups, N = K = 2048: 18.0

@@ -3,6 +3,7 @@
 // its only store, so D is written once and never read back. Up to 64 rows (a decode batch) both work
 // row by row on the vector units, beside the weights' stream; beyond, on the matrix units.
 #include "gemm_mid_tile.hpp"
+#include "grouped.hpp"
 #include "lora.hpp"
 #include "skinny.hpp"
 #include "store16.hpp"
@@ -89,8 +90,11 @@ template <int DT>
 __global__ __launch_bounds__(256, 2) void k_lora(GemmArgs a, LoraArgs lo, int64_t Rp, int tiles_m, int tiles_n) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[mid::LDS_BYTES];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // (an XCD's workgroups take a contiguous eighth of the tiles, in bands of eight tile rows)
+  const int total = tiles_m * tiles_n, share = (total + 7) >> 3, lid = ((int)blockIdx.x & 7) * share + ((int)blockIdx.x >> 3);
+  if (lid >= total) return;
   int tm, tn;
-  gemm::tile_coords(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  grouped::band_tile<8>(lid, tiles_m, tiles_n, tm, tn);
   const Expand<DT> expand{lo, Rp, a.M, a.N, lane};
   const int64_t m0 = 128 * (int64_t)tm, n0 = mid::BN * (int64_t)tn;
   const int64_t left = a.M - m0;
@@ -233,14 +237,15 @@ hipError_t launch(const GemmArgs& a, const LoraArgs& lo, hipStream_t st) {
   if (a.M <= 48) return launch_skinny<DT, 3>(a, lo, Rp, st);
   if (a.M <= 64) return launch_skinny<DT, 4>(a, lo, Rp, st);
   const int64_t tm = (a.M + 127) / 128, tn = (a.N + mid::BN - 1) / mid::BN;
-  if (tm * tn > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (tm * tn > 0x7FFFFFF0) return hipErrorInvalidValue;
   if (lo.R > 0 && lo.n > 0) {
     const dim3 grid((uint32_t)((a.M + 31) / 32), (uint32_t)((lo.R + 127) / 128), (uint32_t)(lo.n < 4 ? lo.n : 4));
     hipLaunchKernelGGL(k_lora_shrink<DT>, grid, dim3(256), 0, st, a, lo, Rp);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(k_lora<DT>, dim3((uint32_t)(tm * tn)), dim3(256), 0, st, a, lo, Rp, (int)tm, (int)tn);
+  hipLaunchKernelGGL(k_lora<DT>, dim3((uint32_t)((tm * tn + 7) / 8 * 8)), dim3(256), 0, st, a, lo,
+                     Rp, (int)tm, (int)tn);
   return hipGetLastError();
 }
 

@@ -202,9 +202,12 @@ struct NoMore {
 
 // One BM x 128 tile at (m0, n0) of the product that `a` describes (M, N, K, A, B, D its own), by four
 // waves with LDS bytes of LDS. more(row0, col0, acc) may add to a wave's sums before the store.
-template <int DT, int BM, bool AK, bool BKM, int BK = 64, class MORE = NoMore, int LDS = LDS_BYTES>
+// Q > 1: Q times four waves share the tile, wave w of part q taking every Q-th K tile from the q-th on in
+// LDS of its own (part q's starts at part 0's + q * LDS); part 0 adds the sums in part order and
+// stores. All waves of the workgroup come here together.
+template <int DT, int BM, bool AK, bool BKM, int BK = 64, class MORE = NoMore, int LDS = LDS_BYTES, int Q = 1>
 __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, uint8_t* lds, int lane, int w,
-                                     const MORE& more = MORE()) {
+                                     const MORE& more = MORE(), int q = 0) {
   typedef Tile<BM, AK, BK> TA;
   typedef Tile<BN, BKM, BK> TB;
   constexpr int MI = BM / 32, STAGE = TA::BYTES + TB::BYTES, NST = LDS / STAGE, PER = TA::COPIES + TB::COPIES;
@@ -222,10 +225,10 @@ __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, 
     for (int n = 0; n < 4; n++) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int nfull = (int)(a.K / BK), tail = (int)(a.K % BK);
   const uint32_t lds0 = gemm::lds_addr(lds);
-  // Tile kt's copies; past the last one they re-read it into a stage that nobody reads again, so
-  // that the counts waited for stay fixed.
-  auto issue = [&](int kt, int stage) {
-    const int64_t k0 = (int64_t)min(kt, nfull - 1) * BK;
+  // The copies of this part's it-th K tile; past the last one they re-read it into a stage that nobody
+  // reads again, so that the counts waited for stay fixed.
+  auto issue = [&](int it, int stage) {
+    const int64_t k0 = (int64_t)min(it * Q + q, nfull - 1) * BK;
     uint64_t ga, gb;
     gemm::sgpr_base2(TA::base(A, a.lda, m0, k0), TB::base(B, a.ldb, n0, k0), ga, gb);
     const uint32_t at = lds0 + stage * STAGE;
@@ -252,10 +255,10 @@ __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, 
 #pragma unroll
     for (int i = 0; i < NST - 1; i++) issue(i, i);
     int cur = 0;
-    for (int kt = 0; kt < nfull; kt++) {
+    for (int it = 0; it < (nfull + Q - 1) / Q; it++) {
       gemm::stage_barrier<(NST - 2) * PER>();
-      issue(kt + NST - 1, cur == 0 ? NST - 1 : cur - 1);
-      multiply(lds + cur * STAGE, std::integral_constant<int, BK / 32>{});
+      issue(it + NST - 1, cur == 0 ? NST - 1 : cur - 1);
+      if (Q == 1 || it * Q + q < nfull) multiply(lds + cur * STAGE, std::integral_constant<int, BK / 32>{});
       cur = cur + 1 == NST ? 0 : cur + 1;
     }
   }
@@ -264,12 +267,34 @@ __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, 
   gemm::stage_barrier<0>();
   if (tail) {
     const int64_t k0 = (int64_t)nfull * BK;
-    TA::fill(TA::base(A, a.lda, m0, k0), ao, tail, lds, w, lane);
-    TB::fill(TB::base(B, a.ldb, n0, k0), bo, tail, lds + TA::BYTES, w, lane);
+    if (q == 0) {
+      TA::fill(TA::base(A, a.lda, m0, k0), ao, tail, lds, w, lane);
+      TB::fill(TB::base(B, a.ldb, n0, k0), bo, tail, lds + TA::BYTES, w, lane);
+    }
     __syncthreads();
-    if (BK == 32 || tail <= 32) multiply(lds, std::integral_constant<int, 1>{});
-    else multiply(lds, std::integral_constant<int, 2>{});
+    if (q == 0) {
+      if (BK == 32 || tail <= 32) multiply(lds, std::integral_constant<int, 1>{});
+      else multiply(lds, std::integral_constant<int, 2>{});
+    }
     __syncthreads();
+  }
+  if constexpr (Q > 1) {
+    static_assert(MI * 16384 <= LDS, "joined sums");
+    uint8_t* mine = lds + MI * 4096 * w + 16 * lane;
+    if (q > 0) {
+#pragma unroll
+      for (int m = 0; m < MI; m++)
+#pragma unroll
+        for (int n = 0; n < 4; n++) *(BSM_LDS f32x4*)(mine + 1024 * (4 * m + n)) = acc[m][n];
+    }
+    __syncthreads();
+    if (q > 0) return;
+#pragma unroll
+    for (int p = 1; p < Q; p++)
+#pragma unroll
+      for (int m = 0; m < MI; m++)
+#pragma unroll
+        for (int n = 0; n < 4; n++) acc[m][n] += *(const BSM_LDS f32x4*)(mine + p * LDS + 1024 * (4 * m + n));
   }
   more(m0 + wa, n0 + wb, acc);
   // the sums leave through LDS in parts of MC blocks of 16 rows a wave

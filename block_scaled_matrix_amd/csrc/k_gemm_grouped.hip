@@ -117,6 +117,22 @@ __global__ __launch_bounds__(256, 2) void k_grouped_mid(GemmArgs a, GroupArgs gr
   else mid::tile<DT, 128, true, BKM>(t, m0, n0, lds, lane, w);
 }
 
+// Fewer tiles than CUs: tiles of 64 (32) rows, and eight waves a tile, each four every other K tile.
+template <int DT, bool BKM>
+__global__ __launch_bounds__(512) void k_grouped_split(GemmArgs a, GroupArgs gr, int tiles_n) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * mid::LDS_BYTES];
+  const int lane = threadIdx.x & 63, w8 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = w8 & 3, q = w8 >> 2;
+  grouped::Spot s;
+  if (!grouped::find_tile<64, 8>(gr, blockIdx.x, tiles_n, lane, s)) return;
+  const GemmArgs t = group_product(a, gr, s.g, s.row0, s.rows);
+  const int64_t m0 = 64 * (int64_t)s.tm, n0 = mid::BN * (int64_t)s.tn;
+  uint8_t* part = lds + q * mid::LDS_BYTES;
+  if (s.rows - 64 * s.tm <= 32)
+    mid::tile<DT, 32, true, BKM, 64, mid::NoMore, mid::LDS_BYTES, 2>(t, m0, n0, part, lane, w, mid::NoMore(), q);
+  else
+    mid::tile<DT, 64, true, BKM, 64, mid::NoMore, mid::LDS_BYTES, 2>(t, m0, n0, part, lane, w, mid::NoMore(), q);
+}
+
 // Few tiles: 16 MT rows x 16 columns a workgroup, its eight waves splitting K (skinny.hpp).
 template <int DT, int MT>
 __global__ __launch_bounds__(skinny::THREADS) void k_grouped_skinny(GemmArgs a, GroupArgs gr, int tiles_n) {
@@ -150,7 +166,11 @@ hipError_t launch_grouped_dt(const GemmArgs& a, const GroupArgs& gr, hipStream_t
   const int64_t used = gr.n < gr.rows ? gr.n : gr.rows, each = (gr.rows + used - 1) / used;
   const bool few = a.b_kmajor && each <= 64 && used * ((a.N + mid::BN - 1) / mid::BN) < 128;
   const int mt = !few ? 0 : each <= 16 ? 1 : each <= 32 ? 2 : 4;
-  const int bm = few ? 16 * mt : (big ? BM : 128), bn = few ? skinny::BN : (big ? BN : mid::BN);
+  // Fewer 128-row tiles than CUs: half as many rows and eight waves a tile (1000 rows over 4 groups,
+  // N = K = 1024, 78 tiles: 13.8 -> 9.7 us; 582 rows, N 1665, K 7227, 70: 69 -> 41 us; 1000 over 4, N 2048, K
+  // 1024, 157: 14.3 -> 10.7 us; at 258 and 314 tiles it is behind, 46.7 to 44.2 and 18.8 to 15.9 us).
+  const bool split = row_tiles(128) * ((a.N + mid::BN - 1) / mid::BN) < 192;
+  const int bm = few ? 16 * mt : (big ? BM : (split ? 64 : 128)), bn = few ? skinny::BN : (big ? BN : mid::BN);
   const int64_t tn = (a.N + bn - 1) / bn, n = (grouped::most_row_tiles(gr.rows, gr.n, bm) * tn + 7) / 8 * 8;
   if (n > 0x7FFFFFFF) return hipErrorInvalidValue;
   const dim3 grid((uint32_t)n);
@@ -158,6 +178,9 @@ hipError_t launch_grouped_dt(const GemmArgs& a, const GroupArgs& gr, hipStream_t
     if (mt == 1) hipLaunchKernelGGL((k_grouped_skinny<DT, 1>), grid, dim3(skinny::THREADS), 0, st, a, gr, (int)tn);
     else if (mt == 2) hipLaunchKernelGGL((k_grouped_skinny<DT, 2>), grid, dim3(skinny::THREADS), 0, st, a, gr, (int)tn);
     else hipLaunchKernelGGL((k_grouped_skinny<DT, 4>), grid, dim3(skinny::THREADS), 0, st, a, gr, (int)tn);
+  } else if (split && !big) {
+    if (a.b_kmajor) hipLaunchKernelGGL((k_grouped_split<DT, true>), grid, dim3(512), 0, st, a, gr, (int)tn);
+    else hipLaunchKernelGGL((k_grouped_split<DT, false>), grid, dim3(512), 0, st, a, gr, (int)tn);
   } else if (!big) {
     if (a.b_kmajor) hipLaunchKernelGGL((k_grouped_mid<DT, true>), grid, dim3(256), 0, st, a, gr, (int)tn);
     else hipLaunchKernelGGL((k_grouped_mid<DT, false>), grid, dim3(256), 0, st, a, gr, (int)tn);

@@ -86,21 +86,24 @@ struct Expand {
   }
 };
 
-template <int DT>
-__global__ __launch_bounds__(256, 2) void k_lora(GemmArgs a, LoraArgs lo, int64_t Rp, int tiles_m, int tiles_n) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[mid::LDS_BYTES];
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+// Q waves' fours a tile (gemm_mid_tile.hpp): 1, or 2 with tiles of 64 rows where there are few.
+template <int DT, int Q>
+__global__ __launch_bounds__(256 * Q, 3 - Q) void k_lora(GemmArgs a, LoraArgs lo, int64_t Rp, int tiles_m, int tiles_n) {
+  constexpr int ROWS = Q == 1 ? 128 : 64;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Q * mid::LDS_BYTES];
+  const int lane = threadIdx.x & 63, wq = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wq & 3, q = wq >> 2;
   // (an XCD's workgroups take a contiguous eighth of the tiles, in bands of eight tile rows)
   const int total = tiles_m * tiles_n, share = (total + 7) >> 3, lid = ((int)blockIdx.x & 7) * share + ((int)blockIdx.x >> 3);
   if (lid >= total) return;
   int tm, tn;
   grouped::band_tile<8>(lid, tiles_m, tiles_n, tm, tn);
   const Expand<DT> expand{lo, Rp, a.M, a.N, lane};
-  const int64_t m0 = 128 * (int64_t)tm, n0 = mid::BN * (int64_t)tn;
+  const int64_t m0 = ROWS * (int64_t)tm, n0 = mid::BN * (int64_t)tn;
   const int64_t left = a.M - m0;
-  if (left <= 32) mid::tile<DT, 32, true, true, 64>(a, m0, n0, lds, lane, w, expand);
-  else if (left <= 64) mid::tile<DT, 64, true, true, 64>(a, m0, n0, lds, lane, w, expand);
-  else mid::tile<DT, 128, true, true, 64>(a, m0, n0, lds, lane, w, expand);
+  uint8_t* part = lds + q * mid::LDS_BYTES;
+  if (left <= 32) mid::tile<DT, 32, true, true, 64, Expand<DT>, mid::LDS_BYTES, Q>(a, m0, n0, part, lane, w, expand, q);
+  else if (ROWS == 64 || left <= 64) mid::tile<DT, 64, true, true, 64, Expand<DT>, mid::LDS_BYTES, Q>(a, m0, n0, part, lane, w, expand, q);
+  else if constexpr (ROWS == 128) mid::tile<DT, 128, true, true, 64, Expand<DT>, mid::LDS_BYTES, Q>(a, m0, n0, part, lane, w, expand, q);
 }
 
 // Eight consecutive 16-bit values as float32.
@@ -236,7 +239,10 @@ hipError_t launch(const GemmArgs& a, const LoraArgs& lo, hipStream_t st) {
   if (a.M <= 32) return launch_skinny<DT, 2>(a, lo, Rp, st);
   if (a.M <= 48) return launch_skinny<DT, 3>(a, lo, Rp, st);
   if (a.M <= 64) return launch_skinny<DT, 4>(a, lo, Rp, st);
-  const int64_t tm = (a.M + 127) / 128, tn = (a.N + mid::BN - 1) / mid::BN;
+  // (fewer 128-row tiles than CUs: bsm_gemm_grouped's rule and figures)
+  const int64_t tn = (a.N + mid::BN - 1) / mid::BN;
+  const bool split = (a.M + 127) / 128 * tn < 192;
+  const int64_t tm = split ? (a.M + 63) / 64 : (a.M + 127) / 128;
   if (tm * tn > 0x7FFFFFF0) return hipErrorInvalidValue;
   if (lo.R > 0 && lo.n > 0) {
     const dim3 grid((uint32_t)((a.M + 31) / 32), (uint32_t)((lo.R + 127) / 128), (uint32_t)(lo.n < 4 ? lo.n : 4));
@@ -244,8 +250,9 @@ hipError_t launch(const GemmArgs& a, const LoraArgs& lo, hipStream_t st) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(k_lora<DT>, dim3((uint32_t)((tm * tn + 7) / 8 * 8)), dim3(256), 0, st, a, lo,
-                     Rp, (int)tm, (int)tn);
+  const dim3 grid((uint32_t)((tm * tn + 7) / 8 * 8));
+  if (split) hipLaunchKernelGGL((k_lora<DT, 2>), grid, dim3(512), 0, st, a, lo, Rp, (int)tm, (int)tn);
+  else hipLaunchKernelGGL((k_lora<DT, 1>), grid, dim3(256), 0, st, a, lo, Rp, (int)tm, (int)tn);
   return hipGetLastError();
 }
 

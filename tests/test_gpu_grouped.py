@@ -213,3 +213,20 @@ def test_few_rows_and_long_k(sizes, ab, d, K):
     """Few tiles and a long sum (the waves split K), with groups far above the average among them."""
     run(sizes, 50, K, ab, "k", d, seed=K, first=1, behind=1, extra=8)
     run(sizes, 50, K, ab, "k", d, 1, bsm.ewise_desc("silu_affine", 0.5, 0.25), seed=K)
+
+
+@pytest.mark.parametrize("major", ["k", "n"])
+@pytest.mark.parametrize("K", [32, 64, 100, 128, 192, 1000])
+def test_fewer_tiles_than_compute_units(K, major):
+    """Two sets of waves share a tile's sum: one, two, three and more K tiles and a partial one."""
+    run([65, 0, 130, 90, 32], 260, K, "bf16", major, seed=K, behind=2)
+    run([100, 200], 260, K, "f16", major, "f32", 1, bsm.ewise_desc("silu_affine", 1.0, 0.5), seed=K)
+
+
+def test_large_tiles():
+    """Groups that the 256 x 256 tile takes (and their ragged ends), both orders of the weight, and long groups of a
+    weight gradient."""
+    for major in "kn":
+        run([1300, 770, 3, 2047], 4100, 72, "bf16", major, seed=6)
+    wgrad([700, 0, 1030], 520, 4200, "bf16", "f32", 1, seed=7)
+    wgrad([700, 0, 1030], 4200, 520, "f16", "f16", 0, seed=8)

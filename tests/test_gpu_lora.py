@@ -112,3 +112,12 @@ def test_same_bits_every_time():
     a = run(mixed(100, 6), 264, 520, 24, 6, seed=8)
     for _ in range(3):
         assert torch.equal(run(mixed(100, 6), 264, 520, 24, 6, seed=8), a)
+
+
+@pytest.mark.parametrize("T,N", [(70, 300), (200, 520), (3300, 1100)])
+@pytest.mark.parametrize("K", [64, 100, 264])
+def test_tile_shapes(T, N, K):
+    """Few tiles (two sets of waves a tile) and many, requests of several rows each, ranks of one step and more."""
+    ids = [(t // 37) % 4 - 1 for t in range(T)]
+    run(ids, N, K, 24, 3, "bf16", seed=T)
+    run(ids, N, K, 72, 3, "f16", "f32", seed=K)

@@ -270,29 +270,40 @@ def _here(stream, *tensors):
     """The stream's handle, once every torch tensor given is known to live on the current device: the kernels
     take addresses, and one of the host or of another device would fault them. Work on another device goes
     under torch.cuda.device of that device."""
-    at = None
+    at = -1
     for t in tensors:
-        if t is None or isinstance(t, int):
+        if t is None or type(t) is int:
             continue
-        if not t.is_cuda:
+        d = t.get_device()
+        if d < 0:
             raise BsmError(-13, f"a tensor on {t.device}: the library takes device memory")
-        if at is None:
+        if d != at:
             import torch
-            at = torch.cuda.current_device()
-        if t.device.index != at:
-            raise BsmError(-13, f"a tensor on {t.device} while the current device is cuda:{at}")
+            if d != torch.cuda.current_device():
+                raise BsmError(-13, f"a tensor on {t.device} while the current device is cuda:{torch.cuda.current_device()}")
+            at = d
+    if stream is None and at >= 0:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(at)   # (current_stream() without the object around it)
     return _stream(stream)
+
+
+_int32 = None
 
 
 def _ints(t, what):
     """Address of a DEVICE array of int32, checked where it is a torch tensor."""
-    if t is not None and not isinstance(t, int):
+    if t is None or type(t) is int:
+        return t
+    global _int32
+    if _int32 is None:
         import torch
-        if t.dtype != torch.int32:
-            raise BsmError(-8, f"{what} must be int32, not {t.dtype}")
-        if not t.is_contiguous():
-            raise BsmError(-5, f"{what} must be contiguous")
-    return _ptr(t)
+        _int32 = torch.int32
+    if t.dtype is not _int32:
+        raise BsmError(-8, f"{what} must be int32, not {t.dtype}")
+    if not t.is_contiguous():
+        raise BsmError(-5, f"{what} must be contiguous")
+    return t.data_ptr()
 
 
 def bsm_gemm_grouped(rows, N, K, n_groups, offsets, ab: str, A, lda, B, ldb, b_major: str, stride_b, d_fmt: str, D, ldd,

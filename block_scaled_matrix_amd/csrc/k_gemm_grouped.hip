@@ -135,7 +135,7 @@ __global__ __launch_bounds__(512) void k_grouped_split(GemmArgs a, GroupArgs gr,
 
 // Few tiles: 16 MT rows x 16 columns a workgroup, its eight waves splitting K (skinny.hpp).
 template <int DT, int MT>
-__global__ __launch_bounds__(skinny::THREADS) void k_grouped_skinny(GemmArgs a, GroupArgs gr, int tiles_n) {
+__global__ __launch_bounds__(skinny::THREADS, MT == 1 ? 4 : 2) void k_grouped_skinny(GemmArgs a, GroupArgs gr, int tiles_n) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[skinny::lds_bytes<MT>()];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   grouped::Spot s;

@@ -167,7 +167,7 @@ __global__ __launch_bounds__(1024) void k_lora_shrink_rows(GemmArgs a, LoraArgs 
 // their way, the adapters' part, row by row: wave w takes rows w, w + 8, ..; lane l sums r 8(l/16) .. +7 of every 32 for column l%16, in
 // float32, the four lanes of a column in a fixed tree. A row reads its own adapter only.
 template <int DT, int MT>
-__global__ __launch_bounds__(skinny::THREADS) void k_lora_skinny(GemmArgs a, LoraArgs lo, int64_t Rp, int tiles_n) {
+__global__ __launch_bounds__(skinny::THREADS, MT == 1 ? 4 : 2) void k_lora_skinny(GemmArgs a, LoraArgs lo, int64_t Rp, int tiles_n) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[skinny::lds_bytes<MT>()];
   __shared__ float adapted[16 * MT][17];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), i = lane & 15, G = lane >> 4;

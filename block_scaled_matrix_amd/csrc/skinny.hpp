@@ -14,6 +14,7 @@
 namespace bsm {
 namespace skinny {
 
+// (Up to 16 rows two workgroups share a CU, 128 registers a lane.)
 constexpr int WAVES = 8, BN = 16, THREADS = 64 * WAVES;
 
 // LDS a workgroup needs: each wave a piece of the weights and MT of X.
@@ -22,12 +23,12 @@ constexpr int lds_bytes() { return WAVES * (1 + MT) * 2048; }
 
 // The sums of this wave's pieces for rows m0 .. + 16 MT - 1 and columns n0 .. + 15: acc[mt] holds row
 // 16 mt + l%16, columns 4(l/16) .. +3. Rows past M and columns past N repeat the last ones.
-// The weights of U pieces (eight are a wave's whole share of K 4096) are asked for before anything else is,
-// then `meanwhile` runs once; X comes from the L2 one piece ahead.
+// P pieces of the weights and of X are in flight per wave, asked for before anything else is; then
+// `meanwhile` runs once.
 template <int DT, int MT, typename F>
 __device__ __forceinline__ void product(const GemmArgs& a, int64_t m0, int64_t n0, int lane, int w, uint8_t* buf,
                                         f32x4 (&acc)[MT], F meanwhile) {
-  constexpr int U = MT < 4 ? 8 : 4;   // (eight beside four blocks of X spill registers)
+  constexpr int P = MT <= 2 ? 4 : MT == 3 ? 3 : 2;   // (what the registers hold)
   const int i = lane & 15, G = lane >> 4, lr = lane >> 3, lc = lane & 7;
   // this lane's rows (8h + lr of a 16-row block) at its chunk lc of a piece, and where they go in LDS
   const uint16_t* b[2];
@@ -44,21 +45,15 @@ __device__ __forceinline__ void product(const GemmArgs& a, int64_t m0, int64_t n
 #pragma unroll
   for (int m = 0; m < MT; m++) acc[m] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int full = (int)(a.K / 64);
-  uint4 fb[U][2], fx[2][MT][2];
-  auto load_w = [&](int p) {
-#pragma unroll
-    for (int u = 0; u < U; u++)
-      if (p + u * WAVES < full) {
-#pragma unroll
-        for (int h = 0; h < 2; h++) fb[u][h] = *(const uint4*)(b[h] + 64 * (int64_t)(p + u * WAVES));
-      }
-  };
-  auto load_x = [&](int p, uint4 (&f)[MT][2]) {
+  uint4 fb[P][2], fx[P][MT][2];
+  auto load = [&](int p, uint4 (&wv)[2], uint4 (&xv)[MT][2]) {
     if (p < full) {
 #pragma unroll
-      for (int m = 0; m < MT; m++)
+      for (int h = 0; h < 2; h++) {
+        wv[h] = *(const uint4*)(b[h] + 64 * (int64_t)p);
 #pragma unroll
-        for (int h = 0; h < 2; h++) f[m][h] = *(const uint4*)(x[m][h] + 64 * (int64_t)p);
+        for (int m = 0; m < MT; m++) xv[m][h] = *(const uint4*)(x[m][h] + 64 * (int64_t)p);
+      }
     }
   };
   auto multiply = [&](const uint4 (&wv)[2], const uint4 (&xv)[MT][2]) {
@@ -76,17 +71,16 @@ __device__ __forceinline__ void product(const GemmArgs& a, int64_t m0, int64_t n
       for (int m = 0; m < MT; m++) acc[m] = lora::mfma16<DT>(bv, lds_read_b128(buf + 2048 * (m + 1) + o), acc[m]);
     }
   };
-  load_w(w);
-  load_x(w, fx[0]);
+#pragma unroll
+  for (int u = 0; u < P; u++) load(w + u * WAVES, fb[u], fx[u]);
   asm volatile("" ::: "memory");   // (the loads stay ahead of what follows)
   meanwhile();
-  for (int p = w; p < full; p += U * WAVES) {
-    if (p != w) load_w(p);
+  for (int p = w; p < full; p += P * WAVES) {
 #pragma unroll
-    for (int u = 0; u < U; u++) {
+    for (int u = 0; u < P; u++) {
       const int q = p + u * WAVES;
-      load_x(q + WAVES, fx[(u + 1) & 1]);
-      if (q < full) multiply(fb[u], fx[u & 1]);
+      if (q < full) multiply(fb[u], fx[u]);
+      load(q + P * WAVES, fb[u], fx[u]);
     }
   }
   if (a.K % 64 && full % WAVES == w) {

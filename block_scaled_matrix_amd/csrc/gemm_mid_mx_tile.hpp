@@ -100,25 +100,32 @@ __device__ __forceinline__ void store_rows(const GemmArgs& a, int64_t m0, int64_
 }
 
 // One BM x 128 tile at (m0, n0) of the product that `a` describes, by four waves with LDS_BYTES of LDS.
-template <int CA, int CB, bool BF, int BM>
-__device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, uint8_t* lds, int lane, int w) {
+// Q 2: eight waves share it, part q's four (LDS of their own, part 1's LDS bytes behind part 0's) taking
+// the q-th half of the whole K tiles; part 0 adds the sums and stores. All waves come here together.
+// `out` is `a` once more, for the store (a copy in LDS leaves the loop more SGPRs).
+template <int CA, int CB, bool BF, int BM, int Q = 1, int LDS = LDS_BYTES>
+__device__ __forceinline__ void tile(const GemmArgs& a, const GemmArgs& out, int64_t m0, int64_t n0, uint8_t* lds, int lane,
+                                     int w, int q = 0) {
   typedef Tile<CA, BM> TA;
   typedef Tile<CB, BN> TB;
   // three scale buffers of A's 128 rows and B's 128, 16 bytes a row, then the stages
   constexpr int GROUP = 4096, RING = 3 * GROUP, STAGE = TA::BYTES + TB::BYTES;
-  constexpr int FIT = (LDS_BYTES - RING) / STAGE, NST = FIT < 6 ? FIT : 6, PER = TA::COPIES + TB::COPIES + 1;
+  constexpr int FIT = (LDS - RING) / STAGE, NST = FIT < 6 ? FIT : 6, PER = TA::COPIES + TB::COPIES + 1;
   constexpr int MI = BM == 128 ? 2 : 1, NI = BM == 32 ? 1 : 2;
-  static_assert(NST >= 2 && NST <= 6 && BM * 512 <= LDS_BYTES, "stages");
+  static_assert(NST >= 2 && NST <= 6 && BM * 512 <= LDS, "stages");
   const int wa = BM == 32 ? 0 : (BM / 2) * (w >> 1), wb = BM == 32 ? 32 * w : 64 * (w & 1);
   const int sh = 8 * (lane >> 5);
   const int64_t lda = a.lda * TA::P::BITS / 8, ldb = a.ldb * TB::P::BITS / 8;
-  const uint8_t* A = (const uint8_t*)a.A + m0 * lda;
-  const uint8_t* B = (const uint8_t*)a.B + n0 * ldb;
+  // this part's whole K tiles: nfull of them from tile t0 on (none: it goes through the motions on tile 0)
+  const int all = (int)(a.K / KT), share = (all + Q - 1) / Q, tail = (int)(a.K % KT);
+  const int nfull = Q == 1 ? all : max(min(all - q * share, share), 0), t0 = nfull > 0 ? q * share : 0, last = max(nfull - 1, 0);
+  const uint8_t* A = (const uint8_t*)a.A + m0 * lda + (int64_t)t0 * TA::P::ROW;
+  const uint8_t* B = (const uint8_t*)a.B + n0 * ldb + (int64_t)t0 * TB::P::ROW;
   uint32_t ao[TA::COPIES], bo[TB::COPIES];
   TA::offsets(lda, a.M - m0, w, lane, ao);
   TB::offsets(ldb, a.N - n0, w, lane, bo);
   uint64_t sfa, sfb;
-  gemm::sgpr_base2(a.SFA + m0 * a.ld_sfa, a.SFB + n0 * a.ld_sfb, sfa, sfb);
+  gemm::sgpr_base2(a.SFA + m0 * a.ld_sfa + 4 * (int64_t)t0, a.SFB + n0 * a.ld_sfb + 4 * (int64_t)t0, sfa, sfb);
   f32x16 acc[MI][NI];
 #pragma unroll
   for (int m = 0; m < MI; m++)
@@ -126,7 +133,6 @@ __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, 
     for (int n = 0; n < NI; n++)
 #pragma unroll
       for (int e = 0; e < 16; e++) acc[m][n][e] = 0.f;
-  const int nfull = (int)(a.K / KT), tail = (int)(a.K % KT);
   const uint32_t lds0 = gemm::lds_addr(lds);
   // Quarter q of scale group g (K tiles 4g ..), this wave's 16 rows of its 64: rows 64q + 16w .. of A's
   // 128 and B's 128, lane l moving the word at place l%4 of row l/4 (mxany::ring_word_offset). Words
@@ -135,7 +141,7 @@ __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, 
     const int op = q >> 1, R = 64 * (q & 1) + 16 * w + (lane >> 2);
     const int word = (lane & 3) ^ ((R >> 4) & 3) ^ ((R >> 6) & 1) ^ (op ? 2 : 0);
     const int64_t rows = op ? a.N - n0 : a.M - m0;
-    const uint32_t off = (uint32_t)(min((int64_t)R, rows - 1) * (op ? a.ld_sfb : a.ld_sfa)) + 4u * (uint32_t)min(4 * g + word, nfull - 1);
+    const uint32_t off = (uint32_t)(min((int64_t)R, rows - 1) * (op ? a.ld_sfb : a.ld_sfa)) + 4u * (uint32_t)min(4 * g + word, last);
     gemm::dma4u(op ? sfb : sfa, off, lds0 + (g % 3) * GROUP + 2048 * op + 16 * (64 * (q & 1) + 16 * w));
   };
   // Tile kt's copies, and with them quarter (kt + 3) % 4 of scale group (kt + 3) / 4: group g comes with
@@ -144,7 +150,7 @@ __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, 
   // Past the last tile the copies repeat the last one's into a stage that nobody reads again, so
   // that the counts waited for stay fixed.
   auto issue = [&](int kt, int stage) {
-    const int64_t k = min(kt, nfull - 1);
+    const int64_t k = min(kt, last);
     uint64_t ga, gb;
     gemm::sgpr_base2(A + k * TA::P::ROW, B + k * TB::P::ROW, ga, gb);
     const uint32_t at = lds0 + RING + stage * STAGE;
@@ -191,15 +197,16 @@ __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, 
     step(std::integral_constant<int, 1>{});
   };
   uint32_t sa[MI], sb[NI];
-  if (nfull > 0) {
+  if (share > 0) {
 #pragma unroll
-    for (int q = 0; q < 3; q++) quarter(0, q);
+    for (int j = 0; j < 3; j++) quarter(0, j);
 #pragma unroll
     for (int i = 0; i < NST - 1; i++) issue(i, i);
     int cur = 0;
-    for (int kt = 0; kt < nfull; kt++) {
+    for (int kt = 0; kt < share; kt++) {
       gemm::stage_barrier<(NST - 2) * PER>();
       issue(kt + NST - 1, cur == 0 ? NST - 1 : cur - 1);
+      if (Q > 1 && kt >= nfull) continue;   // (the other part has one more; its barriers are joined)
       const uint8_t* sc = lds + ((kt >> 2) % 3) * GROUP;
 #pragma unroll
       for (int m = 0; m < MI; m++) sa[m] = *(const BSM_LDS uint32_t*)(sc + mxany::ring_word_offset(0, wa + 32 * m + (lane & 31), kt & 3));
@@ -211,34 +218,66 @@ __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, 
   }
   gemm::stage_barrier<0>();
   if (tail) {
-    TA::fill(A + (int64_t)nfull * TA::P::ROW, ao, tail * TA::P::BITS / 8, lds + RING, w, lane);
-    TB::fill(B + (int64_t)nfull * TB::P::ROW, bo, tail * TB::P::BITS / 8, lds + RING + TA::BYTES, w, lane);
-    // (each lane reads its rows' words itself: once per tile)
+    const int64_t kt = all - t0;            // (from this part's bases)
+    if (q == 0) {
+      TA::fill(A + kt * TA::P::ROW, ao, tail * TA::P::BITS / 8, lds + RING, w, lane);
+      TB::fill(B + kt * TB::P::ROW, bo, tail * TB::P::BITS / 8, lds + RING + TA::BYTES, w, lane);
+      // (each lane reads its rows' words itself: once per tile)
 #pragma unroll
-    for (int m = 0; m < MI; m++)
-      sa[m] = mxany::mask_scale_word(mxany::load_scale_word(a.SFA, a.ld_sfa, m0, a.M, wa + 32 * m + (lane & 31), nfull), nfull, a.K / 32);
+      for (int m = 0; m < MI; m++)
+        sa[m] = mxany::mask_scale_word(mxany::load_scale_word(a.SFA, a.ld_sfa, m0, a.M, wa + 32 * m + (lane & 31), all), all, a.K / 32);
 #pragma unroll
-    for (int n = 0; n < NI; n++)
-      sb[n] = mxany::mask_scale_word(mxany::load_scale_word(a.SFB, a.ld_sfb, n0, a.N, wb + 32 * n + (lane & 31), nfull), nfull, a.K / 32);
+      for (int n = 0; n < NI; n++)
+        sb[n] = mxany::mask_scale_word(mxany::load_scale_word(a.SFB, a.ld_sfb, n0, a.N, wb + 32 * n + (lane & 31), all), all, a.K / 32);
+    }
     __syncthreads();
-    multiply(0, sa, sb);
+    if (q == 0) multiply(0, sa, sb);
     __syncthreads();
   }
-  // register 4q + e of a block is row l%32, column 8q + 4(l/32) + e
+  if constexpr (Q > 1) {
+    uint8_t* mine = lds + MI * NI * 4096 * w + 16 * lane;
+    static_assert(MI * NI * 16384 <= LDS, "joined sums");
+    if (q > 0) {
 #pragma unroll
-  for (int m = 0; m < MI; m++)
+      for (int m = 0; m < MI; m++)
 #pragma unroll
-    for (int n = 0; n < NI; n++)
+        for (int n = 0; n < NI; n++)
 #pragma unroll
-      for (int q = 0; q < 4; q++) {
-        const int r = wa + 32 * m + (lane & 31), c = wb / 4 + 8 * n + 2 * q + (lane >> 5);
+          for (int e = 0; e < 4; e++)
+            *(BSM_LDS f32x4*)(mine + 1024 * (4 * (NI * m + n) + e)) =
+                f32x4{acc[m][n][4 * e], acc[m][n][4 * e + 1], acc[m][n][4 * e + 2], acc[m][n][4 * e + 3]};
+    }
+    __syncthreads();
+    if (q == 0) {
+#pragma unroll
+      for (int m = 0; m < MI; m++)
+#pragma unroll
+        for (int n = 0; n < NI; n++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) {
+            const f32x4 v = *(const BSM_LDS f32x4*)(mine + LDS + 1024 * (4 * (NI * m + n) + e));
+#pragma unroll
+            for (int u = 0; u < 4; u++) acc[m][n][4 * e + u] += v[u];
+          }
+    }
+  }
+  // register 4e + u of a block is row l%32, column 8e + 4(l/32) + u
+  if (q == 0) {
+#pragma unroll
+    for (int m = 0; m < MI; m++)
+#pragma unroll
+      for (int n = 0; n < NI; n++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+        const int r = wa + 32 * m + (lane & 31), c = wb / 4 + 8 * n + 2 * e + (lane >> 5);
         const f32x16& v = acc[m][n];
         lds_write_b128(lds + 512 * r + 16 * (c ^ (r & 15)),
-                       make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
-                                  __float_as_uint(v[4 * q + 3])));
+                       make_uint4(__float_as_uint(v[4 * e]), __float_as_uint(v[4 * e + 1]), __float_as_uint(v[4 * e + 2]),
+                                  __float_as_uint(v[4 * e + 3])));
       }
+  }
   __syncthreads();
-  store_rows<BM>(a, m0, n0, lds, lane, w);
+  if (q == 0) store_rows<BM>(out, m0, n0, lds, lane, w);
 }
 
 }  // namespace midmx

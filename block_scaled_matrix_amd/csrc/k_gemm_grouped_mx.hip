@@ -21,9 +21,16 @@ static hipError_t launch_tuned(const GemmArgs& a, const GroupArgs& gr, hipStream
 }
 
 hipError_t launch_gemm_grouped_mx(const GemmArgs& a, const GroupArgs& gr, hipStream_t st) {
-  // Few rows a group: 64 rows over 32 groups (E4M3 x E2M1, N 4096, K 4096) 65.6 us against 162 us on 256 x 256
-  // tiles; at 512 and 2048 rows a group those are faster (MXFP8 317 against 448 us, MXFP4 329 against 590 us).
-  if (gr.rows / gr.n < 192) return launch_gemm_grouped_mx_mid(a, gr, st);
+  // 256 x 256 tiles (in rounds over the 256 CUs) or 128 x 128 ones (512 slots, 0.6 of the large tile's
+  // rate on even groups), with half a tile lost per group and half a round at the end on the small
+  // ones: at 512 and 2048 rows a group the large are faster (8190 rows over 16 groups, N 8192, K 4096 in
+  // MXFP8 317 against 448 us; 16381 over 8, N 4096, K 8192 in MXFP4 329 against 590 us); 64 rows over 32 groups
+  // (E4M3 x E2M1, N = K = 4096) took 162 us on them, 57 us on the small ones, 1000 rows over 4 groups (N 2048,
+  // K 1024) 30 us.
+  auto row_tiles = [&](double bm) { return gr.n == 1 ? (double)((gr.rows + (int64_t)bm - 1) / (int64_t)bm) : gr.rows / bm + 0.5 * gr.n; };
+  const double large = (double)(((int64_t)(row_tiles(BM) * ((a.N + BN - 1) / BN)) + 255) / 256) * 256 * BM * BN;
+  const double small = (row_tiles(128) * ((a.N + 127) / 128) + 256) * 128 * 128 / 0.6;
+  if (gr.rows / gr.n < 192 || small < large) return launch_gemm_grouped_mx_mid(a, gr, st);
   const bool f32 = a.d_fmt == BSM_F32;
   if (a.dtype == BSM_E2M1 && a.dtype_b == BSM_E2M1)
     return f32 ? launch_tuned<4, 4, 4, BSM_F32>(a, gr, st) : launch_tuned<4, 4, 4, BSM_BF16>(a, gr, st);

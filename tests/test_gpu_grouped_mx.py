@@ -58,8 +58,9 @@ def run(sizes, N, K, a="e4m3", b="e4m3", fast=0, d="bf16", accum=0, ew=None, see
         tol = 1e-5 * mag
         if fast:
             for k in range(0, K, 32):
-                p = (xv[lo:hi, None, k:k + 32] * wv[i][None, :, k:k + 32]).abs()
-                tol += torch.minimum(p, p.amax(-1, keepdim=True) * 2.0 ** -13).sum(-1) if hi > lo else 0
+                for r in range(lo, hi, 64):
+                    p = (xv[r:min(r + 64, hi), None, k:k + 32] * wv[i][None, :, k:k + 32]).abs()
+                    tol[r - lo:r - lo + 64] += torch.minimum(p, p.amax(-1, keepdim=True) * 2.0 ** -13).sum(-1)
         if accum:
             ref = ref + D0[lo:hi, :N].double()
             tol = tol + 2.0 ** -23 * (mag + D0[lo:hi, :N].double().abs())
@@ -133,3 +134,16 @@ def test_matches_the_product_of_one_group():
                                      xsd.stride(0), "e2m1", wd, K, 0, wsd, wsd.stride(1), 0, 0, "f32", D, N)
     bsm.bsm_gemm_block_scale(rows, N, K, "e4m3", xd, K, xsd, xsd.stride(0), "e2m1", wd, K, wsd, wsd.stride(1), E, N)
     assert ((D - E).abs().double().cpu() <= 2e-5 * (xv.abs() @ wv[0].abs().T)).all()
+
+
+@pytest.mark.parametrize("a,b,fast", PAIRS)
+@pytest.mark.parametrize("K", [32, 128, 160, 256, 384, 1184])
+def test_fewer_tiles_than_compute_units(K, a, b, fast):
+    """Two sets of waves share a tile's K: none, one and more whole K tiles each, an odd one, and a partial one."""
+    run([65, 0, 130, 90, 32, 1], 260, K, a, b, fast, "f32", seed=K, behind=2, extra=16)
+
+
+@pytest.mark.parametrize("a,b,fast", PAIRS)
+def test_large_tiles(a, b, fast):
+    """Groups that the 256 x 256 kernels take, and their ragged ends."""
+    run([700, 300, 3, 520], 4100, 160, a, b, fast, "bf16", seed=6)

@@ -46,16 +46,19 @@ __device__ __forceinline__ void band_tile(int li, int tiles_m, int tiles_n, int&
   tn = in / size;
 }
 
-// Tile `pid` of the launch (wave-uniform result; false: no such tile). Tiles are numbered group by
-// group, inside a group in bands of GROUP_M tile rows walked column by column, and the numbers are
-// dealt to the XCDs (workgroup p runs on XCD p % 8) in eight contiguous ranges, so that the
-// workgroups of one XCD share a group's weight panels in its L2.
-template <int BM, int GROUP_M>
-__device__ __forceinline__ bool find_tile(const GroupArgs& gr, int pid, int tiles_n, int lane, Spot& s) {
+// Tile `pid` of the launch (wave-uniform result; false: no such tile). Group g has count(rows of g) row
+// tiles of tiles_n tiles each. Tiles are numbered group by group, inside a group in bands of GROUP_M
+// tile rows walked column by column, and the numbers are dealt to the XCDs (workgroup p runs on XCD
+// p % 8) in eight contiguous ranges, so that the workgroups of one XCD share a group's weight panels
+// in its L2. On return `used` is the number of pids that the split at hand can have tiles for (a
+// multiple of 8).
+template <int GROUP_M, typename F>
+__device__ __forceinline__ bool find_tile_of(const GroupArgs& gr, int pid, int tiles_n, int lane, F count, Spot& s,
+                                             int& used) {
   auto tiles_of = [&](int i, int& lo, int& hi) {
     if (i < gr.n) group_range(gr, i, lo, hi);
     else lo = hi = 0;
-    return (int)(((int64_t)(hi - lo) + BM - 1) / BM);
+    return count(hi - lo);
   };
   int lo, hi;
   int t = tiles_of(lane, lo, hi), incl = wave_inclusive_scan(t);
@@ -65,6 +68,7 @@ __device__ __forceinline__ bool find_tile(const GroupArgs& gr, int pid, int tile
     all += __builtin_amdgcn_readlane(wave_inclusive_scan(tiles_of(i0 + lane, l, h)), 63);
   }
   const int total = all * tiles_n, chunk = (total + 7) >> 3;
+  used = 8 * chunk;
   const int lid = (pid & 7) * chunk + (pid >> 3);
   if ((pid >> 3) >= chunk || lid >= total) return false;
   const int rt = lid / tiles_n;
@@ -90,6 +94,13 @@ __device__ __forceinline__ bool find_tile(const GroupArgs& gr, int pid, int tile
     before += __builtin_amdgcn_readlane(incl, 63);
   }
   return false;
+}
+
+// With tiles of BM rows.
+template <int BM, int GROUP_M>
+__device__ __forceinline__ bool find_tile(const GroupArgs& gr, int pid, int tiles_n, int lane, Spot& s) {
+  int used;
+  return find_tile_of<GROUP_M>(gr, pid, tiles_n, lane, [](int rows) { return (int)(((int64_t)rows + BM - 1) / BM); }, s, used);
 }
 
 // Row tiles that `rows` rows in n groups can need at most.

@@ -35,20 +35,45 @@ __device__ __forceinline__ void* row_ptr(const GemmArgs& a, int64_t elements) {
   return (uint8_t*)a.D + elements * (a.d_fmt == BSM_F32 ? 4 : 2);
 }
 
+// The product of one group of rows out of the call's: operands and output moved to it.
+__device__ __forceinline__ GemmArgs group_product(const GemmArgs& a, const GroupArgs& gr, int g, int row0, int rows) {
+  GemmArgs t = a;
+  t.M = rows;
+  t.A = (const uint16_t*)a.A + (int64_t)row0 * a.lda;
+  t.B = (const uint16_t*)a.B + (int64_t)g * gr.stride_b;
+  t.D = (float*)row_ptr(a, (int64_t)row0 * a.ldd);
+  return t;
+}
+
+// Tiles of 256 x 256 for a group's whole 256 rows (kFull and more of the last ones count as whole), then, for the
+// rows behind them, tiles of 128 (64, 32) x 128 in the same launch: they fill the last round.
+constexpr int kFull = 193;
+__device__ __forceinline__ int large_tiles(int rows) { return rows / 256 + (rows % 256 >= kFull ? 1 : 0); }
+__device__ __forceinline__ int rest_tiles(int rows) { const int r = rows % 256; return r >= kFull ? 0 : (r + 127) / 128; }
+
 template <int DT, bool BKM>
-__global__ __launch_bounds__(256, 1) void k_grouped(GemmArgs a, GroupArgs gr, int tiles_n) {
+__global__ __launch_bounds__(256, 1) void k_grouped(GemmArgs a, GroupArgs gr, int large_n, int rest_n) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * STAGE_BYTES];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   grouped::Spot s;
-  if (!grouped::find_tile<BM, 4>(gr, blockIdx.x, tiles_n, lane, s)) return;
-  GemmArgs t = a;
-  t.M = s.rows;
-  t.A = (const uint16_t*)a.A + (int64_t)s.row0 * a.lda;
-  t.B = (const uint16_t*)a.B + (int64_t)s.g * gr.stride_b;
-  f32x4 acc[8][8];
-  tile_product<DT, true, BKM>(t, s.tm, s.tn, lds, lane, w, acc);
-  store_out<DT>(a, row_ptr(a, (int64_t)s.row0 * a.ldd), s.rows, (int64_t)s.tm * BM + 128 * (w >> 1),
-                (int64_t)s.tn * BN + 128 * (w & 1), lane, acc, lds + 32768 * w);
+  int used;
+  if (grouped::find_tile_of<4>(gr, blockIdx.x, large_n, lane, large_tiles, s, used)) {
+    const GemmArgs t = group_product(a, gr, s.g, s.row0, s.rows);
+    f32x4 acc[8][8];
+    tile_product<DT, true, BKM>(t, s.tm, s.tn, lds, lane, w, acc);
+    store_out<DT>(t, t.D, s.rows, (int64_t)s.tm * BM + 128 * (w >> 1), (int64_t)s.tn * BN + 128 * (w & 1), lane, acc,
+                  lds + 32768 * w);
+    return;
+  }
+  const int pid = (int)blockIdx.x - used;
+  if (pid < 0 || !grouped::find_tile_of<8>(gr, pid, rest_n, lane, rest_tiles, s, used)) return;
+  const GemmArgs t = group_product(a, gr, s.g, s.row0, s.rows);
+  const int64_t m0 = (int64_t)(s.rows / 256) * 256 + 128 * s.tm, n0 = mid::BN * (int64_t)s.tn;
+  const int left = s.rows - (int)m0;
+  constexpr int LDS = 2 * STAGE_BYTES;
+  if (left <= 32) mid::tile<DT, 32, true, BKM, 64, mid::NoMore, LDS>(t, m0, n0, lds, lane, w);
+  else if (left <= 64) mid::tile<DT, 64, true, BKM, 64, mid::NoMore, LDS>(t, m0, n0, lds, lane, w);
+  else mid::tile<DT, 128, true, BKM, 64, mid::NoMore, LDS>(t, m0, n0, lds, lane, w);
 }
 
 // Workgroup p runs on XCD p % 8. Every XCD gets a contiguous eighth of each group's tiles (groups in
@@ -88,16 +113,6 @@ __global__ __launch_bounds__(256, PER_CU) void k_grouped_wgrad(GemmArgs a, Group
   if (!wgrad_tile(blockIdx.x, gr.n, tiles_m, tiles_n, s)) return;
   mid::tile<DT, BM, false, false, BK, mid::NoMore, LDS>(wgrad_product(a, gr, s.g), BM * (int64_t)s.tm,
                                                         mid::BN * (int64_t)s.tn, lds, lane, w);
-}
-
-// The product of one group of rows out of the call's: operands and output moved to it.
-__device__ __forceinline__ GemmArgs group_product(const GemmArgs& a, const GroupArgs& gr, int g, int row0, int rows) {
-  GemmArgs t = a;
-  t.M = rows;
-  t.A = (const uint16_t*)a.A + (int64_t)row0 * a.lda;
-  t.B = (const uint16_t*)a.B + (int64_t)g * gr.stride_b;
-  t.D = (float*)row_ptr(a, (int64_t)row0 * a.ldd);
-  return t;
 }
 
 // Tiles of 128 rows, a group's last one of as few as hold its rows. Bands of eight tile rows: an XCD's 64
@@ -150,15 +165,16 @@ __global__ __launch_bounds__(skinny::THREADS, MT == 1 ? 4 : 2) void k_grouped_sk
 
 template <int DT>
 hipError_t launch_grouped_dt(const GemmArgs& a, const GroupArgs& gr, hipStream_t st) {
-  // 256 x 256 or 128 x 128 tiles: what each would take, in rounds over the 256 CUs (512 slots) and at the
-  // rates that each reaches on even groups (1.15 and 0.97 PFLOP/s), with half a tile lost per group
-  // and, on the small tiles, half a round at the end. 16381 rows over 16 groups, N 4096, K 8192: 1155
-  // and 1180 us; 8190 rows over 8 groups, N 2048 (288 large tiles, the second round nearly empty): 400
-  // and 357 us.
+  // 256 x 256 tiles (and small ones for the rest of a group) where groups are long and the large tiles,
+  // 0.45 a group fewer than the rows would fill, leave little of their last round over the 256 CUs empty.
+  // Even groups, small tiles alone against both: 16381 rows over 16 groups (N 4096, K 8192) 1124 and 987 us, 8190 over
+  // 8 (N 2048, K 8192) 290 and 227 us; groups of a router's split 1158 and 1163, 360 and 307 us. Short groups
+  // (16384 rows over 64, N 4096, K 2048, uneven) 392 and 454 us; one and a half rounds (6000 rows, N = K =
+  // 4096) 185 and 215 us; half a round (8190 over 8, N 1024, K 4096) 66 and 103 us.
   auto row_tiles = [&](double bm) { return gr.n == 1 ? (double)((gr.rows + (int64_t)bm - 1) / (int64_t)bm) : gr.rows / bm + 0.5 * gr.n; };
-  const double large = (double)(((int64_t)(row_tiles(BM) * ((a.N + BN - 1) / BN)) + 255) / 256) * 256 * BM * BN / 1.15;
-  const double small = (row_tiles(128) * ((a.N + mid::BN - 1) / mid::BN) + 256) * 128 * mid::BN / 0.97;
-  const bool big = gr.rows / gr.n >= 192 && large < small;
+  const double whole = gr.n == 1 ? (double)(gr.rows / BM) : gr.rows / (double)BM - 0.45 * gr.n;
+  const double rounds = whole * ((a.N + BN - 1) / BN) / 256, last = rounds - (int64_t)rounds;
+  const bool big = gr.rows / gr.n >= 768 && rounds >= 0.85 * ((int64_t)rounds + (last > 0.05));
   // Sixteen columns a workgroup where 128-column tiles would leave half the CUs without one: 16 rows of
   // one group, N = K = 4096 (32 such tiles) 21.8 -> 11.0 us, 64 rows 29.9 -> 15.2 us, 8 rows over 8 groups,
   // N 1024, K 2048 (64) 12.4 -> 9.3 us; even at 128 of them (32 rows over 8 groups, N = K = 2048: 18.0
@@ -184,8 +200,14 @@ hipError_t launch_grouped_dt(const GemmArgs& a, const GroupArgs& gr, hipStream_t
   } else if (!big) {
     if (a.b_kmajor) hipLaunchKernelGGL((k_grouped_mid<DT, true>), grid, dim3(256), 0, st, a, gr, (int)tn);
     else hipLaunchKernelGGL((k_grouped_mid<DT, false>), grid, dim3(256), 0, st, a, gr, (int)tn);
-  } else if (a.b_kmajor) hipLaunchKernelGGL((k_grouped<DT, true>), grid, dim3(256), 0, st, a, gr, (int)tn);
-  else hipLaunchKernelGGL((k_grouped<DT, false>), grid, dim3(256), 0, st, a, gr, (int)tn);
+  } else {
+    const int64_t rest = 2 * used * ((a.N + mid::BN - 1) / mid::BN);
+    if (n + rest > 0x7FFFFFF0) return hipErrorInvalidValue;
+    const dim3 both((uint32_t)(n + (rest + 7) / 8 * 8));
+    const int rest_n = (int)((a.N + mid::BN - 1) / mid::BN);
+    if (a.b_kmajor) hipLaunchKernelGGL((k_grouped<DT, true>), both, dim3(256), 0, st, a, gr, (int)tn, rest_n);
+    else hipLaunchKernelGGL((k_grouped<DT, false>), both, dim3(256), 0, st, a, gr, (int)tn, rest_n);
+  }
   return hipGetLastError();
 }
 

@@ -227,6 +227,7 @@ def test_large_tiles():
     """Groups that the 256 x 256 tile takes (and their ragged ends), both orders of the weight, and long groups of a
     weight gradient."""
     for major in "kn":
-        run([1300, 770, 3, 2047], 3484, 72, "bf16", major, seed=6)
+        run([1300, 770, 3, 2047], 4100, 72, "bf16", major, seed=6)
+        run([1300, 770, 3 * 256 + 193, 0, 2047 + 192], 3400, 200, "bf16", major, "f32", 1, seed=5, first=1, behind=3, extra=8)
     wgrad([700, 0, 1030], 520, 4200, "bf16", "f32", 1, seed=7)
     wgrad([700, 0, 1030], 4200, 520, "f16", "f16", 0, seed=8)

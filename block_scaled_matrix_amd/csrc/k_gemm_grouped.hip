@@ -104,15 +104,17 @@ __device__ __forceinline__ GemmArgs wgrad_product(const GemmArgs& a, const Group
   return t;
 }
 
-template <int DT, int BM, int BK, int PER_CU>
-__global__ __launch_bounds__(256, PER_CU) void k_grouped_wgrad(GemmArgs a, GroupArgs gr, int tiles_m, int tiles_n) {
-  constexpr int LDS = 160 * 1024 / PER_CU;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[LDS];
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+// PER_CU workgroups of Q times four waves share a CU; Q > 1: the waves' fours share a tile's rows.
+template <int DT, int BM, int BK, int PER_CU, int Q = 1>
+__global__ __launch_bounds__(256 * Q, PER_CU * Q) void k_grouped_wgrad(GemmArgs a, GroupArgs gr, int tiles_m, int tiles_n) {
+  constexpr int LDS = 160 * 1024 / PER_CU / Q;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Q * LDS];
+  const int lane = threadIdx.x & 63, wq = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wq & 3, q = wq >> 2;
   WgradSpot s;
   if (!wgrad_tile(blockIdx.x, gr.n, tiles_m, tiles_n, s)) return;
-  mid::tile<DT, BM, false, false, BK, mid::NoMore, LDS>(wgrad_product(a, gr, s.g), BM * (int64_t)s.tm,
-                                                        mid::BN * (int64_t)s.tn, lds, lane, w);
+  mid::tile<DT, BM, false, false, BK, mid::NoMore, LDS, Q>(wgrad_product(a, gr, s.g), BM * (int64_t)s.tm,
+                                                           mid::BN * (int64_t)s.tn, lds + q * LDS, lane, w,
+                                                           mid::NoMore(), q);
 }
 
 // Tiles of 128 rows, a group's last one of as few as hold its rows. Bands of eight tile rows: an XCD's 64
@@ -224,12 +226,16 @@ static hipError_t launch_wgrad_dt(const GemmArgs& a, const GroupArgs& gr, hipStr
   // N 520) 15.0 us against 18.5 us on two. Tiles of 256 rows where groups have rows enough for a long loop and the tiles fill the CUs: 16381
   // rows over 8 groups (M 4096, N 2048) 306 us against 343 us on 128; 1021 over 32 (M 1000, N 520) 21.1
   // against 19.8 us. (The dense GEMM's 256 x 256 tile: 350 and 40 us.)
+  // Few tiles of long groups: eight waves a tile, each four every other 64 rows (16000 rows over 2 groups, M =
+  // N = 1024 80 -> 68 us; 4000 in one, 43 -> 38 us; at 250 rows a group it is behind).
   const int64_t tn = (a.N + mid::BN - 1) / mid::BN;
   const bool tall = gr.rows / gr.n >= 192 && (a.M + 255) / 256 * tn * gr.n >= 512;
   const int64_t tm = tall ? (a.M + 255) / 256 : (a.M + 127) / 128, share = (tm * tn + 7) / 8;
   if (share > 0x7FFFFFFF / 8 / gr.n) return hipErrorInvalidValue;
   const dim3 grid((uint32_t)(share * 8 * gr.n));
   if (tall) hipLaunchKernelGGL((k_grouped_wgrad<DT, 256, 32, 2>), grid, dim3(256), 0, st, a, gr, (int)tm, (int)tn);
+  else if (gr.rows / gr.n >= 1000 && tm * tn * gr.n < 192)
+    hipLaunchKernelGGL((k_grouped_wgrad<DT, 128, 64, 1, 2>), grid, dim3(512), 0, st, a, gr, (int)tm, (int)tn);
   else if (gr.rows / gr.n < 64) hipLaunchKernelGGL((k_grouped_wgrad<DT, 128, 32, 4>), grid, dim3(256), 0, st, a, gr, (int)tm, (int)tn);
   else hipLaunchKernelGGL((k_grouped_wgrad<DT, 128, 64, 2>), grid, dim3(256), 0, st, a, gr, (int)tm, (int)tn);
   return hipGetLastError();

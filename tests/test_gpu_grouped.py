@@ -223,6 +223,13 @@ def test_fewer_tiles_than_compute_units(K, major):
     run([100, 200], 260, K, "f16", major, "f32", 1, bsm.ewise_desc("silu_affine", 1.0, 0.5), seed=K)
 
 
+@pytest.mark.parametrize("sizes", [[1024], [1100], [1500, 0, 1663], [64, 1985]])
+def test_wgrad_of_few_tiles(sizes):
+    """Two sets of waves share a group's rows: an odd and an even number of K tiles, a partial one."""
+    wgrad(sizes, 200, 140, "bf16", "f32", 1, seed=3, first=1, behind=2)
+    wgrad(sizes, 200, 140, "f16", "f16", 0, seed=4, extra=8, pad=8)
+
+
 def test_large_tiles():
     """Groups that the 256 x 256 tile takes (and their ragged ends), both orders of the weight, and long groups of a
     weight gradient."""

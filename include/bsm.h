@@ -388,8 +388,9 @@ int bsm_gemm_grouped_block_scale(int64_t rows, int64_t N, int64_t K, int32_t n_g
  *   D[t,n] = f(x),  x = (accum ? D[t,n] : 0) + sum_k X(t,k) * W(n,k)
  *                       + sum_r U(t,r) * LB_a(n,r),   U(t,r) = scale[a] * sum_k X(t,k) * LA_a(r,k),
  * a = adapter[t]; a row whose adapter lies outside 0 .. n_adapters - 1 (say -1) has none. Products
- * and sums in float32, U kept in float32 (both call and caller may rely on it: the adapter's part
- * is not rounded to the operands' format), D rounded once.
+ * and sums in float32, U kept in float32 (the adapter's part is not rounded to the operands'
+ * format on its way), D rounded once. An adapter's weights reach the rows that chose it and no
+ * others, infinities and NaN included.
  *   rows, N, K, R: R is the adapters' rank, 0 .. 256 (0: the projection alone; adapters of a smaller
  *              rank are padded with zero rows of LA or zero columns of LB);
  *   adapter:   DEVICE array of `rows` int32, 4-byte aligned, any order and repetition;

@@ -121,3 +121,10 @@ def test_tile_shapes(T, N, K):
     ids = [(t // 37) % 4 - 1 for t in range(T)]
     run(ids, N, K, 24, 3, "bf16", seed=T)
     run(ids, N, K, 72, 3, "f16", "f32", seed=K)
+
+
+@pytest.mark.parametrize("T,L,R", [(1100, 3, 24), (1100, 40, 24), (1300, 40, 130), (90, 3, 256)])
+def test_shrink_by_rows_and_by_tiles(T, L, R):
+    """Both forms of the shrink: few adapters and many, blocks of rows of one adapter and of many."""
+    run(mixed(T, L, 2), 72, 200, R, L, "bf16", seed=R)
+    run([(t // 50) % L for t in range(T)], 72, 200, R, L, "f16", "f32", seed=T)

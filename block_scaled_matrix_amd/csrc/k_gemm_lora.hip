@@ -1,6 +1,6 @@
 // k_gemm_lora.hip - a shared projection with a low-rank adapter chosen per row (lora.hpp has the
 // formula). Two launches: the shrink writes U, the projection adds U LB^T to its accumulators before
-// its only store, so D is written once and never read back. Up to 64 rows (a decode batch) both work
+// its only store, so D is written once and never read back. For decode batches both adapters' parts work
 // row by row on the vector units, beside the weights' stream; beyond, on the matrix units.
 #include "gemm_mid_tile.hpp"
 #include "grouped.hpp"
@@ -239,6 +239,11 @@ hipError_t launch(const GemmArgs& a, const LoraArgs& lo, hipStream_t st) {
   if (a.M <= 32) return launch_skinny<DT, 2>(a, lo, Rp, st);
   if (a.M <= 48) return launch_skinny<DT, 3>(a, lo, Rp, st);
   if (a.M <= 64) return launch_skinny<DT, 4>(a, lo, Rp, st);
+  // Beyond 64 rows still in one round of workgroups: 100 rows, N 2048, K 4096 (256) 31.1 -> 20.5 us on tiles and
+  // here; at 512 (128 rows, N 4096) 31.5 and 34.9 us. With many adapters, which a tile's expand takes one after
+  // another, further: 100 rows of 64 adapters 61.2 -> 20.2 us, 200 (512) 61.1 -> 33.2 us.
+  const int64_t wgs = (a.M + 63) / 64 * ((a.N + skinny::BN - 1) / skinny::BN);
+  if (wgs <= 256 || (lo.n >= 32 && wgs <= 768)) return launch_skinny<DT, 4>(a, lo, Rp, st);
   // (fewer 128-row tiles than CUs: bsm_gemm_grouped's rule and figures)
   const int64_t tn = (a.N + mid::BN - 1) / mid::BN;
   const bool split = (a.M + 127) / 128 * tn < 192;

@@ -114,7 +114,7 @@ def test_same_bits_every_time():
         assert torch.equal(run(mixed(100, 6), 264, 520, 24, 6, seed=8), a)
 
 
-@pytest.mark.parametrize("T,N", [(70, 300), (200, 520), (3300, 1100)])
+@pytest.mark.parametrize("T,N", [(70, 4200), (200, 1500), (3300, 1100), (260, 520)])
 @pytest.mark.parametrize("K", [64, 100, 264])
 def test_tile_shapes(T, N, K):
     """Few tiles (two sets of waves a tile) and many, requests of several rows each, ranks of one step and more."""
@@ -126,5 +126,6 @@ def test_tile_shapes(T, N, K):
 @pytest.mark.parametrize("T,L,R", [(1100, 3, 24), (1100, 40, 24), (1300, 40, 130), (90, 3, 256)])
 def test_shrink_by_rows_and_by_tiles(T, L, R):
     """Both forms of the shrink: few adapters and many, blocks of rows of one adapter and of many."""
-    run(mixed(T, L, 2), 72, 200, R, L, "bf16", seed=R)
-    run([(t // 50) % L for t in range(T)], 72, 200, R, L, "f16", "f32", seed=T)
+    for N in (72, 1400):                    # (1400: too many workgroups of 16 columns)
+        run(mixed(T, L, 2), N, 200, R, L, "bf16", seed=R)
+        run([(t // 50) % L for t in range(T)], N, 200, R, L, "f16", "f32", seed=T)

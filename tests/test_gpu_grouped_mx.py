@@ -147,3 +147,11 @@ def test_fewer_tiles_than_compute_units(K, a, b, fast):
 def test_large_tiles(a, b, fast):
     """Groups that the 256 x 256 kernels take, and their ragged ends."""
     run([700, 300, 3, 520], 4100, 160, a, b, fast, "bf16", seed=6)
+
+
+def test_many_groups_of_few_rows():
+    """Exact E4M3 x E2M1 of up to 16 rows a group on average, single groups far above it, and tiles in plenty."""
+    sizes = [(7 * i) % 9 for i in range(40)] + [70, 0, 33]
+    for K in (96, 160, 1056):
+        run(sizes, 1300, K, "e4m3", "e2m1", 0, "bf16", 1, None, K, first=1, behind=2, extra=16)
+        run(sizes, 1300, K, "e4m3", "e2m1", 0, "f32", 0, bsm.ewise_desc("silu_affine", 0.5, 0.25), K)

@@ -129,3 +129,63 @@ def test_shrink_by_rows_and_by_tiles(T, L, R):
     for N in (72, 1400):                    # (1400: too many workgroups of 16 columns)
         run(mixed(T, L, 2), N, 200, R, L, "bf16", seed=R)
         run([(t // 50) % L for t in range(T)], N, 200, R, L, "f16", "f32", seed=T)
+
+
+def nonfinite_case(ids, N, ab, kind, bits, seed):
+    """Operands with infinities and NaN in LB (`kind` "weight") or adapters of an infinite scale ("u", "both"), the values
+    of U of few bits (small integers: its lower terms are zero, and so are some of its values) or of many, and the
+    64-bit result by the definition, products one by one."""
+    g = torch.Generator().manual_seed(seed)
+    T, K, R, L = len(ids), 40, 12, 3
+    few = lambda *s: torch.randint(-2, 3, s, generator=g).to(DT[ab])
+    mk = few if bits == "few" else lambda *s: torch.randn(*s, generator=g).to(DT[ab])
+    x, la, lb = mk(T, K), mk(L, R, K), mk(L, N, R)
+    w = torch.randn(N, K, generator=g).to(DT[ab])
+    scale = torch.tensor([1.0, 0.5, 2.0])
+    if kind in ("weight", "both"):
+        for a, n, r, v in ((0, 3, 0, "inf"), (0, 17, 11, "-inf"), (1, 0, 5, "-inf"), (1, N - 1, 3, "inf"), (1, 20, 2, "nan"),
+                           (0, 30, 1, "inf"), (0, 30, 2, "-inf"), (2, 33, 7, "inf")):
+            lb[a, n, r] = float(v)
+    if kind in ("u", "both"):
+        scale[1], scale[2] = float("inf"), float("-inf")
+    if kind == "u":                                 # (sums of one sign: every output of adapters 1 and 2 infinite)
+        x, la, lb = (t.abs().where(t != 0, torch.ones_like(t)) for t in (x, la, lb))
+    u = scale[torch.tensor(ids).clamp_min(0), None].double() * torch.stack(
+        [(x[t].double() * la[max(a, 0)].double()).sum(-1) for t, a in enumerate(ids)])
+    ref, mag = torch.empty(T, N, dtype=torch.float64), torch.empty(T, N, dtype=torch.float64)
+    for t, a in enumerate(ids):
+        p = x[t].double() * w.double()
+        q = u[t] * lb[max(a, 0)].double() if a >= 0 else torch.zeros(N, R, dtype=torch.float64)
+        ref[t], mag[t] = p.sum(-1) + q.sum(-1), p.abs().sum(-1) + q.abs().sum(-1)
+    if kind == "weight":                            # (U's own error reaches the finite outputs)
+        um = torch.stack([(x[t].double() * la[max(a, 0)].double()).abs().sum(-1) * scale[max(a, 0)].double() for t, a in enumerate(ids)])
+        for t, a in enumerate(ids):
+            if a >= 0:
+                mag[t] = (x[t].double() * w.double()).abs().sum(-1) + (um[t] * lb[a].double().abs()).sum(-1)
+    return x, w, la, lb, scale, ref, mag, T, K, R, L
+
+
+@pytest.mark.parametrize("ab", ["bf16", "f16"])
+@pytest.mark.parametrize("kind", ["weight", "u", "both"])
+@pytest.mark.parametrize("bits", ["few", "many"])
+@pytest.mark.parametrize("T,N", [(16, 40), (64, 40), (200, 1500), (70, 4200), (3300, 1100)])
+def test_infinities_follow_the_definition(T, N, bits, kind, ab):
+    """An infinite weight or U gives what the formula gives, infinity or NaN, whichever kernel the sizes choose; the other
+    outputs stay finite and within the bound."""
+    ids = [(t // 37) % 4 - 1 if t % 5 else t % 3 for t in range(T)]
+    x, w, la, lb, scale, ref, mag, T, K, R, L = nonfinite_case(ids, N, ab, kind, bits, T + N)
+    xd, wd, lad, lbd = (padded(t).cuda() for t in (x, w, la, lb))
+    D = torch.empty(T, up(N, 4), device="cuda")
+    ws = torch.full((bsm.bsm_gemm_lora_workspace(T, R),), 0xFF, dtype=torch.uint8, device="cuda")
+    say("lora, not finite", T, N, bits, kind, ab)
+    bsm.bsm_gemm_lora(T, N, K, R, L, torch.tensor(ids, dtype=torch.int32, device="cuda"), ab, xd, xd.stride(0), wd, wd.stride(0),
+                      lad, lad.stride(1), lad.stride(0), lbd, lbd.stride(1), lbd.stride(0), scale.cuda(), ws, "f32", D, D.stride(0))
+    got = D.cpu()[:, :N].double()
+    assert torch.isinf(ref).any() and torch.isfinite(ref).any()
+    wrong = torch.isnan(got) != torch.isnan(ref)
+    assert not wrong.any(), ("NaN", int(wrong.sum()), wrong.nonzero()[:4].tolist())
+    wrong = torch.isinf(got) != torch.isinf(ref)
+    wrong |= torch.isinf(ref) & (got != ref)
+    assert not wrong.any(), ("infinity", int(wrong.sum()), wrong.nonzero()[:4].tolist())
+    fine = torch.isfinite(ref)
+    check(got[fine], ref[fine], mag[fine], K + R + 4, "f32", (T, N))

@@ -129,6 +129,8 @@ __device__ __forceinline__ f32x4 expand_step(const USplit& u, uint4 b, f32x4 d) 
 // and expand_step gets finite operands, the others zero. Every step is looked at: zero times a value is NaN where
 // it is not finite, summed in one instruction a value of U and one a pair of weights (8190 rows of rank 64, N 8192,
 // K 4096: 595 us without it, 600 with it; integer tests of the exponents take twice the instructions and cost 1.3%).
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ float zeros_of(const UPart& u, float z) {
 #pragma unroll
   for (int e = 0; e < 8; e++) z = __builtin_fmaf(u.v[e], 0.f, z);

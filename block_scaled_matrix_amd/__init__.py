@@ -26,7 +26,7 @@ EXPORTS = ("bsm_image_stride", "bsm_tile_box_load", "bsm_tile_box_store", "bsm_t
            "bsm_gemm_block_scale", "bsm_gemm_ewise", "bsm_gemm_block_scale_ewise", "bsm_gemm_block_scale_major",
            "bsm_gemm_block_scale_fastacc", "bsm_gemm_grouped", "bsm_gemm_grouped_wgrad",
            "bsm_gemm_grouped_block_scale", "bsm_gemm_lora", "bsm_gemm_lora_workspace",
-           "bsm_debug_stream_mix_bf16", "bsm_debug_mfma_loop", "bsm_tile_add_scalar_f32", "bsm_debug_fragments", "bsm_debug_fragment_shape", "bsm_last_error")
+           "bsm_debug_grouped_route", "bsm_debug_stream_mix_bf16", "bsm_debug_mfma_loop", "bsm_tile_add_scalar_f32", "bsm_debug_fragments", "bsm_debug_fragment_shape", "bsm_last_error")
 
 
 class BsmError(RuntimeError):
@@ -93,6 +93,8 @@ def lib():
                                     I64, C.c_int, C.POINTER(bsm_ewise), P]
         L.bsm_tile_add_scalar_f32.argtypes = [P, P, I64, C.c_float, P]
         L.bsm_debug_stream_mix_bf16.argtypes = [P, P, P, I64, P]
+        L.bsm_debug_grouped_route.restype = C.c_char_p
+        L.bsm_debug_grouped_route.argtypes = [C.c_char, I64, I64, I64, I64, I64, I32, I32, I32, C.c_char, C.c_int, C.c_int]
         L.bsm_debug_mfma_loop.argtypes = [I32, I64, I32, P, P]
         L.bsm_debug_fragments.argtypes = [P, I64, I64, C.c_char, P, P]
         L.bsm_debug_fragment_shape.restype = None
@@ -359,6 +361,15 @@ def bsm_debug_fragments(src, rows: int, kdim: int, major: str, dump, stream=None
 
 def bsm_debug_stream_mix_bf16(src, dst, add, n: int, stream=None):
     _check(lib().bsm_debug_stream_mix_bf16(_ptr(src), _ptr(dst), _ptr(add), n, _stream(stream)))
+
+
+def bsm_debug_grouped_route(call: str, rows, N, K=0, n=1, M=0, R=0, a_fmt: str = "bf16", b_fmt: str = "bf16", b_major: str = "k",
+                            fast=0, shrink=0) -> str:
+    name = lib().bsm_debug_grouped_route(call.encode(), rows, M, N, K, R, n, DTYPE[a_fmt], DTYPE[b_fmt], b_major.encode(), fast,
+                                         shrink)
+    if name is None:
+        raise BsmError(-13 if call not in "gwma" else -9, bsm_last_error())
+    return name.decode()
 
 
 def bsm_debug_mfma_loop(kind: str, workgroups: int, iters: int, out, stream=None):

@@ -783,6 +783,30 @@ int bsm_debug_stream_mix_bf16(const void* src, void* dst, void* add, int64_t n, 
   return ok();
 }
 
+const char* bsm_debug_grouped_route(char call, int64_t rows, int64_t M, int64_t N, int64_t K, int64_t R, int32_t n, int32_t a_fmt,
+                                    int32_t b_fmt, char b_major, int fast, int shrink) {
+  if (rows < 1 || rows > 0x7FFFFFFF || N < 1 || N > 0x7FFFFFFF || M < 0 || M > 0x7FFFFFFF || K < 0 || K > 0x7FFFFFFF || R < 0 ||
+      R > 256 || n < 1 || n > 65536 || (call == 'w' && M < 1)) {
+    fail(BSM_E_SHAPE, "bsm_debug_grouped_route: a size is out of range");
+    return nullptr;
+  }
+  bsm::GemmArgs g{};
+  g.M = call == 'a' ? rows : M; g.N = N; g.K = K; g.dtype = a_fmt; g.dtype_b = b_fmt; g.b_kmajor = b_major == 'k'; g.mx_window = fast;
+  bsm::GroupArgs gr{};
+  gr.n = n; gr.rows = (int32_t)rows;
+  bsm::LoraArgs lo{};
+  lo.n = n; lo.R = (int32_t)R;
+  ok();
+  switch (call) {
+    case 'g': return bsm::route_gemm_grouped(g, gr);
+    case 'w': return bsm::route_gemm_grouped_wgrad(g, gr);
+    case 'm': return bsm::route_gemm_grouped_mx(g, gr);
+    case 'a': return shrink ? bsm::route_gemm_lora_shrink(g, lo) : bsm::route_gemm_lora(g, lo);
+  }
+  fail(BSM_E_ARG, "bsm_debug_grouped_route: call '%c' is not 'g', 'w', 'm' or 'a'", call);
+  return nullptr;
+}
+
 int bsm_debug_mfma_loop(int32_t kind, int64_t workgroups, int32_t iters, float* out, void* stream) {
   if (kind != BSM_BF16 && kind != BSM_E4M3 && kind != BSM_E2M1)
     return fail(BSM_E_DTYPE, "kind %d: the MFMA loop takes BSM_BF16, BSM_E4M3 or BSM_E2M1", kind);

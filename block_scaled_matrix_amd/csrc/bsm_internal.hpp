@@ -120,6 +120,15 @@ struct LoraArgs {
 // a.A K-major (M, K), a.B K-major (N, K); M, N > 0.
 hipError_t launch_gemm_lora(const GemmArgs& a, const LoraArgs& lo, hipStream_t st);
 
+// The kernels that those calls launch for the sizes given (host only, by the launches' own rules): their names in the
+// sources, with the template's tile where there are several.
+const char* route_gemm_grouped(const GemmArgs& a, const GroupArgs& gr);
+const char* route_gemm_grouped_wgrad(const GemmArgs& a, const GroupArgs& gr);
+const char* route_gemm_grouped_mx(const GemmArgs& a, const GroupArgs& gr);
+const char* route_gemm_grouped_mx_mid(const GemmArgs& a, const GroupArgs& gr);
+const char* route_gemm_lora(const GemmArgs& a, const LoraArgs& lo);
+const char* route_gemm_lora_shrink(const GemmArgs& a, const LoraArgs& lo);
+
 // Diagnostics (k_diag.hip): the box copy's traffic mix on flat bf16 buffers of n elements
 // (n a multiple of 8, 16-byte aligned), and workgroups x 256 lanes of back-to-back MFMAs of
 // `kind` (BSM_BF16, BSM_E4M3, BSM_E2M1), iters x 16 per wave, one float per lane to out.

@@ -165,8 +165,19 @@ __global__ __launch_bounds__(skinny::THREADS, MT == 1 ? 4 : 2) void k_grouped_sk
   if (w < MT) skinny::store4<DT>(t, m0 + 16 * w + (lane & 15), n0 + 4 * (lane >> 4), acc[0]);
 }
 
-template <int DT>
-hipError_t launch_grouped_dt(const GemmArgs& a, const GroupArgs& gr, hipStream_t st) {
+// The kernels of a call, and the rules that choose among them.
+enum GroupedTile { SKINNY_16, SKINNY_32, SKINNY_64, SPLIT, MID, LARGE };
+constexpr const char* kGroupedNames[] = {"k_grouped_skinny<1>", "k_grouped_skinny<2>", "k_grouped_skinny<4>",
+                                         "k_grouped_split", "k_grouped_mid", "k_grouped"};
+
+GroupedTile grouped_tile(const GemmArgs& a, const GroupArgs& gr) {
+  // Sixteen columns a workgroup where 128-column tiles would leave half the CUs without one: 16 rows of
+  // one group, N = K = 4096 (32 such tiles) 21.8 -> 11.0 us, 64 rows 29.9 -> 15.2 us, 8 rows over 8 groups,
+  // N 1024, K 2048 (64) 12.4 -> 9.3 us; even at 128 of them (32 rows over 8 groups, N = K = 2048: 18.0
+  // and 18.2 us) and behind for more rows a group (500 rows, N = K = 2048: 21.8 and 27.1 us).
+  const int64_t used = gr.n < gr.rows ? gr.n : gr.rows, each = (gr.rows + used - 1) / used;
+  if (a.b_kmajor && each <= 64 && used * ((a.N + mid::BN - 1) / mid::BN) < 128)
+    return each <= 16 ? SKINNY_16 : each <= 32 ? SKINNY_32 : SKINNY_64;
   // 256 x 256 tiles (and small ones for the rest of a group) where groups are long and the large tiles,
   // 0.45 a group fewer than the rows would fill, leave little of their last round over the 256 CUs empty.
   // Even groups, small tiles alone against both: 16381 rows over 16 groups (N 4096, K 8192) 1124 and 987 us, 8190 over
@@ -176,41 +187,62 @@ hipError_t launch_grouped_dt(const GemmArgs& a, const GroupArgs& gr, hipStream_t
   auto row_tiles = [&](double bm) { return gr.n == 1 ? (double)((gr.rows + (int64_t)bm - 1) / (int64_t)bm) : gr.rows / bm + 0.5 * gr.n; };
   const double whole = gr.n == 1 ? (double)(gr.rows / BM) : gr.rows / (double)BM - 0.45 * gr.n;
   const double rounds = whole * ((a.N + BN - 1) / BN) / 256, last = rounds - (int64_t)rounds;
-  const bool big = gr.rows / gr.n >= 768 && rounds >= 0.85 * ((int64_t)rounds + (last > 0.05));
-  // Sixteen columns a workgroup where 128-column tiles would leave half the CUs without one: 16 rows of
-  // one group, N = K = 4096 (32 such tiles) 21.8 -> 11.0 us, 64 rows 29.9 -> 15.2 us, 8 rows over 8 groups,
-  // N 1024, K 2048 (64) 12.4 -> 9.3 us; even at 128 of them (32 rows over 8 groups, N = K = 2048: 18.0
-  // and 18.2 us) and behind for more rows a group (500 rows, N = K = 2048: 21.8 and 27.1 us).
-  const int64_t used = gr.n < gr.rows ? gr.n : gr.rows, each = (gr.rows + used - 1) / used;
-  const bool few = a.b_kmajor && each <= 64 && used * ((a.N + mid::BN - 1) / mid::BN) < 128;
-  const int mt = !few ? 0 : each <= 16 ? 1 : each <= 32 ? 2 : 4;
+  if (gr.rows / gr.n >= 768 && rounds >= 0.85 * ((int64_t)rounds + (last > 0.05))) return LARGE;
   // Fewer 128-row tiles than CUs: half as many rows and eight waves a tile (1000 rows over 4 groups,
   // N = K = 1024, 78 tiles: 13.8 -> 9.7 us; 582 rows, N 1665, K 7227, 70: 69 -> 41 us; 1000 over 4, N 2048, K
   // 1024, 157: 14.3 -> 10.7 us; at 258 and 314 tiles it is behind, 46.7 to 44.2 and 18.8 to 15.9 us).
-  const bool split = row_tiles(128) * ((a.N + mid::BN - 1) / mid::BN) < 192;
-  const int bm = few ? 16 * mt : (big ? BM : (split ? 64 : 128)), bn = few ? skinny::BN : (big ? BN : mid::BN);
+  return row_tiles(128) * ((a.N + mid::BN - 1) / mid::BN) < 192 ? SPLIT : MID;
+}
+
+template <int DT>
+hipError_t launch_grouped_dt(const GemmArgs& a, const GroupArgs& gr, hipStream_t st) {
+  const GroupedTile tile = grouped_tile(a, gr);
+  const int bm = tile == SKINNY_16 ? 16 : tile == SKINNY_32 ? 32 : tile <= SPLIT ? 64 : tile == MID ? 128 : BM;
+  const int bn = tile <= SKINNY_64 ? skinny::BN : tile == LARGE ? BN : mid::BN;
   const int64_t tn = (a.N + bn - 1) / bn, n = (grouped::most_row_tiles(gr.rows, gr.n, bm) * tn + 7) / 8 * 8;
   if (n > 0x7FFFFFFF) return hipErrorInvalidValue;
   const dim3 grid((uint32_t)n);
-  if (few) {
-    if (mt == 1) hipLaunchKernelGGL((k_grouped_skinny<DT, 1>), grid, dim3(skinny::THREADS), 0, st, a, gr, (int)tn);
-    else if (mt == 2) hipLaunchKernelGGL((k_grouped_skinny<DT, 2>), grid, dim3(skinny::THREADS), 0, st, a, gr, (int)tn);
-    else hipLaunchKernelGGL((k_grouped_skinny<DT, 4>), grid, dim3(skinny::THREADS), 0, st, a, gr, (int)tn);
-  } else if (split && !big) {
-    if (a.b_kmajor) hipLaunchKernelGGL((k_grouped_split<DT, true>), grid, dim3(512), 0, st, a, gr, (int)tn);
-    else hipLaunchKernelGGL((k_grouped_split<DT, false>), grid, dim3(512), 0, st, a, gr, (int)tn);
-  } else if (!big) {
-    if (a.b_kmajor) hipLaunchKernelGGL((k_grouped_mid<DT, true>), grid, dim3(256), 0, st, a, gr, (int)tn);
-    else hipLaunchKernelGGL((k_grouped_mid<DT, false>), grid, dim3(256), 0, st, a, gr, (int)tn);
-  } else {
-    const int64_t rest = 2 * used * ((a.N + mid::BN - 1) / mid::BN);
-    if (n + rest > 0x7FFFFFF0) return hipErrorInvalidValue;
-    const dim3 both((uint32_t)(n + (rest + 7) / 8 * 8));
-    const int rest_n = (int)((a.N + mid::BN - 1) / mid::BN);
-    if (a.b_kmajor) hipLaunchKernelGGL((k_grouped<DT, true>), both, dim3(256), 0, st, a, gr, (int)tn, rest_n);
-    else hipLaunchKernelGGL((k_grouped<DT, false>), both, dim3(256), 0, st, a, gr, (int)tn, rest_n);
+  switch (tile) {
+    case SKINNY_16: hipLaunchKernelGGL((k_grouped_skinny<DT, 1>), grid, dim3(skinny::THREADS), 0, st, a, gr, (int)tn); break;
+    case SKINNY_32: hipLaunchKernelGGL((k_grouped_skinny<DT, 2>), grid, dim3(skinny::THREADS), 0, st, a, gr, (int)tn); break;
+    case SKINNY_64: hipLaunchKernelGGL((k_grouped_skinny<DT, 4>), grid, dim3(skinny::THREADS), 0, st, a, gr, (int)tn); break;
+    case SPLIT:
+      if (a.b_kmajor) hipLaunchKernelGGL((k_grouped_split<DT, true>), grid, dim3(512), 0, st, a, gr, (int)tn);
+      else hipLaunchKernelGGL((k_grouped_split<DT, false>), grid, dim3(512), 0, st, a, gr, (int)tn);
+      break;
+    case MID:
+      if (a.b_kmajor) hipLaunchKernelGGL((k_grouped_mid<DT, true>), grid, dim3(256), 0, st, a, gr, (int)tn);
+      else hipLaunchKernelGGL((k_grouped_mid<DT, false>), grid, dim3(256), 0, st, a, gr, (int)tn);
+      break;
+    case LARGE: {
+      const int64_t rest_n = (a.N + mid::BN - 1) / mid::BN, rest = 2 * (gr.n < gr.rows ? gr.n : gr.rows) * rest_n;
+      if (n + rest > 0x7FFFFFF0) return hipErrorInvalidValue;
+      const dim3 both((uint32_t)(n + (rest + 7) / 8 * 8));
+      if (a.b_kmajor) hipLaunchKernelGGL((k_grouped<DT, true>), both, dim3(256), 0, st, a, gr, (int)tn, (int)rest_n);
+      else hipLaunchKernelGGL((k_grouped<DT, false>), both, dim3(256), 0, st, a, gr, (int)tn, (int)rest_n);
+      break;
+    }
   }
   return hipGetLastError();
+}
+
+enum WgradTile { TALL, WGRAD_SPLIT, FEW_ROWS, SQUARE };
+constexpr const char* kWgradNames[] = {"k_grouped_wgrad<256, 32, 2, 1>", "k_grouped_wgrad<128, 64, 1, 2>",
+                                       "k_grouped_wgrad<128, 32, 4, 1>", "k_grouped_wgrad<128, 64, 2, 1>"};
+
+WgradTile wgrad_tile_kind(const GemmArgs& a, const GroupArgs& gr) {
+  const int64_t tn = (a.N + mid::BN - 1) / mid::BN, each = gr.rows / gr.n;
+  // Tiles of 256 rows where groups have rows enough for a long loop and the tiles fill the CUs: 16381
+  // rows over 8 groups (M 4096, N 2048) 306 us against 343 us on 128; 1021 over 32 (M 1000, N 520) 21.1
+  // against 19.8 us. (The dense GEMM's 256 x 256 tile: 350 and 40 us.)
+  if (each >= 192 && (a.M + 255) / 256 * tn * gr.n >= 512) return TALL;
+  // Few tiles of long groups: eight waves a tile, each four every other 64 rows (16000 rows over 2 groups, M =
+  // N = 1024 80 -> 68 us; 4000 in one, 43 -> 38 us; at 250 rows a group it is behind).
+  if (each >= 1000 && (a.M + 127) / 128 * tn * gr.n < 192) return WGRAD_SPLIT;
+  // Few rows a group: the loop is a step or two and loads, sums and stores of different tiles overlap, so
+  // four workgroups share a CU (K tiles of 32, 40 KiB of LDS each): 1021 rows over 32 groups (M 1000,
+  // N 520) 15.0 us against 18.5 us on two.
+  return each < 64 ? FEW_ROWS : SQUARE;
 }
 
 }  // namespace
@@ -221,28 +253,25 @@ hipError_t launch_gemm_grouped(const GemmArgs& a, const GroupArgs& gr, hipStream
 
 template <int DT>
 static hipError_t launch_wgrad_dt(const GemmArgs& a, const GroupArgs& gr, hipStream_t st) {
-  // Few rows a group: the loop is a step or two and loads, sums and stores of different tiles overlap, so
-  // four workgroups share a CU (K tiles of 32, 40 KiB of LDS each): 1021 rows over 32 groups (M 1000,
-  // N 520) 15.0 us against 18.5 us on two. Tiles of 256 rows where groups have rows enough for a long loop and the tiles fill the CUs: 16381
-  // rows over 8 groups (M 4096, N 2048) 306 us against 343 us on 128; 1021 over 32 (M 1000, N 520) 21.1
-  // against 19.8 us. (The dense GEMM's 256 x 256 tile: 350 and 40 us.)
-  // Few tiles of long groups: eight waves a tile, each four every other 64 rows (16000 rows over 2 groups, M =
-  // N = 1024 80 -> 68 us; 4000 in one, 43 -> 38 us; at 250 rows a group it is behind).
-  const int64_t tn = (a.N + mid::BN - 1) / mid::BN;
-  const bool tall = gr.rows / gr.n >= 192 && (a.M + 255) / 256 * tn * gr.n >= 512;
-  const int64_t tm = tall ? (a.M + 255) / 256 : (a.M + 127) / 128, share = (tm * tn + 7) / 8;
+  const WgradTile tile = wgrad_tile_kind(a, gr);
+  const int64_t bm = tile == TALL ? 256 : 128, tn = (a.N + mid::BN - 1) / mid::BN, tm = (a.M + bm - 1) / bm;
+  const int64_t share = (tm * tn + 7) / 8;
   if (share > 0x7FFFFFFF / 8 / gr.n) return hipErrorInvalidValue;
   const dim3 grid((uint32_t)(share * 8 * gr.n));
-  if (tall) hipLaunchKernelGGL((k_grouped_wgrad<DT, 256, 32, 2>), grid, dim3(256), 0, st, a, gr, (int)tm, (int)tn);
-  else if (gr.rows / gr.n >= 1000 && tm * tn * gr.n < 192)
-    hipLaunchKernelGGL((k_grouped_wgrad<DT, 128, 64, 1, 2>), grid, dim3(512), 0, st, a, gr, (int)tm, (int)tn);
-  else if (gr.rows / gr.n < 64) hipLaunchKernelGGL((k_grouped_wgrad<DT, 128, 32, 4>), grid, dim3(256), 0, st, a, gr, (int)tm, (int)tn);
-  else hipLaunchKernelGGL((k_grouped_wgrad<DT, 128, 64, 2>), grid, dim3(256), 0, st, a, gr, (int)tm, (int)tn);
+  switch (tile) {
+    case TALL: hipLaunchKernelGGL((k_grouped_wgrad<DT, 256, 32, 2>), grid, dim3(256), 0, st, a, gr, (int)tm, (int)tn); break;
+    case WGRAD_SPLIT: hipLaunchKernelGGL((k_grouped_wgrad<DT, 128, 64, 1, 2>), grid, dim3(512), 0, st, a, gr, (int)tm, (int)tn); break;
+    case FEW_ROWS: hipLaunchKernelGGL((k_grouped_wgrad<DT, 128, 32, 4>), grid, dim3(256), 0, st, a, gr, (int)tm, (int)tn); break;
+    case SQUARE: hipLaunchKernelGGL((k_grouped_wgrad<DT, 128, 64, 2>), grid, dim3(256), 0, st, a, gr, (int)tm, (int)tn); break;
+  }
   return hipGetLastError();
 }
 
 hipError_t launch_gemm_grouped_wgrad(const GemmArgs& a, const GroupArgs& gr, hipStream_t st) {
   return a.dtype == BSM_BF16 ? launch_wgrad_dt<BSM_BF16>(a, gr, st) : launch_wgrad_dt<BSM_F16>(a, gr, st);
 }
+
+const char* route_gemm_grouped(const GemmArgs& a, const GroupArgs& gr) { return kGroupedNames[grouped_tile(a, gr)]; }
+const char* route_gemm_grouped_wgrad(const GemmArgs& a, const GroupArgs& gr) { return kWgradNames[wgrad_tile_kind(a, gr)]; }
 
 }  // namespace bsm

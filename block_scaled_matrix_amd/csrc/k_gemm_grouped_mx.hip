@@ -20,7 +20,8 @@ static hipError_t launch_tuned(const GemmArgs& a, const GroupArgs& gr, hipStream
   return hipGetLastError();
 }
 
-hipError_t launch_gemm_grouped_mx(const GemmArgs& a, const GroupArgs& gr, hipStream_t st) {
+// Whether a call takes the 256 x 256 tiles.
+static bool large_tiles(const GemmArgs& a, const GroupArgs& gr) {
   // 256 x 256 tiles (in rounds over the 256 CUs) or 128 x 128 ones (512 slots, 0.6 of the large tile's
   // rate on even groups), with half a tile lost per group and half a round at the end on the small
   // ones: at 512 and 2048 rows a group the large are faster (8190 rows over 16 groups, N 8192, K 4096 in
@@ -30,11 +31,22 @@ hipError_t launch_gemm_grouped_mx(const GemmArgs& a, const GroupArgs& gr, hipStr
   auto row_tiles = [&](double bm) { return gr.n == 1 ? (double)((gr.rows + (int64_t)bm - 1) / (int64_t)bm) : gr.rows / bm + 0.5 * gr.n; };
   const double large = (double)(((int64_t)(row_tiles(BM) * ((a.N + BN - 1) / BN)) + 255) / 256) * 256 * BM * BN;
   const double small = (row_tiles(128) * ((a.N + 127) / 128) + 256) * 128 * 128 / 0.6;
-  if (gr.rows / gr.n < 192 || small < large) return launch_gemm_grouped_mx_mid(a, gr, st);
+  return gr.rows / gr.n >= 192 && small >= large;
+}
+
+// Of those, whether it runs on the general kernel (exact products of 8-bit operands, mixed pairs) or the tuned one.
+static bool general_kernel(const GemmArgs& a) { return a.dtype != BSM_E2M1 && (a.dtype_b == BSM_E2M1 || !a.mx_window); }
+
+const char* route_gemm_grouped_mx(const GemmArgs& a, const GroupArgs& gr) {
+  if (!large_tiles(a, gr)) return route_gemm_grouped_mx_mid(a, gr);
+  return general_kernel(a) ? "k_gemm_mx_any" : "k_gemm_mx";
+}
+
+hipError_t launch_gemm_grouped_mx(const GemmArgs& a, const GroupArgs& gr, hipStream_t st) {
+  if (!large_tiles(a, gr)) return launch_gemm_grouped_mx_mid(a, gr, st);
+  if (general_kernel(a)) return launch_gemm_grouped_mx_any(a, gr, st);
   const bool f32 = a.d_fmt == BSM_F32;
-  if (a.dtype == BSM_E2M1 && a.dtype_b == BSM_E2M1)
-    return f32 ? launch_tuned<4, 4, 4, BSM_F32>(a, gr, st) : launch_tuned<4, 4, 4, BSM_BF16>(a, gr, st);
-  if (a.dtype_b == BSM_E2M1 || !a.mx_window) return launch_gemm_grouped_mx_any(a, gr, st);
+  if (a.dtype == BSM_E2M1) return f32 ? launch_tuned<4, 4, 4, BSM_F32>(a, gr, st) : launch_tuned<4, 4, 4, BSM_BF16>(a, gr, st);
   return f32 ? launch_tuned<0, 0, 0, BSM_F32>(a, gr, st) : launch_tuned<0, 0, 0, BSM_BF16>(a, gr, st);
 }
 

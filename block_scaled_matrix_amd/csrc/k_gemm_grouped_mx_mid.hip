@@ -48,26 +48,33 @@ static __global__ __launch_bounds__(512) void k_grouped_mx_split(GemmArgs a, Gro
   else midmx::tile<CA, CB, BF, 64, 2, LDS>(a, late, m0, n0, part, lane, w, q);
 }
 
-template <int CA, int CB, bool BF>
-static hipError_t launch_mid(const GemmArgs& a, const GroupArgs& gr, hipStream_t st) {
+enum MidTile { ROWS32, SPLIT, MID };
+static MidTile mid_tile(const GemmArgs& a, const GroupArgs& gr) {
   const int64_t tn = (a.N + midmx::BN - 1) / midmx::BN, used = gr.n < gr.rows ? gr.n : gr.rows;
   // (300 rows over 4 groups, N 1024, K 4096: E4M3 x E2M1 35.1 -> 22.1 us, E2M1 pairs 21.8 -> 15.5 us; 64 over 8,
   // N 2048, K 4096: 19.5 -> 17.8 us)
-  const bool split = (gr.rows / 128 + (used + 1) / 2) * tn < 192;
+  if ((gr.rows / 128 + (used + 1) / 2) * tn < 192) return SPLIT;
   // Exact E4M3 x E2M1 of up to 16 rows a group: its conversions leave room for a third workgroup (64 rows over 32
   // groups, N = K = 4096 62.1 -> 57.3 us, 512 rows 83.8 -> 78.6 us; E4M3 pairs 101 -> 104 us, the others the same).
-  if constexpr (BF && CB == 4) {
-    if (!split && gr.rows / gr.n <= 16) {
-      const int64_t m = (grouped::most_row_tiles(gr.rows, gr.n, 32) * tn + 7) / 8 * 8;
-      if (m > 0x7FFFFFFF) return hipErrorInvalidValue;
-      hipLaunchKernelGGL((k_grouped_mx_rows32<CA, CB, BF>), dim3((uint32_t)m), dim3(256), 0, st, a, gr, (int)tn);
-      return hipGetLastError();
-    }
-  }
-  const int64_t n = (grouped::most_row_tiles(gr.rows, gr.n, split ? 64 : 128) * tn + 7) / 8 * 8;
+  const bool exact_mixed = a.dtype == BSM_E4M3 && a.dtype_b == BSM_E2M1 && !a.mx_window;
+  return exact_mixed && gr.rows / gr.n <= 16 ? ROWS32 : MID;
+}
+
+const char* route_gemm_grouped_mx_mid(const GemmArgs& a, const GroupArgs& gr) {
+  constexpr const char* names[] = {"k_grouped_mx_rows32", "k_grouped_mx_split", "k_grouped_mx_mid"};
+  return names[mid_tile(a, gr)];
+}
+
+template <int CA, int CB, bool BF>
+static hipError_t launch_mid(const GemmArgs& a, const GroupArgs& gr, hipStream_t st) {
+  const MidTile tile = mid_tile(a, gr);
+  const int64_t tn = (a.N + midmx::BN - 1) / midmx::BN, bm = tile == ROWS32 ? 32 : tile == SPLIT ? 64 : 128;
+  const int64_t n = (grouped::most_row_tiles(gr.rows, gr.n, bm) * tn + 7) / 8 * 8;
   if (n > 0x7FFFFFFF) return hipErrorInvalidValue;
-  if (split) hipLaunchKernelGGL((k_grouped_mx_split<CA, CB, BF>), dim3((uint32_t)n), dim3(512), 0, st, a, gr, (int)tn);
-  else hipLaunchKernelGGL((k_grouped_mx_mid<CA, CB, BF>), dim3((uint32_t)n), dim3(256), 0, st, a, gr, (int)tn);
+  const dim3 grid((uint32_t)n);
+  if (tile == SPLIT) hipLaunchKernelGGL((k_grouped_mx_split<CA, CB, BF>), grid, dim3(512), 0, st, a, gr, (int)tn);
+  else if (tile == MID) hipLaunchKernelGGL((k_grouped_mx_mid<CA, CB, BF>), grid, dim3(256), 0, st, a, gr, (int)tn);
+  else if constexpr (BF && CB == 4) hipLaunchKernelGGL((k_grouped_mx_rows32<CA, CB, BF>), grid, dim3(256), 0, st, a, gr, (int)tn);
   return hipGetLastError();
 }
 

@@ -219,54 +219,60 @@ __global__ __launch_bounds__(skinny::THREADS, MT == 1 ? 4 : 2) void k_lora_skinn
   }
 }
 
-template <int DT, int MT>
-hipError_t launch_skinny(const GemmArgs& a, const LoraArgs& lo, int64_t Rp, hipStream_t st) {
-  const int64_t tn = (a.N + skinny::BN - 1) / skinny::BN, n = (a.M + 16 * MT - 1) / (16 * MT) * tn;
-  if (n > 0x7FFFFFFF) return hipErrorInvalidValue;
-  if (lo.n > 0) {
-    hipLaunchKernelGGL(k_lora_shrink_rows<DT>, dim3((uint32_t)a.M, (uint32_t)(Rp / 32)), dim3(1024), 0, st, a, lo, Rp);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  hipLaunchKernelGGL((k_lora_skinny<DT, MT>), dim3((uint32_t)n), dim3(skinny::THREADS), 0, st, a, lo, Rp, (int)tn);
-  return hipGetLastError();
-}
+// The projection's kernel, and the shrink's before it.
+enum Projection { SKINNY_16, SKINNY_32, SKINNY_48, SKINNY_64, SPLIT, TILES };
+enum Shrink { NO_SHRINK, ROWS, SHRINK_TILES };
 
-template <int DT>
-hipError_t launch(const GemmArgs& a, const LoraArgs& lo, hipStream_t st) {
-  const int64_t Rp = lora::padded_rank(lo.R);
-  if (a.M <= 16) return launch_skinny<DT, 1>(a, lo, Rp, st);
-  if (a.M <= 32) return launch_skinny<DT, 2>(a, lo, Rp, st);
-  if (a.M <= 48) return launch_skinny<DT, 3>(a, lo, Rp, st);
-  if (a.M <= 64) return launch_skinny<DT, 4>(a, lo, Rp, st);
+Projection projection_of(const GemmArgs& a, const LoraArgs& lo) {
+  if (a.M <= 64) return a.M <= 16 ? SKINNY_16 : a.M <= 32 ? SKINNY_32 : a.M <= 48 ? SKINNY_48 : SKINNY_64;
   // Beyond 64 rows still in one round of workgroups: 100 rows, N 2048, K 4096 (256) 31.1 -> 20.5 us on tiles and
   // here; at 512 (128 rows, N 4096) 31.5 and 34.9 us. With many adapters, which a tile's expand takes one after
   // another, further: 100 rows of 64 adapters 61.2 -> 20.2 us, 200 (512) 61.1 -> 33.2 us.
   const int64_t wgs = (a.M + 63) / 64 * ((a.N + skinny::BN - 1) / skinny::BN);
-  if (wgs <= 256 || (lo.n >= 32 && wgs <= 768)) return launch_skinny<DT, 4>(a, lo, Rp, st);
+  if (wgs <= 256 || (lo.n >= 32 && wgs <= 768)) return SKINNY_64;
   // (fewer 128-row tiles than CUs: bsm_gemm_grouped's rule and figures)
-  const int64_t tn = (a.N + mid::BN - 1) / mid::BN;
-  const bool split = (a.M + 127) / 128 * tn < 192;
-  const int64_t tm = split ? (a.M + 63) / 64 : (a.M + 127) / 128;
+  return (a.M + 127) / 128 * ((a.N + mid::BN - 1) / mid::BN) < 192 ? SPLIT : TILES;
+}
+
+Shrink shrink_of(const GemmArgs& a, const LoraArgs& lo) {
+  if (lo.R == 0 || lo.n == 0) return NO_SHRINK;
+  if (projection_of(a, lo) <= SKINNY_64) return ROWS;
+  // Row by row while that is little work (U values / 32), tiles beyond. Tiles against rows, N 2048, K 4096, 8
+  // adapters: 300 rows of rank 16 45.5 and 32.6 us, 1000 rows 47.0 and 39.9 us, 2000 rows 67.1 and 70.8 us; 1000
+  // rows of rank 64 49.8 and 68.7 us. A tile runs once per adapter among its 32 rows (100 rows of 64
+  // adapters: 204 and 61 us), so with many adapters rows go further.
+  const int64_t work = a.M * (lora::padded_rank(lo.R) / 32);
+  return work <= 1024 || (lo.n >= 32 && work <= 4096) ? ROWS : SHRINK_TILES;
+}
+
+template <int DT>
+hipError_t launch(const GemmArgs& a, const LoraArgs& lo, hipStream_t st) {
+  const Projection kind = projection_of(a, lo);
+  const Shrink shrink = shrink_of(a, lo);
+  const int64_t Rp = lora::padded_rank(lo.R);
+  const int64_t bm = kind <= SKINNY_64 ? 16 * (kind + 1) : kind == SPLIT ? 64 : 128;
+  const int64_t bn = kind <= SKINNY_64 ? skinny::BN : mid::BN;
+  const int64_t tm = (a.M + bm - 1) / bm, tn = (a.N + bn - 1) / bn;
   if (tm * tn > 0x7FFFFFF0) return hipErrorInvalidValue;
-  if (lo.R > 0 && lo.n > 0) {
-    // Row by row while that is little work (U values / 32), tiles beyond. Tiles against rows, N 2048, K 4096, 8
-    // adapters: 300 rows of rank 16 45.5 and 32.6 us, 1000 rows 47.0 and 39.9 us, 2000 rows 67.1 and 70.8 us; 1000
-    // rows of rank 64 49.8 and 68.7 us. A tile runs once per adapter among its 32 rows (100 rows of 64
-    // adapters: 204 and 61 us), so with many adapters rows go further.
-    const int64_t work = a.M * (Rp / 32);
-    if (work <= 1024 || (lo.n >= 32 && work <= 4096)) {
-      hipLaunchKernelGGL(k_lora_shrink_rows<DT>, dim3((uint32_t)a.M, (uint32_t)(Rp / 32)), dim3(1024), 0, st, a, lo, Rp);
-    } else {
-      const dim3 grid((uint32_t)((a.M + 31) / 32), (uint32_t)((lo.R + 127) / 128), (uint32_t)(lo.n < 4 ? lo.n : 4));
-      hipLaunchKernelGGL(k_lora_shrink<DT>, grid, dim3(256), 0, st, a, lo, Rp);
-    }
+  if (shrink == ROWS) {
+    hipLaunchKernelGGL(k_lora_shrink_rows<DT>, dim3((uint32_t)a.M, (uint32_t)(Rp / 32)), dim3(1024), 0, st, a, lo, Rp);
+  } else if (shrink == SHRINK_TILES) {
+    const dim3 grid((uint32_t)((a.M + 31) / 32), (uint32_t)((lo.R + 127) / 128), (uint32_t)(lo.n < 4 ? lo.n : 4));
+    hipLaunchKernelGGL(k_lora_shrink<DT>, grid, dim3(256), 0, st, a, lo, Rp);
+  }
+  if (shrink != NO_SHRINK) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const dim3 grid((uint32_t)((tm * tn + 7) / 8 * 8));
-  if (split) hipLaunchKernelGGL((k_lora<DT, 2>), grid, dim3(512), 0, st, a, lo, Rp, (int)tm, (int)tn);
-  else hipLaunchKernelGGL((k_lora<DT, 1>), grid, dim3(256), 0, st, a, lo, Rp, (int)tm, (int)tn);
+  const dim3 few((uint32_t)(tm * tn)), grid((uint32_t)((tm * tn + 7) / 8 * 8));
+  switch (kind) {
+    case SKINNY_16: hipLaunchKernelGGL((k_lora_skinny<DT, 1>), few, dim3(skinny::THREADS), 0, st, a, lo, Rp, (int)tn); break;
+    case SKINNY_32: hipLaunchKernelGGL((k_lora_skinny<DT, 2>), few, dim3(skinny::THREADS), 0, st, a, lo, Rp, (int)tn); break;
+    case SKINNY_48: hipLaunchKernelGGL((k_lora_skinny<DT, 3>), few, dim3(skinny::THREADS), 0, st, a, lo, Rp, (int)tn); break;
+    case SKINNY_64: hipLaunchKernelGGL((k_lora_skinny<DT, 4>), few, dim3(skinny::THREADS), 0, st, a, lo, Rp, (int)tn); break;
+    case SPLIT: hipLaunchKernelGGL((k_lora<DT, 2>), grid, dim3(512), 0, st, a, lo, Rp, (int)tm, (int)tn); break;
+    case TILES: hipLaunchKernelGGL((k_lora<DT, 1>), grid, dim3(256), 0, st, a, lo, Rp, (int)tm, (int)tn); break;
+  }
   return hipGetLastError();
 }
 
@@ -274,6 +280,15 @@ hipError_t launch(const GemmArgs& a, const LoraArgs& lo, hipStream_t st) {
 
 hipError_t launch_gemm_lora(const GemmArgs& a, const LoraArgs& lo, hipStream_t st) {
   return a.dtype == BSM_BF16 ? launch<BSM_BF16>(a, lo, st) : launch<BSM_F16>(a, lo, st);
+}
+
+const char* route_gemm_lora(const GemmArgs& a, const LoraArgs& lo) {
+  constexpr const char* names[] = {"k_lora_skinny<1>", "k_lora_skinny<2>", "k_lora_skinny<3>", "k_lora_skinny<4>", "k_lora<2>", "k_lora<1>"};
+  return names[projection_of(a, lo)];
+}
+const char* route_gemm_lora_shrink(const GemmArgs& a, const LoraArgs& lo) {
+  constexpr const char* names[] = {"", "k_lora_shrink_rows", "k_lora_shrink"};
+  return names[shrink_of(a, lo)];
 }
 
 }  // namespace bsm

@@ -453,6 +453,15 @@ int bsm_debug_stream_mix_bf16(const void* src, void* dst, void* add, int64_t n, 
  * 4-byte aligned. workgroups and iters in 1 .. 2^20. */
 int bsm_debug_mfma_loop(int32_t kind, int64_t workgroups, int32_t iters, float* out, void* stream);
 
+/* Diagnostic: the name of the kernel that a call on groups of rows launches for these sizes, by the launches' own
+ * rules (no HIP call is made), with the tile in brackets where a kernel has several: call 'g' bsm_gemm_grouped,
+ * 'w' bsm_gemm_grouped_wgrad (with M), 'm' bsm_gemm_grouped_block_scale, 'a' bsm_gemm_lora (n: adapters, R: rank;
+ * shrink 1: the kernel before the projection, "" where there is none). n: groups. a_fmt, b_fmt, b_major and fast as
+ * for the call ('m': the formats; else unused), arguments a call does not have 0. A static string, or NULL where an
+ * argument is out of range (rows, N, n >= 1). */
+const char* bsm_debug_grouped_route(char call, int64_t rows, int64_t M, int64_t N, int64_t K, int64_t R, int32_t n,
+                                    int32_t a_fmt, int32_t b_fmt, char b_major, int fast, int shrink);
+
 /* Message describing the last nonzero status returned on this thread. */
 const char* bsm_last_error(void);
 

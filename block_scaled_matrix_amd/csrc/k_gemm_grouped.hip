@@ -8,6 +8,7 @@
 // rows: they are clamped away on the load (grouped) or zeroed (wgrad, the partial last K tile) and
 // never stored. Two tiles: the dense GEMM's 256 x 256 (gemm_dense_tile.hpp) and 32 / 64 / 128 x 128
 // (gemm_mid_tile.hpp).
+#include <algorithm>
 #include "gemm_dense_tile.hpp"
 #include "gemm_mid_tile.hpp"
 #include "skinny.hpp"
@@ -183,11 +184,13 @@ GroupedTile grouped_tile(const GemmArgs& a, const GroupArgs& gr) {
   // Even groups, small tiles alone against both: 16381 rows over 16 groups (N 4096, K 8192) 1124 and 987 us, 8190 over
   // 8 (N 2048, K 8192) 290 and 227 us; groups of a router's split 1158 and 1163, 360 and 307 us. Short groups
   // (16384 rows over 64, N 4096, K 2048, uneven) 392 and 454 us; one and a half rounds (6000 rows, N = K =
-  // 4096) 185 and 215 us; half a round (8190 over 8, N 1024, K 4096) 66 and 103 us.
+  // 4096) 185 and 215 us; half a round (8190 over 8, N 1024, K 4096) 66 and 103 us; a twentieth (1000 rows, N = K =
+  // 1024) 9.3 and 35 us, (994 rows, N 537, K 7577) 47 and 189 us: one round at least has to be begun.
   auto row_tiles = [&](double bm) { return gr.n == 1 ? (double)((gr.rows + (int64_t)bm - 1) / (int64_t)bm) : gr.rows / bm + 0.5 * gr.n; };
   const double whole = gr.n == 1 ? (double)(gr.rows / BM) : gr.rows / (double)BM - 0.45 * gr.n;
   const double rounds = whole * ((a.N + BN - 1) / BN) / 256, last = rounds - (int64_t)rounds;
-  if (gr.rows / gr.n >= 768 && rounds >= 0.85 * ((int64_t)rounds + (last > 0.05))) return LARGE;
+  const double begun = (double)std::max<int64_t>((int64_t)rounds + (last > 0.05), 1);
+  if (gr.rows / gr.n >= 768 && rounds >= 0.85 * begun) return LARGE;
   // Fewer 128-row tiles than CUs: half as many rows and eight waves a tile (1000 rows over 4 groups,
   // N = K = 1024, 78 tiles: 13.8 -> 9.7 us; 582 rows, N 1665, K 7227, 70: 69 -> 41 us; 1000 over 4, N 2048, K
   // 1024, 157: 14.3 -> 10.7 us; at 258 and 314 tiles it is behind, 46.7 to 44.2 and 18.8 to 15.9 us).

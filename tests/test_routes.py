@@ -64,3 +64,16 @@ def test_refusals():
     with pytest.raises(bsm.BsmError) as e:
         bsm.bsm_debug_grouped_route("x", 10, 10)
     assert e.value.status == "BSM_E_ARG"
+
+
+def test_large_tiles_only_where_they_fill_the_chip():
+    """The grouped products' 256 x 256 tiles need the best part of a round over 256 CUs, however long the groups. (An even
+    group's last rows take a large tile from 193 of them on.)"""
+    fewest = 1 << 30
+    for n in (1, 2, 3, 8, 16):
+        for rows in (768, 994, 1000, 1024, 1500, 2000, 3000, 5000, 8190, 16381, 100000):
+            for N in (1, 16, 256, 257, 537, 1024, 1280, 2048, 4100, 8192):
+                for major in "kn":
+                    if bsm.bsm_debug_grouped_route("g", rows * n, N, 4096, n, b_major=major) == "k_grouped":
+                        fewest = min(fewest, n * (rows // 256 + (rows % 256 >= 193)) * -(-N // 256))
+    assert 0.85 * 256 <= fewest < 1 << 30

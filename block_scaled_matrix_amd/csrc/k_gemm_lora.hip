@@ -236,13 +236,16 @@ Projection projection_of(const GemmArgs& a, const LoraArgs& lo) {
 
 Shrink shrink_of(const GemmArgs& a, const LoraArgs& lo) {
   if (lo.R == 0 || lo.n == 0) return NO_SHRINK;
-  if (projection_of(a, lo) <= SKINNY_64) return ROWS;
-  // Row by row while that is little work (U values / 32), tiles beyond. Tiles against rows, N 2048, K 4096, 8
-  // adapters: 300 rows of rank 16 45.5 and 32.6 us, 1000 rows 47.0 and 39.9 us, 2000 rows 67.1 and 70.8 us; 1000
-  // rows of rank 64 49.8 and 68.7 us. A tile runs once per adapter among its 32 rows (100 rows of 64
-  // adapters: 204 and 61 us), so with many adapters rows go further.
+  // Row by row while that is little work (U values / 32), tiles beyond, whichever projection follows. A row reads its
+  // whole adapter, a tile its 32 rows' adapters one after another, so with many adapters rows go further. Rows
+  // against tiles, whole calls (N 256, K 8192, requests of many rows): 400 rows of rank 64 (800) 61 and 62 us, 1000 of
+  // rank 64 (2000) 92 and 67, of rank 128 (4000) 150 and 72; every row an adapter of its own choice, 8 adapters 1000
+  // of rank 64 102 and 104, of rank 128 176 and 107; 40 adapters 1000 of rank 64 135 and 273, of rank 128 251 and
+  // 280 (requests of many rows 157 and 71), 3000 of rank 128 (12000) 758 and 679 (420 and 133). Where they cross hardly
+  // moves with K (512 to 8192): over 3 K, 4 ranks, 70 to 3000 rows, 1 to 40 adapters and N 256 and 2048 this choice
+  // takes 2% longer than the better form of each (1.6 times at worst).
   const int64_t work = a.M * (lora::padded_rank(lo.R) / 32);
-  return work <= 1024 || (lo.n >= 32 && work <= 4096) ? ROWS : SHRINK_TILES;
+  return work <= (lo.n >= 32 ? 3000 : 1024) ? ROWS : SHRINK_TILES;
 }
 
 template <int DT>

@@ -42,9 +42,10 @@ LORA = {
     ("k_lora_skinny<2>", "k_lora_shrink_rows"): [(31, 136, 200, 40, 7)],
     ("k_lora_skinny<3>", "k_lora_shrink_rows"): [(47, 136, 200, 16, 7)],
     ("k_lora_skinny<4>", "k_lora_shrink_rows"): [(63, 136, 200, 16, 7), (200, 136, 520, 12, 5)],
+    ("k_lora_skinny<4>", "k_lora_shrink"): [(1000, 250, 520, 130, 8)],
     ("k_lora<2>", "k_lora_shrink_rows"): [(200, 1500, 264, 24, 3)],
     ("k_lora<2>", "k_lora_shrink"): [(1100, 1100, 264, 72, 3)],
-    ("k_lora<1>", "k_lora_shrink_rows"): [(3300, 1100, 200, 24, 40)],
+    ("k_lora<1>", "k_lora_shrink_rows"): [(2900, 1100, 200, 24, 40)],
     ("k_lora<1>", "k_lora_shrink"): [(3300, 1100, 200, 130, 3)],
     ("k_lora<1>", ""): [(3300, 1100, 200, 0, 3)],
 }

@@ -77,3 +77,15 @@ def test_large_tiles_only_where_they_fill_the_chip():
                     if bsm.bsm_debug_grouped_route("g", rows * n, N, 4096, n, b_major=major) == "k_grouped":
                         fewest = min(fewest, n * (rows // 256 + (rows % 256 >= 193)) * -(-N // 256))
     assert 0.85 * 256 <= fewest < 1 << 30
+
+
+def test_the_shrink_goes_by_its_own_work():
+    """Which kernel forms U depends on rows, rank and adapters, not on the width of the projection behind it."""
+    seen = set()
+    for rows in (1, 16, 65, 100, 300, 1000, 1024, 2000, 5000, 16384):
+        for rank in (1, 16, 32, 64, 128, 256):
+            for n in (1, 8, 31, 32, 64, 1000):
+                kinds = {bsm.bsm_debug_grouped_route("a", rows, N, 4096, n, R=rank, shrink=1) for N in (1, 16, 256, 1024, 4096, 16384)}
+                assert len(kinds) == 1, (rows, rank, n, kinds)
+                seen |= kinds
+    assert seen == {"k_lora_shrink", "k_lora_shrink_rows"}

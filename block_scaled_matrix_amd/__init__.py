@@ -290,19 +290,19 @@ def _here(stream, *tensors):
     return _stream(stream)
 
 
-_int32 = None
+_dtypes = {}
 
 
-def _ints(t, what):
-    """Address of a DEVICE array of int32, checked where it is a torch tensor."""
+def _array(t, dtype: str, what):
+    """Address of a DEVICE array that is read element by element, its type and order checked where it is a torch tensor."""
     if t is None or type(t) is int:
         return t
-    global _int32
-    if _int32 is None:
+    want = _dtypes.get(dtype)
+    if want is None:
         import torch
-        _int32 = torch.int32
-    if t.dtype is not _int32:
-        raise BsmError(-8, f"{what} must be int32, not {t.dtype}")
+        want = _dtypes[dtype] = getattr(torch, dtype)
+    if t.dtype is not want:
+        raise BsmError(-8, f"{what} must be {dtype}, not {t.dtype}")
     if not t.is_contiguous():
         raise BsmError(-5, f"{what} must be contiguous")
     return t.data_ptr()
@@ -311,7 +311,7 @@ def _ints(t, what):
 def bsm_gemm_grouped(rows, N, K, n_groups, offsets, ab: str, A, lda, B, ldb, b_major: str, stride_b, d_fmt: str, D, ldd,
                      accum=0, ew: bsm_ewise | None = None, stream=None):
     s = _here(stream, offsets, A, B, D)
-    _check(lib().bsm_gemm_grouped(rows, N, K, n_groups, _ints(offsets, "offsets"), DTYPE[ab], _ptr(A), lda, _ptr(B), ldb,
+    _check(lib().bsm_gemm_grouped(rows, N, K, n_groups, _array(offsets, "int32", "offsets"), DTYPE[ab], _ptr(A), lda, _ptr(B), ldb,
                                   b_major.encode(), stride_b, DTYPE[d_fmt], _ptr(D), ldd, accum,
                                   C.byref(ew) if ew is not None else None, s))
 
@@ -319,7 +319,7 @@ def bsm_gemm_grouped(rows, N, K, n_groups, offsets, ab: str, A, lda, B, ldb, b_m
 def bsm_gemm_grouped_wgrad(rows, M, N, n_groups, offsets, ab: str, A, lda, B, ldb, d_fmt: str, D, ldd, stride_d, accum=0,
                            stream=None):
     s = _here(stream, offsets, A, B, D)
-    _check(lib().bsm_gemm_grouped_wgrad(rows, M, N, n_groups, _ints(offsets, "offsets"), DTYPE[ab], _ptr(A), lda, _ptr(B), ldb,
+    _check(lib().bsm_gemm_grouped_wgrad(rows, M, N, n_groups, _array(offsets, "int32", "offsets"), DTYPE[ab], _ptr(A), lda, _ptr(B), ldb,
                                         DTYPE[d_fmt], _ptr(D), ldd, stride_d, accum, s))
 
 
@@ -327,7 +327,7 @@ def bsm_gemm_grouped_block_scale(rows, N, K, n_groups, offsets, a_fmt: str, A, l
                                  SFB, ld_sfb, stride_sfb, fast, d_fmt: str, D, ldd, accum=0, ew: bsm_ewise | None = None,
                                  stream=None):
     s = _here(stream, offsets, A, SFA, B, SFB, D)
-    _check(lib().bsm_gemm_grouped_block_scale(rows, N, K, n_groups, _ints(offsets, "offsets"), DTYPE[a_fmt], _ptr(A), lda,
+    _check(lib().bsm_gemm_grouped_block_scale(rows, N, K, n_groups, _array(offsets, "int32", "offsets"), DTYPE[a_fmt], _ptr(A), lda,
                                               _ptr(SFA), ld_sfa, DTYPE[b_fmt], _ptr(B), ldb, stride_b, _ptr(SFB), ld_sfb,
                                               stride_sfb, fast, DTYPE[d_fmt], _ptr(D), ldd, accum,
                                               C.byref(ew) if ew is not None else None, s))
@@ -339,10 +339,11 @@ def bsm_gemm_lora_workspace(rows, R) -> int:
 
 def bsm_gemm_lora(rows, N, K, R, n_adapters, adapter, ab: str, X, ldx, W, ldw, LA, ld_la, stride_la, LB, ld_lb, stride_lb, scale,
                   workspace, d_fmt: str, D, ldd, accum=0, ew: bsm_ewise | None = None, stream=None):
+    ids, scales = _array(adapter, "int32", "adapter"), _array(scale, "float32", "scale")
     s = _here(stream, adapter, X, W, LA, LB, scale, workspace, D)
-    _check(lib().bsm_gemm_lora(rows, N, K, R, n_adapters, _ints(adapter, "adapter"), DTYPE[ab], _ptr(X), ldx, _ptr(W), ldw,
-                               _ptr(LA), ld_la, stride_la, _ptr(LB), ld_lb, stride_lb, _ptr(scale), _ptr(workspace),
-                               DTYPE[d_fmt], _ptr(D), ldd, accum, C.byref(ew) if ew is not None else None, s))
+    _check(lib().bsm_gemm_lora(rows, N, K, R, n_adapters, ids, DTYPE[ab], _ptr(X), ldx, _ptr(W), ldw, _ptr(LA), ld_la, stride_la,
+                               _ptr(LB), ld_lb, stride_lb, scales, _ptr(workspace), DTYPE[d_fmt], _ptr(D), ldd, accum,
+                               C.byref(ew) if ew is not None else None, s))
 
 
 def bsm_tile_add_scalar_f32(src, dst, n: int, s: float, stream=None):

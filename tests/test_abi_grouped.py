@@ -146,3 +146,11 @@ def test_adapter_refusals():
     for rows, R in ((-1, 8), (8, 300), (1 << 31, 8)):
         expect("BSM_E_SHAPE", bsm.bsm_gemm_lora_workspace, rows=rows, R=R)
     expect("BSM_E_ARG", lora, scale=torch.ones(4))
+
+
+def test_scales_of_another_type_are_refused():
+    """The adapters' scales are read as float32, one after another: a tensor of another type or with gaps is refused, as
+    the offsets and the rows' adapters are (before its device is looked at)."""
+    for t in (torch.float64, torch.bfloat16, torch.float16, torch.int32):
+        expect("BSM_E_DTYPE", lora, scale=torch.ones(4, dtype=t))
+    expect("BSM_E_ALIGN", lora, scale=torch.ones(8)[::2])

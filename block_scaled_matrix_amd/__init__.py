@@ -293,41 +293,58 @@ def _here(stream, *tensors):
 _dtypes = {}
 
 
-def _array(t, dtype: str, what):
-    """Address of a DEVICE array that is read element by element, its type and order checked where it is a torch tensor."""
+def _array(t, dtype: str, what, least):
+    """Address of a DEVICE array of at least `least` elements, its type, order and length checked where it is a torch tensor."""
     if t is None or type(t) is int:
         return t
-    want = _dtypes.get(dtype)
-    if want is None:
+    if dtype not in _dtypes:
         import torch
-        want = _dtypes[dtype] = getattr(torch, dtype)
-    if t.dtype is not want:
+        _dtypes[dtype] = getattr(torch, dtype)
+    if t.dtype is not _dtypes[dtype]:
         raise BsmError(-8, f"{what} must be {dtype}, not {t.dtype}")
     if not t.is_contiguous():
         raise BsmError(-5, f"{what} must be contiguous")
+    if t.numel() < least:
+        raise BsmError(-9, f"{what} holds {t.numel()} elements, the call takes {least}")
+    return t.data_ptr()
+
+
+def _workspace(t, least):
+    if t is None or type(t) is int:
+        return t
+    if not t.is_contiguous():
+        raise BsmError(-5, "workspace must be contiguous")
+    if t.numel() * t.element_size() < least:
+        raise BsmError(-9, f"workspace holds {t.numel() * t.element_size()} bytes, the call takes {least}")
     return t.data_ptr()
 
 
 def bsm_gemm_grouped(rows, N, K, n_groups, offsets, ab: str, A, lda, B, ldb, b_major: str, stride_b, d_fmt: str, D, ldd,
                      accum=0, ew: bsm_ewise | None = None, stream=None):
+    # (a call without groups, rows or columns reads no offsets)
+    off = _array(offsets, "int32", "offsets", n_groups + 1 if n_groups > 0 and rows > 0 and N > 0 else 0)
     s = _here(stream, offsets, A, B, D)
-    _check(lib().bsm_gemm_grouped(rows, N, K, n_groups, _array(offsets, "int32", "offsets"), DTYPE[ab], _ptr(A), lda, _ptr(B), ldb,
+    _check(lib().bsm_gemm_grouped(rows, N, K, n_groups, off, DTYPE[ab], _ptr(A), lda, _ptr(B), ldb,
                                   b_major.encode(), stride_b, DTYPE[d_fmt], _ptr(D), ldd, accum,
                                   C.byref(ew) if ew is not None else None, s))
 
 
 def bsm_gemm_grouped_wgrad(rows, M, N, n_groups, offsets, ab: str, A, lda, B, ldb, d_fmt: str, D, ldd, stride_d, accum=0,
                            stream=None):
+    # (a call without groups, rows of D or columns reads no offsets)
+    off = _array(offsets, "int32", "offsets", n_groups + 1 if n_groups > 0 and M > 0 and N > 0 else 0)
     s = _here(stream, offsets, A, B, D)
-    _check(lib().bsm_gemm_grouped_wgrad(rows, M, N, n_groups, _array(offsets, "int32", "offsets"), DTYPE[ab], _ptr(A), lda, _ptr(B), ldb,
+    _check(lib().bsm_gemm_grouped_wgrad(rows, M, N, n_groups, off, DTYPE[ab], _ptr(A), lda, _ptr(B), ldb,
                                         DTYPE[d_fmt], _ptr(D), ldd, stride_d, accum, s))
 
 
 def bsm_gemm_grouped_block_scale(rows, N, K, n_groups, offsets, a_fmt: str, A, lda, SFA, ld_sfa, b_fmt: str, B, ldb, stride_b,
                                  SFB, ld_sfb, stride_sfb, fast, d_fmt: str, D, ldd, accum=0, ew: bsm_ewise | None = None,
                                  stream=None):
+    # (a call without groups, rows or columns reads no offsets)
+    off = _array(offsets, "int32", "offsets", n_groups + 1 if n_groups > 0 and rows > 0 and N > 0 else 0)
     s = _here(stream, offsets, A, SFA, B, SFB, D)
-    _check(lib().bsm_gemm_grouped_block_scale(rows, N, K, n_groups, _array(offsets, "int32", "offsets"), DTYPE[a_fmt], _ptr(A), lda,
+    _check(lib().bsm_gemm_grouped_block_scale(rows, N, K, n_groups, off, DTYPE[a_fmt], _ptr(A), lda,
                                               _ptr(SFA), ld_sfa, DTYPE[b_fmt], _ptr(B), ldb, stride_b, _ptr(SFB), ld_sfb,
                                               stride_sfb, fast, DTYPE[d_fmt], _ptr(D), ldd, accum,
                                               C.byref(ew) if ew is not None else None, s))
@@ -339,10 +356,13 @@ def bsm_gemm_lora_workspace(rows, R) -> int:
 
 def bsm_gemm_lora(rows, N, K, R, n_adapters, adapter, ab: str, X, ldx, W, ldw, LA, ld_la, stride_la, LB, ld_lb, stride_lb, scale,
                   workspace, d_fmt: str, D, ldd, accum=0, ew: bsm_ewise | None = None, stream=None):
-    ids, scales = _array(adapter, "int32", "adapter"), _array(scale, "float32", "scale")
+    with_adapters = n_adapters > 0 and R > 0 and K > 0 and N > 0
+    ids = _array(adapter, "int32", "adapter", rows if with_adapters else 0)
+    scales = _array(scale, "float32", "scale", n_adapters if with_adapters else 0)
+    work = _workspace(workspace, rows * ((R + 31) // 32 * 32) * 4 if with_adapters else 0)
     s = _here(stream, adapter, X, W, LA, LB, scale, workspace, D)
     _check(lib().bsm_gemm_lora(rows, N, K, R, n_adapters, ids, DTYPE[ab], _ptr(X), ldx, _ptr(W), ldw, _ptr(LA), ld_la, stride_la,
-                               _ptr(LB), ld_lb, stride_lb, scales, _ptr(workspace), DTYPE[d_fmt], _ptr(D), ldd, accum,
+                               _ptr(LB), ld_lb, stride_lb, scales, work, DTYPE[d_fmt], _ptr(D), ldd, accum,
                                C.byref(ew) if ew is not None else None, s))
 
 

@@ -154,3 +154,29 @@ def test_scales_of_another_type_are_refused():
     for t in (torch.float64, torch.bfloat16, torch.float16, torch.int32):
         expect("BSM_E_DTYPE", lora, scale=torch.ones(4, dtype=t))
     expect("BSM_E_ALIGN", lora, scale=torch.ones(8)[::2])
+
+
+def test_short_arrays_are_refused():
+    """Arrays whose length a call fixes are refused where a tensor is too short: the kernels would read (and, in the
+    workspace, write) past its end. Arguments that a call does not use may have any length."""
+    ints = lambda n: torch.zeros(n, dtype=torch.int32)
+    for fn in (grouped, wgrad, mx):
+        expect("BSM_E_SHAPE", fn, offsets=ints(4))
+        expect("BSM_E_ARG", fn, offsets=ints(5))                         # (long enough: on the host)
+        fn(n_groups=0, offsets=0, a=0, d=0)
+    expect("BSM_E_SHAPE", lora, adapter=ints(99))
+    expect("BSM_E_SHAPE", lora, scale=torch.ones(3))
+    need = bsm.bsm_gemm_lora_workspace(100, 16)
+    expect("BSM_E_SHAPE", lora, ws=torch.zeros(need - 1, dtype=torch.uint8))
+    expect("BSM_E_SHAPE", lora, ws=torch.zeros(need // 4 - 1))
+    expect("BSM_E_ALIGN", lora, ws=torch.zeros(need, 2, dtype=torch.uint8)[:, 0])
+    expect("BSM_E_ARG", lora, adapter=ints(100))
+    expect("BSM_E_ARG", lora, ws=torch.zeros(need // 4))
+    expect("BSM_E_ARG", grouped, rows=0, offsets=ints(1))
+    expect("BSM_E_ARG", mx, N=0, offsets=ints(1))
+    expect("BSM_E_SHAPE", wgrad, rows=0, offsets=ints(1))               # (empty groups' outputs are written)
+    expect("BSM_E_ARG", wgrad, M=0, offsets=ints(1))
+    for unused in (dict(n=0), dict(R=0), dict(K=0), dict(N=0)):
+        expect("BSM_E_ARG", lora, adapter=ints(1), **unused)             # (refused for its device alone)
+        expect("BSM_E_ARG", lora, scale=torch.ones(1), **unused)
+        expect("BSM_E_ARG", lora, ws=torch.zeros(1), **unused)

@@ -55,7 +55,7 @@ static MidTile mid_tile(const GemmArgs& a, const GroupArgs& gr) {
   // N 2048, K 4096: 19.5 -> 17.8 us)
   if ((gr.rows / 128 + (used + 1) / 2) * tn < 192) return SPLIT;
   // Exact E4M3 x E2M1 of up to 16 rows a group: its conversions leave room for a third workgroup (64 rows over 32
-  // groups, N = K = 4096 62.1 -> 57.3 us, 512 rows 83.8 -> 78.6 us; E4M3 pairs 101 -> 104 us, the others the same).
+  // groups, N = K = 4096 62 -> 56 us, 512 rows 83.8 -> 78.6 us; E4M3 pairs 101 -> 104 us, the others the same).
   const bool exact_mixed = a.dtype == BSM_E4M3 && a.dtype_b == BSM_E2M1 && !a.mx_window;
   return exact_mixed && gr.rows / gr.n <= 16 ? ROWS32 : MID;
 }

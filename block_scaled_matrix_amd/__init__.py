@@ -25,7 +25,9 @@ EXPORTS = ("bsm_image_stride", "bsm_tile_box_load", "bsm_tile_box_store", "bsm_t
            "bsm_tile_box_load_steps", "bsm_tile_box_store_steps", "bsm_tile_gather4", "bsm_tile_scatter4", "bsm_gemm",
            "bsm_gemm_block_scale", "bsm_gemm_ewise", "bsm_gemm_block_scale_ewise", "bsm_gemm_block_scale_major",
            "bsm_gemm_block_scale_fastacc", "bsm_gemm_grouped", "bsm_gemm_grouped_wgrad",
-           "bsm_gemm_grouped_block_scale", "bsm_gemm_lora", "bsm_gemm_lora_workspace",
+           "bsm_gemm_grouped_block_scale", "bsm_gemm_lora", "bsm_gemm_lora_workspace", "bsm_router_balance",
+           "bsm_router_balance_workspace", "bsm_router_balance_grad", "bsm_block_scale_save", "bsm_block_scale_restore",
+           "bsm_block_scale_ewise_grad",
            "bsm_debug_grouped_route", "bsm_debug_stream_mix_bf16", "bsm_debug_mfma_loop", "bsm_tile_add_scalar_f32", "bsm_debug_fragments", "bsm_debug_fragment_shape", "bsm_last_error")
 
 
@@ -91,6 +93,13 @@ def lib():
         L.bsm_gemm_lora_workspace.argtypes = [I64, I64]
         L.bsm_gemm_lora.argtypes = [I64, I64, I64, I64, I32, P, I32, P, I64, P, I64, P, I64, I64, P, I64, I64, P, P, I32, P,
                                     I64, C.c_int, C.POINTER(bsm_ewise), P]
+        L.bsm_router_balance_workspace.restype = I64
+        L.bsm_router_balance_workspace.argtypes = [I64, I32]
+        L.bsm_router_balance.argtypes = [I64, I32, I32, I32, P, I64, P, C.c_float, P, P, P, P, P]
+        L.bsm_router_balance_grad.argtypes = [I64, I32, I32, I32, P, I64, P, P, C.c_float, P, I32, P, I64, C.c_int, P]
+        L.bsm_block_scale_save.argtypes = [I64, I64, I32, P, I64, I32, P, I64, P, I64, P]
+        L.bsm_block_scale_restore.argtypes = [I64, I64, I32, P, I64, P, I64, I32, P, I64, C.POINTER(bsm_ewise), P]
+        L.bsm_block_scale_ewise_grad.argtypes = [I64, I64, I32, P, I64, P, I64, I32, P, I64, P, I64, C.POINTER(bsm_ewise), P]
         L.bsm_tile_add_scalar_f32.argtypes = [P, P, I64, C.c_float, P]
         L.bsm_debug_stream_mix_bf16.argtypes = [P, P, P, I64, P]
         L.bsm_debug_grouped_route.restype = C.c_char_p
@@ -104,7 +113,8 @@ def lib():
                       "bsm_tile_scatter4", "bsm_gemm",
                       "bsm_gemm_block_scale", "bsm_gemm_ewise", "bsm_gemm_block_scale_ewise",
                       "bsm_gemm_block_scale_major", "bsm_gemm_block_scale_fastacc", "bsm_gemm_grouped",
-                      "bsm_gemm_grouped_wgrad", "bsm_gemm_grouped_block_scale", "bsm_gemm_lora", "bsm_tile_add_scalar_f32",
+                      "bsm_gemm_grouped_wgrad", "bsm_gemm_grouped_block_scale", "bsm_gemm_lora", "bsm_router_balance", "bsm_router_balance_grad",
+                      "bsm_block_scale_save", "bsm_block_scale_restore", "bsm_block_scale_ewise_grad", "bsm_tile_add_scalar_f32",
                       "bsm_debug_fragments", "bsm_debug_stream_mix_bf16", "bsm_debug_mfma_loop"):
             getattr(L, rc_fn).restype = C.c_int
         _lib = L
@@ -364,6 +374,93 @@ def bsm_gemm_lora(rows, N, K, R, n_adapters, adapter, ab: str, X, ldx, W, ldw, L
     _check(lib().bsm_gemm_lora(rows, N, K, R, n_adapters, ids, DTYPE[ab], _ptr(X), ldx, _ptr(W), ldw, _ptr(LA), ld_la, stride_la,
                                _ptr(LB), ld_lb, stride_lb, scales, work, DTYPE[d_fmt], _ptr(D), ldd, accum,
                                C.byref(ew) if ew is not None else None, s))
+
+
+def _rows(t, dtype: str, what, rows, n, ld, chunk=1):
+    """Address of a DEVICE matrix of `rows` rows of n elements, ld apart; where it is a torch tensor, of the type that
+    the call says (codes and scales: of one byte), its rows contiguous, and reaching to the last row's end, in whole
+    chunks where the kernels read it in such."""
+    if t is None or type(t) is int:
+        return t
+    if ESIZE[dtype] == 1:
+        if t.element_size() != 1:
+            raise BsmError(-8, f"{what} must have elements of one byte, not {t.dtype}")
+    elif t.dtype is not _torch_type(dtype):
+        raise BsmError(-8, f"{what} must be {dtype}, not {t.dtype}")
+    if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise BsmError(-5, f"{what}: a row's elements must lie one after another")
+    if rows > 0 and n > 0:
+        have = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
+        need = (rows - 1) * ld + -(-n // chunk) * chunk
+        if have < need:
+            raise BsmError(-9, f"{what} holds {have} elements from its start on, the call takes {need}")
+    return t.data_ptr()
+
+
+def _torch_type(fmt: str):
+    name = {"f32": "float32", "f16": "float16", "bf16": "bfloat16"}[fmt]
+    if name not in _dtypes:
+        import torch
+        _dtypes[name] = getattr(torch, name)
+    return _dtypes[name]
+
+
+def _float_fmt(fmt: str, what):
+    if fmt not in ("f32", "bf16", "f16"):
+        raise BsmError(-8, f"{what} = {fmt} is not f32, bf16 or f16")
+
+
+def bsm_router_balance_workspace(rows, n_experts) -> int:
+    return _check(lib().bsm_router_balance_workspace(rows, n_experts))
+
+
+def bsm_router_balance(rows, n_experts, k, l_fmt: str, logits, ldl, ids, scale, counts, offsets, loss, workspace=None, stream=None):
+    _float_fmt(l_fmt, "l_fmt")
+    x = _rows(logits, l_fmt, "logits", rows, n_experts, ldl)
+    i = _array(ids, "int32", "ids", rows * k)
+    c, o = _array(counts, "int32", "counts", n_experts + 1), _array(offsets, "int32", "offsets", n_experts + 1)
+    f = _array(loss, "float32", "loss", 1)
+    work = _workspace(workspace, lib().bsm_router_balance_workspace(rows, n_experts))
+    s = _here(stream, logits, ids, counts, offsets, loss, workspace)
+    _check(lib().bsm_router_balance(rows, n_experts, k, DTYPE[l_fmt], x, ldl, i, scale, c, o, f, work, s))
+
+
+def bsm_router_balance_grad(rows, n_experts, k, l_fmt: str, logits, ldl, ids, counts, scale, dloss, d_fmt: str, D, ldd, accum=0,
+                            stream=None):
+    _float_fmt(l_fmt, "l_fmt")
+    _float_fmt(d_fmt, "d_fmt")
+    x = _rows(logits, l_fmt, "logits", rows, n_experts, ldl)
+    i = _array(ids, "int32", "ids", rows * k)
+    c, g = _array(counts, "int32", "counts", n_experts + 1), _array(dloss, "float32", "dloss", 1)
+    d = _rows(D, d_fmt, "D", rows, n_experts, ldd)
+    s = _here(stream, logits, ids, counts, dloss, D)
+    _check(lib().bsm_router_balance_grad(rows, n_experts, k, DTYPE[l_fmt], x, ldl, i, c, scale, g, DTYPE[d_fmt], d, ldd, accum, s))
+
+
+def bsm_block_scale_save(rows, K, x_fmt: str, X, ldx, fmt: str, Q, ldq, SF, ld_sf, stream=None):
+    _float_fmt(x_fmt, "x_fmt")
+    x = _rows(X, x_fmt, "X", rows, K, ldx, 4 if x_fmt == "f32" else 8)
+    q, f = _rows(Q, "u8", "Q", rows, K, ldq), _rows(SF, "u8", "SF", rows, (K + 31) // 32, ld_sf)
+    s = _here(stream, X, Q, SF)
+    _check(lib().bsm_block_scale_save(rows, K, DTYPE[x_fmt], x, ldx, DTYPE[fmt], q, ldq, f, ld_sf, s))
+
+
+def bsm_block_scale_restore(rows, K, fmt: str, Q, ldq, SF, ld_sf, d_fmt: str, D, ldd, ew: bsm_ewise | None = None, stream=None):
+    _float_fmt(d_fmt, "d_fmt")
+    q, f = _rows(Q, "u8", "Q", rows, K, ldq, 8), _rows(SF, "u8", "SF", rows, (K + 31) // 32, ld_sf)
+    d = _rows(D, d_fmt, "D", rows, K, ldd)
+    s = _here(stream, Q, SF, D)
+    _check(lib().bsm_block_scale_restore(rows, K, DTYPE[fmt], q, ldq, f, ld_sf, DTYPE[d_fmt], d, ldd,
+                                         C.byref(ew) if ew is not None else None, s))
+
+
+def bsm_block_scale_ewise_grad(rows, K, fmt: str, Q, ldq, SF, ld_sf, dy_fmt: str, dY, lddy, D, ldd, ew: bsm_ewise, stream=None):
+    _float_fmt(dy_fmt, "dy_fmt")
+    q, f = _rows(Q, "u8", "Q", rows, K, ldq, 8), _rows(SF, "u8", "SF", rows, (K + 31) // 32, ld_sf)
+    y, d = _rows(dY, dy_fmt, "dY", rows, K, lddy, 4 if dy_fmt == "f32" else 8), _rows(D, dy_fmt, "D", rows, K, ldd)
+    s = _here(stream, Q, SF, dY, D)
+    _check(lib().bsm_block_scale_ewise_grad(rows, K, DTYPE[fmt], q, ldq, f, ld_sf, DTYPE[dy_fmt], y, lddy, d, ldd,
+                                            C.byref(ew) if ew is not None else None, s))
 
 
 def bsm_tile_add_scalar_f32(src, dst, n: int, s: float, stream=None):

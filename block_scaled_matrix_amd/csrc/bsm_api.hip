@@ -8,6 +8,8 @@
 
 #include "../../include/bsm.h"
 #include "bsm_internal.hpp"
+#include "kept.hpp"
+#include "router.hpp"
 
 namespace {
 
@@ -753,6 +755,176 @@ int bsm_gemm_lora(int64_t rows, int64_t N, int64_t K, int64_t R, int32_t n_adapt
   }
   hipError_t e = bsm::launch_gemm_lora(g, lo, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "bsm_gemm_lora");
+  return ok();
+}
+
+static int check_router(int64_t rows, int32_t n_experts, int32_t k, int32_t l_fmt, const void* logits, int64_t ldl,
+                        const int32_t* ids, bsm::RouterArgs* a) {
+  if (l_fmt != BSM_F32 && l_fmt != BSM_BF16 && l_fmt != BSM_F16) return fail(BSM_E_DTYPE, "l_fmt = %d is not F32, BF16 or F16", l_fmt);
+  if (n_experts < 1 || n_experts > 1024) return fail(BSM_E_SHAPE, "n_experts = %d not in 1 .. 1024", n_experts);
+  if (k < 1 || k > 1024) return fail(BSM_E_SHAPE, "k = %d not in 1 .. 1024", k);
+  if (rows < 0 || rows * (__int128)k > 0x7FFFFFFF) return fail(BSM_E_SHAPE, "rows = %lld, k = %d: rows * k out of range", (long long)rows, k);
+  const int es = elem_size(l_fmt);
+  if (rows > 0) {
+    if (!logits || !ids) return fail(BSM_E_NULL, "logits or ids is NULL");
+    if ((uintptr_t)logits % es || (uintptr_t)ids % 4) return fail(BSM_E_ALIGN, "logits and ids must be aligned to their elements");
+    if (ldl < n_experts) return fail(BSM_E_ALIGN, "ldl = %lld must be >= n_experts", (long long)ldl);
+    if (ldl > (int64_t(1) << 31)) return fail(BSM_E_SHAPE, "ldl = %lld out of range", (long long)ldl);
+  }
+  a->rows = rows; a->E = n_experts; a->k = k; a->l_fmt = l_fmt;
+  a->logits = logits; a->ldl = ldl; a->ids = ids;
+  a->vec = (uintptr_t)logits % (4 * es) == 0 && ldl % 4 == 0;
+  return BSM_OK;
+}
+
+int64_t bsm_router_balance_workspace(int64_t rows, int32_t n_experts) {
+  if (rows < 0 || rows > 0x7FFFFFFF) return fail(BSM_E_SHAPE, "rows = %lld out of range", (long long)rows);
+  if (n_experts < 1 || n_experts > 1024) return fail(BSM_E_SHAPE, "n_experts = %d not in 1 .. 1024", n_experts);
+  ok();
+  return bsm::balance_workspace(rows, n_experts);
+}
+
+int bsm_router_balance(int64_t rows, int32_t n_experts, int32_t k, int32_t l_fmt, const void* logits, int64_t ldl,
+                       const int32_t* ids, float scale, int32_t* counts, int32_t* offsets, float* loss, void* workspace,
+                       void* stream) {
+  bsm::RouterArgs a{};
+  int rc;
+  if ((rc = check_router(rows, n_experts, k, l_fmt, logits, ldl, ids, &a))) return rc;
+  const int64_t wsb = bsm::balance_workspace(rows, n_experts), es = elem_size(l_fmt);
+  if (!counts || !offsets || !loss) return fail(BSM_E_NULL, "counts, offsets or loss is NULL");
+  if ((uintptr_t)counts % 4 || (uintptr_t)offsets % 4 || (uintptr_t)loss % 4)
+    return fail(BSM_E_ALIGN, "counts, offsets and loss must be 4-byte aligned");
+  if (wsb > 0 && !workspace) return fail(BSM_E_NULL, "workspace is NULL");
+  if (wsb > 0 && (uintptr_t)workspace % 16) return fail(BSM_E_ALIGN, "workspace not 16-byte aligned");
+  const Range out[] = {block_range(counts, 1, 0, 1, 0, n_experts + int64_t(1), 32), block_range(offsets, 1, 0, 1, 0, n_experts + int64_t(1), 32),
+                       block_range(loss, 1, 0, 1, 0, 1, 32), Range{(uintptr_t)workspace, (uintptr_t)workspace + (uintptr_t)wsb}};
+  for (int i = 0; i < 4; i++) {
+    if (i == 3 && wsb == 0) break;
+    if (rows > 0 && (overlap(out[i], block_range(logits, 1, 0, rows, ldl, n_experts, (int)(8 * es))) ||
+                     overlap(out[i], block_range(ids, 1, 0, 1, 0, rows * k, 32))))
+      return fail(BSM_E_ALIAS, "logits or ids overlap an output or the workspace");
+    for (int j = 0; j < i; j++)
+      if (overlap(out[i], out[j])) return fail(BSM_E_ALIAS, "counts, offsets, loss and workspace overlap");
+  }
+  a.counts = counts; a.offsets = offsets; a.loss = loss; a.scale = scale;
+  hipError_t e = bsm::launch_router_balance(a, workspace, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "bsm_router_balance");
+  return ok();
+}
+
+int bsm_router_balance_grad(int64_t rows, int32_t n_experts, int32_t k, int32_t l_fmt, const void* logits, int64_t ldl,
+                            const int32_t* ids, const int32_t* counts, float scale, const float* dloss, int32_t d_fmt, void* D,
+                            int64_t ldd, int accum, void* stream) {
+  bsm::RouterArgs a{};
+  int rc;
+  if ((rc = check_flag(accum, "accum"))) return rc;
+  if ((rc = check_router(rows, n_experts, k, l_fmt, logits, ldl, ids, &a))) return rc;
+  if (d_fmt != BSM_F32 && d_fmt != l_fmt) return fail(BSM_E_DTYPE, "d_fmt = %d is neither F32 nor the logits' format", d_fmt);
+  if (rows == 0) return ok();
+  const int ds = elem_size(d_fmt), es = elem_size(l_fmt);
+  if (!counts || !D) return fail(BSM_E_NULL, "counts or D is NULL");
+  if ((uintptr_t)counts % 4 || (uintptr_t)dloss % 4 || (uintptr_t)D % ds)
+    return fail(BSM_E_ALIGN, "counts, dloss and D must be aligned to their elements");
+  if (ldd < n_experts) return fail(BSM_E_ALIGN, "ldd = %lld must be >= n_experts", (long long)ldd);
+  if (ldd > (int64_t(1) << 31)) return fail(BSM_E_SHAPE, "ldd = %lld out of range", (long long)ldd);
+  const Range rd = block_range(D, 1, 0, rows, ldd, n_experts, 8 * ds);
+  if (overlap(rd, block_range(logits, 1, 0, rows, ldl, n_experts, 8 * es)) || overlap(rd, block_range(ids, 1, 0, 1, 0, rows * k, 32)) ||
+      overlap(rd, block_range(counts, 1, 0, 1, 0, n_experts + int64_t(1), 32)) || (dloss && overlap(rd, block_range(dloss, 1, 0, 1, 0, 1, 32))))
+    return fail(BSM_E_ALIAS, "an input overlaps D");
+  a.counts = const_cast<int32_t*>(counts); a.scale = scale;
+  bsm::RouterGradArgs g{};
+  g.dloss = dloss; g.D = D; g.ldd = ldd; g.d_fmt = d_fmt; g.accum = accum;
+  g.vec = (uintptr_t)D % (4 * ds) == 0 && ldd % 4 == 0;
+  hipError_t e = bsm::launch_router_balance_grad(a, g, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "bsm_router_balance_grad");
+  return ok();
+}
+
+// Rows of kept activations and the sizes they share.
+static int check_kept(int64_t rows, int64_t K, int32_t fmt, const uint8_t* Q, int64_t ldq, const uint8_t* SF, int64_t ld_sf) {
+  if (fmt != BSM_E4M3 && fmt != BSM_E5M2) return fail(BSM_E_DTYPE, "fmt = %d is neither E4M3 nor E5M2", fmt);
+  if (rows < 0 || rows > 0x7FFFFFFF) return fail(BSM_E_SHAPE, "rows = %lld out of range", (long long)rows);
+  if (K < 0 || K > (int64_t(1) << 24)) return fail(BSM_E_SHAPE, "K = %lld not in 0 .. 2^24", (long long)K);
+  if (rows == 0 || K == 0) return BSM_OK;
+  if (!Q || !SF) return fail(BSM_E_NULL, "Q or SF is NULL");
+  if ((uintptr_t)Q % 16) return fail(BSM_E_ALIGN, "Q not 16-byte aligned");
+  if ((uintptr_t)SF % 4) return fail(BSM_E_ALIGN, "SF not 4-byte aligned");
+  if (ldq < K || ldq % 16) return fail(BSM_E_ALIGN, "ldq = %lld must be >= K and a multiple of 16", (long long)ldq);
+  if (ld_sf < (K + 31) / 32 || ld_sf % 4) return fail(BSM_E_ALIGN, "ld_sf = %lld must be >= ceil(K/32) and a multiple of 4", (long long)ld_sf);
+  if (ldq > (int64_t(1) << 31) || ld_sf > (int64_t(1) << 31)) return fail(BSM_E_SHAPE, "ldq or ld_sf out of range");
+  return BSM_OK;
+}
+
+static int check_rows_of(const void* p, int64_t K, int64_t ld, int32_t fmt, const char* name) {
+  if (!p) return fail(BSM_E_NULL, "%s is NULL", name);
+  if ((uintptr_t)p % 16) return fail(BSM_E_ALIGN, "%s not 16-byte aligned", name);
+  const int q = fmt == BSM_F32 ? 4 : 8;
+  if (ld < K || ld % q) return fail(BSM_E_ALIGN, "the leading dimension %lld of %s must be >= K and a multiple of %d", (long long)ld, name, q);
+  if (ld > (int64_t(1) << 31)) return fail(BSM_E_SHAPE, "the leading dimension %lld of %s is out of range", (long long)ld, name);
+  return BSM_OK;
+}
+
+static bool float_fmt(int32_t f) { return f == BSM_F32 || f == BSM_BF16 || f == BSM_F16; }
+
+int bsm_block_scale_save(int64_t rows, int64_t K, int32_t x_fmt, const void* X, int64_t ldx, int32_t fmt, uint8_t* Q, int64_t ldq,
+                         uint8_t* SF, int64_t ld_sf, void* stream) {
+  int rc;
+  if (!float_fmt(x_fmt)) return fail(BSM_E_DTYPE, "x_fmt = %d is not F32, BF16 or F16", x_fmt);
+  if ((rc = check_kept(rows, K, fmt, Q, ldq, SF, ld_sf))) return rc;
+  if (rows == 0 || K == 0) return ok();
+  if ((rc = check_rows_of(X, K, ldx, x_fmt, "X"))) return rc;
+  const Range rx = block_range(X, 1, 0, rows, ldx, K, 8 * elem_size(x_fmt)), rq = block_range(Q, 1, 0, rows, ldq, K, 8),
+              rs = block_range(SF, 1, 0, rows, ld_sf, (K + 31) / 32, 8);
+  if (overlap(rx, rq) || overlap(rx, rs) || overlap(rq, rs)) return fail(BSM_E_ALIAS, "X, Q and SF overlap");
+  bsm::KeptArgs a{};
+  a.rows = rows; a.K = K; a.fmt = fmt; a.Q = Q; a.ldq = ldq; a.SF = SF; a.ld_sf = ld_sf;
+  a.x_fmt = x_fmt; a.X = X; a.ldx = ldx;
+  hipError_t e = bsm::launch_block_scale_save(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "bsm_block_scale_save");
+  return ok();
+}
+
+int bsm_block_scale_restore(int64_t rows, int64_t K, int32_t fmt, const uint8_t* Q, int64_t ldq, const uint8_t* SF, int64_t ld_sf,
+                            int32_t d_fmt, void* D, int64_t ldd, const bsm_ewise* ew, void* stream) {
+  int rc;
+  if (ew && (rc = check_ewise(ew))) return rc;
+  if (!float_fmt(d_fmt)) return fail(BSM_E_DTYPE, "d_fmt = %d is not F32, BF16 or F16", d_fmt);
+  if ((rc = check_kept(rows, K, fmt, Q, ldq, SF, ld_sf))) return rc;
+  if (rows == 0 || K == 0) return ok();
+  if ((rc = check_rows_of(D, K, ldd, d_fmt, "D"))) return rc;
+  const Range rd = block_range(D, 1, 0, rows, ldd, K, 8 * elem_size(d_fmt));
+  if (overlap(rd, block_range(Q, 1, 0, rows, ldq, K, 8)) || overlap(rd, block_range(SF, 1, 0, rows, ld_sf, (K + 31) / 32, 8)))
+    return fail(BSM_E_ALIAS, "Q or SF overlaps D");
+  bsm::KeptArgs a{};
+  a.rows = rows; a.K = K; a.fmt = fmt; a.Q = const_cast<uint8_t*>(Q); a.ldq = ldq; a.SF = const_cast<uint8_t*>(SF); a.ld_sf = ld_sf;
+  a.x_fmt = d_fmt; a.D = D; a.ldd = ldd;
+  if (ew) { a.ew_op = ew->op; a.ew_scale = ew->scale; a.ew_bias = ew->bias; }
+  hipError_t e = bsm::launch_block_scale_restore(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "bsm_block_scale_restore");
+  return ok();
+}
+
+int bsm_block_scale_ewise_grad(int64_t rows, int64_t K, int32_t fmt, const uint8_t* Q, int64_t ldq, const uint8_t* SF,
+                               int64_t ld_sf, int32_t dy_fmt, const void* dY, int64_t lddy, void* D, int64_t ldd,
+                               const bsm_ewise* ew, void* stream) {
+  int rc;
+  if (!ew) return fail(BSM_E_NULL, "ew is NULL");
+  if ((rc = check_ewise(ew))) return rc;
+  if (!float_fmt(dy_fmt)) return fail(BSM_E_DTYPE, "dy_fmt = %d is not F32, BF16 or F16", dy_fmt);
+  if ((rc = check_kept(rows, K, fmt, Q, ldq, SF, ld_sf))) return rc;
+  if (rows == 0 || K == 0) return ok();
+  if ((rc = check_rows_of(dY, K, lddy, dy_fmt, "dY")) || (rc = check_rows_of(D, K, ldd, dy_fmt, "D"))) return rc;
+  const int bits = 8 * elem_size(dy_fmt);
+  const Range rd = block_range(D, 1, 0, rows, ldd, K, bits);
+  if (overlap(rd, block_range(Q, 1, 0, rows, ldq, K, 8)) || overlap(rd, block_range(SF, 1, 0, rows, ld_sf, (K + 31) / 32, 8)))
+    return fail(BSM_E_ALIAS, "Q or SF overlaps D");
+  if (!(D == dY && ldd == lddy) && overlap(rd, block_range(dY, 1, 0, rows, lddy, K, bits))) return fail(BSM_E_ALIAS, "dY overlaps D");
+  bsm::KeptArgs a{};
+  a.rows = rows; a.K = K; a.fmt = fmt; a.Q = const_cast<uint8_t*>(Q); a.ldq = ldq; a.SF = const_cast<uint8_t*>(SF); a.ld_sf = ld_sf;
+  a.x_fmt = dy_fmt; a.X = dY; a.ldx = lddy; a.D = D; a.ldd = ldd;
+  a.ew_op = ew->op; a.ew_scale = ew->scale; a.ew_bias = ew->bias;
+  hipError_t e = bsm::launch_block_scale_ewise_grad(a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "bsm_block_scale_ewise_grad");
   return ok();
 }
 

@@ -1,0 +1,429 @@
+// k_router.hip - counts, offsets and balance loss of a router's choices, and the loss's gradient.
+//
+//   p_t = softmax(l_t), c_e = assignments of expert e, n = rows kept (those with an expert among their ids),
+//   f_e = c_e / (k n), P_e = sum_t p_te / n over the rows kept
+//   loss = s E sum_e f_e P_e,   dl_te = g s E / n p_te (f_e - sum_j f_j p_tj)
+//
+// The gradient needs the counts but not P, so each direction reads the logits once and nothing but the
+// counts passes between them. LPR lanes share a row (a power of two, four experts a lane and vector, J
+// vectors), so a lane keeps the same experts for every row it sees: f stays in its registers, and P's
+// column sums are register sums, joined at the end across the wave's rows, the workgroup's waves (LDS)
+// and the workgroups (a second launch over at most 256 of them), all in a fixed order. A lane adds at
+// most 64 rows in float32, then into a double: a sum over any number of rows keeps its bits. Counts are
+// integers, so the LDS atomics that make them cannot change a result by their order.
+// Bound: the logits' bytes for many rows; a launch and a chain of dependent loads for few, so up to
+// kOneGroup logits a single workgroup does everything in one launch.
+#include "grouped.hpp"
+#include "router.hpp"
+#include "../../include/bsm.h"
+
+namespace bsm {
+namespace {
+
+constexpr int THREADS = 512, WAVES = THREADS / 64, JOIN = 1024;
+constexpr int kMaxGroups = 256;
+constexpr int64_t kOneGroup = 16384;
+
+template <int F>
+__device__ __forceinline__ float load1(const void* p, int64_t i) {
+  if constexpr (F == BSM_F32) return ((const float*)p)[i];
+  else if constexpr (F == BSM_BF16) return bf16_bits_to_f32(((const uint16_t*)p)[i]);
+  else return f16_bits_to_f32(((const uint16_t*)p)[i]);
+}
+// Four consecutive values from element i on, those at or past `left` -infinity.
+template <int F>
+__device__ __forceinline__ void load4(const void* p, int64_t i, int left, bool vec, float (&v)[4]) {
+  if (vec && left >= 4) {
+    if constexpr (F == BSM_F32) {
+      const f32x4 x = *(const f32x4*)((const float*)p + i);
+#pragma unroll
+      for (int e = 0; e < 4; e++) v[e] = x[e];
+    } else {
+      const uint2 x = *(const uint2*)((const uint16_t*)p + i);
+      const uint32_t w[2] = {x.x, x.y};
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        const uint16_t h = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+        v[e] = F == BSM_BF16 ? bf16_bits_to_f32(h) : f16_bits_to_f32(h);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; e++) v[e] = e < left ? load1<F>(p, i + e) : -INFINITY;
+}
+
+template <int LPR>
+__device__ __forceinline__ float row_max(float v) {
+#pragma unroll
+  for (int d = 1; d < LPR; d *= 2) v = fmaxf(v, __shfl_xor(v, d));
+  return v;
+}
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int d = 1; d < LPR; d *= 2) v += __shfl_xor(v, d);
+  return v;
+}
+
+// One row's softmax in this lane's registers: in the logits, out exp(l - max) and the factor 1 / sum. A
+// row without a finite logit above -infinity has no softmax: every probability is 0. NaN and +infinity
+// make the row NaN, as the formula does.
+template <int LPR, int J>
+__device__ __forceinline__ float row_softmax(float (&v)[J][4]) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < J; j++)
+#pragma unroll
+    for (int e = 0; e < 4; e++) m = fmaxf(m, v[j][e]);
+  m = row_max<LPR>(m);
+  // (fmaxf passes over NaN; a row of NaN and -infinity has max -infinity and must stay NaN)
+  float s = 0.0f;
+#pragma unroll
+  for (int j = 0; j < J; j++)
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      v[j][e] = v[j][e] == -INFINITY ? 0.0f : exp_f32(v[j][e] - m);
+      s += v[j][e];
+    }
+  s = row_sum<LPR>(s);
+  return s == 0.0f ? 0.0f : 1.0f / s;
+}
+
+// Whether a row has an expert among its ids, for every lane of the row; with `count`, counts them.
+template <int LPR>
+__device__ __forceinline__ bool row_kept(const RouterArgs& a, int64_t row, bool in, int lr, int lane, int* count) {
+  bool any = false;
+  for (int j0 = 0; j0 < a.k; j0 += LPR) {
+    const int j = j0 + lr;
+    const int id = in && j < a.k ? a.ids[row * a.k + j] : -1;
+    const bool ok = id >= 0 && id < a.E;
+    if (ok && count) atomicAdd(count + id, 1);
+    any |= ok;
+  }
+  const uint64_t mine = (LPR == 64 ? ~0ull : ((1ull << LPR) - 1)) << (lane & ~(LPR - 1));
+  return (__ballot(any) & mine) != 0;
+}
+
+// Exclusive sums, the loss and the outputs, by the whole workgroup of NT lanes: cnt[0 .. E - 1], kept and the column sums
+// psum in LDS; E <= 1024, two experts a lane. wscan and wred: LDS of one value a wave.
+template <int NT>
+__device__ __forceinline__ void finish(const RouterArgs& a, const int* cnt, int kept, const double* psum, int* wscan, double* wred) {
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6;
+  const bool h0 = 2 * t < a.E, h1 = 2 * t + 1 < a.E;
+  const int c0 = h0 ? cnt[2 * t] : 0, c1 = h1 ? cnt[2 * t + 1] : 0;
+  double part = (h0 ? (double)c0 * psum[2 * t] : 0.0) + (h1 ? (double)c1 * psum[2 * t + 1] : 0.0);
+  const int incl = grouped::wave_inclusive_scan(c0 + c1);
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) part += __shfl_xor(part, d);
+  if (lane == 63) { wscan[w] = incl; wred[w] = part; }
+  __syncthreads();
+  int before = incl - c0 - c1, all = 0;
+  double sum = 0.0;
+#pragma unroll
+  for (int q = 0; q < NT / 64; q++) {
+    if (q < w) before += wscan[q];
+    all += wscan[q];
+    sum += wred[q];
+  }
+  if (h0) { a.counts[2 * t] = c0; a.offsets[2 * t] = before; }
+  if (h1) { a.counts[2 * t + 1] = c1; a.offsets[2 * t + 1] = before + c0; }
+  if (t == 0) {
+    a.counts[a.E] = kept;
+    a.offsets[a.E] = all;
+    const double n = kept;
+    a.loss[0] = kept ? (float)(a.scale * (a.E * sum / (n * n * a.k))) : 0.0f;
+  }
+}
+
+// Where a workgroup's sums go: column sums (doubles) and counts in rows of an even number of experts, and its kept rows.
+struct Parts { double* sums; int* counts; int* kept; int ld; };
+
+// ONE: the only workgroup, which finishes too. Otherwise workgroup b's sums go to row b of `parts`.
+template <int F, int LPR, int J, bool ONE>
+__global__ __launch_bounds__(THREADS) void k_balance(RouterArgs a, Parts parts) {
+  constexpr int RPW = 64 / LPR, E4 = 4 * LPR * J, U = J == 1 ? 4 : 2;
+  __shared__ double total[E4];
+  __shared__ double sums[E4 > 256 ? 1 : WAVES][E4];
+  __shared__ int cnt[E4];
+  __shared__ int kept_all;
+  const int t = threadIdx.x, lane = t & 63, w = t >> 6, lr = lane & (LPR - 1), sub = lane / LPR;
+  for (int i = t; i < E4; i += THREADS) { cnt[i] = 0; total[i] = 0.0; }
+  if (t == 0) kept_all = 0;
+  __syncthreads();
+  double dsum[J][4] = {};
+  float fsum[J][4] = {};
+  int kept = 0, since = 0;
+  const int64_t step = (int64_t)gridDim.x * WAVES * RPW;
+  for (int64_t r0 = ((int64_t)blockIdx.x * WAVES + w) * RPW; r0 < a.rows; r0 += U * step) {
+    // U rows of logits are asked for before the first is worked on
+    float v[U][J][4];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int64_t row = r0 + u * step + sub;
+#pragma unroll
+      for (int j = 0; j < J; j++) {
+        const int e0 = 4 * (LPR * j + lr);
+        load4<F>(a.logits, row * a.ldl + e0, row < a.rows ? a.E - e0 : 0, a.vec, v[u][j]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const int64_t row = r0 + u * step + sub;
+      const bool keep = row_kept<LPR>(a, row, row < a.rows, lr, lane, cnt);
+      const float inv = row_softmax<LPR, J>(v[u]);
+      kept += keep && lr == 0;
+#pragma unroll
+      for (int j = 0; j < J; j++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) fsum[j][e] += keep ? v[u][j][e] * inv : 0.0f;
+    }
+    if (++since == 64 / U) {
+      since = 0;
+#pragma unroll
+      for (int j = 0; j < J; j++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) { dsum[j][e] += fsum[j][e]; fsum[j][e] = 0.0f; }
+    }
+  }
+  if (kept) atomicAdd(&kept_all, kept);
+#pragma unroll
+  for (int j = 0; j < J; j++)
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      double d = dsum[j][e] + fsum[j][e];
+#pragma unroll
+      for (int s = LPR; s < 64; s *= 2) d += __shfl_xor(d, s);
+      dsum[j][e] = d;
+    }
+  if constexpr (E4 <= 256) {
+    if (sub == 0)
+#pragma unroll
+      for (int j = 0; j < J; j++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) sums[w][4 * (LPR * j + lr) + e] = dsum[j][e];
+    __syncthreads();
+    for (int i = t; i < E4; i += THREADS) {
+      double d = 0.0;
+#pragma unroll
+      for (int q = 0; q < WAVES; q++) d += sums[q][i];
+      total[i] = d;
+    }
+  } else {
+    // (one wave after another: a wave's lanes hold different experts)
+    for (int q = 0; q < WAVES; q++) {
+      if (w == q)
+#pragma unroll
+        for (int j = 0; j < J; j++)
+#pragma unroll
+          for (int e = 0; e < 4; e++) total[4 * (LPR * j + lr) + e] += dsum[j][e];
+      __syncthreads();
+    }
+  }
+  __syncthreads();
+  if constexpr (ONE) {
+    __shared__ int wscan[WAVES];
+    __shared__ double wred[WAVES];
+    finish<THREADS>(a, cnt, kept_all, total, wscan, wred);
+  } else {
+    for (int i = t; i < a.E; i += THREADS) {
+      parts.sums[(int64_t)blockIdx.x * parts.ld + i] = total[i];
+      parts.counts[(int64_t)blockIdx.x * parts.ld + i] = cnt[i];
+    }
+    if (t == 0) parts.kept[blockIdx.x] = kept_all;
+  }
+}
+
+// Joins the workgroups' sums: a lane adds two experts' of every slices-th workgroup (16 and 8 bytes a load: with 128
+// experts 16 of 256 workgroups, all in flight at once), then the slices meet in LDS.
+__global__ __launch_bounds__(JOIN) void k_balance_join(RouterArgs a, Parts parts, int groups) {
+  __shared__ double red[2 * JOIN];
+  __shared__ int num[2 * JOIN];
+  __shared__ double total[1024];
+  __shared__ int cnt[1024];
+  __shared__ int kept_all;
+  __shared__ int wscan[JOIN / 64];
+  __shared__ double wred[JOIN / 64];
+  const int t = threadIdx.x, pairs = (a.E + 1) / 2;
+  int cols = 1;
+  while (cols < pairs) cols *= 2;   // at most 512
+  const int slices = JOIN / cols, s = t / cols, c = t & (cols - 1);
+  double d0 = 0.0, d1 = 0.0;
+  int n0 = 0, n1 = 0;
+  if (c < pairs) {
+#pragma unroll 16
+    for (int b = s; b < groups; b += slices) {
+      const double2 d = *(const double2*)(parts.sums + (int64_t)b * parts.ld + 2 * c);
+      const int2 n = *(const int2*)(parts.counts + (int64_t)b * parts.ld + 2 * c);
+      d0 += d.x; n0 += n.x;
+      if (2 * c + 1 < a.E) { d1 += d.y; n1 += n.y; }
+    }
+  }
+  red[2 * t] = d0; red[2 * t + 1] = d1;
+  num[2 * t] = n0; num[2 * t + 1] = n1;
+  if (t < 64) {
+    int k = 0;
+    for (int b = t; b < groups; b += 64) k += parts.kept[b];
+    k = grouped::wave_inclusive_scan(k);
+    if (t == 63) kept_all = k;
+  }
+  __syncthreads();
+  for (int i = t; i < 2 * cols; i += JOIN) {
+    double d = 0.0;
+    int n = 0;
+    for (int q = 0; q < slices; q++) { d += red[2 * q * cols + i]; n += num[2 * q * cols + i]; }
+    total[i] = d;
+    cnt[i] = n;
+  }
+  __syncthreads();
+  finish<JOIN>(a, cnt, kept_all, total, wscan, wred);
+}
+
+// The gradient: one pass, each row's probabilities made again from its logits.
+template <int F, int LPR, int J>
+__global__ __launch_bounds__(256) void k_balance_grad(RouterArgs a, RouterGradArgs g) {
+  constexpr int RPW = 64 / LPR;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, lr = lane & (LPR - 1), sub = lane / LPR;
+  const int n = a.counts[a.E];
+  const float over = n > 0 ? 1.0f / ((float)a.k * (float)n) : 0.0f;
+  const float coef = n > 0 ? (g.dloss ? *g.dloss : 1.0f) * a.scale * (float)a.E / (float)n : 0.0f;
+  float f[J][4];
+#pragma unroll
+  for (int j = 0; j < J; j++)
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+      const int i = 4 * (LPR * j + lr) + e;
+      f[j][e] = i < a.E ? (float)a.counts[i] * over : 0.0f;
+    }
+  const int64_t step = (int64_t)gridDim.x * 4 * RPW;
+  for (int64_t r0 = ((int64_t)blockIdx.x * 4 + w) * RPW; r0 < a.rows; r0 += step) {
+    const int64_t row = r0 + sub;
+    const bool in = row < a.rows;
+    float v[J][4];
+#pragma unroll
+    for (int j = 0; j < J; j++) {
+      const int e0 = 4 * (LPR * j + lr);
+      load4<F>(a.logits, row * a.ldl + e0, in ? a.E - e0 : 0, a.vec, v[j]);
+    }
+    const bool keep = row_kept<LPR>(a, row, in, lr, lane, nullptr);
+    const float inv = row_softmax<LPR, J>(v);
+    float dot = 0.0f;
+#pragma unroll
+    for (int j = 0; j < J; j++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        v[j][e] *= inv;
+        dot += f[j][e] * v[j][e];
+      }
+    dot = row_sum<LPR>(dot);
+    if (!in) continue;
+#pragma unroll
+    for (int j = 0; j < J; j++) {
+      const int e0 = 4 * (LPR * j + lr), left = a.E - e0;
+      if (left <= 0) continue;
+      float o[4];
+#pragma unroll
+      for (int e = 0; e < 4; e++) o[e] = keep ? coef * v[j][e] * (f[j][e] - dot) : 0.0f;
+      const int64_t at = row * g.ldd + e0;
+      if (g.d_fmt == BSM_F32) {
+        float* p = (float*)g.D + at;
+        if (g.vec && left >= 4) {
+          f32x4 x = {o[0], o[1], o[2], o[3]};
+          if (g.accum) x += *(const f32x4*)p;
+          *(f32x4*)p = x;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+            if (e < left) p[e] = g.accum ? p[e] + o[e] : o[e];
+        }
+      } else if constexpr (F != BSM_F32) {
+        uint16_t* p = (uint16_t*)g.D + at;
+        auto bits = [](float x) { return F == BSM_BF16 ? f32_to_bf16_bits(x) : f32_to_f16_bits(x); };
+        auto val = [](uint16_t h) { return F == BSM_BF16 ? bf16_bits_to_f32(h) : f16_bits_to_f32(h); };
+        if (g.vec && left >= 4) {
+          if (g.accum) {
+            const uint2 y = *(const uint2*)p;
+            o[0] += val((uint16_t)y.x); o[1] += val((uint16_t)(y.x >> 16));
+            o[2] += val((uint16_t)y.y); o[3] += val((uint16_t)(y.y >> 16));
+          }
+          *(uint2*)p = make_uint2(bits(o[0]) | (uint32_t)bits(o[1]) << 16, bits(o[2]) | (uint32_t)bits(o[3]) << 16);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; e++)
+            if (e < left) p[e] = bits(g.accum ? val(p[e]) + o[e] : o[e]);
+        }
+      }
+    }
+  }
+}
+
+int lanes_per_row(int E) { return E <= 16 ? 4 : E <= 32 ? 8 : E <= 64 ? 16 : E <= 128 ? 32 : 64; }
+
+int64_t groups_of(int64_t rows, int E) {
+  if (rows * E <= kOneGroup) return 1;
+  const int64_t per = WAVES * (64 / lanes_per_row(E));
+  return std::min<int64_t>((rows + per - 1) / per, kMaxGroups);
+}
+
+// f with the row layout for E experts: f(LPR, J).
+template <class FN>
+void with_layout(int E, FN f) {
+  using std::integral_constant;
+  if (E <= 16) f(integral_constant<int, 4>{}, integral_constant<int, 1>{});
+  else if (E <= 32) f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+  else if (E <= 64) f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  else if (E <= 128) f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+  else if (E <= 256) f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  else if (E <= 512) f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  else f(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+}
+
+template <int F>
+void launch_balance(const RouterArgs& a, const Parts& parts, int64_t groups, hipStream_t st) {
+  with_layout(a.E, [&](auto lpr, auto j) {
+    constexpr int LPR = decltype(lpr)::value, J = decltype(j)::value;
+    if (groups == 1) hipLaunchKernelGGL((k_balance<F, LPR, J, true>), dim3(1), dim3(THREADS), 0, st, a, parts);
+    else hipLaunchKernelGGL((k_balance<F, LPR, J, false>), dim3((uint32_t)groups), dim3(THREADS), 0, st, a, parts);
+  });
+}
+
+template <int F>
+void launch_grad(const RouterArgs& a, const RouterGradArgs& g, hipStream_t st) {
+  const int64_t per = 4 * (64 / lanes_per_row(a.E));
+  const dim3 grid((uint32_t)std::min<int64_t>((a.rows + per - 1) / per, 2048));
+  with_layout(a.E, [&](auto lpr, auto j) {
+    hipLaunchKernelGGL((k_balance_grad<F, decltype(lpr)::value, decltype(j)::value>), grid, dim3(256), 0, st, a, g);
+  });
+}
+
+}  // namespace
+
+int64_t balance_workspace(int64_t rows, int E) {
+  const int64_t n = groups_of(rows, E), ld = (E + 1) / 2 * 2;
+  return n == 1 ? 0 : n * (ld * (int64_t)(sizeof(double) + sizeof(int)) + (int64_t)sizeof(int));
+}
+
+hipError_t launch_router_balance(const RouterArgs& a, void* workspace, hipStream_t st) {
+  const int64_t n = groups_of(a.rows, a.E);
+  Parts parts{};
+  if (n > 1) {
+    parts.ld = (a.E + 1) / 2 * 2;
+    parts.sums = (double*)workspace;
+    parts.counts = (int*)(parts.sums + n * parts.ld);
+    parts.kept = parts.counts + n * parts.ld;
+  }
+  if (a.l_fmt == BSM_F32) launch_balance<BSM_F32>(a, parts, n, st);
+  else if (a.l_fmt == BSM_BF16) launch_balance<BSM_BF16>(a, parts, n, st);
+  else launch_balance<BSM_F16>(a, parts, n, st);
+  if (n > 1) hipLaunchKernelGGL(k_balance_join, dim3(1), dim3(JOIN), 0, st, a, parts, (int)n);
+  return hipGetLastError();
+}
+
+hipError_t launch_router_balance_grad(const RouterArgs& a, const RouterGradArgs& g, hipStream_t st) {
+  if (a.l_fmt == BSM_F32) launch_grad<BSM_F32>(a, g, st);
+  else if (a.l_fmt == BSM_BF16) launch_grad<BSM_BF16>(a, g, st);
+  else launch_grad<BSM_F16>(a, g, st);
+  return hipGetLastError();
+}
+
+}  // namespace bsm

@@ -412,6 +412,73 @@ int bsm_gemm_lora(int64_t rows, int64_t N, int64_t K, int64_t R, int32_t n_adapt
 /* Bytes of that workspace, or a negative status for rows or R out of range. */
 int64_t bsm_gemm_lora_workspace(int64_t rows, int64_t R);
 
+/* Counts, offsets and balance loss of a router's choices, before its experts' products. With p_t the softmax of row t's
+ * logits, c_e the assignments of expert e, and n the rows kept (those with an expert among their ids):
+ *   f_e = c_e / (k n),  P_e = (sum over the rows kept of p_te) / n,  loss = scale * E * sum_e f_e P_e.
+ *   rows:      0 .. 2^31 - 1, with rows * k at most 2^31 - 1;
+ *   n_experts: E, 1 .. 1024;  k: ids a row, 1 .. 1024;
+ *   l_fmt:     BSM_F32, BSM_BF16 or BSM_F16: logits(t,e) = logits[t*ldl + e], ldl >= E, aligned to its elements
+ *              (16 bytes and ldl a multiple of 4 load fastest);
+ *   ids:       DEVICE array of rows * k int32, 4-byte aligned, the row's experts in any order; an id outside 0 .. E - 1
+ *              (say -1) is no expert, and a row of such ids (padding behind the last sequence) is left out of counts,
+ *              means and gradient, whatever its logits;
+ *   counts:    DEVICE, E + 1 int32: the experts' assignments, then n;
+ *   offsets:   DEVICE, E + 1 int32: their exclusive sums, the `offsets` of the grouped products once the rows are sorted
+ *              by expert;
+ *   loss:      DEVICE, one float32 (0 where no row is kept);
+ *   workspace: DEVICE, 16-byte aligned, bsm_router_balance_workspace(rows, n_experts) bytes (0 for few rows: may be NULL);
+ *              holds nothing from one call to the next. Calls that may run at the same time need one each.
+ * Probabilities are float32, their sums float64. A logit of -infinity has probability 0; a row kept whose logits are all
+ * -infinity has none at all (it counts among n). NaN and +infinity make the row's probabilities NaN. Every output is
+ * written, for 0 rows too. The same inputs give the same bits. The inputs must not overlap the outputs. */
+int bsm_router_balance(int64_t rows, int32_t n_experts, int32_t k, int32_t l_fmt, const void* logits, int64_t ldl,
+                       const int32_t* ids, float scale, int32_t* counts, int32_t* offsets, float* loss, void* workspace,
+                       void* stream);
+/* Bytes of that workspace, or a negative status for rows or n_experts out of range. */
+int64_t bsm_router_balance_workspace(int64_t rows, int32_t n_experts);
+
+/* The gradient of that loss in the logits (the counts are constants to it), times *dloss:
+ *   D[t,e] = (accum ? D[t,e] : 0) + dloss * scale * E / n * p_te * (f_e - sum_j f_j p_tj),  0 on rows not kept.
+ *   counts:    what bsm_router_balance wrote for the same ids;
+ *   dloss:     DEVICE, one float32, or NULL for 1;
+ *   d_fmt:     BSM_F32 or l_fmt (else BSM_E_DTYPE); D aligned to its elements, ldd >= E;
+ *   accum:     0 or 1: 1 adds to the gradient that reaches the logits through the experts' weights.
+ * rows, n_experts, k, l_fmt, logits, ldl, ids and scale as above. No input may overlap D. */
+int bsm_router_balance_grad(int64_t rows, int32_t n_experts, int32_t k, int32_t l_fmt, const void* logits, int64_t ldl,
+                            const int32_t* ids, const int32_t* counts, float scale, const float* dloss, int32_t d_fmt, void* D,
+                            int64_t ldd, int accum, void* stream);
+
+/* Activations kept in 8 bits for the backward pass: X(t,k) = X[t*ldx + k] as block-scaled codes, in the layout that the
+ * block-scaled products read (OCP MX blocks of 32 along the row):
+ *   SF[t*ld_sf + k/32] = e + 127, e the smallest integer with max |X| over the block's finite values <= max_fmt * 2^e
+ *   (448 or 57344; e at least -127), Q[t*ldq + k] = X(t,k) * 2^-e rounded to nearest even.
+ * No finite value saturates: normal codes are off by at most 2^-4 (E4M3) or 2^-3 (E5M2) of the value, smaller ones by at
+ * most 2^(e-10) or 2^(e-17). NaN is kept as NaN, an infinity as the format's (E4M3 has none: NaN), without touching the
+ * block's scale.
+ *   x_fmt:     BSM_BF16, BSM_F16 or BSM_F32; X 16-byte aligned, ldx a multiple of 8 (16-bit) or 4 (F32);
+ *   fmt:       BSM_E4M3 or BSM_E5M2; Q 16-byte aligned, ldq a multiple of 16;
+ *   SF:        4-byte aligned, ld_sf >= ceil(K/32) and a multiple of 4;
+ *   rows 0 .. 2^31 - 1, K 0 .. 2^24, any K (the last block is shorter). Bytes of Q past a row's K and of SF past its
+ *   blocks are not written; X spans whole rows (rows * ldx). X must not overlap Q or SF, nor they each other. */
+int bsm_block_scale_save(int64_t rows, int64_t K, int32_t x_fmt, const void* X, int64_t ldx, int32_t fmt, uint8_t* Q, int64_t ldq,
+                         uint8_t* SF, int64_t ld_sf, void* stream);
+
+/* The kept values back: D[t*ldd + k] = f(dec(Q[t*ldq + k]) * 2^(SF[t*ld_sf + k/32] - 127)), rounded to d_fmt (BSM_BF16,
+ * BSM_F16 or BSM_F32); in F16 a finite value beyond the format's range becomes its largest. f as for bsm_gemm_ewise (an
+ * activation made again from its kept input), or ew NULL for none. A scale code of 0xFF makes its block NaN. Q, ldq, SF
+ * and ld_sf as above (Q spans whole rows); D 16-byte aligned, ldd a multiple of 8 (16-bit) or 4 (F32). Q and SF must not
+ * overlap D. */
+int bsm_block_scale_restore(int64_t rows, int64_t K, int32_t fmt, const uint8_t* Q, int64_t ldq, const uint8_t* SF, int64_t ld_sf,
+                            int32_t d_fmt, void* D, int64_t ldd, const bsm_ewise* ew, void* stream);
+
+/* The gradient through the epilogue f whose input x was kept: D[t,k] = dY[t,k] * f'(x(t,k)), in float32, rounded to dY's
+ * format dy_fmt (BSM_BF16, BSM_F16 or BSM_F32; in F16 a finite value beyond the range becomes its largest). f'(x) = scale
+ * * s (1 + x (1 - s)), s = 1 / (1 + exp(-x)), and its limits at the infinities (BSM_EW_NONE: 1). ew is required. dY and D
+ * as X and D above; D may be dY (in place, lddy == ldd) and must not otherwise overlap an input. */
+int bsm_block_scale_ewise_grad(int64_t rows, int64_t K, int32_t fmt, const uint8_t* Q, int64_t ldq, const uint8_t* SF,
+                               int64_t ld_sf, int32_t dy_fmt, const void* dY, int64_t lddy, void* D, int64_t ldd,
+                               const bsm_ewise* ew, void* stream);
+
 /* Element-wise scalar add on float32 ([TOE] "A Load, Compute, and Store Example"
  * adds one to a (2,32,3,4) tile; [TP] "Scalar compositions"): dst[i] = src[i] + s,
  * i < n, each lane moving 16-byte vectors. src, dst 16-byte aligned; they may be

@@ -1,0 +1,123 @@
+"""CPU tests: what the calls around the products of a training step refuse, before any HIP call."""
+import pytest
+import torch
+
+import block_scaled_matrix_amd as bsm
+
+FAKE = 1 << 40          # a fake device address, never dereferenced (checks fail first)
+AT = [FAKE + (i << 36) for i in range(12)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def L():
+    import os
+    if not os.path.exists(bsm.LIB_PATH):
+        from block_scaled_matrix_amd import _build
+        _build.build()
+    return bsm.lib()
+
+
+def expect(code, fn, **changed):
+    with pytest.raises(bsm.BsmError) as e:
+        fn(**changed)
+    assert e.value.status == code, (changed, e.value.status, str(e.value))
+
+
+def balance(rows=1000, E=64, k=4, fmt="bf16", logits=AT[0], ldl=64, ids=AT[1], scale=1.0, counts=AT[2], offsets=AT[3], loss=AT[4],
+            ws=AT[5]):
+    bsm.bsm_router_balance(rows, E, k, fmt, logits, ldl, ids, scale, counts, offsets, loss, ws, 0)
+
+
+def balance_grad(rows=1000, E=64, k=4, fmt="bf16", logits=AT[0], ldl=64, ids=AT[1], counts=AT[2], scale=1.0, dloss=AT[3],
+                 d_fmt="f32", d=AT[4], ldd=64, accum=0):
+    bsm.bsm_router_balance_grad(rows, E, k, fmt, logits, ldl, ids, counts, scale, dloss, d_fmt, d, ldd, accum, 0)
+
+
+@pytest.mark.parametrize("fn", [balance, balance_grad])
+def test_router_refusals(fn):
+    for name, bad in (("BSM_E_DTYPE", dict(fmt="e4m3")), ("BSM_E_SHAPE", dict(E=0)), ("BSM_E_SHAPE", dict(E=1025, ldl=1032, ldd=1032)),
+                      ("BSM_E_SHAPE", dict(k=0)), ("BSM_E_SHAPE", dict(k=1025)), ("BSM_E_SHAPE", dict(rows=-1)),
+                      ("BSM_E_SHAPE", dict(rows=1 << 31)), ("BSM_E_SHAPE", dict(rows=1 << 30, k=4)), ("BSM_E_NULL", dict(logits=0)),
+                      ("BSM_E_NULL", dict(ids=0)), ("BSM_E_NULL", dict(counts=0)), ("BSM_E_ALIGN", dict(logits=AT[0] + 1)),
+                      ("BSM_E_ALIGN", dict(ids=AT[1] + 2)), ("BSM_E_ALIGN", dict(counts=AT[2] + 2)), ("BSM_E_ALIGN", dict(ldl=63)),
+                      ("BSM_E_SHAPE", dict(ldl=1 << 32)),
+                      ("BSM_E_ARG", dict(logits=torch.zeros(1000, 64, dtype=torch.bfloat16))),
+                      ("BSM_E_DTYPE", dict(logits=torch.zeros(1000, 64))), ("BSM_E_DTYPE", dict(ids=torch.zeros(4000, dtype=torch.int64))),
+                      ("BSM_E_SHAPE", dict(ids=torch.zeros(3999, dtype=torch.int32))),
+                      ("BSM_E_SHAPE", dict(logits=torch.zeros(999, 64, dtype=torch.bfloat16))),
+                      ("BSM_E_SHAPE", dict(counts=torch.zeros(64, dtype=torch.int32)))):
+        bad = {k: v for k, v in bad.items() if not (k == "ldd" and fn is balance)}
+        expect(name, fn, **bad)
+
+
+def test_balance_refusals():
+    for name, bad in (("BSM_E_NULL", dict(offsets=0)), ("BSM_E_NULL", dict(loss=0)), ("BSM_E_NULL", dict(ws=0)),
+                      ("BSM_E_ALIGN", dict(offsets=AT[3] + 1)), ("BSM_E_ALIGN", dict(loss=AT[4] + 2)), ("BSM_E_ALIGN", dict(ws=AT[5] + 8)),
+                      ("BSM_E_ALIAS", dict(counts=AT[3] + 256)), ("BSM_E_ALIAS", dict(loss=AT[2] + 256)),
+                      ("BSM_E_ALIAS", dict(counts=AT[0] + 64)), ("BSM_E_ALIAS", dict(ws=AT[1])), ("BSM_E_ALIAS", dict(offsets=AT[1] + 15996)),
+                      ("BSM_E_DTYPE", dict(loss=torch.zeros(1, dtype=torch.float64))),
+                      ("BSM_E_SHAPE", dict(offsets=torch.zeros(64, dtype=torch.int32))),
+                      ("BSM_E_SHAPE", dict(ws=torch.zeros(bsm.bsm_router_balance_workspace(1000, 64) - 1, dtype=torch.uint8)))):
+        expect(name, balance, **bad)
+    assert bsm.bsm_router_balance_workspace(8, 64) == 0 and bsm.bsm_router_balance_workspace(0, 1) == 0
+    for rows, E in ((-1, 4), (1 << 31, 4), (4, 0), (4, 1025)):
+        expect("BSM_E_SHAPE", bsm.bsm_router_balance_workspace, rows=rows, n_experts=E)
+
+
+def test_balance_grad_refusals():
+    for name, bad in (("BSM_E_NULL", dict(d=0)), ("BSM_E_ALIGN", dict(d=AT[4] + 2)), ("BSM_E_ALIGN", dict(dloss=AT[3] + 2)),
+                      ("BSM_E_ALIGN", dict(ldd=63)), ("BSM_E_DTYPE", dict(d_fmt="f16")), ("BSM_E_DTYPE", dict(d_fmt="u8")),
+                      ("BSM_E_ARG", dict(accum=2)), ("BSM_E_ALIAS", dict(d=AT[0] + 64)), ("BSM_E_ALIAS", dict(d=AT[2])),
+                      ("BSM_E_ALIAS", dict(d=AT[3])), ("BSM_E_ALIAS", dict(d=AT[1] + 64)),
+                      ("BSM_E_SHAPE", dict(d=torch.zeros(999, 64))), ("BSM_E_ARG", dict(d=torch.zeros(1000, 64)))):
+        expect(name, balance_grad, **bad)
+    balance_grad(rows=0, logits=0, ids=0, counts=0, d=0)
+
+
+def save(rows=100, K=100, x_fmt="bf16", x=AT[0], ldx=104, fmt="e4m3", q=AT[1], ldq=112, sf=AT[2], ld_sf=4):
+    bsm.bsm_block_scale_save(rows, K, x_fmt, x, ldx, fmt, q, ldq, sf, ld_sf, 0)
+
+
+def restore(rows=100, K=100, fmt="e4m3", q=AT[1], ldq=112, sf=AT[2], ld_sf=4, d_fmt="bf16", d=AT[3], ldd=104, ew=None):
+    bsm.bsm_block_scale_restore(rows, K, fmt, q, ldq, sf, ld_sf, d_fmt, d, ldd, ew, 0)
+
+
+def ewise_grad(rows=100, K=100, fmt="e4m3", q=AT[1], ldq=112, sf=AT[2], ld_sf=4, dy_fmt="bf16", dy=AT[0], lddy=104, d=AT[3], ldd=104,
+               ew=bsm.ewise_desc()):
+    bsm.bsm_block_scale_ewise_grad(rows, K, fmt, q, ldq, sf, ld_sf, dy_fmt, dy, lddy, d, ldd, ew, 0)
+
+
+@pytest.mark.parametrize("fn", [save, restore, ewise_grad])
+def test_kept_refusals(fn):
+    for name, bad in (("BSM_E_DTYPE", dict(fmt="e2m1")), ("BSM_E_DTYPE", dict(fmt="f16")), ("BSM_E_SHAPE", dict(rows=-1)),
+                      ("BSM_E_SHAPE", dict(rows=1 << 31)), ("BSM_E_SHAPE", dict(K=-1)), ("BSM_E_SHAPE", dict(K=(1 << 24) + 1)),
+                      ("BSM_E_NULL", dict(q=0)), ("BSM_E_NULL", dict(sf=0)), ("BSM_E_ALIGN", dict(q=AT[1] + 8)),
+                      ("BSM_E_ALIGN", dict(sf=AT[2] + 2)), ("BSM_E_ALIGN", dict(ldq=96)), ("BSM_E_ALIGN", dict(ldq=120)),
+                      ("BSM_E_ALIGN", dict(ld_sf=3)), ("BSM_E_ALIGN", dict(ld_sf=6)), ("BSM_E_ALIGN", dict(K=112, ld_sf=0)),
+                      ("BSM_E_DTYPE", dict(q=torch.zeros(100, 112))), ("BSM_E_SHAPE", dict(q=torch.zeros(99, 112, dtype=torch.uint8))),
+                      ("BSM_E_SHAPE", dict(sf=torch.zeros(99, 4, dtype=torch.uint8))),
+                      ("BSM_E_ARG", dict(q=torch.zeros(100, 112, dtype=torch.uint8)))):
+        expect(name, fn, **bad)
+    for none in (dict(rows=0), dict(K=0)):
+        fn(q=0, sf=0, **none)
+
+
+def test_save_refusals():
+    for name, bad in (("BSM_E_DTYPE", dict(x_fmt="e4m3")), ("BSM_E_NULL", dict(x=0)), ("BSM_E_ALIGN", dict(x=AT[0] + 8)),
+                      ("BSM_E_ALIGN", dict(ldx=96)), ("BSM_E_ALIGN", dict(ldx=100)), ("BSM_E_ALIGN", dict(x_fmt="f32", ldx=102)),
+                      ("BSM_E_ALIAS", dict(q=AT[0] + 16)), ("BSM_E_ALIAS", dict(sf=AT[0] + 16)), ("BSM_E_ALIAS", dict(sf=AT[1] + 16)),
+                      ("BSM_E_SHAPE", dict(x=torch.zeros(99 * 104 + 100, dtype=torch.bfloat16))),
+                      ("BSM_E_DTYPE", dict(x=torch.zeros(100, 104)))):
+        expect(name, save, **bad)
+
+
+def test_restore_and_gradient_refusals():
+    for fn, f in ((restore, "d_fmt"), (ewise_grad, "dy_fmt")):
+        for name, bad in (("BSM_E_DTYPE", {f: "u16"}), ("BSM_E_NULL", dict(d=0)), ("BSM_E_ALIGN", dict(d=AT[3] + 8)),
+                          ("BSM_E_ALIGN", dict(ldd=96)), ("BSM_E_ALIGN", dict(ldd=100)), ("BSM_E_ALIAS", dict(d=AT[1] + 16)),
+                          ("BSM_E_ALIAS", dict(d=AT[2] + 16)), ("BSM_E_ARG", dict(ew=bsm.ewise_desc(7))),
+                          ("BSM_E_SHAPE", dict(d=torch.zeros(99, 104, dtype=torch.bfloat16)))):
+            expect(name, fn, **bad)
+    for name, bad in (("BSM_E_NULL", dict(dy=0)), ("BSM_E_ALIGN", dict(lddy=100)), ("BSM_E_ALIAS", dict(dy=AT[3] + 16)),
+                      ("BSM_E_ALIAS", dict(dy=AT[3], lddy=112)), ("BSM_E_NULL", dict(ew=None))):
+        expect(name, ewise_grad, **bad)

@@ -27,7 +27,8 @@ EXPORTS = ("bsm_image_stride", "bsm_tile_box_load", "bsm_tile_box_store", "bsm_t
            "bsm_gemm_block_scale_fastacc", "bsm_gemm_grouped", "bsm_gemm_grouped_wgrad",
            "bsm_gemm_grouped_block_scale", "bsm_gemm_lora", "bsm_gemm_lora_workspace", "bsm_router_balance",
            "bsm_router_balance_workspace", "bsm_router_balance_grad", "bsm_block_scale_save", "bsm_block_scale_restore",
-           "bsm_block_scale_ewise_grad",
+           "bsm_block_scale_ewise_grad", "bsm_gemm_cross_entropy", "bsm_gemm_cross_entropy_workspace",
+           "bsm_gemm_cross_entropy_grad", "bsm_gemm_cross_entropy_grad_workspace",
            "bsm_debug_grouped_route", "bsm_debug_stream_mix_bf16", "bsm_debug_mfma_loop", "bsm_tile_add_scalar_f32", "bsm_debug_fragments", "bsm_debug_fragment_shape", "bsm_last_error")
 
 
@@ -100,6 +101,12 @@ def lib():
         L.bsm_block_scale_save.argtypes = [I64, I64, I32, P, I64, I32, P, I64, P, I64, P]
         L.bsm_block_scale_restore.argtypes = [I64, I64, I32, P, I64, P, I64, I32, P, I64, C.POINTER(bsm_ewise), P]
         L.bsm_block_scale_ewise_grad.argtypes = [I64, I64, I32, P, I64, P, I64, I32, P, I64, P, I64, C.POINTER(bsm_ewise), P]
+        L.bsm_gemm_cross_entropy_workspace.restype = L.bsm_gemm_cross_entropy_grad_workspace.restype = I64
+        L.bsm_gemm_cross_entropy_workspace.argtypes = [I64, I64]
+        L.bsm_gemm_cross_entropy_grad_workspace.argtypes = [I64, I64, I64, I64]
+        L.bsm_gemm_cross_entropy.argtypes = [I64, I64, I64, I32, P, I64, P, I64, P, P, P, P, P]
+        L.bsm_gemm_cross_entropy_grad.argtypes = [I64, I64, I64, I32, P, I64, P, I64, P, P, P, I64, P, I32, P, I64, I32, P, I64,
+                                                  C.c_int, P]
         L.bsm_tile_add_scalar_f32.argtypes = [P, P, I64, C.c_float, P]
         L.bsm_debug_stream_mix_bf16.argtypes = [P, P, P, I64, P]
         L.bsm_debug_grouped_route.restype = C.c_char_p
@@ -114,7 +121,8 @@ def lib():
                       "bsm_gemm_block_scale", "bsm_gemm_ewise", "bsm_gemm_block_scale_ewise",
                       "bsm_gemm_block_scale_major", "bsm_gemm_block_scale_fastacc", "bsm_gemm_grouped",
                       "bsm_gemm_grouped_wgrad", "bsm_gemm_grouped_block_scale", "bsm_gemm_lora", "bsm_router_balance", "bsm_router_balance_grad",
-                      "bsm_block_scale_save", "bsm_block_scale_restore", "bsm_block_scale_ewise_grad", "bsm_tile_add_scalar_f32",
+                      "bsm_block_scale_save", "bsm_block_scale_restore", "bsm_block_scale_ewise_grad",
+                      "bsm_gemm_cross_entropy", "bsm_gemm_cross_entropy_grad", "bsm_tile_add_scalar_f32",
                       "bsm_debug_fragments", "bsm_debug_stream_mix_bf16", "bsm_debug_mfma_loop"):
             getattr(L, rc_fn).restype = C.c_int
         _lib = L
@@ -461,6 +469,44 @@ def bsm_block_scale_ewise_grad(rows, K, fmt: str, Q, ldq, SF, ld_sf, dy_fmt: str
     s = _here(stream, Q, SF, dY, D)
     _check(lib().bsm_block_scale_ewise_grad(rows, K, DTYPE[fmt], q, ldq, f, ld_sf, DTYPE[dy_fmt], y, lddy, d, ldd,
                                             C.byref(ew) if ew is not None else None, s))
+
+
+def bsm_gemm_cross_entropy_workspace(rows, N) -> int:
+    return _check(lib().bsm_gemm_cross_entropy_workspace(rows, N))
+
+
+def bsm_gemm_cross_entropy_grad_workspace(rows, N, K, piece=0) -> int:
+    return _check(lib().bsm_gemm_cross_entropy_grad_workspace(rows, N, K, piece))
+
+
+def _operand_fmt(ab: str):
+    if ab not in ("bf16", "f16"):
+        raise BsmError(-8, f"ab = {ab} is neither bf16 nor f16")
+
+
+def bsm_gemm_cross_entropy(rows, N, K, ab: str, X, ldx, W, ldw, labels, loss, lse, workspace, stream=None):
+    _operand_fmt(ab)
+    x, v = _rows(X, ab, "X", rows, K, ldx, 8), _rows(W, ab, "W", N if rows > 0 else 0, K, ldw, 8)
+    i = _array(labels, "int32", "labels", rows)
+    f, g = _array(loss, "float32", "loss", rows), _array(lse, "float32", "lse", rows)
+    work = _workspace(workspace, lib().bsm_gemm_cross_entropy_workspace(rows, N))
+    s = _here(stream, X, W, labels, loss, lse, workspace)
+    _check(lib().bsm_gemm_cross_entropy(rows, N, K, DTYPE[ab], x, ldx, v, ldw, i, f, g, work, s))
+
+
+def bsm_gemm_cross_entropy_grad(rows, N, K, ab: str, X, ldx, W, ldw, labels, lse, dloss, piece, workspace, dx_fmt: str, dX, lddx,
+                                dw_fmt: str, dW, lddw, accum=0, stream=None):
+    _operand_fmt(ab)
+    _float_fmt(dx_fmt, "dx_fmt")
+    _float_fmt(dw_fmt, "dw_fmt")
+    x, v = _rows(X, ab, "X", rows, K, ldx, 8), _rows(W, ab, "W", N if rows > 0 else 0, K, ldw, 8)
+    i = _array(labels, "int32", "labels", rows)
+    f, g = _array(lse, "float32", "lse", rows), _array(dloss, "float32", "dloss", rows)
+    dx, dw = _rows(dX, dx_fmt, "dX", rows, K, lddx), _rows(dW, dw_fmt, "dW", N, K, lddw)
+    work = _workspace(workspace, lib().bsm_gemm_cross_entropy_grad_workspace(rows, N, K, piece) if rows > 0 and K > 0 else 0)
+    s = _here(stream, X, W, labels, lse, dloss, dX, dW, workspace)
+    _check(lib().bsm_gemm_cross_entropy_grad(rows, N, K, DTYPE[ab], x, ldx, v, ldw, i, f, g, piece, work, DTYPE[dx_fmt], dx, lddx,
+                                             DTYPE[dw_fmt], dw, lddw, accum, s))
 
 
 def bsm_tile_add_scalar_f32(src, dst, n: int, s: float, stream=None):

@@ -10,6 +10,7 @@
 #include "bsm_internal.hpp"
 #include "kept.hpp"
 #include "router.hpp"
+#include "xent.hpp"
 
 namespace {
 
@@ -925,6 +926,122 @@ int bsm_block_scale_ewise_grad(int64_t rows, int64_t K, int32_t fmt, const uint8
   a.ew_op = ew->op; a.ew_scale = ew->scale; a.ew_bias = ew->bias;
   hipError_t e = bsm::launch_block_scale_ewise_grad(a, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "bsm_block_scale_ewise_grad");
+  return ok();
+}
+
+// Sizes and operands that the loss and its gradient share. No launch has more than 2^31 - 1 workgroups of the smallest
+// tile (16 columns a row tile of 128), which these sizes keep.
+static int check_xent_sizes(int64_t rows, int64_t N, int64_t K) {
+  if (rows < 0 || N < 1 || K < 0 || rows > 0x7FFFFFFF || N > 0x7FFFFFFF || K > (int64_t(1) << 22))
+    return fail(BSM_E_SHAPE, "rows, N, K = %lld, %lld, %lld out of range", (long long)rows, (long long)N, (long long)K);
+  if (((rows + 63) / 64) * ((N + 63) / 64) > 0x7FFFFFFF || (rows + 63) / 64 * ((K + 63) / 64) > 0x7FFFFFFF)
+    return fail(BSM_E_SHAPE, "rows, N, K = %lld, %lld, %lld: too many tiles for a launch", (long long)rows, (long long)N, (long long)K);
+  return BSM_OK;
+}
+
+static int check_xent(int64_t rows, int64_t N, int64_t K, int32_t ab, const void* X, int64_t ldx, const void* W, int64_t ldw,
+                      const int32_t* labels, const float* lse, bsm::XentArgs* a) {
+  if (K > 0 && (ldx > (int64_t(1) << 22) || ldw > (int64_t(1) << 22)))
+    return fail(BSM_E_SHAPE, "ldx, ldw must be at most 2^22 elements (32-bit in-tile offsets)");
+  if (rows > 0) {
+    if (!labels || !lse) return fail(BSM_E_NULL, "labels or lse is NULL");
+    if ((uintptr_t)labels % 4 || (uintptr_t)lse % 4) return fail(BSM_E_ALIGN, "labels and lse must be 4-byte aligned");
+    if (K > 0) {
+      if (!X || !W) return fail(BSM_E_NULL, "X or W is NULL");
+      if ((uintptr_t)X % 16 || (uintptr_t)W % 16) return fail(BSM_E_ALIGN, "X and W must be 16-byte aligned");
+      if (ldx < K || ldx % 8) return fail(BSM_E_ALIGN, "ldx = %lld must be >= K and a multiple of 8", (long long)ldx);
+      if (ldw < K || ldw % 8) return fail(BSM_E_ALIGN, "ldw = %lld must be >= K and a multiple of 8", (long long)ldw);
+    }
+  }
+  a->rows = rows; a->N = N; a->K = K; a->dtype = ab;
+  a->X = X; a->ldx = ldx; a->W = W; a->ldw = ldw; a->labels = labels;
+  return BSM_OK;
+}
+
+int64_t bsm_gemm_cross_entropy_workspace(int64_t rows, int64_t N) {
+  int rc;
+  if ((rc = check_xent_sizes(rows, N, 0))) return rc;
+  ok();
+  return bsm::xent_workspace(rows, N);
+}
+
+int bsm_gemm_cross_entropy(int64_t rows, int64_t N, int64_t K, int32_t ab, const void* X, int64_t ldx, const void* W, int64_t ldw,
+                           const int32_t* labels, float* loss, float* lse, void* workspace, void* stream) {
+  int rc;
+  if (ab != BSM_F16 && ab != BSM_BF16) return fail(BSM_E_DTYPE, "ab = %d: bsm_gemm_cross_entropy takes F16 or BF16", ab);
+  if ((rc = check_xent_sizes(rows, N, K))) return rc;
+  bsm::XentArgs a{};
+  if ((rc = check_xent(rows, N, K, ab, X, ldx, W, ldw, labels, lse, &a))) return rc;
+  if (rows == 0) return ok();
+  if (!loss || !workspace) return fail(BSM_E_NULL, "loss or workspace is NULL");
+  if ((uintptr_t)loss % 4) return fail(BSM_E_ALIGN, "loss not 4-byte aligned");
+  if ((uintptr_t)workspace % 16) return fail(BSM_E_ALIGN, "workspace not 16-byte aligned");
+  const Range out[] = {block_range(loss, 1, 0, 1, 0, rows, 32), block_range(lse, 1, 0, 1, 0, rows, 32),
+                       Range{(uintptr_t)workspace, (uintptr_t)workspace + (uintptr_t)bsm::xent_workspace(rows, N)}};
+  for (int i = 0; i < 3; i++) {
+    if (overlap(out[i], block_range(labels, 1, 0, 1, 0, rows, 32)) ||
+        (K > 0 && (overlap(out[i], block_range(X, 1, 0, rows, ldx, K, 16)) || overlap(out[i], block_range(W, 1, 0, N, ldw, K, 16)))))
+      return fail(BSM_E_ALIAS, "an input overlaps loss, lse or the workspace");
+    for (int j = 0; j < i; j++)
+      if (overlap(out[i], out[j])) return fail(BSM_E_ALIAS, "loss, lse and workspace overlap");
+  }
+  a.loss = loss; a.lse = lse;
+  hipError_t e = bsm::launch_xent(a, workspace, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "bsm_gemm_cross_entropy");
+  return ok();
+}
+
+int64_t bsm_gemm_cross_entropy_grad_workspace(int64_t rows, int64_t N, int64_t K, int64_t piece) {
+  int rc;
+  if ((rc = check_xent_sizes(rows, N, K))) return rc;
+  if (piece < 0 || piece > 0x7FFFFFFF) return fail(BSM_E_SHAPE, "piece = %lld out of range", (long long)piece);
+  ok();
+  return bsm::xent_grad_workspace(rows, N, K, piece);
+}
+
+int bsm_gemm_cross_entropy_grad(int64_t rows, int64_t N, int64_t K, int32_t ab, const void* X, int64_t ldx, const void* W,
+                                int64_t ldw, const int32_t* labels, const float* lse, const float* dloss, int64_t piece,
+                                void* workspace, int32_t dx_fmt, void* dX, int64_t lddx, int32_t dw_fmt, void* dW, int64_t lddw,
+                                int accum, void* stream) {
+  int rc;
+  if ((rc = check_flag(accum, "accum"))) return rc;
+  if (ab != BSM_F16 && ab != BSM_BF16) return fail(BSM_E_DTYPE, "ab = %d: bsm_gemm_cross_entropy_grad takes F16 or BF16", ab);
+  if (dX && dx_fmt != BSM_F32 && dx_fmt != ab) return fail(BSM_E_DTYPE, "dx_fmt = %d is neither F32 nor the operands' format", dx_fmt);
+  if (dW && dw_fmt != BSM_F32 && dw_fmt != ab) return fail(BSM_E_DTYPE, "dw_fmt = %d is neither F32 nor the operands' format", dw_fmt);
+  const int64_t wsb = bsm_gemm_cross_entropy_grad_workspace(rows, N, K, piece);
+  if (wsb < 0) return (int)wsb;
+  bsm::XentArgs a{};
+  if ((rc = check_xent(rows, N, K, ab, X, ldx, W, ldw, labels, lse, &a))) return rc;
+  if (K == 0 || (!dX && !dW) || (rows == 0 && !dW)) return ok();
+  if (rows > 0) {
+    if (!dloss || !workspace) return fail(BSM_E_NULL, "dloss or workspace is NULL");
+    if ((uintptr_t)dloss % 4) return fail(BSM_E_ALIGN, "dloss not 4-byte aligned");
+    if ((uintptr_t)workspace % 16) return fail(BSM_E_ALIGN, "workspace not 16-byte aligned");
+    if (dX && (rc = check_out(dX, K, lddx, dx_fmt))) return rc;
+  }
+  if (dW && (rc = check_out(dW, K, lddw, dw_fmt))) return rc;
+  Range out[3];
+  int n = 0;
+  if (dW) out[n++] = block_range(dW, 1, 0, N, lddw, K, dw_fmt == BSM_F32 ? 32 : 16);
+  if (rows > 0) {
+    if (dX) out[n++] = block_range(dX, 1, 0, rows, lddx, K, dx_fmt == BSM_F32 ? 32 : 16);
+    out[n++] = Range{(uintptr_t)workspace, (uintptr_t)workspace + (uintptr_t)wsb};
+    const Range in[] = {block_range(X, 1, 0, rows, ldx, K, 16), block_range(W, 1, 0, N, ldw, K, 16), block_range(labels, 1, 0, 1, 0, rows, 32),
+                        block_range(lse, 1, 0, 1, 0, rows, 32), block_range(dloss, 1, 0, 1, 0, rows, 32)};
+    for (int i = 0; i < n; i++) {
+      for (const Range& r : in)
+        if (overlap(out[i], r)) return fail(BSM_E_ALIAS, "an input overlaps an output or the workspace");
+      for (int j = 0; j < i; j++)
+        if (overlap(out[i], out[j])) return fail(BSM_E_ALIAS, "dX, dW and workspace overlap");
+    }
+  }
+  a.lse = const_cast<float*>(lse);
+  bsm::XentGradArgs g{};
+  g.dloss = dloss; g.piece = piece;
+  g.dX = rows > 0 ? dX : nullptr; g.lddx = lddx; g.dx_fmt = dx_fmt;
+  g.dW = dW; g.lddw = lddw; g.dw_fmt = dw_fmt; g.accum = accum;
+  hipError_t e = bsm::launch_xent_grad(a, g, workspace, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "bsm_gemm_cross_entropy_grad");
   return ok();
 }
 

@@ -1,0 +1,363 @@
+// k_gemm_xent.hip - softmax cross entropy of a projection onto a large vocabulary, without keeping the logits.
+//
+//   z = X W^T (rows x N),  lse_t = log sum_v exp z_tv,  loss_t = lse_t - z_t,label
+//   G_tv = (exp(z_tv - lse_t) - [v = label_t]) dloss_t,  dX = G W,  dW = G^T X
+//
+// Loss: the GEMM tiles' accumulators hold the logits; each wave reduces its block to a pair per row (xent.hpp) and the
+// logits end there: rows x N / 64 pairs leave the chip instead of rows x N logits. A second launch joins a row's
+// pairs in a fixed order.
+// Gradient: the vocabulary is cut into pieces. A piece's logits are made again (2 rows N K operations more than an
+// implementation that had kept them; the alternative, float32 logits of a batch, is 1 GB for 8190 x 32001), become G
+// in the accumulators and leave as 16-bit values, which two products then read: dX += G W_piece and dW_piece = G^T X.
+// G is rounded to the operands' format because the matrix unit takes it so: half a step (2^-8 in bf16, 2^-11 in f16) of
+// each term, independent from term to term. In f16 the weights are brought to 2^15 at most by a power of two found
+// on the device, so a probability keeps all its bits down to 2^-29 of the largest weight, and the products' sums are
+// scaled back in float32.
+// Tiles: gemm_dense_tile.hpp (256 x 256) where they fill the chip, gemm_mid_tile.hpp (32 / 64 / 128 x 128) otherwise, and
+// for the loss of few rows skinny.hpp. dX with few tiles is cut along the vocabulary into parts that are summed in a
+// fixed order.
+#include <algorithm>
+#include "gemm_dense_tile.hpp"
+#include "gemm_mid_tile.hpp"
+#include "skinny.hpp"
+#include "store16.hpp"
+#include "xent.hpp"
+
+namespace bsm {
+namespace {
+
+using namespace dense;
+
+// A wave's 128 x 128 block of the 256 x 256 tile, stored in d_fmt.
+template <int DT>
+__device__ __forceinline__ void store_out(const GemmArgs& a, int64_t row0, int64_t col0, int lane, const f32x4 (&acc)[8][8],
+                                          uint8_t* region) {
+  if (a.d_fmt == BSM_F32) store_tile16(a.D, a.ldd, a.M, a.N, row0, col0, lane, 1.0f, acc, region, a.accum, 0, 0.0f, 0.0f);
+  else gemm::store_tile16_bits<DT>((uint16_t*)a.D, a.ldd, a.M, a.N, row0, col0, lane, acc, region, a.accum, 0, 0.0f, 0.0f);
+}
+
+// One 256 x 256 tile: the product, what EP makes of the sums, and their store unless EP stored them.
+template <int DT, bool AK, bool BKM, class EP>
+__global__ __launch_bounds__(256, 1) void k_xent_large(GemmArgs a, EP ep, int tiles_m, int tiles_n) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * STAGE_BYTES];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int tm, tn;
+  gemm::tile_coords(blockIdx.x, tiles_m, tiles_n, tm, tn);
+  f32x4 acc[8][8];
+  tile_product<DT, AK, BKM>(a, tm, tn, lds, lane, w, acc);
+  const int64_t row0 = (int64_t)tm * BM + 128 * (w >> 1), col0 = (int64_t)tn * BN + 128 * (w & 1);
+  ep(row0, col0, acc);
+  if constexpr (!EP::kStores) store_out<DT>(a, row0, col0, lane, acc, lds + 32768 * w);
+}
+
+// Tiles of BM x 128 (K-major A: of as few rows as hold the last ones), `parts` of the product's K side by side: part p takes
+// K elements p * per .. and writes its own sums, stride_d elements behind part p - 1's.
+struct Parts { int n; int64_t per, stride_d; };
+template <int DT, bool AK, bool BKM, class EP, int BM = 128, int BK = 64, int PER_CU = 2, int Q = 1>
+__global__ __launch_bounds__(256 * Q, PER_CU * Q) void k_xent_mid(GemmArgs a, EP ep, int tiles_m, int tiles_n, Parts parts) {
+  constexpr int LDS = 160 * 1024 / PER_CU / Q;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Q * LDS];
+  const int lane = threadIdx.x & 63, wq = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wq & 3, q = wq >> 2;
+  int tm, tn, pid = blockIdx.x;
+  if (parts.n > 1) {
+    const int tiles = tiles_m * tiles_n, p = pid / tiles;
+    pid -= p * tiles;
+    const int64_t k0 = p * parts.per;
+    a.A = (const uint16_t*)a.A + (AK ? k0 : k0 * a.lda);
+    a.B = (const uint16_t*)a.B + (BKM ? k0 : k0 * a.ldb);
+    a.K = min(parts.per, a.K - k0);
+    a.D += p * parts.stride_d;
+  }
+  gemm::tile_coords(pid, tiles_m, tiles_n, tm, tn);
+  const int64_t m0 = BM * (int64_t)tm, n0 = mid::BN * (int64_t)tn;
+  uint8_t* mine = lds + q * LDS;
+  if constexpr (AK && BM == 128) {
+    const int64_t left = a.M - m0;
+    if (left <= 32) return mid::tile<DT, 32, AK, BKM, BK, EP, LDS, Q>(a, m0, n0, mine, lane, w, ep, q);
+    if (left <= 64) return mid::tile<DT, 64, AK, BKM, BK, EP, LDS, Q>(a, m0, n0, mine, lane, w, ep, q);
+  }
+  mid::tile<DT, BM, AK, BKM, BK, EP, LDS, Q>(a, m0, n0, mine, lane, w, ep, q);
+}
+
+// The loss of up to 64 rows: 16 columns a workgroup, its eight waves splitting K (skinny.hpp).
+template <int DT, int MT>
+__global__ __launch_bounds__(skinny::THREADS, MT == 1 ? 4 : 2) void k_xent_skinny(GemmArgs a, xent::Stats ep) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[skinny::lds_bytes<MT>()];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t n0 = skinny::BN * (int64_t)blockIdx.x;
+  f32x4 acc[MT];
+  skinny::product<DT, MT>(a, 0, n0, lane, w, lds + w * (1 + MT) * 2048, acc, []() {});
+  skinny::join<MT>(lds, lane, w, acc);
+  if (w < MT) {
+    f32x4 one[1][1] = {{acc[0]}};
+    ep(16 * w, n0, one);
+  }
+}
+
+// A row's pairs (b, s) joined: lse = log sum s 2^b. 16 rows a workgroup, 64 lanes a row, each every 64th slot; then the
+// lanes meet in a fixed order. Everything is relative to exponents of base 2^(1/log2 e as float), so the last step, in
+// double, divides by that float.
+__global__ __launch_bounds__(1024) void k_xent_join(XentArgs a, const float2* part, const float* at, int slots) {
+  __shared__ float2 meet[16][16];
+  const int t = threadIdx.x, r = t & 15, q = t >> 4;
+  const int64_t row = 16 * (int64_t)blockIdx.x + r;
+  float m = -INFINITY, s = 0.0f;
+  auto add = [&](float b, float v) {
+    const float top = fmaxf(m, b);
+    const float z = top == -INFINITY ? 0.0f : top;   // (nothing but -infinity so far; NaN comes with its s)
+    s = s * __builtin_amdgcn_exp2f(m - z) + v * __builtin_amdgcn_exp2f(b - z);
+    m = top;
+  };
+  if (row < a.rows) {
+#pragma unroll 4
+    for (int i = q; i < slots; i += 64) {
+      const float2 p = part[i * a.rows + row];
+      add(p.x, p.y);
+    }
+  }
+#pragma unroll
+  for (int d = 16; d < 64; d *= 2) {
+    const float b = __shfl_xor(m, d), v = __shfl_xor(s, d);
+    add(b, v);
+  }
+  if ((t & 63) < 16) meet[t >> 6][r] = make_float2(m, s);
+  __syncthreads();
+  if (t < 16 && row < a.rows) {
+    m = -INFINITY;
+    s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 16; w++) add(meet[w][r].x, meet[w][r].y);
+    const double lse = ((double)m + (double)__builtin_amdgcn_logf(s)) / (double)xent::kLog2e;
+    const int64_t lab = a.labels[row];
+    a.lse[row] = (float)lse;
+    a.loss[row] = lab >= 0 && lab < a.N ? (float)(lse - (double)at[row]) : 0.0f;
+  }
+}
+
+// f16: by[0] = 2^15 / s on the weights before they are rounded, by[1] = s / 2^15 on the sums, s the smallest power of two
+// that no finite weight of a row with a label exceeds.
+__global__ __launch_bounds__(1024) void k_xent_range(XentArgs a, const float* dloss, float* by) {
+  __shared__ float meet[16];
+  float top = 0.0f;
+  for (int64_t i = threadIdx.x; i < a.rows; i += 1024) {
+    const float d = __builtin_fabsf(dloss[i]);
+    const int32_t lab = a.labels[i];
+    if (lab >= 0 && lab < a.N && d < INFINITY) top = fmaxf(top, d);
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+  if ((threadIdx.x & 63) == 0) meet[threadIdx.x >> 6] = top;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 16; w++) top = fmaxf(top, meet[w]);
+    const uint32_t bits = __float_as_uint(top);
+    // exponent of s: top <= 2^e; kept where 2^15 / s and s / 2^15 are normal
+    int e = (int)(bits >> 23) - 127 + ((bits & 0x7FFFFFu) ? 1 : 0);
+    e = top == 0.0f ? 0 : max(e, -110);
+    by[0] = __uint_as_float((uint32_t)(127 + 15 - e) << 23);
+    by[1] = __uint_as_float((uint32_t)(127 - 15 + e) << 23);
+  }
+}
+
+// dX from its float32 parts, summed in their order: four columns a lane.
+template <int OUT>
+__global__ __launch_bounds__(256) void k_xent_sum(const float* F, int parts, int64_t stride, int64_t ldf, int64_t rows, int64_t K,
+                                                  void* D, int64_t ldd) {
+  const int64_t per = (K + 3) / 4, i = blockIdx.x * (int64_t)256 + threadIdx.x;
+  if (i >= rows * per) return;
+  const int64_t row = i / per, col = 4 * (i - row * per);
+  f32x4 v = *(const f32x4*)(F + row * ldf + col);
+  for (int p = 1; p < parts; p++) v += *(const f32x4*)(F + p * stride + row * ldf + col);
+#pragma unroll
+  for (int e = 0; e < 4; e++)
+    if (col + e < K) {
+      if constexpr (OUT == BSM_F32) ((float*)D)[row * ldd + col + e] = v[e];
+      else ((uint16_t*)D)[row * ldd + col + e] = gemm::to_bits16<OUT>(v[e]);
+    }
+}
+
+// Share of the chip's time that the product's own operations take, with tm x tn tiles of `area` elements, `slots` of them
+// at a time.
+double filled(int64_t M, int64_t N, int64_t tm, int64_t tn, int64_t area, int64_t slots) {
+  const int64_t rounds = (tm * tn + slots - 1) / slots;
+  return (double)M * N / ((double)rounds * slots * area);
+}
+
+enum Tile { SKINNY, SPLIT, MID, LARGE };
+
+Tile tile_for(int64_t M, int64_t N) {
+  const int64_t m128 = (M + 127) / 128, n128 = (N + 127) / 128, m256 = (M + 255) / 256, n256 = (N + 255) / 256;
+  if (M <= 64 && n128 < 128) return SKINNY;
+  if (m128 * n128 < 192) return SPLIT;
+  return filled(M, N, m256, n256, 65536, 256) >= 0.85 * filled(M, N, m128, n128, 16384, 512) ? LARGE : MID;
+}
+
+int slot_width(Tile t) { return t == SKINNY ? 16 : t == LARGE ? 128 : 64; }
+int64_t slots_of(int64_t rows, int64_t N) {
+  const int w = slot_width(tile_for(rows, N));
+  return (N + w - 1) / w;
+}
+
+// z = X W_piece^T for `cols` columns from `first` on, into EP.
+template <int DT, class EP>
+void launch_logits(const GemmArgs& g, Tile tile, const EP& ep, hipStream_t st) {
+  const int64_t t = tile == LARGE ? 256 : 128, tm = (g.M + t - 1) / t, tn = (g.N + t - 1) / t;
+  const dim3 grid((uint32_t)(tm * tn));
+  const Parts one{1, 0, 0};
+  if (tile == LARGE) hipLaunchKernelGGL((k_xent_large<DT, true, true, EP>), grid, dim3(256), 0, st, g, ep, (int)tm, (int)tn);
+  else if (tile == MID) hipLaunchKernelGGL((k_xent_mid<DT, true, true, EP>), grid, dim3(256), 0, st, g, ep, (int)tm, (int)tn, one);
+  else {
+    const int64_t m64 = (g.M + 63) / 64;
+    hipLaunchKernelGGL((k_xent_mid<DT, true, true, EP, 64, 64, 1, 2>), dim3((uint32_t)(m64 * tn)), dim3(512), 0, st, g, ep, (int)m64,
+                       (int)tn, one);
+  }
+}
+
+GemmArgs logits_of(const XentArgs& a) {
+  GemmArgs g{};
+  g.M = a.rows; g.N = a.N; g.K = a.K; g.dtype = a.dtype;
+  g.A = a.X; g.lda = a.ldx; g.B = a.W; g.ldb = a.ldw;
+  return g;
+}
+
+template <int DT>
+hipError_t launch_loss(const XentArgs& a, float2* part, float* at, hipStream_t st) {
+  const Tile tile = tile_for(a.rows, a.N);
+  const GemmArgs g = logits_of(a);
+  const xent::Stats ep{a.labels, part, at, a.rows, a.N, slot_width(tile)};
+  if (tile == SKINNY) {
+    const dim3 grid((uint32_t)((a.N + skinny::BN - 1) / skinny::BN));
+    if (a.rows <= 16) hipLaunchKernelGGL((k_xent_skinny<DT, 1>), grid, dim3(skinny::THREADS), 0, st, g, ep);
+    else if (a.rows <= 32) hipLaunchKernelGGL((k_xent_skinny<DT, 2>), grid, dim3(skinny::THREADS), 0, st, g, ep);
+    else hipLaunchKernelGGL((k_xent_skinny<DT, 4>), grid, dim3(skinny::THREADS), 0, st, g, ep);
+  } else {
+    launch_logits<DT>(g, tile, ep, st);
+  }
+  hipLaunchKernelGGL(k_xent_join, dim3((uint32_t)((a.rows + 15) / 16)), dim3(1024), 0, st, a, part, at, (int)slots_of(a.rows, a.N));
+  return hipGetLastError();
+}
+
+// How a gradient is made: `piece` columns at a time, dX in `parts` parts (each of a piece's columns).
+struct Plan {
+  int64_t piece, pieces, ldg, ldf;
+  int parts;
+  int64_t per;      // columns of a part
+  bool sums;        // dX through float32 sums in the workspace
+  int64_t g_bytes, f_bytes, bytes;
+};
+
+// One piece takes what 1 GiB of G holds: more pieces cost dX its sums' way through memory once a piece.
+constexpr int64_t kPieceBytes = int64_t(1) << 30;
+
+Plan plan_of(int64_t rows, int64_t N, int64_t K, int64_t piece) {
+  Plan p{};
+  if (piece <= 0) piece = std::max<int64_t>(kPieceBytes / (2 * std::max<int64_t>(rows, 1)), 4096);
+  piece = std::min(piece, int64_t(1) << 21);   // (G's rows: 32-bit offsets in a tile)
+  p.pieces = (N + piece - 1) / piece;
+  const int64_t even = (N + p.pieces - 1) / p.pieces;            // pieces of one length
+  p.piece = std::min<int64_t>((even + 255) / 256 * 256, N);
+  p.pieces = (N + p.piece - 1) / p.piece;
+  p.ldg = (p.piece + 63) / 64 * 64;
+  const int64_t tiles = ((rows + 127) / 128) * ((K + 127) / 128);
+  p.parts = (int)std::max<int64_t>(1, std::min<int64_t>(512 / std::max<int64_t>(tiles, 1), p.piece / 512));
+  p.per = ((p.piece + p.parts - 1) / p.parts + 63) / 64 * 64;
+  p.parts = (int)((p.piece + p.per - 1) / p.per);
+  p.sums = p.parts > 1 || p.pieces > 1;
+  p.ldf = (K + 3) / 4 * 4;
+  p.g_bytes = (rows * p.ldg * 2 + 255) / 256 * 256;
+  p.f_bytes = p.sums ? (p.parts * rows * p.ldf * 4 + 255) / 256 * 256 : 0;
+  p.bytes = 256 + p.g_bytes + p.f_bytes;
+  return p;
+}
+
+template <int DT>
+hipError_t launch_grad(const XentArgs& a, const XentGradArgs& g, const Plan& p, uint8_t* workspace, hipStream_t st) {
+  float* by = (float*)workspace;
+  uint16_t* G = (uint16_t*)(workspace + 256);
+  float* F = (float*)(workspace + 256 + p.g_bytes);
+  const float* up = nullptr;
+  const float* down = nullptr;
+  if (DT == BSM_F16 && a.rows > 0) {
+    hipLaunchKernelGGL(k_xent_range, dim3(1), dim3(1024), 0, st, a, g.dloss, by);
+    up = by;
+    down = by + 1;
+  }
+  const Parts one{1, 0, 0};
+  const bool direct = !p.sums || (p.parts == 1 && g.dx_fmt == BSM_F32);
+  for (int64_t c0 = 0, at = 0; c0 < a.N; c0 += p.piece, at++) {
+    const int64_t cols = std::min(p.piece, a.N - c0);
+    const uint16_t* W = (const uint16_t*)a.W + c0 * a.ldw;
+    if (a.rows > 0) {
+      GemmArgs z = logits_of(a);
+      z.N = cols; z.B = W;
+      z.D = (float*)G; z.ldd = p.ldg; z.d_fmt = DT;
+      Tile tile = tile_for(a.rows, cols);
+      if (tile == SKINNY) tile = SPLIT;
+      launch_logits<DT>(z, tile, xent::Grad{a.labels, a.lse, g.dloss, up, a.rows, a.N, c0}, st);
+    }
+    if (g.dX && a.rows > 0) {
+      GemmArgs x{};
+      x.M = a.rows; x.N = a.K; x.K = cols; x.dtype = DT;
+      x.A = G; x.lda = p.ldg; x.B = W; x.ldb = a.ldw;
+      x.accum = at > 0;
+      if (direct) { x.D = (float*)g.dX; x.ldd = g.lddx; x.d_fmt = g.dx_fmt; }
+      else { x.D = F; x.ldd = p.ldf; x.d_fmt = BSM_F32; }
+      const xent::Times ep{down};
+      const int64_t m128 = (a.rows + 127) / 128, n128 = (a.K + 127) / 128, m256 = (a.rows + 255) / 256, n256 = (a.K + 255) / 256;
+      if (p.parts == 1 && tile_for(x.M, x.N) == LARGE)
+        hipLaunchKernelGGL((k_xent_large<DT, true, false, xent::Times>), dim3((uint32_t)(m256 * n256)), dim3(256), 0, st, x, ep, (int)m256, (int)n256);
+      else {
+        // (the last piece may be short: a part without columns adds nothing)
+        const int parts = (int)((cols + p.per - 1) / p.per);
+        hipLaunchKernelGGL((k_xent_mid<DT, true, false, xent::Times>), dim3((uint32_t)(m128 * n128 * parts)), dim3(256), 0, st, x, ep, (int)m128,
+                           (int)n128, Parts{parts, p.per, a.rows * p.ldf});
+      }
+    }
+    if (g.dW) {
+      GemmArgs w{};
+      w.M = cols; w.N = a.K; w.K = a.rows; w.dtype = DT;
+      w.A = G; w.lda = p.ldg; w.B = a.X; w.ldb = a.ldx;
+      w.D = (float*)((uint8_t*)g.dW + c0 * g.lddw * (g.dw_fmt == BSM_F32 ? 4 : 2)); w.ldd = g.lddw; w.d_fmt = g.dw_fmt; w.accum = g.accum;
+      const xent::Times ep{down};
+      const int64_t m128 = (cols + 127) / 128, n128 = (a.K + 127) / 128, m256 = (cols + 255) / 256, n256 = (a.K + 255) / 256;
+      if (a.rows >= 192 && tile_for(w.M, w.N) == LARGE)
+        hipLaunchKernelGGL((k_xent_large<DT, false, false, xent::Times>), dim3((uint32_t)(m256 * n256)), dim3(256), 0, st, w, ep, (int)m256, (int)n256);
+      else if (a.rows < 64)
+        hipLaunchKernelGGL((k_xent_mid<DT, false, false, xent::Times, 128, 32, 4>), dim3((uint32_t)(m128 * n128)), dim3(256), 0, st, w, ep,
+                           (int)m128, (int)n128, one);
+      else
+        hipLaunchKernelGGL((k_xent_mid<DT, false, false, xent::Times>), dim3((uint32_t)(m128 * n128)), dim3(256), 0, st, w, ep, (int)m128,
+                           (int)n128, one);
+    }
+  }
+  if (g.dX && a.rows > 0 && !direct) {
+    const int64_t n = a.rows * ((a.K + 3) / 4);
+    const dim3 grid((uint32_t)((n + 255) / 256));
+    auto sum = [&](auto out) {
+      hipLaunchKernelGGL((k_xent_sum<decltype(out)::value>), grid, dim3(256), 0, st, F, p.parts, a.rows * p.ldf, p.ldf, a.rows, a.K, g.dX, g.lddx);
+    };
+    if (g.dx_fmt == BSM_F32) sum(std::integral_constant<int, BSM_F32>{});
+    else sum(std::integral_constant<int, DT>{});
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t xent_workspace(int64_t rows, int64_t N) { return (slots_of(rows, N) * rows * 8 + 15) / 16 * 16 + rows * 4; }
+
+hipError_t launch_xent(const XentArgs& a, void* workspace, hipStream_t st) {
+  float2* part = (float2*)workspace;
+  float* at = (float*)((uint8_t*)workspace + (slots_of(a.rows, a.N) * a.rows * 8 + 15) / 16 * 16);
+  return a.dtype == BSM_BF16 ? launch_loss<BSM_BF16>(a, part, at, st) : launch_loss<BSM_F16>(a, part, at, st);
+}
+
+int64_t xent_grad_workspace(int64_t rows, int64_t N, int64_t K, int64_t piece) { return plan_of(rows, N, K, piece).bytes; }
+
+hipError_t launch_xent_grad(const XentArgs& a, const XentGradArgs& g, void* workspace, hipStream_t st) {
+  const Plan p = plan_of(a.rows, a.N, a.K, g.piece);
+  return a.dtype == BSM_BF16 ? launch_grad<BSM_BF16>(a, g, p, (uint8_t*)workspace, st)
+                             : launch_grad<BSM_F16>(a, g, p, (uint8_t*)workspace, st);
+}
+
+}  // namespace bsm

@@ -121,3 +121,60 @@ def test_restore_and_gradient_refusals():
     for name, bad in (("BSM_E_NULL", dict(dy=0)), ("BSM_E_ALIGN", dict(lddy=100)), ("BSM_E_ALIAS", dict(dy=AT[3] + 16)),
                       ("BSM_E_ALIAS", dict(dy=AT[3], lddy=112)), ("BSM_E_NULL", dict(ew=None))):
         expect(name, ewise_grad, **bad)
+
+
+def xent(rows=100, N=1000, K=64, ab="bf16", x=AT[0], ldx=64, w=AT[1], ldw=64, labels=AT[2], loss=AT[3], lse=AT[4], ws=AT[5]):
+    bsm.bsm_gemm_cross_entropy(rows, N, K, ab, x, ldx, w, ldw, labels, loss, lse, ws, 0)
+
+
+def xent_grad(rows=100, N=1000, K=64, ab="bf16", x=AT[0], ldx=64, w=AT[1], ldw=64, labels=AT[2], lse=AT[4], dloss=AT[3], piece=0,
+              ws=AT[5], dx_fmt="bf16", dx=AT[6], lddx=64, dw_fmt="f32", dw=AT[7], lddw=64, accum=0):
+    bsm.bsm_gemm_cross_entropy_grad(rows, N, K, ab, x, ldx, w, ldw, labels, lse, dloss, piece, ws, dx_fmt, dx, lddx, dw_fmt, dw, lddw,
+                                    accum, 0)
+
+
+@pytest.mark.parametrize("fn", [xent, xent_grad])
+def test_cross_entropy_refusals(fn):
+    for name, bad in (("BSM_E_DTYPE", dict(ab="f32")), ("BSM_E_DTYPE", dict(ab="e4m3")), ("BSM_E_SHAPE", dict(rows=-1)),
+                      ("BSM_E_SHAPE", dict(rows=1 << 31)), ("BSM_E_SHAPE", dict(N=0)), ("BSM_E_SHAPE", dict(N=1 << 31)),
+                      ("BSM_E_SHAPE", dict(K=-1)), ("BSM_E_SHAPE", dict(K=(1 << 22) + 1)), ("BSM_E_SHAPE", dict(rows=1 << 30, N=1 << 30)),
+                      ("BSM_E_SHAPE", dict(ldx=1 << 23)), ("BSM_E_SHAPE", dict(ldw=1 << 23)), ("BSM_E_NULL", dict(x=0)),
+                      ("BSM_E_NULL", dict(w=0)), ("BSM_E_NULL", dict(labels=0)), ("BSM_E_NULL", dict(lse=0)), ("BSM_E_NULL", dict(ws=0)),
+                      ("BSM_E_ALIGN", dict(x=AT[0] + 8)), ("BSM_E_ALIGN", dict(w=AT[1] + 2)), ("BSM_E_ALIGN", dict(labels=AT[2] + 2)),
+                      ("BSM_E_ALIGN", dict(lse=AT[4] + 1)), ("BSM_E_ALIGN", dict(ws=AT[5] + 8)), ("BSM_E_ALIGN", dict(ldx=56)),
+                      ("BSM_E_ALIGN", dict(ldw=68)), ("BSM_E_ALIAS", dict(ws=AT[1])), ("BSM_E_ALIAS", dict(ws=AT[0] + 64)),
+                      ("BSM_E_ARG", dict(x=torch.zeros(100, 64, dtype=torch.bfloat16))), ("BSM_E_DTYPE", dict(x=torch.zeros(100, 64))),
+                      ("BSM_E_SHAPE", dict(w=torch.zeros(999, 64, dtype=torch.bfloat16))),
+                      ("BSM_E_SHAPE", dict(labels=torch.zeros(99, dtype=torch.int32))),
+                      ("BSM_E_DTYPE", dict(labels=torch.zeros(100, dtype=torch.int64))),
+                      ("BSM_E_DTYPE", dict(lse=torch.zeros(100, dtype=torch.float64))),
+                      ("BSM_E_SHAPE", dict(ws=torch.zeros(64, dtype=torch.uint8)))):
+        expect(name, fn, **bad)
+
+
+def test_cross_entropy_loss_refusals():
+    for name, bad in (("BSM_E_NULL", dict(loss=0)), ("BSM_E_ALIGN", dict(loss=AT[3] + 2)), ("BSM_E_ALIAS", dict(loss=AT[4] + 8)),
+                      ("BSM_E_ALIAS", dict(loss=AT[0] + 4)), ("BSM_E_ALIAS", dict(lse=AT[2] + 4)), ("BSM_E_ALIAS", dict(lse=AT[5] + 4)),
+                      ("BSM_E_SHAPE", dict(loss=torch.zeros(99)))):
+        expect(name, xent, **bad)
+    xent(rows=0, x=0, w=0, labels=0, loss=0, lse=0, ws=0)
+    for rows, N in ((-1, 4), (1 << 31, 4), (4, 0), (4, 1 << 31)):
+        expect("BSM_E_SHAPE", bsm.bsm_gemm_cross_entropy_workspace, rows=rows, N=N)
+    assert bsm.bsm_gemm_cross_entropy_workspace(0, 5) == 0
+
+
+def test_cross_entropy_grad_refusals():
+    for name, bad in (("BSM_E_NULL", dict(dloss=0)), ("BSM_E_ALIGN", dict(dloss=AT[3] + 2)), ("BSM_E_ARG", dict(accum=2)),
+                      ("BSM_E_DTYPE", dict(dx_fmt="f16")), ("BSM_E_DTYPE", dict(dw_fmt="u8")), ("BSM_E_ALIGN", dict(dx=AT[6] + 8)),
+                      ("BSM_E_ALIGN", dict(dw=AT[7] + 8)), ("BSM_E_ALIGN", dict(lddx=56)), ("BSM_E_ALIGN", dict(lddx=68)),
+                      ("BSM_E_ALIGN", dict(lddw=60)), ("BSM_E_SHAPE", dict(piece=-1)), ("BSM_E_ALIAS", dict(dx=AT[0] + 1024)),
+                      ("BSM_E_ALIAS", dict(dw=AT[1])), ("BSM_E_ALIAS", dict(dw=AT[6] + 1024)), ("BSM_E_ALIAS", dict(dx=AT[5])),
+                      ("BSM_E_ALIAS", dict(dw=AT[3])), ("BSM_E_ALIAS", dict(dx=AT[4] - 64)),
+                      ("BSM_E_SHAPE", dict(dx=torch.zeros(99, 64, dtype=torch.bfloat16))), ("BSM_E_SHAPE", dict(dw=torch.zeros(999, 64))),
+                      ("BSM_E_DTYPE", dict(dw=torch.zeros(1000, 64, dtype=torch.bfloat16)))):
+        expect(name, xent_grad, **bad)
+    xent_grad(K=0, ldx=0, ldw=0, x=0, w=0)
+    xent_grad(dx=None, dw=None)
+    xent_grad(rows=0, dw=None, x=0, w=0, labels=0, lse=0, dloss=0, ws=0)
+    for bad in (dict(rows=-1), dict(N=0), dict(K=-1), dict(piece=-1), dict(piece=1 << 31)):
+        expect("BSM_E_SHAPE", bsm.bsm_gemm_cross_entropy_grad_workspace, **{**dict(rows=4, N=4, K=4, piece=0), **bad})

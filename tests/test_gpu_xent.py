@@ -1,0 +1,167 @@
+"""GPU parity: cross entropy of a projection onto a vocabulary and its gradients, against 64 bits (bounds in xent_util)."""
+import pytest
+import torch
+
+import block_scaled_matrix_amd as bsm
+from grouped_util import DT, up
+from gpu_util import say
+from xent_util import check_grad, check_loss, inputs, reference, wide
+
+pytestmark = pytest.mark.gpu
+
+
+def both(rows, N, K, ab="bf16", seed=0, extra=0, **kw):
+    x, w, labels, dloss = inputs(rows, N, K, ab, seed + rows + N + K)
+    _, lse = check_loss(x, w, labels, ab, extra=extra)
+    return check_grad(x, w, labels, dloss, lse, ab, extra=extra, **kw)
+
+
+@pytest.mark.parametrize("ab", ["bf16", "f16"])
+@pytest.mark.parametrize("rows,N,K", [(1, 1, 1), (1, 2, 8), (2, 15, 7), (3, 16, 64), (5, 17, 65), (16, 63, 33), (17, 64, 136), (31, 65, 520),
+                                      (33, 129, 40), (63, 250, 72), (64, 1000, 100), (65, 1000, 8), (130, 257, 264), (200, 4099, 1000),
+                                      (300, 128, 24)])
+def test_sizes(rows, N, K, ab):
+    both(rows, N, K, ab)
+
+
+@pytest.mark.parametrize("ab", ["bf16", "f16"])
+@pytest.mark.parametrize("rows,N,K", [
+    (4, 33000, 40), (64, 20001, 64), (700, 9001, 48),     # whole vocabularies: the loss on mid tiles of 32, 64 and 128 rows
+    (4096, 4100, 40), (3900, 4500, 72),                   # logits on the large tile
+    (4096, 300, 4096), (200, 4096, 4096), (2100, 5000, 2056),   # and the gradients on it, dX in one part and in several
+    (1, 5000, 4096)])
+def test_tiles(rows, N, K, ab):
+    both(rows, N, K, ab, extra=rows % 2)
+
+
+@pytest.mark.parametrize("ab", ["bf16", "f16"])
+@pytest.mark.parametrize("rows,N,K", [(3, 700, 40), (130, 700, 200), (40, 3000, 64), (4096, 600, 4096)])
+def test_formats_accumulation_and_pieces(rows, N, K, ab):
+    for dx, dw, accum, piece in ((ab, "f32", 1, 256), ("f32", ab, 1, 0), ("f32", "f32", 0, 300), (ab, ab, 0, 1)):
+        both(rows, N, K, ab, dx_fmt=dx, dw_fmt=dw, accum=accum, piece=piece, extra=1)
+
+
+def test_one_gradient_alone():
+    both(130, 700, 72, want="x")
+    both(130, 700, 72, want="w", piece=256)
+    both(130, 700, 72, want="")
+
+
+def test_no_rows_and_no_width():
+    x, w, labels, dloss = inputs(0, 40, 16, "bf16", 1)
+    bsm.bsm_gemm_cross_entropy(0, 40, 16, "bf16", x, 16, w, 16, labels, dloss, dloss, None)
+    for accum in (0, 1):
+        dw = torch.full((40, 16), 3.0, dtype=torch.bfloat16, device="cuda")
+        bsm.bsm_gemm_cross_entropy_grad(0, 40, 16, "bf16", None, 16, None, 16, None, None, None, 0, None, "bf16", None, 16, "bf16", dw, 16, accum)
+        assert (dw == 3.0 * accum).all()
+    loss, lse = torch.empty(5, device="cuda"), torch.empty(5, device="cuda")
+    work = torch.empty(bsm.bsm_gemm_cross_entropy_workspace(5, 40), dtype=torch.uint8, device="cuda")
+    labels = torch.tensor([0, 39, 40, -1, 7], dtype=torch.int32, device="cuda")
+    bsm.bsm_gemm_cross_entropy(5, 40, 0, "bf16", None, 0, None, 0, labels, loss, lse, work)
+    want = torch.log(torch.tensor(40.0))
+    assert (lse.cpu() - want).abs().max() < 1e-6 and (loss.cpu() - want * torch.tensor([1.0, 1, 0, 0, 1])).abs().max() < 1e-6
+
+
+@pytest.mark.parametrize("rows,N", [(40, 300), (500, 20000)])
+def test_rows_without_a_label(rows, N):
+    """No label at all; labels far outside; such a row's NaN stays in its row of logits."""
+    x, w, labels, dloss = inputs(rows, N, 64, "bf16", 2)
+    for bad in (-1, N, 2 ** 31 - 1, -2 ** 31):
+        none = torch.full_like(labels, bad)
+        loss, lse = check_loss(x, w, none, "bf16")
+        assert not loss.any()
+        dx, dw = check_grad(x, w, none, dloss, lse, "bf16")
+        assert not dx[:, :64].any() and not dw[:, :64].any()
+    # a padding row of NaN with a NaN weight: its G is 0, but X enters dW as 0 * NaN, so its X must be finite for dW
+    labels[3] = -1
+    dl = dloss.clone()
+    dl[3] = float("nan")
+    y = x.clone()
+    y[3] = float("nan")
+    _, lse = check_loss(x, w, labels, "bf16")
+    loss2, lse2 = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    work = torch.empty(bsm.bsm_gemm_cross_entropy_workspace(rows, N), dtype=torch.uint8, device="cuda")
+    bsm.bsm_gemm_cross_entropy(rows, N, 64, "bf16", y, 64, w, 64, labels, loss2, lse2, work)
+    keep = torch.arange(rows, device="cuda") != 3
+    assert torch.equal(lse2[keep], lse[keep]) and torch.isnan(lse2[3]) and loss2[3] == 0
+    dx = torch.empty(rows, 64, dtype=torch.bfloat16, device="cuda")
+    ref, _ = check_grad(x, w, labels, dloss, lse, "bf16")
+    gw = torch.empty(bsm.bsm_gemm_cross_entropy_grad_workspace(rows, N, 64, 0), dtype=torch.uint8, device="cuda")
+    bsm.bsm_gemm_cross_entropy_grad(rows, N, 64, "bf16", y, 64, w, 64, labels, lse2, dl, 0, gw, "bf16", dx, 64, "bf16", None, 64)
+    assert torch.equal(dx, ref[:, :64]) and not dx[3].any()
+
+
+@pytest.mark.parametrize("rows,N", [(20, 100), (20, 30000), (700, 9000)])
+def test_large_and_infinite_logits(rows, N):
+    """Logits far apart (probabilities that underflow), equal ones, and infinities of the operands."""
+    x, w, labels, dloss = inputs(rows, N, 16, "bf16", 5, spread=120.0)
+    loss, lse = check_loss(x, w, labels, "bf16")
+    check_grad(x, w, labels, dloss, lse, "bf16")
+    z = torch.zeros_like(w)
+    _, lse = check_loss(x, z, labels, "bf16")
+    check_grad(x, z, labels, dloss, lse, "bf16")
+    # a column of -infinity for every row: probability 0
+    x2, w2 = x.abs() + 0.5, w.clone()
+    w2[7] = -float("inf")
+    lab = torch.where(labels == 7, 8, labels)
+    loss, lse = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    work = torch.empty(bsm.bsm_gemm_cross_entropy_workspace(rows, N), dtype=torch.uint8, device="cuda")
+    bsm.bsm_gemm_cross_entropy(rows, N, 16, "bf16", x2, 16, w2, 16, lab, loss, lse, work)
+    keep = torch.cat((w2[:7], w2[8:]))
+    want = torch.logsumexp(x2.double() @ keep.double().T.contiguous(), 1)
+    assert ((lse.double() - want).abs() <= 1e-5 * want.abs()).all()      # (16 products of up to a few thousand)
+    # NaN in one row of X, and +infinity in another, show in their rows alone
+    x3 = x.clone()
+    x3[2, 3] = float("nan")
+    w3 = w.abs() + 0.01
+    x3[5] = x3[5].abs()
+    x3[5, 1] = float("inf")
+    bsm.bsm_gemm_cross_entropy(rows, N, 16, "bf16", x3, 16, w3, 16, labels, loss, lse, work)
+    bad = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    bad[2] = bad[5] = True
+    assert torch.isnan(lse[bad]).all() and torch.isfinite(lse[~bad]).all()
+
+
+def test_f16_weights_of_every_size():
+    """The weights' power of two: tiny, huge, zero and one row far above the rest."""
+    x, w, labels, _ = inputs(90, 500, 40, "f16", 9)
+    _, lse = check_loss(x, w, labels, "f16")
+    for d in (torch.full((90,), 2.0 ** -40), torch.full((90,), 1e30), torch.zeros(90), torch.rand(90) * 1e-3, torch.full((90,), -1.0)):
+        dx_fmt = dw_fmt = "f32"
+        check_grad(x, w, labels, d.cuda(), lse, "f16", dx_fmt, dw_fmt)
+    d = torch.full((90,), 1e-6)
+    d[4] = 1.0
+    check_grad(x, w, labels, d.cuda(), lse, "f16")
+
+
+@pytest.mark.parametrize("rows,N,K", [(24, 30011, 256), (1500, 3000, 200), (4096, 4096, 64)])
+def test_same_bits_on_every_call(rows, N, K):
+    x, w, labels, dloss = inputs(rows, N, K, "bf16", 4)
+    a = check_loss(x, w, labels, "bf16")
+    g = check_grad(x, w, labels, dloss, a[1], "bf16")
+    for _ in range(3):
+        b = check_loss(x, w, labels, "bf16")
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    h = check_grad(x, w, labels, dloss, a[1], "bf16")
+    assert torch.equal(g[0], h[0]) and torch.equal(g[1], h[1])
+
+
+def test_gradient_against_differences():
+    """d (sum of weighted losses) / dx and / dw by central differences of the 64-bit loss."""
+    x, w, labels, dloss = inputs(5, 9, 6, "bf16", 3)
+    _, lse = check_loss(x, w, labels, "bf16")
+    dx, dw = check_grad(x, w, labels, dloss, lse, "bf16", "f32", "f32")
+    f = lambda a, b: float((torch.where((labels >= 0) & (labels < 9), torch.logsumexp(a @ b.T, 1) -
+                                        (a @ b.T).gather(1, labels.clamp(0, 8).long()[:, None])[:, 0], 0.0) * dloss.double()).sum())
+    X, W, h = x.double(), w.double(), 1e-5
+    for t, g, n in ((X, dx, 5), (W, dw, 9)):
+        for i in range(n):
+            for k in range(6):
+                keep = float(t[i, k])
+                t[i, k] = keep + h
+                hi = f(X, W)
+                t[i, k] = keep - h
+                lo = f(X, W)
+                t[i, k] = keep
+                # G is rounded to bf16: 2^-8 of sum |G| |operand|, weights 0.2, values to 3
+                assert abs((hi - lo) / (2 * h) - float(g[i, k])) < 2.0 ** -8 * 5

@@ -28,16 +28,8 @@ namespace {
 
 using namespace dense;
 
-// A wave's 128 x 128 block of the 256 x 256 tile, stored in d_fmt.
-template <int DT>
-__device__ __forceinline__ void store_out(const GemmArgs& a, int64_t row0, int64_t col0, int lane, const f32x4 (&acc)[8][8],
-                                          uint8_t* region) {
-  if (a.d_fmt == BSM_F32) store_tile16(a.D, a.ldd, a.M, a.N, row0, col0, lane, 1.0f, acc, region, a.accum, 0, 0.0f, 0.0f);
-  else gemm::store_tile16_bits<DT>((uint16_t*)a.D, a.ldd, a.M, a.N, row0, col0, lane, acc, region, a.accum, 0, 0.0f, 0.0f);
-}
-
-// One 256 x 256 tile: the product, what EP makes of the sums, and their store unless EP stored them.
-template <int DT, bool AK, bool BKM, class EP>
+// One 256 x 256 tile: the product, what EP makes of the sums, and their store in OUT unless EP keeps none.
+template <int DT, bool AK, bool BKM, int OUT, bool ACC, class EP>
 __global__ __launch_bounds__(256, 1) void k_xent_large(GemmArgs a, EP ep, int tiles_m, int tiles_n) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * STAGE_BYTES];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -47,7 +39,9 @@ __global__ __launch_bounds__(256, 1) void k_xent_large(GemmArgs a, EP ep, int ti
   tile_product<DT, AK, BKM>(a, tm, tn, lds, lane, w, acc);
   const int64_t row0 = (int64_t)tm * BM + 128 * (w >> 1), col0 = (int64_t)tn * BN + 128 * (w & 1);
   ep(row0, col0, acc);
-  if constexpr (!EP::kStores) store_out<DT>(a, row0, col0, lane, acc, lds + 32768 * w);
+  if constexpr (EP::kStores) return;
+  else if constexpr (OUT == BSM_F32) store_tile16(a.D, a.ldd, a.M, a.N, row0, col0, lane, 1.0f, acc, lds + 32768 * w, ACC, 0, 0.0f, 0.0f);
+  else gemm::store_tile16_bits<OUT>((uint16_t*)a.D, a.ldd, a.M, a.N, row0, col0, lane, acc, lds + 32768 * w, ACC, 0, 0.0f, 0.0f);
 }
 
 // Tiles of BM x 128 (K-major A: of as few rows as hold the last ones), `parts` of the product's K side by side: part p takes
@@ -204,13 +198,28 @@ void launch_logits(const GemmArgs& g, Tile tile, const EP& ep, hipStream_t st) {
   const int64_t t = tile == LARGE ? 256 : 128, tm = (g.M + t - 1) / t, tn = (g.N + t - 1) / t;
   const dim3 grid((uint32_t)(tm * tn));
   const Parts one{1, 0, 0};
-  if (tile == LARGE) hipLaunchKernelGGL((k_xent_large<DT, true, true, EP>), grid, dim3(256), 0, st, g, ep, (int)tm, (int)tn);
+  if (tile == LARGE) hipLaunchKernelGGL((k_xent_large<DT, true, true, DT, false, EP>), grid, dim3(256), 0, st, g, ep, (int)tm, (int)tn);
   else if (tile == MID) hipLaunchKernelGGL((k_xent_mid<DT, true, true, EP>), grid, dim3(256), 0, st, g, ep, (int)tm, (int)tn, one);
   else {
     const int64_t m64 = (g.M + 63) / 64;
     hipLaunchKernelGGL((k_xent_mid<DT, true, true, EP, 64, 64, 1, 2>), dim3((uint32_t)(m64 * tn)), dim3(512), 0, st, g, ep, (int)m64,
                        (int)tn, one);
   }
+}
+
+// A gradient's product on 256 x 256 tiles, B's rows along K, stored in the format of `g`.
+template <int DT, bool AK, class EP>
+void launch_large(const GemmArgs& g, const EP& ep, int64_t tm, int64_t tn, hipStream_t st) {
+  auto go = [&](auto out, auto acc) {
+    hipLaunchKernelGGL((k_xent_large<DT, AK, false, decltype(out)::value, decltype(acc)::value, EP>), dim3((uint32_t)(tm * tn)), dim3(256), 0,
+                       st, g, ep, (int)tm, (int)tn);
+  };
+  auto with = [&](auto out) {
+    if (g.accum) go(out, std::true_type{});
+    else go(out, std::false_type{});
+  };
+  if (g.d_fmt == BSM_F32) with(std::integral_constant<int, BSM_F32>{});
+  else with(std::integral_constant<int, DT>{});
 }
 
 GemmArgs logits_of(const XentArgs& a) {
@@ -282,6 +291,7 @@ hipError_t launch_grad(const XentArgs& a, const XentGradArgs& g, const Plan& p, 
     up = by;
     down = by + 1;
   }
+  using Times = xent::Times<DT == BSM_F16>;
   const Parts one{1, 0, 0};
   const bool direct = !p.sums || (p.parts == 1 && g.dx_fmt == BSM_F32);
   for (int64_t c0 = 0, at = 0; c0 < a.N; c0 += p.piece, at++) {
@@ -302,14 +312,14 @@ hipError_t launch_grad(const XentArgs& a, const XentGradArgs& g, const Plan& p, 
       x.accum = at > 0;
       if (direct) { x.D = (float*)g.dX; x.ldd = g.lddx; x.d_fmt = g.dx_fmt; }
       else { x.D = F; x.ldd = p.ldf; x.d_fmt = BSM_F32; }
-      const xent::Times ep{down};
+      const Times ep{down};
       const int64_t m128 = (a.rows + 127) / 128, n128 = (a.K + 127) / 128, m256 = (a.rows + 255) / 256, n256 = (a.K + 255) / 256;
       if (p.parts == 1 && tile_for(x.M, x.N) == LARGE)
-        hipLaunchKernelGGL((k_xent_large<DT, true, false, xent::Times>), dim3((uint32_t)(m256 * n256)), dim3(256), 0, st, x, ep, (int)m256, (int)n256);
+        launch_large<DT, true>(x, ep, m256, n256, st);
       else {
         // (the last piece may be short: a part without columns adds nothing)
         const int parts = (int)((cols + p.per - 1) / p.per);
-        hipLaunchKernelGGL((k_xent_mid<DT, true, false, xent::Times>), dim3((uint32_t)(m128 * n128 * parts)), dim3(256), 0, st, x, ep, (int)m128,
+        hipLaunchKernelGGL((k_xent_mid<DT, true, false, Times>), dim3((uint32_t)(m128 * n128 * parts)), dim3(256), 0, st, x, ep, (int)m128,
                            (int)n128, Parts{parts, p.per, a.rows * p.ldf});
       }
     }
@@ -318,15 +328,15 @@ hipError_t launch_grad(const XentArgs& a, const XentGradArgs& g, const Plan& p, 
       w.M = cols; w.N = a.K; w.K = a.rows; w.dtype = DT;
       w.A = G; w.lda = p.ldg; w.B = a.X; w.ldb = a.ldx;
       w.D = (float*)((uint8_t*)g.dW + c0 * g.lddw * (g.dw_fmt == BSM_F32 ? 4 : 2)); w.ldd = g.lddw; w.d_fmt = g.dw_fmt; w.accum = g.accum;
-      const xent::Times ep{down};
+      const Times ep{down};
       const int64_t m128 = (cols + 127) / 128, n128 = (a.K + 127) / 128, m256 = (cols + 255) / 256, n256 = (a.K + 255) / 256;
       if (a.rows >= 192 && tile_for(w.M, w.N) == LARGE)
-        hipLaunchKernelGGL((k_xent_large<DT, false, false, xent::Times>), dim3((uint32_t)(m256 * n256)), dim3(256), 0, st, w, ep, (int)m256, (int)n256);
+        launch_large<DT, false>(w, ep, m256, n256, st);
       else if (a.rows < 64)
-        hipLaunchKernelGGL((k_xent_mid<DT, false, false, xent::Times, 128, 32, 4>), dim3((uint32_t)(m128 * n128)), dim3(256), 0, st, w, ep,
+        hipLaunchKernelGGL((k_xent_mid<DT, false, false, Times, 128, 32, 4>), dim3((uint32_t)(m128 * n128)), dim3(256), 0, st, w, ep,
                            (int)m128, (int)n128, one);
       else
-        hipLaunchKernelGGL((k_xent_mid<DT, false, false, xent::Times>), dim3((uint32_t)(m128 * n128)), dim3(256), 0, st, w, ep, (int)m128,
+        hipLaunchKernelGGL((k_xent_mid<DT, false, false, Times>), dim3((uint32_t)(m128 * n128)), dim3(256), 0, st, w, ep, (int)m128,
                            (int)n128, one);
     }
   }

@@ -33,6 +33,18 @@ constexpr float kLog2e = 0x1.715476p+0f;    // log2 e as float; what it lacks is
 // A wave's block of logits, MI x NJ blocks of 16 x 16 at (row0, col0): acc[m][n][e] is row row0 + 16m + l%16, column
 // col0 + 16n + 4(l/16) + e. Columns at or past N do not exist.
 
+// One row of blocks in registers of its own: what follows changes copies. (Accumulators that a branch behind the K loop
+// changes made the compiler move up to 480 of them about in every turn of the 256 x 256 tile's loop: 2123 us for
+// 8190 x 32001 x 4096 against 1603 us.)
+template <int NJ>
+__device__ __forceinline__ void take(const f32x4 (&row)[NJ], f32x4 (&v)[NJ]) {
+#pragma unroll
+  for (int n = 0; n < NJ; n++) {
+    v[n] = row[n];
+    asm volatile("" : "+v"(v[n]));
+  }
+}
+
 // Its rows' part of the log-sum-exp: base b, the largest logit times log2 e, and s = sum 2^(z log2 e - b), to slot
 // col0 / width; and the logit of the rows' labels that lie in it. b is a float that the join takes as it is, so its
 // rounding cancels; the exponent's own fma rounds once.
@@ -51,20 +63,21 @@ struct Stats {
     float2* to = part + (col0 / width) * rows;
 #pragma unroll
     for (int m = 0; m < MI; m++) {
+      f32x4 v[NJ];
+      take(acc[m], v);
       const int64_t row = row0 + 16 * m + (lane & 15);
       if (edge) {
-        int left = (int)(N - col0) - 4 * G;
-        asm volatile("" : "+v"(left));   // (the comparisons' masks would be kept over all m, in scalar registers that spill)
+        const int left = (int)(N - col0) - 4 * G;
 #pragma unroll
         for (int n = 0; n < NJ; n++)
 #pragma unroll
-          for (int e = 0; e < 4; e++) acc[m][n][e] = 16 * n + e < left ? acc[m][n][e] : -INFINITY;
+          for (int e = 0; e < 4; e++) v[n][e] = 16 * n + e < left ? v[n][e] : -INFINITY;
       }
       float top = -INFINITY;
 #pragma unroll
       for (int n = 0; n < NJ; n++)
 #pragma unroll
-        for (int e = 0; e < 4; e++) top = fmaxf(top, acc[m][n][e]);
+        for (int e = 0; e < 4; e++) top = fmaxf(top, v[n][e]);
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
       const float b = top * kLog2e, from = top == -INFINITY ? 0.0f : b;
@@ -72,7 +85,7 @@ struct Stats {
 #pragma unroll
       for (int n = 0; n < NJ; n++)
 #pragma unroll
-        for (int e = 0; e < 4; e++) s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[m][n][e], kLog2e, -from));
+        for (int e = 0; e < 4; e++) s += __builtin_amdgcn_exp2f(__builtin_fmaf(v[n][e], kLog2e, -from));
       s += __shfl_xor(s, 16);
       s += __shfl_xor(s, 32);
       const bool in = row < rows;
@@ -85,7 +98,7 @@ struct Stats {
 #pragma unroll
         for (int n = 0; n < NJ; n++)
 #pragma unroll
-          for (int e = 0; e < 4; e++) z = 16 * n + e == o ? acc[m][n][e] : z;
+          for (int e = 0; e < 4; e++) z = 16 * n + e == o ? v[n][e] : z;
         if (mine) at[row] = z;
       }
     }
@@ -112,14 +125,16 @@ struct Grad {
       const int64_t lab = in ? labels[row] : -1;
       const bool has = lab >= 0 && lab < vocabulary;
       const float d = has ? dloss[row] * f : 0.0f, l = has ? lse[row] : 0.0f;
+      f32x4 v[NJ];
+      take(acc[m], v);
       // 2^(z log2 e - l log2 e), the second product in two floats
       const float hi = l * kLog2e, lo = __builtin_fmaf(l, kLog2e, -hi);
 #pragma unroll
       for (int n = 0; n < NJ; n++)
 #pragma unroll
         for (int e = 0; e < 4; e++) {
-          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[m][n][e], kLog2e, -hi) - lo);
-          acc[m][n][e] = has ? p * d : 0.0f;
+          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(v[n][e], kLog2e, -hi) - lo);
+          v[n][e] = has ? p * d : 0.0f;
         }
       const int64_t off = lab - first - col0;
       const bool mine = has && off >= 0 && off < 16 * NJ && ((off >> 2) & 3) == G;
@@ -129,24 +144,28 @@ struct Grad {
 #pragma unroll
         for (int n = 0; n < NJ; n++)
 #pragma unroll
-          for (int e = 0; e < 4; e++) acc[m][n][e] -= 16 * n + e == o ? d : 0.0f;
+          for (int e = 0; e < 4; e++) v[n][e] -= 16 * n + e == o ? d : 0.0f;
       }
+#pragma unroll
+      for (int n = 0; n < NJ; n++) acc[m][n] = v[n];
     }
   }
 };
 
-// Sums times a power of two on the device (f16), or as they are.
+// Sums as they are, or times a power of two on the device (f16).
+template <bool BY>
 struct Times {
   static constexpr bool kStores = false;
   const float* by;
   template <int MI, int NJ>
   __device__ __forceinline__ void operator()(int64_t, int64_t, f32x4 (&acc)[MI][NJ]) const {
-    if (!by) return;
-    const float f = *by;
+    if constexpr (BY) {
+      const float f = *by;
 #pragma unroll
-    for (int m = 0; m < MI; m++)
+      for (int m = 0; m < MI; m++)
 #pragma unroll
-      for (int n = 0; n < NJ; n++) acc[m][n] *= f;
+        for (int n = 0; n < NJ; n++) acc[m][n] *= f;
+    }
   }
 };
 

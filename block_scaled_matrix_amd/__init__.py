@@ -27,7 +27,7 @@ EXPORTS = ("bsm_image_stride", "bsm_tile_box_load", "bsm_tile_box_store", "bsm_t
            "bsm_gemm_block_scale_fastacc", "bsm_gemm_grouped", "bsm_gemm_grouped_wgrad",
            "bsm_gemm_grouped_block_scale", "bsm_gemm_lora", "bsm_gemm_lora_workspace", "bsm_router_balance",
            "bsm_router_balance_workspace", "bsm_router_balance_grad", "bsm_block_scale_save", "bsm_block_scale_restore",
-           "bsm_block_scale_ewise_grad", "bsm_gemm_cross_entropy", "bsm_gemm_cross_entropy_workspace",
+           "bsm_block_scale_ewise_grad", "bsm_gemm_grouped_wgrad_block_scale", "bsm_gemm_cross_entropy", "bsm_gemm_cross_entropy_workspace",
            "bsm_gemm_cross_entropy_grad", "bsm_gemm_cross_entropy_grad_workspace",
            "bsm_debug_grouped_route", "bsm_debug_stream_mix_bf16", "bsm_debug_mfma_loop", "bsm_tile_add_scalar_f32", "bsm_debug_fragments", "bsm_debug_fragment_shape", "bsm_last_error")
 
@@ -101,6 +101,8 @@ def lib():
         L.bsm_block_scale_save.argtypes = [I64, I64, I32, P, I64, I32, P, I64, P, I64, P]
         L.bsm_block_scale_restore.argtypes = [I64, I64, I32, P, I64, P, I64, I32, P, I64, C.POINTER(bsm_ewise), P]
         L.bsm_block_scale_ewise_grad.argtypes = [I64, I64, I32, P, I64, P, I64, I32, P, I64, P, I64, C.POINTER(bsm_ewise), P]
+        L.bsm_gemm_grouped_wgrad_block_scale.argtypes = [I64, I64, I64, I32, P, I32, P, I64, I32, P, I64, P, I64, I32, P, I64, I64,
+                                                         C.c_int, P]
         L.bsm_gemm_cross_entropy_workspace.restype = L.bsm_gemm_cross_entropy_grad_workspace.restype = I64
         L.bsm_gemm_cross_entropy_workspace.argtypes = [I64, I64]
         L.bsm_gemm_cross_entropy_grad_workspace.argtypes = [I64, I64, I64, I64]
@@ -122,7 +124,7 @@ def lib():
                       "bsm_gemm_block_scale_major", "bsm_gemm_block_scale_fastacc", "bsm_gemm_grouped",
                       "bsm_gemm_grouped_wgrad", "bsm_gemm_grouped_block_scale", "bsm_gemm_lora", "bsm_router_balance", "bsm_router_balance_grad",
                       "bsm_block_scale_save", "bsm_block_scale_restore", "bsm_block_scale_ewise_grad",
-                      "bsm_gemm_cross_entropy", "bsm_gemm_cross_entropy_grad", "bsm_tile_add_scalar_f32",
+                      "bsm_gemm_grouped_wgrad_block_scale", "bsm_gemm_cross_entropy", "bsm_gemm_cross_entropy_grad", "bsm_tile_add_scalar_f32",
                       "bsm_debug_fragments", "bsm_debug_stream_mix_bf16", "bsm_debug_mfma_loop"):
             getattr(L, rc_fn).restype = C.c_int
         _lib = L
@@ -469,6 +471,20 @@ def bsm_block_scale_ewise_grad(rows, K, fmt: str, Q, ldq, SF, ld_sf, dy_fmt: str
     s = _here(stream, Q, SF, dY, D)
     _check(lib().bsm_block_scale_ewise_grad(rows, K, DTYPE[fmt], q, ldq, f, ld_sf, DTYPE[dy_fmt], y, lddy, d, ldd,
                                             C.byref(ew) if ew is not None else None, s))
+
+
+def bsm_gemm_grouped_wgrad_block_scale(rows, M, N, n_groups, offsets, ab: str, A, lda, b_fmt: str, B, ldb, SFB, ld_sfb, d_fmt: str,
+                                       D, ldd, stride_d, accum=0, stream=None):
+    _operand_fmt(ab)
+    # (a call without groups, rows of D or columns reads no offsets)
+    some = n_groups > 0 and M > 0 and N > 0
+    off = _array(offsets, "int32", "offsets", n_groups + 1 if some else 0)
+    r = rows if some else 0
+    x, c = _rows(A, ab, "A", r, M, lda, 8), _rows(B, "u8", "B", r, N, ldb, 16)
+    f = _rows(SFB, "u8", "SFB", r, (N + 31) // 32, ld_sfb, 4)
+    s = _here(stream, offsets, A, B, SFB, D)
+    _check(lib().bsm_gemm_grouped_wgrad_block_scale(rows, M, N, n_groups, off, DTYPE[ab], x, lda, DTYPE[b_fmt], c, ldb, f, ld_sfb,
+                                                    DTYPE[d_fmt], _ptr(D), ldd, stride_d, accum, s))
 
 
 def bsm_gemm_cross_entropy_workspace(rows, N) -> int:

@@ -929,6 +929,53 @@ int bsm_block_scale_ewise_grad(int64_t rows, int64_t K, int32_t fmt, const uint8
   return ok();
 }
 
+int bsm_gemm_grouped_wgrad_block_scale(int64_t rows, int64_t M, int64_t N, int32_t n_groups, const int32_t* offsets, int32_t ab,
+                                       const void* A, int64_t lda, int32_t b_fmt, const uint8_t* B, int64_t ldb,
+                                       const uint8_t* SFB, int64_t ld_sfb, int32_t d_fmt, void* D, int64_t ldd, int64_t stride_d,
+                                       int accum, void* stream) {
+  int rc;
+  if ((rc = check_flag(accum, "accum"))) return rc;
+  if (ab != BSM_F16 && ab != BSM_BF16) return fail(BSM_E_DTYPE, "ab = %d: the weight gradient takes dY in F16 or BF16", ab);
+  if (b_fmt != BSM_E4M3 && b_fmt != BSM_E5M2) return fail(BSM_E_DTYPE, "b_fmt = %d is neither E4M3 nor E5M2", b_fmt);
+  if (d_fmt != BSM_F32 && d_fmt != ab) return fail(BSM_E_DTYPE, "d_fmt = %d is neither F32 nor dY's format", d_fmt);
+  if (M < 0 || N < 0 || M > 0x7FFFFFFF || N > 0x7FFFFFFF)
+    return fail(BSM_E_SHAPE, "M, N = %lld, %lld out of range", (long long)M, (long long)N);
+  if ((rc = check_groups(rows, n_groups, offsets))) return rc;
+  if (M == 0 || N == 0 || n_groups == 0) return ok();
+  if ((rc = check_out(D, N, ldd, d_fmt))) return rc;
+  if (n_groups > 1) {
+    if (stride_d < 0 || stride_d > (int64_t(1) << 44)) return fail(BSM_E_SHAPE, "stride_d = %lld out of range", (long long)stride_d);
+    if (stride_d % (d_fmt == BSM_F32 ? 4 : 8)) return fail(BSM_E_ALIGN, "stride_d = %lld: outputs must start 16-byte aligned", (long long)stride_d);
+    if (stride_d < (M - 1) * ldd + N) return fail(BSM_E_ALIAS, "stride_d = %lld: the groups' outputs overlap", (long long)stride_d);
+  } else {
+    stride_d = 0;
+  }
+  const Range rd = block_range(D, n_groups, stride_d, M, ldd, N, d_fmt == BSM_F32 ? 32 : 16);
+  if (overlap(rd, block_range(offsets, 1, 0, 1, 0, n_groups + int64_t(1), 32))) return fail(BSM_E_ALIAS, "offsets overlap D");
+  if (rows > 0) {
+    if (!A || !B || !SFB) return fail(BSM_E_NULL, "A, B or SFB is NULL");
+    if ((uintptr_t)A % 16 || (uintptr_t)B % 16) return fail(BSM_E_ALIGN, "A and B must be 16-byte aligned");
+    if ((uintptr_t)SFB % 4) return fail(BSM_E_ALIGN, "SFB not 4-byte aligned");
+    if (lda < M || lda % 8) return fail(BSM_E_ALIGN, "lda = %lld must be >= M and a multiple of 8", (long long)lda);
+    if (ldb < N || ldb % 16) return fail(BSM_E_ALIGN, "ldb = %lld must be >= N and a multiple of 16", (long long)ldb);
+    if (ld_sfb < (N + 31) / 32 || ld_sfb % 4) return fail(BSM_E_ALIGN, "ld_sfb = %lld must be >= ceil(N/32) and a multiple of 4", (long long)ld_sfb);
+    if (lda > (int64_t(1) << 22) || ldb > (int64_t(1) << 23) || ld_sfb > (int64_t(1) << 23))
+      return fail(BSM_E_SHAPE, "leading dimensions too large for 32-bit in-tile offsets");
+    if (overlap(rd, block_range(A, 1, 0, rows, lda, M, 16)) || overlap(rd, block_range(B, 1, 0, rows, ldb, N, 8)) ||
+        overlap(rd, block_range(SFB, 1, 0, rows, ld_sfb, (N + 31) / 32, 8)))
+      return fail(BSM_E_ALIAS, "A, B or SFB overlaps D");
+  }
+  bsm::GemmArgs g{};
+  g.M = M; g.N = N; g.dtype = ab; g.dtype_b = b_fmt;
+  g.A = A; g.lda = lda; g.B = B; g.ldb = ldb; g.SFB = SFB; g.ld_sfb = ld_sfb;
+  g.D = (float*)D; g.ldd = ldd; g.d_fmt = d_fmt; g.accum = accum;
+  bsm::GroupArgs gr{};
+  gr.offsets = offsets; gr.n = n_groups; gr.rows = (int32_t)rows; gr.stride_d = stride_d;
+  hipError_t e = bsm::launch_gemm_kept_wgrad(g, gr, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "bsm_gemm_grouped_wgrad_block_scale");
+  return ok();
+}
+
 // Sizes and operands that the loss and its gradient share. No launch has more than 2^31 - 1 workgroups of the smallest
 // tile (16 columns a row tile of 128), which these sizes keep.
 static int check_xent_sizes(int64_t rows, int64_t N, int64_t K) {

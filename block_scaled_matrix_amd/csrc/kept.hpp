@@ -3,6 +3,7 @@
 #pragma once
 #include <stdint.h>
 #include "bsm_device.hpp"
+#include "bsm_internal.hpp"
 #include "../../include/bsm.h"
 
 namespace bsm {
@@ -22,6 +23,8 @@ struct KeptArgs {
 hipError_t launch_block_scale_save(const KeptArgs& a, hipStream_t st);
 hipError_t launch_block_scale_restore(const KeptArgs& a, hipStream_t st);
 hipError_t launch_block_scale_ewise_grad(const KeptArgs& a, hipStream_t st);
+// As launch_gemm_grouped_wgrad, B the codes (dtype_b BSM_E4M3 or BSM_E5M2) and SFB their scales.
+hipError_t launch_gemm_kept_wgrad(const GemmArgs& a, const GroupArgs& gr, hipStream_t st);
 
 namespace kept {
 

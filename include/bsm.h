@@ -479,6 +479,21 @@ int bsm_block_scale_ewise_grad(int64_t rows, int64_t K, int32_t fmt, const uint8
                                int64_t ld_sf, int32_t dy_fmt, const void* dY, int64_t lddy, void* D, int64_t ldd,
                                const bsm_ewise* ew, void* stream);
 
+/* The weight gradient of bsm_gemm_grouped from activations kept in 8 bits (bsm_block_scale_save):
+ *   D_g[m,n] = (accum ? D_g[m,n] : 0) + sum_{r in group g} A(r,m) * B(r,n),
+ *   A(r,m) = A[r*lda + m] (dY, F16 or BF16),  B(r,n) = dec(B[r*ldb + n]) * 2^(SFB[r*ld_sfb + n/32] - 127),
+ * the result of bsm_gemm_grouped_wgrad on the restored activations, without them in memory: B(r,n) is taken in ab's format,
+ * which is exact inside its range (F16: finite values beyond 65504 become it and values below 2^-14 round to f16's
+ * subnormals; BF16: below 2^-126 likewise).
+ *   b_fmt:     BSM_E4M3 or BSM_E5M2; B 16-byte aligned, ldb >= N and a multiple of 16, at most 2^23;
+ *   SFB:       4-byte aligned, ld_sfb >= ceil(N/32) and a multiple of 4, at most 2^23. Both span whole rows; any N.
+ * Everything else as for bsm_gemm_grouped_wgrad; A, B, SFB and offsets must not overlap D. The same inputs give the same
+ * bits on every call. */
+int bsm_gemm_grouped_wgrad_block_scale(int64_t rows, int64_t M, int64_t N, int32_t n_groups, const int32_t* offsets, int32_t ab,
+                                       const void* A, int64_t lda, int32_t b_fmt, const uint8_t* B, int64_t ldb,
+                                       const uint8_t* SFB, int64_t ld_sfb, int32_t d_fmt, void* D, int64_t ldd, int64_t stride_d,
+                                       int accum, void* stream);
+
 /* Softmax cross entropy of a projection onto a large vocabulary, without keeping its logits: with z = X W^T in float32,
  *   lse[t] = log sum_n exp z(t,n),   loss[t] = lse[t] - z(t,label_t),
  * X(t,k) = X[t*ldx + k], W(n,k) = W[n*ldw + k].

@@ -178,3 +178,29 @@ def test_cross_entropy_grad_refusals():
     xent_grad(rows=0, dw=None, x=0, w=0, labels=0, lse=0, dloss=0, ws=0)
     for bad in (dict(rows=-1), dict(N=0), dict(K=-1), dict(piece=-1), dict(piece=1 << 31)):
         expect("BSM_E_SHAPE", bsm.bsm_gemm_cross_entropy_grad_workspace, **{**dict(rows=4, N=4, K=4, piece=0), **bad})
+
+
+def kept_wgrad(rows=100, M=64, N=100, n_groups=4, offsets=AT[8], ab="bf16", a=AT[0], lda=64, b_fmt="e4m3", b=AT[1], ldb=112, sf=AT[2],
+               ld_sf=4, d_fmt="f32", d=AT[3], ldd=104, stride_d=8192, accum=0):
+    bsm.bsm_gemm_grouped_wgrad_block_scale(rows, M, N, n_groups, offsets, ab, a, lda, b_fmt, b, ldb, sf, ld_sf, d_fmt, d, ldd, stride_d,
+                                           accum, 0)
+
+
+def test_kept_weight_gradient_refusals():
+    for name, bad in (("BSM_E_NULL", dict(offsets=0)), ("BSM_E_NULL", dict(a=0)), ("BSM_E_NULL", dict(b=0)), ("BSM_E_NULL", dict(sf=0)),
+                      ("BSM_E_NULL", dict(d=0)), ("BSM_E_ALIGN", dict(a=AT[0] + 8)), ("BSM_E_ALIGN", dict(b=AT[1] + 8)),
+                      ("BSM_E_ALIGN", dict(sf=AT[2] + 2)), ("BSM_E_ALIGN", dict(d=AT[3] + 4)), ("BSM_E_ALIGN", dict(lda=60)),
+                      ("BSM_E_ALIGN", dict(lda=68)), ("BSM_E_ALIGN", dict(ldb=96)), ("BSM_E_ALIGN", dict(ldb=104)),
+                      ("BSM_E_ALIGN", dict(ld_sf=3)), ("BSM_E_ALIGN", dict(N=129, ldb=144, ldd=132, stride_d=1 << 14, ld_sf=4)),
+                      ("BSM_E_ALIGN", dict(ldd=96)), ("BSM_E_ALIGN", dict(stride_d=8194)), ("BSM_E_ALIAS", dict(stride_d=6400)),
+                      ("BSM_E_SHAPE", dict(rows=-1)), ("BSM_E_SHAPE", dict(rows=1 << 31)), ("BSM_E_SHAPE", dict(M=-1)),
+                      ("BSM_E_SHAPE", dict(N=1 << 31)), ("BSM_E_SHAPE", dict(n_groups=65537)), ("BSM_E_SHAPE", dict(lda=1 << 23)),
+                      ("BSM_E_SHAPE", dict(ldb=1 << 24)), ("BSM_E_DTYPE", dict(ab="f32")), ("BSM_E_DTYPE", dict(b_fmt="e2m1")),
+                      ("BSM_E_DTYPE", dict(d_fmt="f16")), ("BSM_E_ARG", dict(accum=2)), ("BSM_E_ALIAS", dict(a=AT[3] + 64)),
+                      ("BSM_E_ALIAS", dict(b=AT[3] + 64)), ("BSM_E_ALIAS", dict(sf=AT[3] + 64)), ("BSM_E_ALIAS", dict(offsets=AT[3] + 8)),
+                      ("BSM_E_DTYPE", dict(a=torch.zeros(100, 64))), ("BSM_E_SHAPE", dict(b=torch.zeros(99, 112, dtype=torch.uint8))),
+                      ("BSM_E_SHAPE", dict(sf=torch.zeros(399, dtype=torch.uint8))), ("BSM_E_SHAPE", dict(offsets=torch.zeros(4, dtype=torch.int32))),
+                      ("BSM_E_ARG", dict(a=torch.zeros(100, 64, dtype=torch.bfloat16)))):
+        expect(name, kept_wgrad, **bad)
+    for none in (dict(M=0), dict(N=0), dict(n_groups=0, offsets=0)):
+        kept_wgrad(a=0, b=0, sf=0, d=0, **none)

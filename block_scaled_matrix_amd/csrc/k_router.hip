@@ -5,8 +5,8 @@
 //   loss = s E sum_e f_e P_e,   dl_te = g s E / n p_te (f_e - sum_j f_j p_tj)
 //
 // The gradient needs the counts but not P, so each direction reads the logits once and nothing but the
-// counts passes between them. LPR lanes share a row (a power of two, four experts a lane and vector, J
-// vectors), so a lane keeps the same experts for every row it sees: f stays in its registers, and P's
+// counts passes between them. LPR lanes share a row (4 to 16, beyond 256 experts 64; four experts a lane and
+// vector, J vectors: lanes of 16 reduce without LDS, and more values a lane are more loads in flight), so a lane keeps the same experts for every row it sees: f stays in its registers, and P's
 // column sums are register sums, joined at the end across the wave's rows, the workgroup's waves (LDS)
 // and the workgroups (a second launch over at most 256 of them), all in a fixed order. A lane adds at
 // most 64 rows in float32, then into a double: a sum over any number of rows keeps its bits. Counts are
@@ -53,18 +53,26 @@ __device__ __forceinline__ void load4(const void* p, int64_t i, int left, bool v
   for (int e = 0; e < 4; e++) v[e] = e < left ? load1<F>(p, i + e) : -INFINITY;
 }
 
-template <int LPR>
-__device__ __forceinline__ float row_max(float v) {
+// The row's reduction to all of its lanes: pairs, quads, halves and rows of 16 by the vector unit's own lane
+// permutations, beyond that through the LDS crossbar.
+template <int CTRL>
+__device__ __forceinline__ float lane_swap(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+template <int LPR, class OP>
+__device__ __forceinline__ float row_reduce(float v, OP op) {
+  v = op(v, lane_swap<0xB1>(v));                             // quad_perm 1 0 3 2
+  v = op(v, lane_swap<0x4E>(v));                             // quad_perm 2 3 0 1
+  if constexpr (LPR >= 8) v = op(v, lane_swap<0x141>(v));    // row_half_mirror
+  if constexpr (LPR >= 16) v = op(v, lane_swap<0x140>(v));   // row_mirror
 #pragma unroll
-  for (int d = 1; d < LPR; d *= 2) v = fmaxf(v, __shfl_xor(v, d));
+  for (int d = 16; d < LPR; d *= 2) v = op(v, __shfl_xor(v, d));
   return v;
 }
 template <int LPR>
-__device__ __forceinline__ float row_sum(float v) {
-#pragma unroll
-  for (int d = 1; d < LPR; d *= 2) v += __shfl_xor(v, d);
-  return v;
-}
+__device__ __forceinline__ float row_max(float v) { return row_reduce<LPR>(v, [](float a, float b) { return fmaxf(a, b); }); }
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v) { return row_reduce<LPR>(v, [](float a, float b) { return a + b; }); }
 
 // One row's softmax in this lane's registers: in the logits, out exp(l - max) and the factor 1 / sum. A
 // row without a finite logit above -infinity has no softmax: every probability is 0. NaN and +infinity
@@ -90,16 +98,22 @@ __device__ __forceinline__ float row_softmax(float (&v)[J][4]) {
   return s == 0.0f ? 0.0f : 1.0f / s;
 }
 
-// Whether a row has an expert among its ids, for every lane of the row; with `count`, counts them.
+// The row's id of this lane's place, -1 where it has none, and, once it is there: whether the row has an expert among
+// its ids, for every lane of the row; with `count`, counts them. (Ids past the first LPR are loaded where they are
+// looked at.)
+__device__ __forceinline__ int first_id(const RouterArgs& a, int64_t row, bool in, int lr) {
+  return in && lr < a.k ? a.ids[row * a.k + lr] : -1;
+}
 template <int LPR>
-__device__ __forceinline__ bool row_kept(const RouterArgs& a, int64_t row, bool in, int lr, int lane, int* count) {
+__device__ __forceinline__ bool row_kept(const RouterArgs& a, int64_t row, bool in, int lr, int lane, int id, int* count) {
   bool any = false;
-  for (int j0 = 0; j0 < a.k; j0 += LPR) {
-    const int j = j0 + lr;
-    const int id = in && j < a.k ? a.ids[row * a.k + j] : -1;
+  for (int j0 = 0;;) {
     const bool ok = id >= 0 && id < a.E;
     if (ok && count) atomicAdd(count + id, 1);
     any |= ok;
+    j0 += LPR;
+    if (j0 >= a.k) break;
+    id = in && j0 + lr < a.k ? a.ids[row * a.k + j0 + lr] : -1;
   }
   const uint64_t mine = (LPR == 64 ? ~0ull : ((1ull << LPR) - 1)) << (lane & ~(LPR - 1));
   return (__ballot(any) & mine) != 0;
@@ -136,13 +150,15 @@ __device__ __forceinline__ void finish(const RouterArgs& a, const int* cnt, int 
   }
 }
 
-// Where a workgroup's sums go: column sums (doubles) and counts in rows of an even number of experts, and its kept rows.
-struct Parts { double* sums; int* counts; int* kept; int ld; };
+// Where a workgroup's sums go: two experts' column sums and counts in 16 bytes, `pairs` of them a workgroup (the
+// column sums rounded to float32 once more: 2^-24 of each), and its kept rows.
+struct Pair { float s0, s1; int c0, c1; };
+struct Parts { Pair* sums; int* kept; int pairs; };
 
 // ONE: the only workgroup, which finishes too. Otherwise workgroup b's sums go to row b of `parts`.
 template <int F, int LPR, int J, bool ONE>
 __global__ __launch_bounds__(THREADS) void k_balance(RouterArgs a, Parts parts) {
-  constexpr int RPW = 64 / LPR, E4 = 4 * LPR * J, U = J == 1 ? 4 : 2;
+  constexpr int RPW = 64 / LPR, E4 = 4 * LPR * J, U = J <= 2 ? 4 : 2;
   __shared__ double total[E4];
   __shared__ double sums[E4 > 256 ? 1 : WAVES][E4];
   __shared__ int cnt[E4];
@@ -158,9 +174,11 @@ __global__ __launch_bounds__(THREADS) void k_balance(RouterArgs a, Parts parts) 
   for (int64_t r0 = ((int64_t)blockIdx.x * WAVES + w) * RPW; r0 < a.rows; r0 += U * step) {
     // U rows of logits are asked for before the first is worked on
     float v[U][J][4];
+    int id[U];
 #pragma unroll
     for (int u = 0; u < U; u++) {
       const int64_t row = r0 + u * step + sub;
+      id[u] = first_id(a, row, row < a.rows, lr);
 #pragma unroll
       for (int j = 0; j < J; j++) {
         const int e0 = 4 * (LPR * j + lr);
@@ -170,7 +188,7 @@ __global__ __launch_bounds__(THREADS) void k_balance(RouterArgs a, Parts parts) 
 #pragma unroll
     for (int u = 0; u < U; u++) {
       const int64_t row = r0 + u * step + sub;
-      const bool keep = row_kept<LPR>(a, row, row < a.rows, lr, lane, cnt);
+      const bool keep = row_kept<LPR>(a, row, row < a.rows, lr, lane, id[u], cnt);
       const float inv = row_softmax<LPR, J>(v[u]);
       kept += keep && lr == 0;
 #pragma unroll
@@ -226,16 +244,17 @@ __global__ __launch_bounds__(THREADS) void k_balance(RouterArgs a, Parts parts) 
     __shared__ double wred[WAVES];
     finish<THREADS>(a, cnt, kept_all, total, wscan, wred);
   } else {
-    for (int i = t; i < a.E; i += THREADS) {
-      parts.sums[(int64_t)blockIdx.x * parts.ld + i] = total[i];
-      parts.counts[(int64_t)blockIdx.x * parts.ld + i] = cnt[i];
-    }
+    // (experts past E have sums and counts of 0: their logits are taken as -infinity)
+    for (int i = t; i < parts.pairs; i += THREADS)
+      *(uint4*)(parts.sums + (int64_t)blockIdx.x * parts.pairs + i) =
+          make_uint4(__float_as_uint((float)total[2 * i]), __float_as_uint((float)total[2 * i + 1]), (uint32_t)cnt[2 * i],
+                     (uint32_t)cnt[2 * i + 1]);
     if (t == 0) parts.kept[blockIdx.x] = kept_all;
   }
 }
 
-// Joins the workgroups' sums: a lane adds two experts' of every slices-th workgroup (16 and 8 bytes a load: with 128
-// experts 16 of 256 workgroups, all in flight at once), then the slices meet in LDS.
+// Joins the workgroups' sums: a lane adds a pair of every slices-th workgroup (with 128 experts 16 of 256, all in flight
+// at once), then the slices meet in LDS.
 __global__ __launch_bounds__(JOIN) void k_balance_join(RouterArgs a, Parts parts, int groups) {
   __shared__ double red[2 * JOIN];
   __shared__ int num[2 * JOIN];
@@ -244,28 +263,35 @@ __global__ __launch_bounds__(JOIN) void k_balance_join(RouterArgs a, Parts parts
   __shared__ int kept_all;
   __shared__ int wscan[JOIN / 64];
   __shared__ double wred[JOIN / 64];
-  const int t = threadIdx.x, pairs = (a.E + 1) / 2;
+  const int t = threadIdx.x;
   int cols = 1;
-  while (cols < pairs) cols *= 2;   // at most 512
+  while (cols < parts.pairs) cols *= 2;   // at most 512
   const int slices = JOIN / cols, s = t / cols, c = t & (cols - 1);
   double d0 = 0.0, d1 = 0.0;
-  int n0 = 0, n1 = 0;
-  if (c < pairs) {
-#pragma unroll 16
-    for (int b = s; b < groups; b += slices) {
-      const double2 d = *(const double2*)(parts.sums + (int64_t)b * parts.ld + 2 * c);
-      const int2 n = *(const int2*)(parts.counts + (int64_t)b * parts.ld + 2 * c);
-      d0 += d.x; n0 += n.x;
-      if (2 * c + 1 < a.E) { d1 += d.y; n1 += n.y; }
+  int n0 = 0, n1 = 0, kept = 0;
+  if (t < 64)
+    for (int b = t; b < groups; b += 64) kept += parts.kept[b];
+  if (c < parts.pairs) {
+    constexpr int AT_ONCE = 16;
+    for (int b0 = s; b0 < groups; b0 += AT_ONCE * slices) {
+      uint4 x[AT_ONCE];
+#pragma unroll
+      for (int i = 0; i < AT_ONCE; i++) {
+        const int b = b0 + i * slices;
+        x[i] = b < groups ? *(const uint4*)(parts.sums + (int64_t)b * parts.pairs + c) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < AT_ONCE; i++) {
+        d0 += __uint_as_float(x[i].x); d1 += __uint_as_float(x[i].y);
+        n0 += (int)x[i].z; n1 += (int)x[i].w;
+      }
     }
   }
   red[2 * t] = d0; red[2 * t + 1] = d1;
   num[2 * t] = n0; num[2 * t + 1] = n1;
   if (t < 64) {
-    int k = 0;
-    for (int b = t; b < groups; b += 64) k += parts.kept[b];
-    k = grouped::wave_inclusive_scan(k);
-    if (t == 63) kept_all = k;
+    kept = grouped::wave_inclusive_scan(kept);
+    if (t == 63) kept_all = kept;
   }
   __syncthreads();
   for (int i = t; i < 2 * cols; i += JOIN) {
@@ -299,13 +325,14 @@ __global__ __launch_bounds__(256) void k_balance_grad(RouterArgs a, RouterGradAr
   for (int64_t r0 = ((int64_t)blockIdx.x * 4 + w) * RPW; r0 < a.rows; r0 += step) {
     const int64_t row = r0 + sub;
     const bool in = row < a.rows;
+    const int id = first_id(a, row, in, lr);
     float v[J][4];
 #pragma unroll
     for (int j = 0; j < J; j++) {
       const int e0 = 4 * (LPR * j + lr);
       load4<F>(a.logits, row * a.ldl + e0, in ? a.E - e0 : 0, a.vec, v[j]);
     }
-    const bool keep = row_kept<LPR>(a, row, in, lr, lane, nullptr);
+    const bool keep = row_kept<LPR>(a, row, in, lr, lane, id, nullptr);
     const float inv = row_softmax<LPR, J>(v);
     float dot = 0.0f;
 #pragma unroll
@@ -357,7 +384,7 @@ __global__ __launch_bounds__(256) void k_balance_grad(RouterArgs a, RouterGradAr
   }
 }
 
-int lanes_per_row(int E) { return E <= 16 ? 4 : E <= 32 ? 8 : E <= 64 ? 16 : E <= 128 ? 32 : 64; }
+int lanes_per_row(int E) { return E <= 16 ? 4 : E <= 32 ? 8 : E <= 256 ? 16 : 64; }
 
 int64_t groups_of(int64_t rows, int E) {
   if (rows * E <= kOneGroup) return 1;
@@ -372,8 +399,8 @@ void with_layout(int E, FN f) {
   if (E <= 16) f(integral_constant<int, 4>{}, integral_constant<int, 1>{});
   else if (E <= 32) f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
   else if (E <= 64) f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
-  else if (E <= 128) f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
-  else if (E <= 256) f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+  else if (E <= 128) f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+  else if (E <= 256) f(integral_constant<int, 16>{}, integral_constant<int, 4>{});
   else if (E <= 512) f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
   else f(integral_constant<int, 64>{}, integral_constant<int, 4>{});
 }
@@ -399,18 +426,17 @@ void launch_grad(const RouterArgs& a, const RouterGradArgs& g, hipStream_t st) {
 }  // namespace
 
 int64_t balance_workspace(int64_t rows, int E) {
-  const int64_t n = groups_of(rows, E), ld = (E + 1) / 2 * 2;
-  return n == 1 ? 0 : n * (ld * (int64_t)(sizeof(double) + sizeof(int)) + (int64_t)sizeof(int));
+  const int64_t n = groups_of(rows, E);
+  return n == 1 ? 0 : n * ((E + 1) / 2 * (int64_t)sizeof(Pair) + (int64_t)sizeof(int));
 }
 
 hipError_t launch_router_balance(const RouterArgs& a, void* workspace, hipStream_t st) {
   const int64_t n = groups_of(a.rows, a.E);
   Parts parts{};
+  parts.pairs = (a.E + 1) / 2;
   if (n > 1) {
-    parts.ld = (a.E + 1) / 2 * 2;
-    parts.sums = (double*)workspace;
-    parts.counts = (int*)(parts.sums + n * parts.ld);
-    parts.kept = parts.counts + n * parts.ld;
+    parts.sums = (Pair*)workspace;
+    parts.kept = (int*)(parts.sums + n * parts.pairs);
   }
   if (a.l_fmt == BSM_F32) launch_balance<BSM_F32>(a, parts, n, st);
   else if (a.l_fmt == BSM_BF16) launch_balance<BSM_BF16>(a, parts, n, st);

@@ -205,9 +205,10 @@ struct NoMore {
 // Q > 1: Q times four waves share the tile, wave w of part q taking every Q-th K tile from the q-th on in
 // LDS of its own (part q's starts at part 0's + q * LDS); part 0 adds the sums in part order and
 // stores. All waves of the workgroup come here together.
+// first < the whole K tiles: the sum begins at that tile and wraps (the same for every call of the tile, so the bits stay).
 template <int DT, int BM, bool AK, bool BKM, int BK = 64, class MORE = NoMore, int LDS = LDS_BYTES, int Q = 1>
 __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, uint8_t* lds, int lane, int w,
-                                     const MORE& more = MORE(), int q = 0) {
+                                     const MORE& more = MORE(), int q = 0, int first = 0) {
   typedef Tile<BM, AK, BK> TA;
   typedef Tile<BN, BKM, BK> TB;
   constexpr int MI = BM / 32, STAGE = TA::BYTES + TB::BYTES, NST = LDS / STAGE, PER = TA::COPIES + TB::COPIES;
@@ -228,7 +229,9 @@ __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, 
   // The copies of this part's it-th K tile; past the last one they re-read it into a stage that nobody
   // reads again, so that the counts waited for stay fixed.
   auto issue = [&](int it, int stage) {
-    const int64_t k0 = (int64_t)min(it * Q + q, nfull - 1) * BK;
+    int kt = min(it * Q + q, nfull - 1) + first;
+    if (kt >= nfull) kt -= nfull;
+    const int64_t k0 = (int64_t)kt * BK;
     uint64_t ga, gb;
     gemm::sgpr_base2(TA::base(A, a.lda, m0, k0), TB::base(B, a.ldb, n0, k0), ga, gb);
     const uint32_t at = lds0 + stage * STAGE;

@@ -22,7 +22,7 @@ namespace {
 
 constexpr int THREADS = 512, WAVES = THREADS / 64, JOIN = 1024;
 constexpr int kMaxGroups = 256;
-constexpr int64_t kOneGroup = 16384;
+constexpr int64_t kOneGroup = 32768;
 
 template <int F>
 __device__ __forceinline__ float load1(const void* p, int64_t i) {
@@ -270,6 +270,7 @@ __global__ __launch_bounds__(JOIN) void k_balance_join(RouterArgs a, Parts parts
   double d0 = 0.0, d1 = 0.0;
   int n0 = 0, n1 = 0, kept = 0;
   if (t < 64)
+#pragma unroll 4
     for (int b = t; b < groups; b += 64) kept += parts.kept[b];
   if (c < parts.pairs) {
     constexpr int AT_ONCE = 16;
@@ -297,6 +298,7 @@ __global__ __launch_bounds__(JOIN) void k_balance_join(RouterArgs a, Parts parts
   for (int i = t; i < 2 * cols; i += JOIN) {
     double d = 0.0;
     int n = 0;
+#pragma unroll 8
     for (int q = 0; q < slices; q++) { d += red[2 * q * cols + i]; n += num[2 * q * cols + i]; }
     total[i] = d;
     cnt[i] = n;
@@ -310,37 +312,54 @@ template <int F, int LPR, int J>
 __global__ __launch_bounds__(256) void k_balance_grad(RouterArgs a, RouterGradArgs g) {
   constexpr int RPW = 64 / LPR;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, lr = lane & (LPR - 1), sub = lane / LPR;
-  const int n = a.counts[a.E];
-  const float over = n > 0 ? 1.0f / ((float)a.k * (float)n) : 0.0f;
-  const float coef = n > 0 ? (g.dloss ? *g.dloss : 1.0f) * a.scale * (float)a.E / (float)n : 0.0f;
-  float f[J][4];
-#pragma unroll
-  for (int j = 0; j < J; j++)
-#pragma unroll
-    for (int e = 0; e < 4; e++) {
-      const int i = 4 * (LPR * j + lr) + e;
-      f[j][e] = i < a.E ? (float)a.counts[i] * over : 0.0f;
-    }
   const int64_t step = (int64_t)gridDim.x * 4 * RPW;
-  for (int64_t r0 = ((int64_t)blockIdx.x * 4 + w) * RPW; r0 < a.rows; r0 += step) {
-    const int64_t row = r0 + sub;
+  int64_t r0 = ((int64_t)blockIdx.x * 4 + w) * RPW;
+  // a row's logits and id are asked for before the row ahead of them (the first: before the counts) is worked on
+  float v[J][4];
+  int id;
+  auto load = [&](int64_t row) {
     const bool in = row < a.rows;
-    const int id = first_id(a, row, in, lr);
-    float v[J][4];
+    id = first_id(a, row, in, lr);
 #pragma unroll
     for (int j = 0; j < J; j++) {
       const int e0 = 4 * (LPR * j + lr);
       load4<F>(a.logits, row * a.ldl + e0, in ? a.E - e0 : 0, a.vec, v[j]);
     }
-    const bool keep = row_kept<LPR>(a, row, in, lr, lane, id, nullptr);
-    const float inv = row_softmax<LPR, J>(v);
+  };
+  load(r0 + sub);
+  float f[J][4];
+  int c[J][4];
+  const int n = a.counts[a.E];
+  const float dl = g.dloss ? *g.dloss : 1.0f;
+#pragma unroll
+  for (int j = 0; j < J; j++)
+#pragma unroll
+    for (int e = 0; e < 4; e++) c[j][e] = a.counts[min(4 * (LPR * j + lr) + e, a.E)];
+  const float over = n > 0 ? 1.0f / ((float)a.k * (float)n) : 0.0f;
+  const float coef = n > 0 ? dl * a.scale * (float)a.E / (float)n : 0.0f;
+#pragma unroll
+  for (int j = 0; j < J; j++)
+#pragma unroll
+    for (int e = 0; e < 4; e++) f[j][e] = 4 * (LPR * j + lr) + e < a.E ? (float)c[j][e] * over : 0.0f;
+  for (; r0 < a.rows; r0 += step) {
+    const int64_t row = r0 + sub;
+    const bool in = row < a.rows;
+    float p[J][4];
+#pragma unroll
+    for (int j = 0; j < J; j++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) p[j][e] = v[j][e];
+    const int now = id;
+    if (r0 + step < a.rows) load(row + step);
+    const bool keep = row_kept<LPR>(a, row, in, lr, lane, now, nullptr);
+    const float inv = row_softmax<LPR, J>(p);
     float dot = 0.0f;
 #pragma unroll
     for (int j = 0; j < J; j++)
 #pragma unroll
       for (int e = 0; e < 4; e++) {
-        v[j][e] *= inv;
-        dot += f[j][e] * v[j][e];
+        p[j][e] *= inv;
+        dot += f[j][e] * p[j][e];
       }
     dot = row_sum<LPR>(dot);
     if (!in) continue;
@@ -350,34 +369,34 @@ __global__ __launch_bounds__(256) void k_balance_grad(RouterArgs a, RouterGradAr
       if (left <= 0) continue;
       float o[4];
 #pragma unroll
-      for (int e = 0; e < 4; e++) o[e] = keep ? coef * v[j][e] * (f[j][e] - dot) : 0.0f;
+      for (int e = 0; e < 4; e++) o[e] = keep ? coef * p[j][e] * (f[j][e] - dot) : 0.0f;
       const int64_t at = row * g.ldd + e0;
       if (g.d_fmt == BSM_F32) {
-        float* p = (float*)g.D + at;
+        float* q = (float*)g.D + at;
         if (g.vec && left >= 4) {
           f32x4 x = {o[0], o[1], o[2], o[3]};
-          if (g.accum) x += *(const f32x4*)p;
-          *(f32x4*)p = x;
+          if (g.accum) x += *(const f32x4*)q;
+          *(f32x4*)q = x;
         } else {
 #pragma unroll
           for (int e = 0; e < 4; e++)
-            if (e < left) p[e] = g.accum ? p[e] + o[e] : o[e];
+            if (e < left) q[e] = g.accum ? q[e] + o[e] : o[e];
         }
       } else if constexpr (F != BSM_F32) {
-        uint16_t* p = (uint16_t*)g.D + at;
+        uint16_t* q = (uint16_t*)g.D + at;
         auto bits = [](float x) { return F == BSM_BF16 ? f32_to_bf16_bits(x) : f32_to_f16_bits(x); };
         auto val = [](uint16_t h) { return F == BSM_BF16 ? bf16_bits_to_f32(h) : f16_bits_to_f32(h); };
         if (g.vec && left >= 4) {
           if (g.accum) {
-            const uint2 y = *(const uint2*)p;
+            const uint2 y = *(const uint2*)q;
             o[0] += val((uint16_t)y.x); o[1] += val((uint16_t)(y.x >> 16));
             o[2] += val((uint16_t)y.y); o[3] += val((uint16_t)(y.y >> 16));
           }
-          *(uint2*)p = make_uint2(bits(o[0]) | (uint32_t)bits(o[1]) << 16, bits(o[2]) | (uint32_t)bits(o[3]) << 16);
+          *(uint2*)q = make_uint2(bits(o[0]) | (uint32_t)bits(o[1]) << 16, bits(o[2]) | (uint32_t)bits(o[3]) << 16);
         } else {
 #pragma unroll
           for (int e = 0; e < 4; e++)
-            if (e < left) p[e] = bits(g.accum ? val(p[e]) + o[e] : o[e]);
+            if (e < left) q[e] = bits(g.accum ? val(q[e]) + o[e] : o[e]);
         }
       }
     }

@@ -14,6 +14,8 @@
 //    conversion at the fragment would be once a wave and need a scale per element; one barrier a K tile, as without it;
 //  - K tiles of 32 rows: 256 rows x 128 columns take 79 KiB of LDS, two workgroups a CU.
 #pragma once
+#include <utility>
+#include "gemm_dense_tile.hpp"
 #include "gemm_mid_tile.hpp"
 #include "kept.hpp"
 
@@ -169,6 +171,192 @@ __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, 
   mid::store<DT, MI, 0, MC>(a, m0 + wa, n0 + wb, lane, acc, lds + MC * 4096 * w);
   mid::store<DT, MI, MC, MC>(a, m0 + wa + 16 * MC, n0 + wb, lane, acc, lds + MC * 4096 * w);
 }
+
+// ---- 256 x 256 tiles: the dense GEMM's (gemm_dense_tile.hpp) with X's k-rows made in LDS ---------------------------------
+// Four waves of 128 x 128, K tiles of 64: 96 KiB through LDS for 256 x 256 x 32 products where two 256 x 128 tiles take 164.
+// Y's two stages are the dense tile's. One buffer holds X's 16-bit k-rows: its fragments are in registers by the middle of a
+// K tile's first 32-K step, so between that step's barrier and the next tile's first reads the waves convert the next
+// tile's codes into it, a unit of eight codes a lane every ninth MFMA slot, each wave its own copies' rows. The codes come
+// through a ring of three stages, a K tile further ahead than Y, so that they are there when the conversion begins.
+namespace large {
+
+// LDS by its byte address.
+template <class T>
+__device__ __forceinline__ BSM_LDS T* at_lds(uint32_t address) { return (BSM_LDS T*)(uintptr_t)address; }
+
+constexpr int BM = 256, BK = 64, COPIES = 13;               // a K tile's copies: 8 of Y, 4 of codes, 1 of scale words
+constexpr int A_STAGE = BM * BK * 2, X_WIDE = BK * 256 * 2, X_RAW = BK * 256, X_SCALES = 4 * 256;
+constexpr int WIDE_AT = 2 * A_STAGE, RAW_AT = WIDE_AT + X_WIDE, SCALES_AT = RAW_AT + 3 * X_RAW;
+constexpr int LDS_BYTES = SCALES_AT + 3 * X_SCALES;
+static_assert(LDS_BYTES >= 4 * 32768 && LDS_BYTES <= 160 * 1024, "the stores' regions");
+
+// The 64 MFMAs of a 32-K step with their side work, as dense::mfma_step_il, the slots as constants (a loop over this much
+// side work is not unrolled any more).
+template <int DT, int FROM, class SIDE, int... I>
+__device__ __forceinline__ void mfma_steps(const dense::Frags& f, f32x4 (&acc)[8][8], SIDE side, std::integer_sequence<int, I...>) {
+  auto one = [&](auto i) {
+    constexpr int mt = decltype(i)::value >> 3, nt = decltype(i)::value & 7;
+    asm volatile("" : "+a"(acc[mt][nt])::"memory");
+    acc[mt][nt] = dense::mfma<DT>(f.b[nt], f.a[mt], acc[mt][nt]);
+    asm volatile("" : "+a"(acc[mt][nt])::"memory");
+    side(std::integral_constant<int, FROM + decltype(i)::value>{});
+  };
+  (one(std::integral_constant<int, I>{}), ...);
+}
+
+template <int DT, int FMT>
+__device__ __forceinline__ void product(const GemmArgs& a, int64_t m0, int64_t n0, uint8_t* lds, int lane, int w, f32x4 (&acc)[8][8]) {
+  using namespace dense;
+  const int wa = 128 * (w >> 1), wb = 128 * (w & 1);
+  const uint16_t* A = (const uint16_t*)a.A;
+  const uint8_t* B = (const uint8_t*)a.B;
+#pragma unroll
+  for (int i = 0; i < 8; i++)
+#pragma unroll
+    for (int j = 0; j < 8; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // Y: copy j of wave w holds k-rows 2w + 8j and the one behind (dense::dma_offsets); the swizzle differs between even
+  // and odd j alone, so two offsets and a scalar step of 16 rows make all eight. Codes: copy j holds k-rows 4(w + 4j) ..
+  // + 3, 16 codes a lane. Scale words: lane l the word l%2 of the wave's row l/2 (a row's second word may lie past its
+  // end: the first again).
+  uint32_t ao[2];
+  // The K tiles: a group's rows seldom are a multiple of 64, and a tail behind the loop (more matrix instructions on the same
+  // accumulators) made the compiler move up to 700 accumulators about in every turn of the loop. So the first tile is the
+  // short one, filled through registers with zeros past its rows; the others follow by copies, and the loop is all there
+  // is. With one tile alone the copies, whose counts stay, read the first row over and over.
+  const int nt = (int)((a.K + BK - 1) / BK), head = (int)a.K - BK * (nt - 1);
+  const int64_t lda = nt > 1 ? a.lda : 0, ldb = nt > 1 ? a.ldb : 0, lds_row = nt > 1 ? a.ld_sfb : 0;
+#pragma unroll
+  for (int j = 0; j < 2; j++) {
+    const int kr = 2 * (w + 4 * j) + (lane >> 5), c = (lane & 31) ^ (int)mn_swz(kr);
+    ao[j] = (uint32_t)((kr * lda + min(m0 + 8 * c, (a.M - 1) & ~int64_t(7)) - m0) * 2);
+  }
+  const uint32_t bo = (uint32_t)((4 * w + (lane >> 4)) * ldb + min(n0 + 16 * (lane & 15), (a.N - 1) & ~int64_t(15)) - n0);
+  const int r16 = (lane >> 1) & 15;
+  const uint32_t so = (uint32_t)((4 * (w + 4 * (r16 >> 2)) + (r16 & 3)) * lds_row + (n0 / 32 + 4 < a.ld_sfb ? 4 * (lane & 1) : 0));
+  const uint32_t lds0 = gemm::lds_addr(lds);
+  auto copy_a = [&](uint64_t base, int stage, int j) {
+    gemm::dma16u(base + (uint64_t)((j >> 1) * 32 * lda), ao[j & 1], lds0 + stage * A_STAGE + 1024 * (w + 4 * j));
+  };
+  auto copy_codes = [&](uint64_t base, int slot, int j) {
+    gemm::dma16u(base + (uint64_t)(16 * j * ldb), bo, lds0 + RAW_AT + slot * X_RAW + 1024 * (w + 4 * j));
+  };
+  auto copy_scales = [&](uint64_t base, int slot) { gemm::dma4u(base, so, lds0 + SCALES_AT + slot * X_SCALES + 256 * w); };
+  // bases of tile t >= 1 (past the last: the last again, into a stage that nobody reads)
+  auto row_of = [&](int t) { return (int64_t)max(BK * (min(t, nt - 1) - 1) + head, 0); };
+  auto at_a = [&](int t) { return A + row_of(t) * lda + m0; };
+  auto at_codes = [&](int t) { return B + row_of(t) * ldb + n0; };
+  auto at_scales = [&](int t) { return a.SFB + row_of(t) * lds_row + n0 / 32; };
+  // unit u = 2j + h: eight codes of k-row 4(w + 4j) + 2h + l/32 at column 8(l%32). The k-row's swizzle does not depend on
+  // j, so two addresses and constant steps make all eight stores; loads are one address a stage.
+  uint32_t to[2];
+#pragma unroll
+  for (int h = 0; h < 2; h++) {
+    const int kr = 4 * w + 2 * h + (lane >> 5);
+    to[h] = lds0 + WIDE_AT + (uint32_t)(kr * 512 + (((lane & 31) ^ (int)mn_swz(kr)) << 4));
+  }
+  const uint32_t from = lds0 + RAW_AT + 1024 * w + 8 * lane;
+  const uint32_t from_scale = lds0 + SCALES_AT + 256 * w + 8 * (lane >> 5) + ((lane & 31) >> 2);
+  auto put = [&](int u, uint32_t c0, uint32_t c1, uint32_t code) {
+    const uint4 x = widen8<DT, FMT>(c0, c1, code);
+    *at_lds<u32x4>(to[u & 1] + 8192 * (u >> 1)) = u32x4{x.x, x.y, x.z, x.w};
+  };
+  u32x2 c;
+  uint32_t code;
+  auto take = [&](int u, int slot) {
+    c = *at_lds<u32x2>(from + slot * X_RAW + 4096 * (u >> 1) + 512 * (u & 1));
+    code = *at_lds<uint8_t>(from_scale + slot * X_SCALES + 32 * (u >> 1) + 16 * (u & 1));
+  };
+  // Fragment addresses (dense::frag_addr): the swizzle depends on the lane alone and block t flips bits 5 .. 7, so one address
+  // an operand makes all of them; step s and half h are constants. Taken anew every K tile (an asm that claims to change
+  // it): otherwise the compiler keeps every address of both stages in registers and the accumulators move about for them.
+  const int G = lane >> 4, i4 = lane & 15;
+  const uint32_t sw = (uint32_t)(4 * (i4 >> 2) ^ 2 * (G & 1));
+  auto frag_base = [&](int wbase) {
+    return (uint32_t)((8 * G + (i4 >> 2)) * 512 + ((((wbase >> 3) + ((i4 & 3) >> 1)) ^ sw) << 4) + 8 * (i4 & 1));
+  };
+  const uint32_t fa = lds0 + frag_base(wa), fb = lds0 + WIDE_AT + frag_base(wb);
+  auto frag = [&](uint32_t base, int s, int t) {
+    uint2 h[2];
+#pragma unroll
+    for (int q = 0; q < 2; q++)
+      h[q] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(at_lds<i16x4>((base ^ (32u * t)) + 16384 * s + 2048 * q)));
+    return make_uint4(h[0].x, h[0].y, h[1].x, h[1].y);
+  };
+  // read r of a step's fragments, in the order of dense::read_one
+  auto read = [&](uint32_t ba, uint32_t bb, int s, int r, Frags& f) {
+    if (r >= 1 && r <= 8) f.b[r - 1] = frag(bb, s, r - 1);
+    else f.a[r == 0 ? 0 : r - 8] = frag(ba, s, r == 0 ? 0 : r - 8);
+  };
+  Frags f0, f1;
+  if (nt > 0) {
+    auto issue_codes = [&](int t, int slot) {
+      uint64_t gb, gs;
+      gemm::sgpr_base2(at_codes(t), at_scales(t), gb, gs);
+#pragma unroll
+      for (int j = 0; j < 4; j++) copy_codes(gb, slot, j);
+      copy_scales(gs, slot);
+    };
+    // the first tile: this wave's rows of codes and of Y
+    const int64_t col = min(n0 + 8 * (lane & 31), (a.N - 1) & ~int64_t(7));
+#pragma unroll
+    for (int u = 0; u < 8; u++) {
+      const int row = 4 * (w + 4 * (u >> 1)) + 2 * (u & 1) + (lane >> 5);
+      uint2 x = make_uint2(0, 0);
+      uint32_t sc = 0;
+      if (row < head) {
+        x = *(const uint2*)(B + row * a.ldb + col);
+        sc = a.SFB[row * a.ld_sfb + col / 32];
+      }
+      put(u, x.x, x.y, sc);
+    }
+    fill_tile_masked<false>(A, a.lda, m0, a.M, 0, head, lds, w, lane);
+    issue_codes(1, 1);
+    const uint64_t base = gemm::sgpr_base(at_a(1));
+#pragma unroll
+    for (int j = 0; j < 8; j++) copy_a(base, 1, j);
+    issue_codes(2, 2);
+    gemm::stage_barrier<COPIES>();   // the first tile is written, the codes of the next have landed
+#pragma unroll
+    for (int r = 0; r < 16; r++) read(fa, fb, 0, r, f0);
+  }
+  int slot = 0;   // tile kt's codes
+  for (int kt = 0; kt < nt; kt++) {
+    const int st = kt & 1, next = slot == 2 ? 0 : slot + 1;
+    uint32_t ta = fa + st * A_STAGE, na = fa + (st ^ 1) * A_STAGE, tb = fb;
+    asm volatile("" : "+v"(ta), "+v"(na), "+v"(tb));
+    uint64_t ga, gb;
+    gemm::sgpr_base2(at_a(kt + 2), at_codes(kt + 3), ga, gb);
+    const uint64_t gs = gemm::sgpr_base(at_scales(kt + 3));
+    auto copy = [&](int d) {
+      if (d < 8) copy_a(ga, st, d);
+      else if (d < 12) copy_codes(gb, slot, d - 8);
+      else copy_scales(gs, slot);
+    };
+    // Side work by MFMA slot g, as in dense::tile_product: the second step's fragments; barrier, nobody reads this tile any
+    // more; the copies of Y's tile kt + 2 and the codes of kt + 3; the codes of kt + 1 into the k-rows; barrier, Y's tile
+    // kt + 1 has landed (and the codes of kt + 2); the next tile's first fragments.
+    constexpr int C0 = 32, CPS = 5, V0 = 34, VPS = 9, LATER = 6, B2 = 107, G2 = 108;
+    static_assert(C0 + CPS * (COPIES - 1) < B2 && V0 + 7 * VPS + LATER < B2 && G2 + 16 <= 128, "side-work schedule");
+    auto side = [&](auto slot_no) {
+      constexpr int g = decltype(slot_no)::value;
+      if constexpr (g < C0 && g % 2 == 0) read(ta, tb, 1, g / 2, f1);
+      if constexpr (g == C0 - 1) gemm::lds_barrier();
+      if constexpr (g >= C0 && (g - C0) % CPS == 0 && (g - C0) / CPS < COPIES) copy((g - C0) / CPS);
+      if constexpr (g >= V0 && (g - V0) % VPS == 0 && (g - V0) / VPS < 8) take((g - V0) / VPS, next);
+      if constexpr (g >= V0 + LATER && (g - V0 - LATER) % VPS == 0 && (g - V0 - LATER) / VPS < 8) put((g - V0 - LATER) / VPS, c[0], c[1], code);
+      if constexpr (g == B2) gemm::stage_barrier<COPIES>();
+      if constexpr (g >= G2 && g - G2 < 16) read(na, tb, 0, g - G2, f0);
+    };
+    pin_frags(f0);
+    mfma_steps<DT, 0>(f0, acc, side, std::make_integer_sequence<int, 64>{});
+    pin_frags(f1);
+    mfma_steps<DT, 64>(f1, acc, side, std::make_integer_sequence<int, 64>{});
+    slot = next;
+  }
+  gemm::stage_barrier<0>();
+}
+
+}  // namespace large
 
 }  // namespace keptmm
 }  // namespace bsm

@@ -1,18 +1,17 @@
 // gemm_kept_tile.hpp - output tiles of the weight gradient D = Y^T X whose X is kept as 8-bit codes with E8M0 scales
-// (kept.hpp), on gfx950 16-bit MFMA: BM rows (Y's columns) x 128 columns (X's), four waves in a 2 x 2 grid.
+// (kept.hpp), on gfx950 16-bit MFMA.
 //
 // The scales run along X's columns, the sum along its rows, so no scale can leave the sum: every code is multiplied by its
 // own scale before the product. A code times its scale has at most four significant bits: as bf16 (as f16 inside that
 // format's range) it is exact, and the product and its sums are those of bsm_gemm_grouped_wgrad on the restored X.
 //
-//  - Y streams HBM -> LDS by direct copies into a ring of three stages, as in gemm_mid_tile.hpp. X's codes and scale words
-//    stream the same way into a ring of their own, one K tile ahead of Y's: half the bytes of 16-bit rows through
-//    HBM, the copy path and the ring;
-//  - while the MFMAs work on K tile t, each wave takes the rows of codes that it copied itself for tile t + 1 out of LDS,
-//    converts them (eight codes a lane: four conversions with the scale in bf16) and writes the 16-bit k-rows that the
-//    fragments are read from, into the second of two buffers. Each code is converted once a workgroup, where
-//    conversion at the fragment would be once a wave and need a scale per element; one barrier a K tile, as without it;
-//  - K tiles of 32 rows: 256 rows x 128 columns take 79 KiB of LDS, two workgroups a CU.
+// Y streams HBM -> LDS by direct copies, as in the other tiles. X's codes and scale words stream the same way: half the
+// bytes of 16-bit rows. Each wave takes the rows of codes that it copied itself out of LDS, converts them (eight codes a lane:
+// four conversions with the scale in bf16) and writes the 16-bit k-rows that the fragments are read from. So a code
+// is converted once a workgroup, where conversion at the fragment would be once a wave and need a scale per element. (Loads
+// into registers instead of copies would make the compiler wait for all copies in flight: it does not count them.)
+// A group's rows seldom are a multiple of a K tile. The first tile is the short one, filled through registers with zeros
+// past its rows, and the others follow by copies.
 #pragma once
 #include <utility>
 #include "gemm_dense_tile.hpp"
@@ -22,16 +21,7 @@
 namespace bsm {
 namespace keptmm {
 
-constexpr int BN = 128, BK = 32;
-constexpr int RAW = BK * BN, SCALES = 4 * 256;       // codes of a K tile; its scale words, 256 bytes a wave
-constexpr int WIDE = BK * BN * 2;                    // the same as 16-bit k-rows
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
-typedef mid::Tile<BN, false, BK> TB;                 // their layout
-
-template <int BM>
-constexpr int a_bytes() { return BM * BK * 2; }
-template <int BM>
-constexpr int lds_bytes() { return 3 * (a_bytes<BM>() + RAW + SCALES) + 2 * WIDE; }
 
 // Eight codes times 2^(code - 127) as the operand's 16-bit format.
 template <int DT, int FMT>
@@ -59,121 +49,177 @@ __device__ __forceinline__ uint4 widen8(uint32_t c0, uint32_t c1, uint32_t code)
   }
 }
 
-// The tile at (m0, n0) of the product that `a` describes: A is Y (K rows of M), B the codes (K rows of N bytes), SFB the
-// scales (ld_sfb bytes a row); K the group's rows. All four waves of the workgroup come here.
-template <int DT, int FMT, int BM>
-__device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, uint8_t* lds, int lane, int w) {
-  typedef mid::Tile<BM, false, BK> TA;
-  constexpr int MI = BM / 32, PER = TA::COPIES + 2, RING = 3;
-  uint8_t* raw = lds + RING * TA::BYTES;
-  uint8_t* words = raw + RING * RAW;
-  uint8_t* wide = words + RING * SCALES;
-  const int wa = (BM / 2) * (w >> 1), wb = 64 * (w & 1);
+// ---- 128 x 128 and 64 x 64 tiles ---------------------------------------------------------------------------------------
+// Four waves, K tiles of 32 in two stages, 34 KiB of LDS (64 x 64: three, 31 KiB): four workgroups share a CU, and one converts or
+// stores while another multiplies. With few tiles and long groups Q sets of four waves share a tile instead, each every Q-th K
+// tile in LDS of its own; their sums meet in a fixed order.
+namespace mid2 {
+
+constexpr int BK = 32;
+
+// BK k-rows of ROWS 16-bit values: chunk c of k-row kr at c ^ swz(kr), so that the eight 32-byte pieces that a half-wave's
+// transposing read touches (k-rows 0 .. 3 and 8 .. 11 of 16) lie in all 64 banks.
+template <int ROWS>
+struct Tile {
+  static constexpr int KROW = ROWS * 2, CPK = KROW / 16, BYTES = BK * KROW, COPIES = BYTES / 4096;
+  __device__ static int swz(int kr) { return ROWS == 128 ? 4 * (kr & 3) ^ 2 * ((kr >> 3) & 1) : 2 * ((kr >> 1) & 1) + 4 * ((kr >> 3) & 1); }
+  // chunk p of the tile as its k-row and column
+  __device__ static int kr(int p) { return p / CPK; }
+  __device__ static int col(int p) { return 8 * ((p % CPK) ^ swz(p / CPK)); }
+  __device__ static uint4 frag(const uint8_t* tile, int lane, int r0) {
+    const int G = lane >> 4, i = lane & 15;
+    uint2 h[2];
+#pragma unroll
+    for (int q = 0; q < 2; q++) {
+      const int k = 8 * G + 4 * q + (i >> 2), o = 2 * r0 + 8 * (i & 3);
+      h[q] = __builtin_bit_cast(uint2, lds_read_tr16(tile + k * KROW + (((o >> 4) ^ swz(k)) << 4) + (o & 15)));
+    }
+    return make_uint4(h[0].x, h[0].y, h[1].x, h[1].y);
+  }
+};
+
+constexpr int RAW = 4096, SCALES = 4 * 256;          // a K tile's codes and scale words: 1024 and 256 bytes a wave
+template <int SIZE, int R>
+constexpr int lds_bytes() { return R * (Tile<SIZE>::BYTES + RAW + SCALES) + Tile<SIZE>::BYTES; }
+static_assert(4 * lds_bytes<128, 2>() <= 160 * 1024 && 4 * lds_bytes<64, 3>() <= 160 * 1024, "four workgroups, or four sets of waves, a CU");
+
+// The SIZE x SIZE tile at (m0, n0) of the product that `a` describes: A is Y (K rows of M), B the codes (K rows of N bytes),
+// SFB the scales (ld_sfb bytes a row); K the group's rows. All 4 Q waves of the workgroup come here; lds is the set's own,
+// all the workgroup's.
+template <int DT, int FMT, int SIZE, int R, int Q>
+__device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, uint8_t* lds, uint8_t* all, int lane, int w, int q) {
+  typedef Tile<SIZE> T;
+  constexpr int MI = SIZE == 128 ? 4 : 1, UNITS = SIZE / 64, GROUPS = SIZE / 8;   // a lane's units of eight codes; units a k-row
+  constexpr int RAW_AT = R * T::BYTES, SCALES_AT = RAW_AT + R * RAW, WIDE_AT = SCALES_AT + R * SCALES, LDS = lds_bytes<SIZE, R>();
+  const int wa = SIZE == 128 ? 64 * (w >> 1) : 16 * w, wb = SIZE == 128 ? 64 * (w & 1) : 0;
   const uint16_t* A = (const uint16_t*)a.A;
   const uint8_t* B = (const uint8_t*)a.B;
-  uint32_t ao[TA::COPIES];
-  TA::offsets(a.lda, m0, a.M, w, lane, ao);
-  // this wave copies rows 8w .. 8w + 7 of codes, 16 a lane, and their scale words (chunks past the operand re-read
-  // its last one; their results are not stored), and converts them: rows 8w + l/16 and + 4, eight codes a lane
-  const int cr = 8 * w + (lane >> 3);
-  const uint32_t bo = (uint32_t)(cr * a.ldb + min(n0 + 16 * (lane & 7), (a.N - 1) & ~int64_t(15)) - n0);
+  uint32_t ao[T::COPIES];
+#pragma unroll
+  for (int j = 0; j < T::COPIES; j++) {
+    const int p = 64 * (w + 4 * j) + lane;
+    ao[j] = (uint32_t)((T::kr(p) * a.lda + min(m0 + T::col(p), (a.M - 1) & ~int64_t(7)) - m0) * 2);
+  }
+  // this wave copies rows 8w .. 8w + 7 of codes, 16 a lane (64 columns: the upper lanes the same again), and their scale
+  // words (chunks past the operand re-read its last one; their results are not stored), and converts them: unit h of lane
+  // l is row 8w + l / GROUPS + h * 64 / GROUPS, codes 8(l % GROUPS) .. + 7
+  constexpr int CHUNKS = SIZE / 16;
+  const uint32_t bo = (uint32_t)((8 * w + ((lane / CHUNKS) & 7)) * a.ldb + min(n0 + 16 * (lane % CHUNKS), (a.N - 1) & ~int64_t(15)) - n0);
   const uint32_t so = (uint32_t)((8 * w + (lane & 7)) * a.ld_sfb);
-  const int vr = 8 * w + (lane >> 4), vc = lane & 15;
+  const int ur = lane / GROUPS, uc = lane % GROUPS;
+  const int64_t word0 = n0 / 128 * 4;                                   // the scale word of the tile's columns,
+  const int byte = (int)(n0 / 32 - word0) + (uc >> 2);                  // this lane's byte of it
   f32x4 acc[MI][4];
 #pragma unroll
   for (int m = 0; m < MI; m++)
 #pragma unroll
     for (int n = 0; n < 4; n++) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int nfull = (int)(a.K / BK), tail = (int)(a.K % BK);
-  const uint32_t lds0 = gemm::lds_addr(lds), raw0 = gemm::lds_addr(raw), words0 = gemm::lds_addr(words);
-  // Copies of codes and scales of tile t, and of Y; past the last tile they re-read it into a stage that nobody reads
-  // again, so that the counts waited for stay fixed.
-  auto issue_codes = [&](int t, int slot) {
-    const int64_t k0 = (int64_t)min(t, nfull - 1) * BK;
-    uint64_t gb, gs;
-    gemm::sgpr_base2(B + k0 * a.ldb + n0, a.SFB + k0 * a.ld_sfb + n0 / 32, gb, gs);
-    gemm::dma16u(gb, bo, raw0 + slot * RAW + 1024 * w);
-    gemm::dma4u(gs, so, words0 + slot * SCALES + 256 * w);
+  const int nt = (int)((a.K + BK - 1) / BK), head = (int)a.K - BK * (nt - 1);
+  const uint32_t lds0 = gemm::lds_addr(lds);
+  // (A stage number that alternates with the loop count is known to the compiler; one kept in a variable cost the
+  // two-stage kernel a seventh of its time.)
+  // The copies of this set's i-th tile. With two stages it is waited for whole, and there are none of the first tile nor past
+  // the last; with three the counts waited for stay fixed: past the last the last again, for the first the one behind it
+  // into a stage not yet used, and none where the first is the only one.
+  auto issue = [&](int i, int stage) {
+    int t = i * Q + q;
+    if (R == 2 ? t < 1 || t >= nt : nt < 2) return;
+    if (R > 2) t = min(max(t, 1), nt - 1);
+    const int64_t k0 = BK * (int64_t)(t - 1) + head;
+    uint64_t ga, gb;
+    gemm::sgpr_base2(A + k0 * a.lda + m0, B + k0 * a.ldb + n0, ga, gb);
+    const uint64_t gs = gemm::sgpr_base(a.SFB + k0 * a.ld_sfb + word0);
+#pragma unroll
+    for (int j = 0; j < T::COPIES; j++) gemm::dma16u(ga, ao[j], lds0 + stage * T::BYTES + 1024 * (w + 4 * j));
+    gemm::dma16u(gb, bo, lds0 + RAW_AT + stage * RAW + 1024 * w);
+    gemm::dma4u(gs, so, lds0 + SCALES_AT + stage * SCALES + 256 * w);
   };
-  auto issue_a = [&](int t, int slot) {
-    const int64_t k0 = (int64_t)min(t, nfull - 1) * BK;
-    const uint64_t ga = gemm::sgpr_base(TA::base(A, a.lda, m0, k0));
-#pragma unroll
-    for (int j = 0; j < TA::COPIES; j++) gemm::dma16u(ga, ao[j], lds0 + slot * TA::BYTES + 1024 * (w + 4 * j));
+  auto put = [&](int h, uint32_t c0, uint32_t c1, uint32_t word) {
+    const int kr = 8 * w + ur + h * (64 / GROUPS);
+    lds_write_b128(lds + WIDE_AT + kr * T::KROW + ((uc ^ T::swz(kr)) << 4), widen8<DT, FMT>(c0, c1, (word >> (8 * byte)) & 255));
   };
-  auto put = [&](int h, uint32_t c0, uint32_t c1, uint32_t word, uint8_t* to) {
-    const int kr = vr + 4 * h;
-    lds_write_b128(to + kr * 256 + ((vc ^ (int)TB::swz(kr)) << 4), widen8<DT, FMT>(c0, c1, (word >> (8 * (vc >> 2))) & 255));
-  };
-  auto convert = [&](int slot, uint8_t* to) {
+  if (q == 0 && nt > 0) {
+    const int64_t col = min(n0 + 8 * uc, (a.N - 1) & ~int64_t(7));
 #pragma unroll
-    for (int h = 0; h < 2; h++) {
-      const u32x2 c = *(const BSM_LDS u32x2*)(raw + slot * RAW + 128 * (vr + 4 * h) + 8 * vc);
-      const uint32_t word = *(const BSM_LDS uint32_t*)(words + slot * SCALES + 256 * w + 4 * ((lane >> 4) + 4 * h));
-      put(h, c[0], c[1], word, to);
-    }
-  };
-  auto multiply = [&](const uint8_t* ta, const uint8_t* tb) {
-    uint4 fa[MI], fb[4];
-#pragma unroll
-    for (int n = 0; n < 4; n++) fb[n] = TB::frag(tb, lane, wb + 16 * n, 0);
-#pragma unroll
-    for (int m = 0; m < MI; m++) fa[m] = TA::frag(ta, lane, wa + 16 * m, 0);
-#pragma unroll
-    for (int m = 0; m < MI; m++)
-#pragma unroll
-      for (int n = 0; n < 4; n++) acc[m][n] = mid::mfma<DT>(fb[n], fa[m], acc[m][n]);
-  };
-  if (nfull > 0) {
-    issue_codes(0, 0);
-    issue_a(0, 0);
-    issue_codes(1, 1);
-    issue_a(1, 1);
-    issue_codes(2, 2);
-    gemm::stage_barrier<2 * PER>();   // tile 0's codes
-    convert(0, wide);
-    int cur = 0;
-    for (int t = 0; t < nfull; t++) {
-      // Y of tile t and the codes of t + 1 have landed, tile t's k-rows are written, and nobody reads t - 1 any more
-      gemm::stage_barrier<PER>();
-      const int last = cur == 0 ? 2 : cur - 1, next = cur == 2 ? 0 : cur + 1;
-      issue_a(t + 2, last);
-      issue_codes(t + 3, cur);
-      if (t + 1 < nfull) convert(next, wide + ((t + 1) & 1) * WIDE);
-      multiply(lds + cur * TA::BYTES, wide + (t & 1) * WIDE);
-      cur = next;
-    }
-  }
-  // every copy has landed and every wave is done with LDS
-  gemm::stage_barrier<0>();
-  if (tail) {
-    const int64_t k0 = (int64_t)nfull * BK;
-    TA::fill(TA::base(A, a.lda, m0, k0), ao, tail, lds, w, lane);
-    const int64_t col = min(n0 + 8 * vc, (a.N - 1) & ~int64_t(7));
-#pragma unroll
-    for (int h = 0; h < 2; h++) {
+    for (int h = 0; h < UNITS; h++) {
+      const int row = 8 * w + ur + h * (64 / GROUPS);
       uint2 c = make_uint2(0, 0);
       uint32_t word = 0;
-      if (vr + 4 * h < tail) {
-        const int64_t row = k0 + vr + 4 * h;
+      if (row < head) {
         c = *(const uint2*)(B + row * a.ldb + col);
-        word = *(const uint32_t*)(a.SFB + row * a.ld_sfb + n0 / 32);
+        word = *(const uint32_t*)(a.SFB + row * a.ld_sfb + word0);
       }
-      put(h, c.x, c.y, word, wide);
+      put(h, c.x, c.y, word);
     }
-    __syncthreads();
-    multiply(lds, wide);
-    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < T::COPIES; j++) {
+      const int p = 64 * (w + 4 * j) + lane;
+      lds_write_b128(lds + 16 * p, T::kr(p) < head ? *(const uint4*)((const uint8_t*)(A + m0) + ao[j]) : make_uint4(0, 0, 0, 0));
+    }
   }
-  // the sums leave through LDS in two parts
-  constexpr int MC = MI / 2;
-  static_assert(MC * 16384 <= lds_bytes<BM>(), "store parts");
+  issue(0, q == 0 ? R - 1 : 0);
+#pragma unroll
+  for (int i = 1; i < R - 1; i++) issue(i, i);
+  int ring = 0;
+  for (int it = 0; it < (nt + Q - 1) / Q; it++) {
+    const int t = it * Q + q, st = R == 2 ? it & 1 : ring;
+    // tile t has landed (the first is written), and nobody reads the one before any more
+    gemm::stage_barrier<(R - 2) * (T::COPIES + 2)>();
+    issue(it + R - 1, R == 2 ? st ^ 1 : ring == 0 ? R - 1 : ring - 1);
+    if (t > 0 && t < nt) {
+#pragma unroll
+      for (int h = 0; h < UNITS; h++) {
+        const int row = ur + h * (64 / GROUPS);   // of the wave's eight
+        const u32x2 c = *(const BSM_LDS u32x2*)(lds + RAW_AT + st * RAW + 1024 * w + SIZE * row + 8 * uc);
+        put(h, c[0], c[1], *(const BSM_LDS uint32_t*)(lds + SCALES_AT + st * SCALES + 256 * w + 4 * row));
+      }
+    }
+    gemm::lds_barrier();
+    if (t < nt) {
+      uint4 fa[MI], fb[4];
+#pragma unroll
+      for (int n = 0; n < 4; n++) fb[n] = T::frag(lds + WIDE_AT, lane, wb + 16 * n);
+#pragma unroll
+      for (int m = 0; m < MI; m++) fa[m] = T::frag(lds + st * T::BYTES, lane, wa + 16 * m);
+#pragma unroll
+      for (int m = 0; m < MI; m++)
+#pragma unroll
+        for (int n = 0; n < 4; n++) acc[m][n] = mid::mfma<DT>(fb[n], fa[m], acc[m][n]);
+    }
+    ring = ring + 1 == R ? 0 : ring + 1;
+  }
+  gemm::stage_barrier<0>();
+  if constexpr (Q > 1) {
+    static_assert(MI * 16384 <= Q * LDS, "joined sums");
+    uint8_t* mine = all + MI * 4096 * w + 16 * lane;
+    for (int p = 1; p < Q; p++) {
+      if (q == p)
+#pragma unroll
+        for (int m = 0; m < MI; m++)
+#pragma unroll
+          for (int n = 0; n < 4; n++) *(BSM_LDS f32x4*)(mine + 1024 * (4 * m + n)) = acc[m][n];
+      __syncthreads();
+      if (q == 0)
+#pragma unroll
+        for (int m = 0; m < MI; m++)
+#pragma unroll
+          for (int n = 0; n < 4; n++) acc[m][n] += *(const BSM_LDS f32x4*)(mine + 1024 * (4 * m + n));
+      __syncthreads();
+    }
+    if (q > 0) return;
+  }
+  // the sums leave through LDS, of 128 rows in two parts
+  constexpr int MC = MI == 4 ? 2 : 1;
+  static_assert(MC * 16384 <= LDS, "store parts");
   mid::store<DT, MI, 0, MC>(a, m0 + wa, n0 + wb, lane, acc, lds + MC * 4096 * w);
-  mid::store<DT, MI, MC, MC>(a, m0 + wa + 16 * MC, n0 + wb, lane, acc, lds + MC * 4096 * w);
+  if constexpr (MI > MC) mid::store<DT, MI, MC, MC>(a, m0 + wa + 16 * MC, n0 + wb, lane, acc, lds + MC * 4096 * w);
 }
 
+}  // namespace mid2
+
 // ---- 256 x 256 tiles: the dense GEMM's (gemm_dense_tile.hpp) with X's k-rows made in LDS ---------------------------------
-// Four waves of 128 x 128, K tiles of 64: 96 KiB through LDS for 256 x 256 x 32 products where two 256 x 128 tiles take 164.
+// Four waves of 128 x 128, K tiles of 64: 112 KiB through LDS for 256 x 256 x 32 products where 256 x 128 tiles take 164 (they
+// ran at 372 us where these take 335, in the same order of groups).
 // Y's two stages are the dense tile's. One buffer holds X's 16-bit k-rows: its fragments are in registers by the middle of a
 // K tile's first 32-K step, so between that step's barrier and the next tile's first reads the waves convert the next
 // tile's codes into it, a unit of eight codes a lane every ninth MFMA slot, each wave its own copies' rows. The codes come
@@ -219,10 +265,9 @@ __device__ __forceinline__ void product(const GemmArgs& a, int64_t m0, int64_t n
   // + 3, 16 codes a lane. Scale words: lane l the word l%2 of the wave's row l/2 (a row's second word may lie past its
   // end: the first again).
   uint32_t ao[2];
-  // The K tiles: a group's rows seldom are a multiple of 64, and a tail behind the loop (more matrix instructions on the same
-  // accumulators) made the compiler move up to 700 accumulators about in every turn of the loop. So the first tile is the
-  // short one, filled through registers with zeros past its rows; the others follow by copies, and the loop is all there
-  // is. With one tile alone the copies, whose counts stay, read the first row over and over.
+  // The short tile first: behind the loop, more matrix instructions on the same accumulators made the compiler move up to
+  // 700 accumulators about in every turn of it. With one tile alone the copies, whose counts stay, read the first row
+  // over and over.
   const int nt = (int)((a.K + BK - 1) / BK), head = (int)a.K - BK * (nt - 1);
   const int64_t lda = nt > 1 ? a.lda : 0, ldb = nt > 1 ? a.ldb : 0, lds_row = nt > 1 ? a.ld_sfb : 0;
 #pragma unroll

@@ -56,13 +56,14 @@ __device__ __forceinline__ bool enter(GemmArgs& a, const GroupArgs& gr, int tile
   return true;
 }
 
-template <int DT, int FMT, int BM>
-__global__ __launch_bounds__(256, 2) void k_kept_wgrad(GemmArgs a, GroupArgs gr, int tiles_m, int tiles_n) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[keptmm::lds_bytes<BM>()];
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+template <int DT, int FMT, int SIZE, int R, int Q>
+__global__ __launch_bounds__(256 * Q, 4) void k_kept_wgrad(GemmArgs a, GroupArgs gr, int tiles_m, int tiles_n) {
+  constexpr int LDS = keptmm::mid2::lds_bytes<SIZE, R>();
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Q * LDS];
+  const int lane = threadIdx.x & 63, wq = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wq & 3, q = wq >> 2;
   int tm, tn;
   if (!enter(a, gr, tiles_m, tiles_n, [](int turn) { return turn; }, tm, tn)) return;
-  keptmm::tile<DT, FMT, BM>(a, BM * (int64_t)tm, keptmm::BN * (int64_t)tn, lds, lane, w);
+  keptmm::mid2::tile<DT, FMT, SIZE, R, Q>(a, SIZE * (int64_t)tm, SIZE * (int64_t)tn, lds + q * LDS, lds, lane, w, q);
 }
 
 // Long groups first: a tile takes its group's rows, and a long one begun last keeps its CU while the others are done (16381
@@ -80,26 +81,51 @@ __global__ __launch_bounds__(256, 1) void k_kept_wgrad_large(GemmArgs a, GroupAr
   else gemm::store_tile16_bits<OUT>((uint16_t*)a.D, a.ldd, a.M, a.N, row0, col0, lane, acc, lds + 32768 * w, ACC, 0, 0.0f, 0.0f);
 }
 
+enum Tile { FEW_SHORT, FEW_LONG, SPLIT, MID, LARGE };
+
+// Times in us, E4M3 codes, float32 sums, groups of one length:
+//  - 256 x 256 from 700 rows a group on, where they fill the best part of a round: 500 / 1000 / 2000 rows, 4096 x 4096
+//    35 / 47 / 72 against 33 / 52 / 89 on 128 x 128; 8 groups of 500 / 1000 rows, 2048 x 2048 64 / 88 against 55 / 107;
+//  - up to 64 tiles of 128 x 128, a quarter of the CUs: 64 x 64, two sets of waves a tile, from 800 rows on four (200 / 500 /
+//    1000 / 4000 rows, 1024 x 1024: two 7.5 / 8.9 / 13.5 / 41, four 7.6 / 9.2 / 12.6 / 34, 128 x 128 10.9 / 15.6 / 24 / 73);
+//  - up to 192: long groups 128 x 128 with four sets of waves (4000 rows, 2048 x 1024 56 against 75 with one set, 57 on 64 x
+//    64; 2 groups of 8000, 1024 x 1024 100, 138 and 103), others 64 x 64 with two (1000 rows, 2048 x 1024 19.5 against
+//    24.7 on 128 x 128; 200 rows 9.3 and 11.0);
+//  - 128 x 128, four workgroups a CU (1021 rows over 32 groups, 1024 x 512 16.2 against 17.4 on 64 x 64).
+Tile tile_for(const GemmArgs& a, const GroupArgs& gr) {
+  const int64_t n = gr.n, each = gr.rows / n, t128 = (a.M + 127) / 128 * ((a.N + 127) / 128) * n;
+  if (each >= 700 && (a.M + 255) / 256 * ((a.N + 255) / 256) * n >= 218) return LARGE;
+  if (t128 <= 64) return each >= 800 ? FEW_LONG : FEW_SHORT;
+  if (t128 <= 192) return each >= 1500 ? SPLIT : FEW_SHORT;
+  return MID;
+}
+
 template <int DT, int FMT>
 hipError_t launch(const GemmArgs& a, const GroupArgs& gr, hipStream_t st) {
-  const int64_t m256 = (a.M + 255) / 256, n256 = (a.N + 255) / 256;
-  const bool large = gr.rows / gr.n >= 192 && m256 * n256 * gr.n >= 218;
-  const int64_t bm = large ? 256 : 128, tm = (a.M + bm - 1) / bm, tn = (a.N + bm - 1) / bm, share = (tm * tn + 7) / 8;
+  const Tile tile = tile_for(a, gr);
+  const int64_t size = tile == LARGE ? 256 : tile == MID || tile == SPLIT ? 128 : 64;
+  const int64_t m = (a.M + size - 1) / size, n = (a.N + size - 1) / size, share = (m * n + 7) / 8;
   if (share > 0x7FFFFFFF / 8 / gr.n) return hipErrorInvalidValue;
   const dim3 grid((uint32_t)(share * 8 * gr.n));
-  if (!large) {
-    hipLaunchKernelGGL((k_kept_wgrad<DT, FMT, 128>), grid, dim3(256), 0, st, a, gr, (int)tm, (int)tn);
-    return hipGetLastError();
+  const int tm = (int)m, tn = (int)n;
+  switch (tile) {
+    case FEW_SHORT: hipLaunchKernelGGL((k_kept_wgrad<DT, FMT, 64, 3, 2>), grid, dim3(512), 0, st, a, gr, tm, tn); break;
+    case FEW_LONG: hipLaunchKernelGGL((k_kept_wgrad<DT, FMT, 64, 3, 4>), grid, dim3(1024), 0, st, a, gr, tm, tn); break;
+    case SPLIT: hipLaunchKernelGGL((k_kept_wgrad<DT, FMT, 128, 2, 4>), grid, dim3(1024), 0, st, a, gr, tm, tn); break;
+    case MID: hipLaunchKernelGGL((k_kept_wgrad<DT, FMT, 128, 2, 1>), grid, dim3(256), 0, st, a, gr, tm, tn); break;
+    case LARGE: {
+      auto go = [&](auto out, auto acc) {
+        hipLaunchKernelGGL((k_kept_wgrad_large<DT, FMT, decltype(out)::value, decltype(acc)::value>), grid, dim3(256), 0, st, a, gr, tm, tn);
+      };
+      auto with = [&](auto out) {
+        if (a.accum) go(out, std::true_type{});
+        else go(out, std::false_type{});
+      };
+      if (a.d_fmt == BSM_F32) with(std::integral_constant<int, BSM_F32>{});
+      else with(std::integral_constant<int, DT>{});
+      break;
+    }
   }
-  auto go = [&](auto out, auto acc) {
-    hipLaunchKernelGGL((k_kept_wgrad_large<DT, FMT, decltype(out)::value, decltype(acc)::value>), grid, dim3(256), 0, st, a, gr, (int)tm, (int)tn);
-  };
-  auto with = [&](auto out) {
-    if (a.accum) go(out, std::true_type{});
-    else go(out, std::false_type{});
-  };
-  if (a.d_fmt == BSM_F32) with(std::integral_constant<int, BSM_F32>{});
-  else with(std::integral_constant<int, DT>{});
   return hipGetLastError();
 }
 

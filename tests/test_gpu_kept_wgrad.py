@@ -90,6 +90,34 @@ def test_tiles(sizes, M, N, ab, fmt):
     wgrad(sizes, M, N, ab, fmt, ab, 1, seed=M)
 
 
+@pytest.mark.parametrize("ab,fmt", [("bf16", "e4m3"), ("bf16", "e5m2"), ("f16", "e4m3"), ("f16", "e5m2")])
+@pytest.mark.parametrize("sizes,M,N", [
+    ([700, 0, 64, 1200, 1, 63, 3000, 1300], 1400, 1250),       # 256 x 256, groups of no row, one, a K tile and a long one
+    ([640, 65, 2000], 2056, 2400), ([768], 4100, 3600),
+    ([30, 0, 75], 300, 400), ([300], 520, 130),                # 64 x 64, two sets of waves
+    ([2001], 200, 130), ([1000, 0, 2100], 260, 70),            # four
+    ([3000, 1700], 1030, 600),                                 # 128 x 128, four sets
+    ([33, 64, 0, 31, 100], 1030, 700)])                        # one
+def test_every_tile(sizes, M, N, ab, fmt):
+    wgrad(sizes, M, N, ab, fmt, "f32", seed=N, first=1, behind=1)
+    wgrad(sizes, M, N, ab, fmt, ab, 1, seed=N, extra=16, pad=8)
+
+
+def test_more_groups_than_are_ranked():
+    """300 groups on 256 x 256 tiles come in their order; 256 are ranked."""
+    for n in (256, 300):
+        rows = [700 + (i * 37) % 100 for i in range(n)]
+        off = offsets_of(rows)
+        M, N = 8, 16
+        y = torch.ones(off[-1], M, dtype=torch.bfloat16, device="cuda")
+        c = torch.full((off[-1], N), 0x38, dtype=torch.uint8, device="cuda")
+        s = torch.full((off[-1], 4), 127, dtype=torch.uint8, device="cuda")
+        D = torch.full((n, M, N), float("nan"), device="cuda")
+        bsm.bsm_gemm_grouped_wgrad_block_scale(off[-1], M, N, n, torch.tensor(off, dtype=torch.int32, device="cuda"), "bf16", y, M, "e4m3",
+                                               c, N, s, 4, "f32", D, N, M * N)
+        assert torch.equal(D, torch.tensor(rows, dtype=torch.float32, device="cuda")[:, None, None].expand(n, M, N))
+
+
 def test_equals_the_gradient_of_restored_activations():
     """The same bits as bsm_gemm_grouped_wgrad where one K tile of 32 rows holds the group, whose products are then one sum."""
     g = torch.Generator().manual_seed(1)

@@ -206,9 +206,10 @@ struct NoMore {
 // LDS of its own (part q's starts at part 0's + q * LDS); part 0 adds the sums in part order and
 // stores. All waves of the workgroup come here together.
 // first < the whole K tiles: the sum begins at that tile and wraps (the same for every call of the tile, so the bits stay).
-template <int DT, int BM, bool AK, bool BKM, int BK = 64, class MORE = NoMore, int LDS = LDS_BYTES, int Q = 1>
+// TERMS 2: A is the sum of two operands, the second `second` elements behind the first; both products make one sum.
+template <int DT, int BM, bool AK, bool BKM, int BK = 64, class MORE = NoMore, int LDS = LDS_BYTES, int Q = 1, int TERMS = 1>
 __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, uint8_t* lds, int lane, int w,
-                                     const MORE& more = MORE(), int q = 0, int first = 0) {
+                                     const MORE& more = MORE(), int q = 0, int first = 0, int64_t second = 0) {
   typedef Tile<BM, AK, BK> TA;
   typedef Tile<BN, BKM, BK> TB;
   constexpr int MI = BM / 32, STAGE = TA::BYTES + TB::BYTES, NST = LDS / STAGE, PER = TA::COPIES + TB::COPIES;
@@ -254,32 +255,35 @@ __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, 
         for (int n = 0; n < 4; n++) acc[m][n] = mfma<DT>(fb[n], fa[m], acc[m][n]);
     }
   };
-  if (nfull > 0) {
+  for (int term = 0; term < TERMS; term++) {
+    if (term > 0) A += second;   // (every wave is done with LDS)
+    if (nfull > 0) {
 #pragma unroll
-    for (int i = 0; i < NST - 1; i++) issue(i, i);
-    int cur = 0;
-    for (int it = 0; it < (nfull + Q - 1) / Q; it++) {
-      gemm::stage_barrier<(NST - 2) * PER>();
-      issue(it + NST - 1, cur == 0 ? NST - 1 : cur - 1);
-      if (Q == 1 || it * Q + q < nfull) multiply(lds + cur * STAGE, std::integral_constant<int, BK / 32>{});
-      cur = cur + 1 == NST ? 0 : cur + 1;
+      for (int i = 0; i < NST - 1; i++) issue(i, i);
+      int cur = 0;
+      for (int it = 0; it < (nfull + Q - 1) / Q; it++) {
+        gemm::stage_barrier<(NST - 2) * PER>();
+        issue(it + NST - 1, cur == 0 ? NST - 1 : cur - 1);
+        if (Q == 1 || it * Q + q < nfull) multiply(lds + cur * STAGE, std::integral_constant<int, BK / 32>{});
+        cur = cur + 1 == NST ? 0 : cur + 1;
+      }
     }
-  }
-  // every copy has landed and every wave is done with LDS (before it is refilled, before the
-  // accumulators pass through it, and before the workgroup can end)
-  gemm::stage_barrier<0>();
-  if (tail) {
-    const int64_t k0 = (int64_t)nfull * BK;
-    if (q == 0) {
-      TA::fill(TA::base(A, a.lda, m0, k0), ao, tail, lds, w, lane);
-      TB::fill(TB::base(B, a.ldb, n0, k0), bo, tail, lds + TA::BYTES, w, lane);
+    // every copy has landed and every wave is done with LDS (before it is refilled, before the
+    // accumulators pass through it, and before the workgroup can end)
+    gemm::stage_barrier<0>();
+    if (tail) {
+      const int64_t k0 = (int64_t)nfull * BK;
+      if (q == 0) {
+        TA::fill(TA::base(A, a.lda, m0, k0), ao, tail, lds, w, lane);
+        TB::fill(TB::base(B, a.ldb, n0, k0), bo, tail, lds + TA::BYTES, w, lane);
+      }
+      __syncthreads();
+      if (q == 0) {
+        if (BK == 32 || tail <= 32) multiply(lds, std::integral_constant<int, 1>{});
+        else multiply(lds, std::integral_constant<int, 2>{});
+      }
+      __syncthreads();
     }
-    __syncthreads();
-    if (q == 0) {
-      if (BK == 32 || tail <= 32) multiply(lds, std::integral_constant<int, 1>{});
-      else multiply(lds, std::integral_constant<int, 2>{});
-    }
-    __syncthreads();
   }
   if constexpr (Q > 1) {
     static_assert(MI * 16384 <= LDS, "joined sums");

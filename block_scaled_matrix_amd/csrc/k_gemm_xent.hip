@@ -10,7 +10,8 @@
 // implementation that had kept them; the alternative, float32 logits of a batch, is 1 GB for 8190 x 32001), become G
 // in the accumulators and leave as 16-bit values, which two products then read: dX += G W_piece and dW_piece = G^T X.
 // G is rounded to the operands' format because the matrix unit takes it so: half a step (2^-8 in bf16, 2^-11 in f16) of
-// each term, independent from term to term. In f16 the weights are brought to 2^15 at most by a power of two found
+// each term, independent from term to term, like the rounding of a 16-bit gradient. A gradient kept in float32 takes G as two
+// such terms, 2^-18 (2^-24) of each left, and twice the product's operations. In f16 the weights are brought to 2^15 at most by a power of two found
 // on the device, so a probability keeps all its bits down to 2^-29 of the largest weight, and the products' sums are
 // scaled back in float32.
 // Tiles: gemm_dense_tile.hpp (256 x 256) where they fill the chip, gemm_mid_tile.hpp (32 / 64 / 128 x 128) otherwise, and
@@ -29,20 +30,25 @@ namespace {
 using namespace dense;
 
 // A product's K cut into n parts side by side: part p takes K elements p * per .. and writes its own sums, stride_d
-// elements behind part p - 1's. Makes `a` the part's product and pid the tile's number in it.
+// elements behind part p - 1's. With two terms of A, `second` elements apart, half of the parts take the second. Makes `a`
+// the part's product and pid the tile's number in it.
 struct Parts {
   int n;
-  int64_t per, stride_d;
+  int64_t per, stride_d, second;
   template <bool AK, bool BKM>
   __device__ __forceinline__ void enter(GemmArgs& a, int tiles, int& pid) const {
     if (n == 1) return;
-    const int p = pid / tiles;
+    int p = pid / tiles;
     pid -= p * tiles;
+    a.D += p * stride_d;
+    if (second) {
+      if (2 * p >= n) a.A = (const uint16_t*)a.A + second;
+      p = 2 * p >= n ? p - n / 2 : p;
+    }
     const int64_t k0 = p * per;
     a.A = (const uint16_t*)a.A + (AK ? k0 : k0 * a.lda);
     a.B = (const uint16_t*)a.B + (BKM ? k0 : k0 * a.ldb);
     a.K = min(per, a.K - k0);
-    a.D += p * stride_d;
   }
 };
 
@@ -63,8 +69,9 @@ __global__ __launch_bounds__(256, 1) void k_xent_large(GemmArgs a, EP ep, int ti
   else gemm::store_tile16_bits<OUT>((uint16_t*)a.D, a.ldd, a.M, a.N, row0, col0, lane, acc, lds + 32768 * w, ACC, 0, 0.0f, 0.0f);
 }
 
-// Tiles of BM x 128 (128-row ones with a K-major A: of as few rows as hold the last ones).
-template <int DT, bool AK, bool BKM, class EP, int BM = 128, int BK = 64, int PER_CU = 2, int Q = 1>
+// Tiles of BM x 128 (128-row ones with a K-major A: of as few rows as hold the last ones). TERMS 2: A's two terms in one
+// sum.
+template <int DT, bool AK, bool BKM, class EP, int BM = 128, int BK = 64, int PER_CU = 2, int Q = 1, int TERMS = 1>
 __global__ __launch_bounds__(256 * Q, PER_CU * Q) void k_xent_mid(GemmArgs a, EP ep, int tiles_m, int tiles_n, Parts parts) {
   constexpr int LDS = 160 * 1024 / PER_CU / Q;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Q * LDS];
@@ -86,7 +93,7 @@ __global__ __launch_bounds__(256 * Q, PER_CU * Q) void k_xent_mid(GemmArgs a, EP
     if (left <= 32) return mid::tile<DT, 32, AK, BKM, BK, EP, LDS, Q>(a, m0, n0, mine, lane, w, ep, q, first);
     if (left <= 64) return mid::tile<DT, 64, AK, BKM, BK, EP, LDS, Q>(a, m0, n0, mine, lane, w, ep, q, first);
   }
-  mid::tile<DT, BM, AK, BKM, BK, EP, LDS, Q>(a, m0, n0, mine, lane, w, ep, q, first);
+  mid::tile<DT, BM, AK, BKM, BK, EP, LDS, Q, TERMS>(a, m0, n0, mine, lane, w, ep, q, first, parts.second);
 }
 
 // The loss of up to 64 rows: 16 columns a workgroup, its eight waves splitting K (skinny.hpp).
@@ -231,7 +238,7 @@ template <int DT, class EP>
 void launch_logits(const GemmArgs& g, Tile tile, const EP& ep, hipStream_t st) {
   const int64_t t = tile == LARGE ? 256 : 128, tm = (g.M + t - 1) / t, tn = (g.N + t - 1) / t;   // (FEW: one row of tiles)
   const dim3 grid((uint32_t)(tm * tn));
-  const Parts one{1, 0, 0};
+  const Parts one{1, 0, 0, 0};
   if (tile == LARGE) hipLaunchKernelGGL((k_xent_large<DT, true, true, DT, false, EP>), grid, dim3(256), 0, st, g, ep, (int)tm, (int)tn, one);
   else if (tile == FEW) hipLaunchKernelGGL((k_xent_mid<DT, true, true, EP, 32, 64, 3>), grid, dim3(256), 0, st, g, ep, (int)tm, (int)tn, one);
   else if (tile == MID) hipLaunchKernelGGL((k_xent_mid<DT, true, true, EP>), grid, dim3(256), 0, st, g, ep, (int)tm, (int)tn, one);
@@ -289,7 +296,7 @@ struct Plan {
   bool large;
   int parts;
   int64_t per;      // columns of a part
-  bool sums;        // dX through float32 sums in the workspace
+  int64_t g_second;             // elements from G's first term to its second
   int64_t g_bytes, f_bytes, bytes;
 };
 
@@ -331,10 +338,11 @@ Plan plan_of(int64_t rows, int64_t N, int64_t K, int64_t piece) {
   p.pieces = (N + p.piece - 1) / p.piece;
   p.ldg = (p.piece + 63) / 64 * 64;
   plan_dx(std::max<int64_t>(rows, 1), std::max<int64_t>(K, 1), p);
-  p.sums = p.parts > 1 || p.pieces > 1;
   p.ldf = (K + 3) / 4 * 4;
-  p.g_bytes = (rows * p.ldg * 2 + 255) / 256 * 256;
-  p.f_bytes = p.sums ? (p.parts * rows * p.ldf * 4 + 255) / 256 * 256 : 0;
+  // (The workspace does not know the gradients' formats: room for both terms, and for twice the parts.)
+  p.g_second = (rows * p.ldg + 127) / 128 * 128;
+  p.g_bytes = p.g_second * 4;
+  p.f_bytes = (2 * p.parts * rows * p.ldf * 4 + 255) / 256 * 256;
   p.bytes = 256 + p.g_bytes + p.f_bytes;
   return p;
 }
@@ -352,8 +360,11 @@ hipError_t launch_grad(const XentArgs& a, const XentGradArgs& g, const Plan& p, 
     down = by + 1;
   }
   using Times = xent::Times<DT == BSM_F16>;
-  const Parts one{1, 0, 0};
-  const bool direct = !p.sums || (p.parts == 1 && g.dx_fmt == BSM_F32);
+  const Parts one{1, 0, 0, 0};
+  // float32 gradients take G as two terms: dX in twice the parts, dW's in one sum
+  const bool two = (g.dX && g.dx_fmt == BSM_F32) || (g.dW && g.dw_fmt == BSM_F32);
+  const int dx_terms = g.dx_fmt == BSM_F32 ? 2 : 1;
+  const bool direct = dx_terms == 1 && p.parts == 1 && p.pieces == 1;
   for (int64_t c0 = 0, at = 0; c0 < a.N; c0 += p.piece, at++) {
     const int64_t cols = std::min(p.piece, a.N - c0);
     const uint16_t* W = (const uint16_t*)a.W + c0 * a.ldw;
@@ -363,18 +374,20 @@ hipError_t launch_grad(const XentArgs& a, const XentGradArgs& g, const Plan& p, 
       z.D = (float*)G; z.ldd = p.ldg; z.d_fmt = DT;
       Tile tile = tile_for(a.rows, cols);
       if (tile == SKINNY) tile = SPLIT;   // (fewer than 128 tiles)
-      launch_logits<DT>(z, tile, xent::Grad{a.labels, a.lse, g.dloss, up, a.rows, a.N, c0}, st);
+      const xent::Weights weights{a.labels, a.lse, g.dloss, up, a.rows, a.N, c0};
+      if (two) launch_logits<DT>(z, tile, xent::GradTwo<DT>{weights, G, p.ldg, p.g_second, cols}, st);
+      else launch_logits<DT>(z, tile, xent::Grad{weights}, st);
     }
     if (g.dX && a.rows > 0) {
       GemmArgs x{};
       x.M = a.rows; x.N = a.K; x.K = cols; x.dtype = DT;
       x.A = G; x.lda = p.ldg; x.B = W; x.ldb = a.ldw;
       x.accum = at > 0;
-      if (direct) { x.D = (float*)g.dX; x.ldd = g.lddx; x.d_fmt = g.dx_fmt; }
+      if (direct) { x.D = (float*)g.dX; x.ldd = g.lddx; x.d_fmt = DT; }
       else { x.D = F; x.ldd = p.ldf; x.d_fmt = BSM_F32; }
       const Times ep{down};
       // (the last piece may be short: parts past its columns have nothing to add)
-      const Parts parts{(int)((cols + p.per - 1) / p.per), p.per, a.rows * p.ldf};
+      const Parts parts{dx_terms * (int)((cols + p.per - 1) / p.per), p.per, a.rows * p.ldf, dx_terms == 2 ? p.g_second : 0};
       const int64_t m128 = (a.rows + 127) / 128, n128 = (a.K + 127) / 128;
       if (p.large) launch_large<DT, true>(x, ep, parts, st);
       else
@@ -392,17 +405,29 @@ hipError_t launch_grad(const XentArgs& a, const XentGradArgs& g, const Plan& p, 
       // another's products (10007 columns, K 1000, float32: 200 rows 16 us against 24 on 256 x 256 and 20 on 128 x 128 at
       // two a CU, 800 rows 27 against 38 and 34; 32000, K 2048: 800 rows 136 and 141, 1600 rows 205 and 201, 3000 rows 378
       // and 363 us).
-      if (a.rows >= 1600 && tile_for(w.M, w.N) == LARGE) launch_large<DT, false>(w, ep, one, st);
-      else
-        hipLaunchKernelGGL((k_xent_mid<DT, false, false, Times, 128, 32, 4>), dim3((uint32_t)(m128 * n128)), dim3(256), 0, st, w, ep,
-                           (int)m128, (int)n128, one);
+      const dim3 grid((uint32_t)(m128 * n128));
+      const bool both = g.dw_fmt == BSM_F32;
+      if (a.rows >= 1600 && tile_for(w.M, w.N) == LARGE) {
+        launch_large<DT, false>(w, ep, one, st);
+        if (both) {
+          // (the second term as a product of its own onto the first: its sums' way through memory is short beside 1600 rows)
+          w.A = G + p.g_second;
+          w.accum = 1;
+          launch_large<DT, false>(w, ep, one, st);
+        }
+      } else if (both) {
+        hipLaunchKernelGGL((k_xent_mid<DT, false, false, Times, 128, 32, 4, 1, 2>), grid, dim3(256), 0, st, w, ep, (int)m128, (int)n128,
+                           Parts{1, 0, 0, p.g_second});
+      } else {
+        hipLaunchKernelGGL((k_xent_mid<DT, false, false, Times, 128, 32, 4>), grid, dim3(256), 0, st, w, ep, (int)m128, (int)n128, one);
+      }
     }
   }
   if (g.dX && a.rows > 0 && !direct) {
     const int64_t n = a.rows * ((a.K + 3) / 4);
     const dim3 grid((uint32_t)((n + 63) / 64));
     auto sum = [&](auto out) {
-      hipLaunchKernelGGL((k_xent_sum<decltype(out)::value>), grid, dim3(256), 0, st, F, p.parts, a.rows * p.ldf, p.ldf, a.rows, a.K, g.dX, g.lddx);
+      hipLaunchKernelGGL((k_xent_sum<decltype(out)::value>), grid, dim3(256), 0, st, F, dx_terms * p.parts, a.rows * p.ldf, p.ldf, a.rows, a.K, g.dX, g.lddx);
     };
     if (g.dx_fmt == BSM_F32) sum(std::integral_constant<int, BSM_F32>{});
     else sum(std::integral_constant<int, DT>{});

@@ -1,8 +1,8 @@
 // xent.hpp - cross entropy of a projection (k_gemm_xent.hip): the calls' arguments, and what a tile of logits becomes
 // while it is still in the accumulators.
 #pragma once
-#include "bsm_device.hpp"
 #include "bsm_internal.hpp"
+#include "store16.hpp"
 
 namespace bsm {
 
@@ -105,15 +105,68 @@ struct Stats {
   }
 };
 
-// The gradient in the logits, (softmax - onehot) times the row's weight, in place. Column 0 of the block is column
-// `first` of the vocabulary. Rows without a label give 0 whatever their logits.
-struct Grad {
-  static constexpr bool kStores = false;
+// The gradient in the logits, (softmax - onehot) times the row's weight. Column 0 of the block is column `first` of the
+// vocabulary. Rows without a label give 0 whatever their logits.
+struct Weights {
   const int32_t* labels;
   const float* lse;
   const float* dloss;
   const float* by;     // a power of two on the weights (f16), or NULL
   int64_t rows, vocabulary, first;
+  // One row of blocks, logits in, gradients out.
+  template <int NJ>
+  __device__ __forceinline__ void turn(int64_t row, int64_t col0, int G, float f, f32x4 (&v)[NJ]) const {
+    const bool in = row < rows;
+    const int64_t lab = in ? labels[row] : -1;
+    const bool has = lab >= 0 && lab < vocabulary;
+    const float d = has ? dloss[row] * f : 0.0f, l = has ? lse[row] : 0.0f;
+    // 2^(z log2 e - l log2 e), the second product in two floats
+    const float hi = l * kLog2e, lo = __builtin_fmaf(l, kLog2e, -hi);
+#pragma unroll
+    for (int n = 0; n < NJ; n++)
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(v[n][e], kLog2e, -hi) - lo);
+        v[n][e] = has ? p * d : 0.0f;
+      }
+    const int64_t off = lab - first - col0;
+    const bool mine = has && off >= 0 && off < 16 * NJ && ((off >> 2) & 3) == G;
+    if (__any(mine)) {
+      // p d - d, not (p - 1) d: one rounding more, half a float step of d
+      const int o = mine ? (int)off - 4 * G : -1;
+#pragma unroll
+      for (int n = 0; n < NJ; n++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) v[n][e] -= 16 * n + e == o ? d : 0.0f;
+    }
+  }
+};
+
+// In place, for the tile's own 16-bit store.
+struct Grad : Weights {
+  static constexpr bool kStores = false;
+  template <int MI, int NJ>
+  __device__ __forceinline__ void operator()(int64_t row0, int64_t col0, f32x4 (&acc)[MI][NJ]) const {
+    const int lane = threadIdx.x & 63;
+    const float f = by ? *by : 1.0f;
+#pragma unroll
+    for (int m = 0; m < MI; m++) {
+      f32x4 v[NJ];
+      take(acc[m], v);
+      turn(row0 + 16 * m + (lane & 15), col0, lane >> 4, f, v);
+#pragma unroll
+      for (int n = 0; n < NJ; n++) acc[m][n] = v[n];
+    }
+  }
+};
+
+// As the sum of two 16-bit terms, rounded and what the rounding dropped, rounded (2^-18 of the value is left in bf16, 2^-24
+// in f16), for gradients kept in float32: `to` and `second` elements behind it.
+template <int DT>
+struct GradTwo : Weights {
+  static constexpr bool kStores = true;
+  uint16_t* to;
+  int64_t ld, second, cols;
   template <int MI, int NJ>
   __device__ __forceinline__ void operator()(int64_t row0, int64_t col0, f32x4 (&acc)[MI][NJ]) const {
     const int lane = threadIdx.x & 63, G = lane >> 4;
@@ -121,33 +174,32 @@ struct Grad {
 #pragma unroll
     for (int m = 0; m < MI; m++) {
       const int64_t row = row0 + 16 * m + (lane & 15);
-      const bool in = row < rows;
-      const int64_t lab = in ? labels[row] : -1;
-      const bool has = lab >= 0 && lab < vocabulary;
-      const float d = has ? dloss[row] * f : 0.0f, l = has ? lse[row] : 0.0f;
       f32x4 v[NJ];
       take(acc[m], v);
-      // 2^(z log2 e - l log2 e), the second product in two floats
-      const float hi = l * kLog2e, lo = __builtin_fmaf(l, kLog2e, -hi);
+      turn(row, col0, G, f, v);
+      if (row < rows)
 #pragma unroll
-      for (int n = 0; n < NJ; n++)
+        for (int n = 0; n < NJ; n++) {
+          const int64_t col = col0 + 16 * n + 4 * G;
+          uint16_t* p = to + row * ld + col;
+          uint16_t h[4], r[4];
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(v[n][e], kLog2e, -hi) - lo);
-          v[n][e] = has ? p * d : 0.0f;
+          for (int e = 0; e < 4; e++) {
+            h[e] = gemm::to_bits16<DT>(v[n][e]);
+            r[e] = gemm::to_bits16<DT>(v[n][e] - gemm::from_bits16<DT>(h[e]));
+          }
+          if (col + 4 <= cols) {
+            *(uint2*)p = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+            *(uint2*)(p + second) = make_uint2(r[0] | (uint32_t)r[1] << 16, r[2] | (uint32_t)r[3] << 16);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+              if (col + e < cols) {
+                p[e] = h[e];
+                p[second + e] = r[e];
+              }
+          }
         }
-      const int64_t off = lab - first - col0;
-      const bool mine = has && off >= 0 && off < 16 * NJ && ((off >> 2) & 3) == G;
-      if (__any(mine)) {
-        // p d - d, not (p - 1) d: one rounding more, half a float step of d
-        const int o = mine ? (int)off - 4 * G : -1;
-#pragma unroll
-        for (int n = 0; n < NJ; n++)
-#pragma unroll
-          for (int e = 0; e < 4; e++) v[n][e] -= 16 * n + e == o ? d : 0.0f;
-      }
-#pragma unroll
-      for (int n = 0; n < NJ; n++) acc[m][n] = v[n];
     }
   }
 };

@@ -515,11 +515,12 @@ int64_t bsm_gemm_cross_entropy_workspace(int64_t rows, int64_t N);
  * 0 on rows without a label (whatever their logits, lse and dloss),
  *   dX[t*lddx + k] = sum_n G(t,n) W(n,k),   dW[n*lddw + k] = (accum ? dW[n*lddw + k] : 0) + sum_t G(t,n) X(t,k),
  * sums in float32, rounded once to their formats. The vocabulary is taken in pieces: a piece's logits are made again, and its
- * part of G is kept in the workspace, rounded to ab's format (in F16 times a power of two that brings the largest |dloss|
+ * part of G is kept in the workspace, rounded to ab's format for a gradient of that format, and as the sum of two such values
+ * (off by at most 2^-18 in BF16, 2^-24 in F16) for one in F32 (in F16 times a power of two that brings the largest |dloss|
  * to 2^15, so that probabilities keep their bits).
  *   lse:       what bsm_gemm_cross_entropy wrote (DEVICE, rows float32);
  *   dloss:     DEVICE, rows float32, 4-byte aligned;
- *   piece:     columns of the vocabulary at once, 0 for the library's choice (1 GiB of G); each piece more costs dX another way
+ *   piece:     columns of the vocabulary at once, 0 for the library's choice (1 GiB of G's values); each piece more costs dX another way
  *              through memory. At most 2^21 are taken at once;
  *   workspace: DEVICE, 16-byte aligned, bsm_gemm_cross_entropy_grad_workspace(rows, N, K, piece) bytes; as above;
  *   dX, dx_fmt, lddx: BSM_F32 or ab; or dX NULL: not wanted;

@@ -5,7 +5,8 @@ ez = K 2^-23 sum|x w| (any order, truncating additions). The exponent's fma roun
 exponential by 2 u of its result; a row's N terms meet in at most 64 + N / 4096 + 32 additions one behind another. So
 log-sum-exp is off by el = ez + (2 |lse| + N / 4096 + 160) u and a loss by ez more and a float's rounding. A probability is off by
 r = ez + el + (4 |z| + 4 |lse| + 8) u of itself, G by |dloss| (p r + 2 u) and its rounding to the operands' format:
-half a step of |G|, in f16 also half a subnormal step, 2^-25 of the largest |dloss| / 2^14. A sum over n terms of G times
+half a step of |G| for a 16-bit gradient, half a step of that again for a float32 one (two terms), in f16 also half a
+subnormal step, 2^-25 of the largest |dloss| / 2^14. A sum over n terms of G times
 the other operand adds n 2^-23 of sum|G| |operand|, and the output its own half step.
 """
 import torch
@@ -86,9 +87,11 @@ def check_grad(x, w, labels, dloss, lse, ab, dx_fmt=None, dw_fmt=None, accum=0, 
     G[torch.arange(rows, device="cuda"), at] -= 1.0
     G = torch.where(has[:, None], G * d, 0.0)
     r = (ez + el)[:, None] + (4 * z.abs() + 4 * rl.abs()[:, None] + 8) * U
-    eG = d.abs() * (p * r + 2 * U) + HALF_STEP[ab] * G.abs() * 1.01
-    if ab == "f16":
-        eG = torch.where(has[:, None], eG + 2.0 ** -25 * float(d.abs().max()) * 2.0 ** -14, 0.0)
+
+    def error(fmt):
+        e = d.abs() * (p * r + 2 * U) + HALF_STEP[ab] ** (2 if fmt == "f32" else 1) * G.abs() * 1.01
+        return torch.where(has[:, None], e + 2.0 ** -25 * float(d.abs().max()) * 2.0 ** -14, 0.0) if ab == "f16" else e
+
     X, W = x.double(), w.double()
 
     def compare(got, ref, err, mag, terms, fmt, what):
@@ -97,12 +100,12 @@ def check_grad(x, w, labels, dloss, lse, ab, dx_fmt=None, dw_fmt=None, accum=0, 
         assert not bad.any(), (what, int(bad.sum()), bad.nonzero()[:4].tolist(), float(((got.double() - ref).abs() / tol).max()))
 
     if "x" in want:
-        compare(dx[:, :K], G @ W, eG @ W.abs(), G.abs() @ W.abs(), N + 64, dx_fmt, "dX")
+        compare(dx[:, :K], G @ W, error(dx_fmt) @ W.abs(), G.abs() @ W.abs(), 2 * N + 64, dx_fmt, "dX")
         assert (dx[:, K:] == 7.0).all()
     if "w" in want:
         ref, mag = G.T.contiguous() @ X, G.abs().T.contiguous() @ X.abs()
         if accum:
             ref, mag = ref + dw0[:, :K].double(), mag + dw0[:, :K].double().abs()
-        compare(dw[:, :K], ref, eG.T.contiguous() @ X.abs(), mag, rows, dw_fmt, "dW")
+        compare(dw[:, :K], ref, error(dw_fmt).T.contiguous() @ X.abs(), mag, 2 * rows, dw_fmt, "dW")
         assert torch.equal(dw[:, K:], dw0[:, K:])
     return dx, dw

@@ -390,29 +390,31 @@ def _rows(t, dtype: str, what, rows, n, ld, chunk=1):
     """Address of a DEVICE matrix of `rows` rows of n elements, ld apart; where it is a torch tensor, of the type that
     the call says ("u8", codes and scales: any of one byte), its rows contiguous, and reaching to the last row's end, in
     whole chunks where the kernels read it in such."""
-    if t is None or type(t) is int:
+    if type(t) is int or t is None:
         return t
-    want = _torch_types.get(dtype) or _torch_type(dtype)
-    if t.dtype is not want and (dtype != "u8" or t.element_size() != 1):
+    if not _torch_types:
+        _fill_torch_types()
+    same = t.dtype is _torch_types[dtype]
+    if same and t.is_contiguous() and t.numel() >= rows * ld:   # (as nearly every call has it)
+        return t.data_ptr()
+    if not same and (dtype != "u8" or t.element_size() != 1):
         raise BsmError(-8, f"{what} must be {dtype}, not {t.dtype}")
     if rows > 0 and n > 0:
-        need = (rows - 1) * ld + (n if chunk == 1 else -(-n // chunk) * chunk)
-        if not (t.is_contiguous() and t.numel() >= need):   # (else the elements from its start on are as many)
-            if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
-                raise BsmError(-5, f"{what}: a row's elements must lie one after another")
-            have = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
-            if have < need:
-                raise BsmError(-9, f"{what} holds {have} elements from its start on, the call takes {need}")
+        if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
+            raise BsmError(-5, f"{what}: a row's elements must lie one after another")
+        need = (rows - 1) * ld + -(-n // chunk) * chunk
+        have = t.untyped_storage().nbytes() // t.element_size() - t.storage_offset()
+        if have < need:
+            raise BsmError(-9, f"{what} holds {have} elements from its start on, the call takes {need}")
     return t.data_ptr()
 
 
 _torch_types = {}
 
 
-def _torch_type(fmt: str):
+def _fill_torch_types():
     import torch
     _torch_types.update(f32=torch.float32, f16=torch.float16, bf16=torch.bfloat16, u8=torch.uint8)
-    return _torch_types[fmt]
 
 
 def _float_fmt(fmt: str, what):

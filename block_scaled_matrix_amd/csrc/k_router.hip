@@ -119,6 +119,24 @@ __device__ __forceinline__ bool row_kept(const RouterArgs& a, int64_t row, bool 
   return (__ballot(any) & mine) != 0;
 }
 
+// Sum over the wave, in lane 63: as grouped::wave_inclusive_scan moves it, a double's halves apart.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double shifted(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, ROWS, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  v += shifted<0x111, 0xF>(v);   // row_shr:1, 2, 4, 8
+  v += shifted<0x112, 0xF>(v);
+  v += shifted<0x114, 0xF>(v);
+  v += shifted<0x118, 0xF>(v);
+  v += shifted<0x142, 0xA>(v);   // row_bcast:15, 31
+  v += shifted<0x143, 0xC>(v);
+  return v;
+}
+
 // Exclusive sums, the loss and the outputs, by the whole workgroup of NT lanes: cnt[0 .. E - 1], kept and the column sums
 // psum in LDS; E <= 1024, two experts a lane. wscan and wred: LDS of one value a wave.
 template <int NT>
@@ -128,8 +146,7 @@ __device__ __forceinline__ void finish(const RouterArgs& a, const int* cnt, int 
   const int c0 = h0 ? cnt[2 * t] : 0, c1 = h1 ? cnt[2 * t + 1] : 0;
   double part = (h0 ? (double)c0 * psum[2 * t] : 0.0) + (h1 ? (double)c1 * psum[2 * t + 1] : 0.0);
   const int incl = grouped::wave_inclusive_scan(c0 + c1);
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) part += __shfl_xor(part, d);
+  part = wave_sum(part);
   if (lane == 63) { wscan[w] = incl; wred[w] = part; }
   __syncthreads();
   int before = incl - c0 - c1, all = 0;
@@ -407,7 +424,8 @@ int lanes_per_row(int E) { return E <= 16 ? 4 : E <= 32 ? 8 : E <= 256 ? 16 : 64
 
 int64_t groups_of(int64_t rows, int E) {
   if (rows * E <= kOneGroup) return 1;
-  const int64_t per = WAVES * (64 / lanes_per_row(E));
+  // (two rows a lane at least: half as many sums to join)
+  const int64_t per = 2 * WAVES * (64 / lanes_per_row(E));
   return std::min<int64_t>((rows + per - 1) / per, kMaxGroups);
 }
 

@@ -14,9 +14,10 @@ except ImportError:  # run as a script
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libbsm.so")
-SOURCES = ["bsm_api.hip", "k_tile.hip", "k_gemm_dense.hip", "k_gemm_grouped.hip", "k_gemm_grouped_mx.hip",
-           "k_gemm_grouped_mx_any.hip", "k_gemm_grouped_mx_mid.hip", "k_gemm_lora.hip", "k_gemm_mx.hip", "k_gemm_mx_any.hip",
-           "k_gemm_mx_mn_a.hip", "k_gemm_mx_mn_b.hip", "k_gemm_mx_mn_ab.hip", "k_gemm_kept.hip", "k_gemm_xent.hip", "k_router.hip", "k_checkpoint.hip", "k_diag.hip"]
+# (the longest first)
+SOURCES = ["k_gemm_xent.hip", "k_gemm_kept.hip", "k_gemm_mx_any.hip", "k_gemm_mx_mn_ab.hip", "k_gemm_mx_mn_a.hip", "k_gemm_mx_mn_b.hip",
+           "k_gemm_grouped.hip", "k_gemm_grouped_mx.hip", "k_gemm_grouped_mx_any.hip", "k_gemm_grouped_mx_mid.hip", "k_gemm_lora.hip",
+           "k_gemm_dense.hip", "k_gemm_mx.hip", "k_router.hip", "k_checkpoint.hip", "k_tile.hip", "bsm_api.hip", "k_diag.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # -packed-fp32-ops: never emit packed fp32 arithmetic (v_pk_*_f32).
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall",
@@ -68,7 +69,8 @@ def build(jobs: int = min(8, os.cpu_count() or 4)) -> str:
     """Compile every source for gfx950 and link libbsm.so next to this file."""
     with tempfile.TemporaryDirectory(prefix="bsm_build_") as tmp:
         objs = [os.path.join(tmp, s.replace(".hip", ".o")) for s in SOURCES]
-        with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        # (processes: the audit of a long assembly is Python's own work)
+        with cf.ProcessPoolExecutor(max_workers=jobs) as ex:
             list(ex.map(_compile, SOURCES, objs))
         out = LIB + ".tmp"
         r = subprocess.run([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", out],

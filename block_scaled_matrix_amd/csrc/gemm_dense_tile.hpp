@@ -179,8 +179,7 @@ __device__ __forceinline__ void store_tile16(float* __restrict__ D, int64_t ldd,
 #pragma unroll
       for (int nt = 0; nt < 8; nt++) {
         const int c = 4 * nt + (lane >> 4);
-        f32x4 v = acc[4 * half + m4][nt];
-        asm volatile("" : "+v"(v));   // (out of the accumulators here, or a K loop before may move them about each turn)
+        const f32x4& v = acc[4 * half + m4][nt];
         const uint4 x = make_uint4(__float_as_uint(sgn * v[0]), __float_as_uint(sgn * v[1]),
                                    __float_as_uint(sgn * v[2]), __float_as_uint(sgn * v[3]));
         lds_write_b128(region + 512 * r + 16 * (c ^ (r & 15)), x);

@@ -69,7 +69,7 @@ __global__ __launch_bounds__(256 * Q, 4) void k_kept_wgrad(GemmArgs a, GroupArgs
 
 // Long groups first: a tile takes its group's rows, and a long one begun last keeps its CU while the others are done (16381
 // rows over 8 groups, the longest 8082 and the seventh in order: 335 us in order).
-template <int DT, int FMT, int OUT>
+template <int DT, int FMT, int OUT, dense::Add ADD>
 __global__ __launch_bounds__(256, 1) void k_kept_wgrad_large(GemmArgs a, GroupArgs gr, int tiles_m, int tiles_n) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[keptmm::large::LDS_BYTES];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -78,7 +78,7 @@ __global__ __launch_bounds__(256, 1) void k_kept_wgrad_large(GemmArgs a, GroupAr
   f32x4 acc[8][8];
   keptmm::large::product<DT, FMT>(a, 256 * (int64_t)tm, 256 * (int64_t)tn, lds, lane, w, acc);
   const int64_t row0 = 256 * (int64_t)tm + 128 * (w >> 1), col0 = 256 * (int64_t)tn + 128 * (w & 1);
-  dense::store_large<OUT>(a, row0, col0, lane, acc, lds + 32768 * w, a.accum);
+  dense::store_large<OUT, ADD>(a, row0, col0, lane, acc, lds + 32768 * w);
 }
 
 enum Tile { FEW_SHORT, FEW_LONG, SPLIT, MID, LARGE };
@@ -114,8 +114,9 @@ hipError_t launch(const GemmArgs& a, const GroupArgs& gr, hipStream_t st) {
     case SPLIT: hipLaunchKernelGGL((k_kept_wgrad<DT, FMT, 128, 2, 4>), grid, dim3(1024), 0, st, a, gr, tm, tn); break;
     case MID: hipLaunchKernelGGL((k_kept_wgrad<DT, FMT, 128, 2, 1>), grid, dim3(256), 0, st, a, gr, tm, tn); break;
     case LARGE:
-      if (a.d_fmt == BSM_F32) hipLaunchKernelGGL((k_kept_wgrad_large<DT, FMT, BSM_F32>), grid, dim3(256), 0, st, a, gr, tm, tn);
-      else hipLaunchKernelGGL((k_kept_wgrad_large<DT, FMT, DT>), grid, dim3(256), 0, st, a, gr, tm, tn);
+      if (a.d_fmt != BSM_F32) hipLaunchKernelGGL((k_kept_wgrad_large<DT, FMT, DT, dense::ASK>), grid, dim3(256), 0, st, a, gr, tm, tn);
+      else if (a.accum) hipLaunchKernelGGL((k_kept_wgrad_large<DT, FMT, BSM_F32, dense::ALWAYS>), grid, dim3(256), 0, st, a, gr, tm, tn);
+      else hipLaunchKernelGGL((k_kept_wgrad_large<DT, FMT, BSM_F32, dense::NEVER>), grid, dim3(256), 0, st, a, gr, tm, tn);
       break;
   }
   return hipGetLastError();

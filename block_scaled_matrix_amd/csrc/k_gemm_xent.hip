@@ -53,7 +53,7 @@ struct Parts {
 };
 
 // One 256 x 256 tile: the product, what EP makes of the sums, and their store in OUT unless EP keeps none.
-template <int DT, bool AK, bool BKM, int OUT, class EP>
+template <int DT, bool AK, bool BKM, int OUT, Add ADD, class EP>
 __global__ __launch_bounds__(256, 1) void k_xent_large(GemmArgs a, EP ep, int tiles_m, int tiles_n, Parts parts) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * STAGE_BYTES];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -64,8 +64,7 @@ __global__ __launch_bounds__(256, 1) void k_xent_large(GemmArgs a, EP ep, int ti
   tile_product<DT, AK, BKM>(a, tm, tn, lds, lane, w, acc);
   const int64_t row0 = (int64_t)tm * BM + 128 * (w >> 1), col0 = (int64_t)tn * BN + 128 * (w & 1);
   ep(row0, col0, acc);
-  // (G and a 16-bit dX are never added to)
-  if constexpr (!EP::kStores) store_large<OUT>(a, row0, col0, lane, acc, lds + 32768 * w, AK && OUT != BSM_F32 ? false : a.accum);
+  if constexpr (!EP::kStores) store_large<OUT, ADD>(a, row0, col0, lane, acc, lds + 32768 * w);
 }
 
 // Tiles of BM x 128 (128-row ones with a K-major A: of as few rows as hold the last ones). TERMS 2: A's two terms in one
@@ -238,7 +237,7 @@ void launch_logits(const GemmArgs& g, Tile tile, const EP& ep, hipStream_t st) {
   const int64_t t = tile == LARGE ? 256 : 128, tm = (g.M + t - 1) / t, tn = (g.N + t - 1) / t;   // (FEW: one row of tiles)
   const dim3 grid((uint32_t)(tm * tn));
   const Parts one{1, 0, 0, 0};
-  if (tile == LARGE) hipLaunchKernelGGL((k_xent_large<DT, true, true, DT, EP>), grid, dim3(256), 0, st, g, ep, (int)tm, (int)tn, one);
+  if (tile == LARGE) hipLaunchKernelGGL((k_xent_large<DT, true, true, DT, NEVER, EP>), grid, dim3(256), 0, st, g, ep, (int)tm, (int)tn, one);
   else if (tile == FEW) hipLaunchKernelGGL((k_xent_mid<DT, true, true, EP, 32, 64, 3>), grid, dim3(256), 0, st, g, ep, (int)tm, (int)tn, one);
   else if (tile == MID) hipLaunchKernelGGL((k_xent_mid<DT, true, true, EP>), grid, dim3(256), 0, st, g, ep, (int)tm, (int)tn, one);
   else {
@@ -252,11 +251,15 @@ void launch_logits(const GemmArgs& g, Tile tile, const EP& ep, hipStream_t st) {
 template <int DT, bool AK, class EP>
 void launch_large(const GemmArgs& g, const EP& ep, const Parts& parts, hipStream_t st) {
   const int64_t tm = (g.M + 255) / 256, tn = (g.N + 255) / 256;
-  const dim3 grid((uint32_t)(tm * tn * parts.n));
-  if (g.d_fmt == BSM_F32)
-    hipLaunchKernelGGL((k_xent_large<DT, AK, false, BSM_F32, EP>), grid, dim3(256), 0, st, g, ep, (int)tm, (int)tn, parts);
-  else
-    hipLaunchKernelGGL((k_xent_large<DT, AK, false, DT, EP>), grid, dim3(256), 0, st, g, ep, (int)tm, (int)tn, parts);
+  auto go = [&](auto out, auto add) {
+    hipLaunchKernelGGL((k_xent_large<DT, AK, false, decltype(out)::value, decltype(add)::value, EP>), dim3((uint32_t)(tm * tn * parts.n)),
+                       dim3(256), 0, st, g, ep, (int)tm, (int)tn, parts);
+  };
+  using std::integral_constant;
+  // (a 16-bit dX is never added to)
+  if (g.d_fmt != BSM_F32) go(integral_constant<int, DT>{}, integral_constant<Add, AK ? NEVER : ASK>{});
+  else if (g.accum) go(integral_constant<int, BSM_F32>{}, integral_constant<Add, ALWAYS>{});
+  else go(integral_constant<int, BSM_F32>{}, integral_constant<Add, NEVER>{});
 }
 
 GemmArgs logits_of(const XentArgs& a) {

@@ -11,11 +11,16 @@
 namespace bsm {
 namespace dense {
 
-// D = round(acc (+ D when `add`)) for the wave's 128 x 128 sub-tile at (row0, col0), OUT BSM_F32, BSM_BF16 or BSM_F16, through
+// Whether D is added to: known when compiled, or by the call's own flag. (A float32 store that asks needs registers for both
+// ways and spills 60: 16381 rows over 8 groups, 4096 x 2048 330 us against 267.)
+enum Add { NEVER, ALWAYS, ASK };
+
+// D = round(acc (+ D)) for the wave's 128 x 128 sub-tile at (row0, col0), OUT BSM_F32, BSM_BF16 or BSM_F16, through
 // 32 KiB of LDS in two halves of 64 rows (region row r keeps its 16-byte chunk c at c ^ (r & 15)).
-template <int OUT>
+template <int OUT, Add ADD>
 __device__ __forceinline__ void store_large(const GemmArgs& a, int64_t row0, int64_t col0, int lane, const f32x4 (&acc)[8][8],
-                                            uint8_t* region, bool add) {
+                                            uint8_t* region) {
+  const bool add = ADD == ASK ? a.accum : ADD == ALWAYS;
 #pragma unroll
   for (int half = 0; half < 2; half++) {
 #pragma unroll

@@ -11,8 +11,9 @@
 // and the workgroups (a second launch over at most 256 of them), all in a fixed order. A lane adds at
 // most 64 rows in float32, then into a double: a sum over any number of rows keeps its bits. Counts are
 // integers, so the LDS atomics that make them cannot change a result by their order.
-// Bound: the logits' bytes for many rows; a launch and a chain of dependent loads for few, so up to
-// kOneGroup logits a single workgroup does everything in one launch.
+// Bound: for many rows the latency of a few loads and reductions behind one another, sixteen waves a CU in turn (32768
+// rows, 128 experts, bf16: 9 us for 8 MB, 4-8 us for the join, the gradient 9.5 us for 17 MB); for few rows launches, so
+// up to kOneGroup logits a single workgroup does everything in one (16 rows, 64 experts: 3.7 us).
 #include "grouped.hpp"
 #include "router.hpp"
 #include "../../include/bsm.h"
@@ -20,7 +21,7 @@
 namespace bsm {
 namespace {
 
-constexpr int THREADS = 512, WAVES = THREADS / 64, JOIN = 1024;
+constexpr int THREADS = 1024, WAVES = THREADS / 64, JOIN = 1024;
 constexpr int kMaxGroups = 256;
 constexpr int64_t kOneGroup = 32768;
 
@@ -175,7 +176,7 @@ struct Parts { Pair* sums; int* kept; int pairs; };
 // ONE: the only workgroup, which finishes too. Otherwise workgroup b's sums go to row b of `parts`.
 template <int F, int LPR, int J, bool ONE>
 __global__ __launch_bounds__(THREADS) void k_balance(RouterArgs a, Parts parts) {
-  constexpr int RPW = 64 / LPR, E4 = 4 * LPR * J, U = J <= 2 ? 4 : 2;
+  constexpr int RPW = 64 / LPR, E4 = 4 * LPR * J, U = 2;
   __shared__ double total[E4];
   __shared__ double sums[E4 > 256 ? 1 : WAVES][E4];
   __shared__ int cnt[E4];

@@ -94,6 +94,28 @@ __global__ __launch_bounds__(256 * Q, PER_CU * Q) void k_xent_mid(GemmArgs a, EP
   mid::tile<DT, BM, AK, BKM, BK, EP, LDS, Q, TERMS>(a, m0, n0, mine, lane, w, ep, q, first, parts.second);
 }
 
+// Both gradients of a piece in one launch, for few rows: dX's tiles and parts, then dW's, all of 128 x 128 with K tiles of 32,
+// four workgroups a CU. Neither fills the chip for long, and they need nothing of one another (one after the other and
+// together, float32 dW: 200 rows x 10007, K 1000 39 and 27 us, 800 rows 79 and 77; 200 x 32000, K 2048 154 and 139; 16-bit dW:
+// 1500 x 4000, K 512 44 and 29 us, 500 x 20000, K 1024 69 and 61).
+template <int DT, int W_TERMS, class EP>
+__global__ __launch_bounds__(256, 4) void k_xent_both(GemmArgs x, GemmArgs y, EP ep, Parts parts, int x_m, int x_n, int y_m, int y_n, int x_grid,
+                                                      int64_t y_second) {
+  constexpr int LDS = 40 * 1024;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[LDS];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int tm, tn, pid = blockIdx.x;
+  if (pid < x_grid) {
+    if (pid >= x_m * x_n * parts.n) return;   // (x_grid is a multiple of 8, so that dW's tiles keep their XCDs)
+    parts.enter<true, false>(x, x_m * x_n, pid);
+    gemm::tile_coords(pid, x_m, x_n, tm, tn);
+    mid::tile<DT, 128, true, false, 32, EP, LDS>(x, 128 * (int64_t)tm, mid::BN * (int64_t)tn, lds, lane, w, ep);
+  } else {
+    gemm::tile_coords(pid - x_grid, y_m, y_n, tm, tn);
+    mid::tile<DT, 128, false, false, 32, EP, LDS, 1, W_TERMS>(y, 128 * (int64_t)tm, mid::BN * (int64_t)tn, lds, lane, w, ep, 0, 0, y_second);
+  }
+}
+
 // The loss of up to 64 rows: 16 columns a workgroup, its eight waves splitting K (skinny.hpp).
 template <int DT, int MT>
 __global__ __launch_bounds__(skinny::THREADS, MT == 1 ? 4 : 2) void k_xent_skinny(GemmArgs a, xent::Stats ep) {
@@ -375,16 +397,32 @@ hipError_t launch_grad(const XentArgs& a, const XentGradArgs& g, const Plan& p, 
       if (two) launch_logits<DT>(z, tile, xent::GradTwo<DT>{weights, G, p.ldg, p.g_second, cols}, st);
       else launch_logits<DT>(z, tile, xent::Grad{weights}, st);
     }
+    GemmArgs x{}, w{};
+    const Times ep{down};
+    // (the last piece may be short: parts past its columns have nothing to add)
+    const Parts parts{dx_terms * (int)((cols + p.per - 1) / p.per), p.per, a.rows * p.ldf, dx_terms == 2 ? p.g_second : 0};
+    const bool dw_large = a.rows >= 1600 && tile_for(cols, a.K) == LARGE, dw_two = g.dw_fmt == BSM_F32;
     if (g.dX && a.rows > 0) {
-      GemmArgs x{};
       x.M = a.rows; x.N = a.K; x.K = cols; x.dtype = DT;
       x.A = G; x.lda = p.ldg; x.B = W; x.ldb = a.ldw;
       x.accum = at > 0;
       if (direct) { x.D = (float*)g.dX; x.ldd = g.lddx; x.d_fmt = DT; }
       else { x.D = F; x.ldd = p.ldf; x.d_fmt = BSM_F32; }
-      const Times ep{down};
-      // (the last piece may be short: parts past its columns have nothing to add)
-      const Parts parts{dx_terms * (int)((cols + p.per - 1) / p.per), p.per, a.rows * p.ldf, dx_terms == 2 ? p.g_second : 0};
+    }
+    if (g.dW) {
+      w.M = cols; w.N = a.K; w.K = a.rows; w.dtype = DT;
+      w.A = G; w.lda = p.ldg; w.B = a.X; w.ldb = a.ldx;
+      w.D = (float*)((uint8_t*)g.dW + c0 * g.lddw * (g.dw_fmt == BSM_F32 ? 4 : 2)); w.ldd = g.lddw; w.d_fmt = g.dw_fmt; w.accum = g.accum;
+    }
+    if (g.dX && g.dW && a.rows > 0 && !p.large && !dw_large) {
+      const int xm = (int)((x.M + 127) / 128), xn = (int)((x.N + 127) / 128), ym = (int)((w.M + 127) / 128), yn = (int)((w.N + 127) / 128);
+      const int xg = (xm * xn * parts.n + 7) / 8 * 8;
+      const dim3 grid((uint32_t)(xg + ym * yn));
+      if (dw_two) hipLaunchKernelGGL((k_xent_both<DT, 2, Times>), grid, dim3(256), 0, st, x, w, ep, parts, xm, xn, ym, yn, xg, p.g_second);
+      else hipLaunchKernelGGL((k_xent_both<DT, 1, Times>), grid, dim3(256), 0, st, x, w, ep, parts, xm, xn, ym, yn, xg, int64_t(0));
+      continue;
+    }
+    if (g.dX && a.rows > 0) {
       const int64_t m128 = (a.rows + 127) / 128, n128 = (a.K + 127) / 128;
       if (p.large) launch_large<DT, true>(x, ep, parts, st);
       else
@@ -392,27 +430,21 @@ hipError_t launch_grad(const XentArgs& a, const XentGradArgs& g, const Plan& p, 
                            (int)n128, parts);
     }
     if (g.dW) {
-      GemmArgs w{};
-      w.M = cols; w.N = a.K; w.K = a.rows; w.dtype = DT;
-      w.A = G; w.lda = p.ldg; w.B = a.X; w.ldb = a.ldx;
-      w.D = (float*)((uint8_t*)g.dW + c0 * g.lddw * (g.dw_fmt == BSM_F32 ? 4 : 2)); w.ldd = g.lddw; w.d_fmt = g.dw_fmt; w.accum = g.accum;
-      const Times ep{down};
       const int64_t m128 = (cols + 127) / 128, n128 = (a.K + 127) / 128;
       // Short sums and many tiles: four workgroups a CU, K tiles of 32, so that one's loads and stores run beside
       // another's products (10007 columns, K 1000, float32: 200 rows 16 us against 24 on 256 x 256 and 20 on 128 x 128 at
       // two a CU, 800 rows 27 against 38 and 34; 32000, K 2048: 800 rows 136 and 141, 1600 rows 205 and 201, 3000 rows 378
       // and 363 us).
       const dim3 grid((uint32_t)(m128 * n128));
-      const bool both = g.dw_fmt == BSM_F32;
-      if (a.rows >= 1600 && tile_for(w.M, w.N) == LARGE) {
+      if (dw_large) {
         launch_large<DT, false>(w, ep, one, st);
-        if (both) {
+        if (dw_two) {
           // (the second term as a product of its own onto the first: its sums' way through memory is short beside 1600 rows)
           w.A = G + p.g_second;
           w.accum = 1;
           launch_large<DT, false>(w, ep, one, st);
         }
-      } else if (both) {
+      } else if (dw_two) {
         hipLaunchKernelGGL((k_xent_mid<DT, false, false, Times, 128, 32, 4, 1, 2>), grid, dim3(256), 0, st, w, ep, (int)m128, (int)n128,
                            Parts{1, 0, 0, p.g_second});
       } else {

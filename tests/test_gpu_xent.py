@@ -42,6 +42,12 @@ def test_formats_accumulation_and_pieces(rows, N, K, ab):
 
 
 def test_one_gradient_alone():
+    """Of few rows, whose gradients otherwise share a launch, and of many."""
+    for ab, f in (("bf16", "bf16"), ("f16", "f32")):
+        both(300, 5000, 264, ab, want="x", dx_fmt=f, dw_fmt=f)
+        both(300, 5000, 264, ab, want="w", dx_fmt=f, dw_fmt=f)
+        both(4096, 520, 4096, ab, want="x", dx_fmt=f, dw_fmt=f)
+        both(1700, 4096, 4096, ab, want="w", dx_fmt=f, dw_fmt=f)
     both(130, 700, 72, want="x")
     both(130, 700, 72, want="w", piece=256)
     both(130, 700, 72, want="")

@@ -979,9 +979,10 @@ int bsm_gemm_grouped_wgrad_block_scale(int64_t rows, int64_t M, int64_t N, int32
 // Sizes and operands that the loss and its gradient share. No launch has more than 2^31 - 1 workgroups of the smallest
 // tile (16 columns a row tile of 128), which these sizes keep.
 static int check_xent_sizes(int64_t rows, int64_t N, int64_t K) {
-  if (rows < 0 || N < 1 || K < 0 || rows > 0x7FFFFFFF || N > 0x7FFFFFFF || K > (int64_t(1) << 22))
+  if (rows < 0 || N < 1 || K < 0 || rows > (int64_t(1) << 25) || N > 0x7FFFFFFF || K > (int64_t(1) << 22))
     return fail(BSM_E_SHAPE, "rows, N, K = %lld, %lld, %lld out of range", (long long)rows, (long long)N, (long long)K);
-  if (((rows + 63) / 64) * ((N + 63) / 64) > 0x7FFFFFFF || (rows + 63) / 64 * ((K + 63) / 64) > 0x7FFFFFFF)
+  // (a launch has fewer than 2^32 lanes, a tile of logits 256; of dX as many, and two parts)
+  if ((rows + 127) / 128 * ((N + 127) / 128) > 0xFFFFFF || (rows + 127) / 128 * ((K + 127) / 128) > 0x7FFFFF)
     return fail(BSM_E_SHAPE, "rows, N, K = %lld, %lld, %lld: too many tiles for a launch", (long long)rows, (long long)N, (long long)K);
   return BSM_OK;
 }

@@ -11,12 +11,12 @@
 // in the accumulators and leave as 16-bit values, which two products then read: dX += G W_piece and dW_piece = G^T X.
 // G is rounded to the operands' format because the matrix unit takes it so: half a step (2^-8 in bf16, 2^-11 in f16) of
 // each term, independent from term to term, like the rounding of a 16-bit gradient. A gradient kept in float32 takes G as two
-// such terms, 2^-18 (2^-24) of each left, and twice the product's operations. In f16 the weights are brought to 2^15 at most by a power of two found
-// on the device, so a probability keeps all its bits down to 2^-29 of the largest weight, and the products' sums are
-// scaled back in float32.
+// such terms, 2^-18 (2^-24) of each left, and twice the product's operations. In f16 the weights are brought to 2^15 at
+// most by a power of two found on the device, so a probability keeps all its bits down to 2^-29 of the largest weight, and
+// the products' sums are scaled back in float32.
 // Tiles: gemm_dense_tile.hpp (256 x 256) where they fill the chip, gemm_mid_tile.hpp (32 / 64 / 128 x 128) otherwise, and
 // for the loss of few rows skinny.hpp. dX with few tiles is cut along the vocabulary into parts that are summed in a
-// fixed order.
+// fixed order; with few rows both gradients share a launch (k_xent_both).
 #include <algorithm>
 #include "gemm_dense_tile.hpp"
 #include "gemm_mid_tile.hpp"
@@ -336,7 +336,7 @@ void plan_dx(int64_t rows, int64_t K, Plan& p) {
       const int64_t per = ((p.piece + parts - 1) / parts + 63) / 64 * 64, n = (p.piece + per - 1) / per;
       const double rounds = (double)((tiles * n + slots - 1) / slots);
       double us = p.pieces * rounds * (2.0 * t * t * per / rate + fixed);
-      if (n > 1 || p.pieces > 1) us += 4.0 + n * p.pieces * rows * K * 8 / 5.0e6;
+      if (n > 1 || p.pieces > 1) us += 4.0 + 8.0 * n * p.pieces * rows * K / 5.0e6;
       if (best == 0.0 || us < best) {
         best = us;
         p.large = large;
@@ -453,10 +453,15 @@ hipError_t launch_grad(const XentArgs& a, const XentGradArgs& g, const Plan& p, 
     }
   }
   if (g.dX && a.rows > 0 && !direct) {
-    const int64_t n = a.rows * ((a.K + 3) / 4);
-    const dim3 grid((uint32_t)((n + 63) / 64));
+    // (slices of rows: a launch has fewer than 2^32 lanes)
+    const int64_t per = (a.K + 3) / 4, most = std::max<int64_t>((int64_t(1) << 26) / per, 1);
     auto sum = [&](auto out) {
-      hipLaunchKernelGGL((k_xent_sum<decltype(out)::value>), grid, dim3(256), 0, st, F, dx_terms * p.parts, a.rows * p.ldf, p.ldf, a.rows, a.K, g.dX, g.lddx);
+      constexpr int OUT = decltype(out)::value;
+      for (int64_t r = 0; r < a.rows; r += most) {
+        const int64_t rows = std::min(most, a.rows - r);
+        hipLaunchKernelGGL((k_xent_sum<OUT>), dim3((uint32_t)((rows * per + 63) / 64)), dim3(256), 0, st, F + r * p.ldf, dx_terms * p.parts,
+                           a.rows * p.ldf, p.ldf, rows, a.K, (uint8_t*)g.dX + r * g.lddx * (OUT == BSM_F32 ? 4 : 2), g.lddx);
+      }
     };
     if (g.dx_fmt == BSM_F32) sum(std::integral_constant<int, BSM_F32>{});
     else sum(std::integral_constant<int, DT>{});

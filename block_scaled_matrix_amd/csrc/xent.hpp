@@ -47,7 +47,7 @@ __device__ __forceinline__ void take(const f32x4 (&row)[NJ], f32x4 (&v)[NJ]) {
 
 // Its rows' part of the log-sum-exp: base b, the largest logit times log2 e, and s = sum 2^(z log2 e - b), to slot
 // col0 / width; and the logit of the rows' labels that lie in it. b is a float that the join takes as it is, so its
-// rounding cancels; the exponent's own fma rounds once.
+// rounding cancels; the exponent's own fma rounds once. (A logit whose b overflows counts as infinite.)
 struct Stats {
   static constexpr bool kStores = true;
   const int32_t* labels;
@@ -80,7 +80,7 @@ struct Stats {
         for (int e = 0; e < 4; e++) top = fmaxf(top, v[n][e]);
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
-      const float b = top * kLog2e, from = top == -INFINITY ? 0.0f : b;
+      const float b = top * kLog2e, from = b == -INFINITY ? 0.0f : b;
       float s = 0.0f;
 #pragma unroll
       for (int n = 0; n < NJ; n++)

@@ -497,14 +497,16 @@ int bsm_gemm_grouped_wgrad_block_scale(int64_t rows, int64_t M, int64_t N, int32
 /* Softmax cross entropy of a projection onto a large vocabulary, without keeping its logits: with z = X W^T in float32,
  *   lse[t] = log sum_n exp z(t,n),   loss[t] = lse[t] - z(t,label_t),
  * X(t,k) = X[t*ldx + k], W(n,k) = W[n*ldw + k].
- *   rows, N, K: rows 0 .. 2^31 - 1 (0: no-op), N (the vocabulary) 1 .. 2^31 - 1, K >= 0;
+ *   rows, N, K: rows 0 .. 2^25 (0: no-op), N (the vocabulary) 1 .. 2^31 - 1, K 0 .. 2^22; ceil(rows/128) * ceil(N/128)
+ *              below 2^24, ceil(rows/128) * ceil(K/128) below 2^23;
  *   ab:        BSM_F16 or BSM_BF16 (X and W);
  *   labels:    DEVICE array of rows int32, 4-byte aligned; a label outside 0 .. N - 1 (say -1: a prompt's row, padding)
  *              is none: its row's loss is 0;
  *   loss, lse: DEVICE, rows float32 each, 4-byte aligned;
  *   workspace: DEVICE, 16-byte aligned, bsm_gemm_cross_entropy_workspace(rows, N) bytes; holds nothing from one call to
  *              the next. Calls that may run at the same time need one each.
- * A row with a logit of NaN or +infinity has lse NaN; one of -infinity counts as exp = 0. Alignment, whole-row buffers and
+ * A row with a logit of NaN or +infinity has lse NaN; one of -infinity counts as exp = 0; logits times log2 e beyond
+ * float32's range count as infinite. Alignment, whole-row buffers and
  * leading dimensions as for bsm_gemm. The same inputs give the same bits. No input may overlap an output or the workspace. */
 int bsm_gemm_cross_entropy(int64_t rows, int64_t N, int64_t K, int32_t ab, const void* X, int64_t ldx, const void* W, int64_t ldw,
                            const int32_t* labels, float* loss, float* lse, void* workspace, void* stream);
@@ -514,14 +516,15 @@ int64_t bsm_gemm_cross_entropy_workspace(int64_t rows, int64_t N);
 /* Its gradients, for the weight dloss[t] of each row's loss: with G(t,n) = (exp(z(t,n) - lse[t]) - [n = label_t]) * dloss[t],
  * 0 on rows without a label (whatever their logits, lse and dloss),
  *   dX[t*lddx + k] = sum_n G(t,n) W(n,k),   dW[n*lddw + k] = (accum ? dW[n*lddw + k] : 0) + sum_t G(t,n) X(t,k),
- * sums in float32, rounded once to their formats. The vocabulary is taken in pieces: a piece's logits are made again, and its
+ * sums in float32, rounded once to their formats. (dW adds 0 * X(t,k) for a row without a label: X must be finite there too.)
+ * The vocabulary is taken in pieces: a piece's logits are made again, and its
  * part of G is kept in the workspace, rounded to ab's format for a gradient of that format, and as the sum of two such values
  * (off by at most 2^-18 in BF16, 2^-24 in F16) for one in F32 (in F16 times a power of two that brings the largest |dloss|
  * to 2^15, so that probabilities keep their bits).
  *   lse:       what bsm_gemm_cross_entropy wrote (DEVICE, rows float32);
  *   dloss:     DEVICE, rows float32, 4-byte aligned;
- *   piece:     columns of the vocabulary at once, 0 for the library's choice (1 GiB of G's values); each piece more costs dX another way
- *              through memory. At most 2^21 are taken at once;
+ *   piece:     columns of the vocabulary at once, 0 for the library's choice (1 GiB of G's values); each piece more costs
+ *              dX another way through memory. At most 2^21 are taken at once;
  *   workspace: DEVICE, 16-byte aligned, bsm_gemm_cross_entropy_grad_workspace(rows, N, K, piece) bytes; as above;
  *   dX, dx_fmt, lddx: BSM_F32 or ab; or dX NULL: not wanted;
  *   dW, dw_fmt, lddw: BSM_F32 or ab; or dW NULL: not wanted. Rows 0: dW = accum ? dW : 0;

@@ -161,6 +161,12 @@ def test_cross_entropy_loss_refusals():
     for rows, N in ((-1, 4), (1 << 31, 4), (4, 0), (4, 1 << 31)):
         expect("BSM_E_SHAPE", bsm.bsm_gemm_cross_entropy_workspace, rows=rows, N=N)
     assert bsm.bsm_gemm_cross_entropy_workspace(0, 5) == 0
+    # rows to 2^25; fewer than 2^24 tiles of 128 x 128 logits and 2^23 of dX
+    for rows, N in (((1 << 25) + 1, 4), (1 << 25, 64 * 128 + 1), (128, 0x7FFFFF81)):
+        expect("BSM_E_SHAPE", bsm.bsm_gemm_cross_entropy_workspace, rows=rows, N=N)
+    assert bsm.bsm_gemm_cross_entropy_workspace(1 << 25, 63 * 128) > 0 and bsm.bsm_gemm_cross_entropy_workspace(128, 0x7FFFFF80) > 0
+    expect("BSM_E_SHAPE", bsm.bsm_gemm_cross_entropy_grad_workspace, rows=1 << 25, N=4, K=32 * 128, piece=0)
+    assert bsm.bsm_gemm_cross_entropy_grad_workspace(1 << 25, 4, 31 * 128, 0) > 0
 
 
 def test_cross_entropy_grad_refusals():

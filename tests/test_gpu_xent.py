@@ -128,6 +128,54 @@ def test_large_and_infinite_logits(rows, N):
     assert torch.isnan(lse[bad]).all() and torch.isfinite(lse[~bad]).all()
 
 
+@pytest.mark.parametrize("rows,N", [(20, 100), (20, 30000), (700, 9000)])
+def test_logits_at_the_end_of_the_range(rows, N):
+    """Beyond 2^127.5 or so they count as infinite: positive ones make lse NaN, negative ones add nothing."""
+    x = torch.zeros(rows, 8, device="cuda").bfloat16()
+    w = torch.zeros(N, 8, device="cuda").bfloat16()
+    x[:, 0], x[:, 1] = 2.0 ** 100, 1.0
+    w[1:, 0], w[0, 1] = -1.875 * 2.0 ** 27, 3.0        # z(., 0) = 3, all others -1.875 * 2^127
+    x[1, 0] = -(2.0 ** 100)                            # this row's others: +1.875 * 2^127
+    x[2, 0] = 2.0 ** 99                                # and half: in range, far below
+    x[4, 1] = 0.0
+    w[0, 0] = 0.0
+    labels = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    loss, lse = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    work = torch.empty(bsm.bsm_gemm_cross_entropy_workspace(rows, N), dtype=torch.uint8, device="cuda")
+    say("logits at the end of the range", rows, N)
+    bsm.bsm_gemm_cross_entropy(rows, N, 8, "bf16", x, 8, w, 8, labels, loss, lse, work)
+    want = torch.full((rows,), 3.0, device="cuda")
+    want[1], want[4] = float("nan"), 0.0
+    assert torch.isnan(lse[1]) and torch.isnan(loss[1])
+    keep = torch.arange(rows, device="cuda") != 1
+    assert (lse[keep] - want[keep]).abs().max() < 1e-6 and loss[keep].abs().max() < 1e-6
+    w[0, 0] = w[1, 0]                                  # nothing but such ones
+    w[0, 1] = 0.0
+    bsm.bsm_gemm_cross_entropy(rows, N, 8, "bf16", x, 8, w, 8, labels, loss, lse, work)
+    assert (lse[[0, 3, 5]] == -float("inf")).all()
+
+
+def test_many_rows_few_columns():
+    """dX of 2^28 values and more: the sum of its parts takes several launches."""
+    rows, K = 66001, 4096
+    x, w, labels, dloss = inputs(rows, 3, K, "bf16", 6)
+    lse = torch.zeros(rows, device="cuda")             # (not the loss's: G is what it makes of these)
+    dx = torch.full((rows, K), 7.0, device="cuda")
+    work = torch.empty(bsm.bsm_gemm_cross_entropy_grad_workspace(rows, 3, K, 0), dtype=torch.uint8, device="cuda")
+    say("cross entropy grad", rows, 3, K)
+    bsm.bsm_gemm_cross_entropy_grad(rows, 3, K, "bf16", x, K, w, K, labels, lse, dloss, 0, work, "f32", dx, K, "f32", None, K)
+    for r in (slice(0, 300), slice(65300, 65700), slice(rows - 300, rows)):
+        z = x[r].double() @ w.double().T.contiguous()
+        has = (labels[r] >= 0)[:, None]
+        G = torch.exp(z)
+        G[torch.arange(z.shape[0], device="cuda"), labels[r].clamp(0).long()] -= 1.0
+        G = torch.where(has, G * dloss[r].double()[:, None], 0.0)
+        ref, mag = G @ w.double(), (torch.exp(z) + 1) * dloss[r].double().abs()[:, None]
+        # z off by K 2^-23 sum |x w|, G by that, 2^-18 for its two terms and a few float32 steps; three terms of dX
+        ez = (K * 2.0 ** -23 * (x[r].double().abs() @ w.double().abs().T.contiguous()) + 2.0 ** -18 + 2.0 ** -20).amax(1, keepdim=True)
+        assert ((dx[r].double() - ref).abs() <= (mag * (ez + 2.0 ** -20)) @ w.double().abs()).all()
+
+
 def test_f16_weights_of_every_size():
     """The weights' power of two: tiny, huge, zero and one row far above the rest."""
     x, w, labels, _ = inputs(90, 500, 40, "f16", 9)

@@ -210,6 +210,8 @@ def test_activation_made_again(d):
     Q, S, v, s = check_save(x, d, "e4m3")
     check_restore(Q, S, v, s, "e4m3", d, bsm.ewise_desc("silu_affine", 1.5, -0.25))
     check_grad(Q, S, v, s, "e4m3", d, op="none")
+    Q, S, v, s = check_save(x, d, "e5m2")
+    check_restore(Q, S, v, s, "e5m2", d, bsm.ewise_desc("silu_affine", 1.5, -0.25))
 
 
 def test_slope_over_its_range():

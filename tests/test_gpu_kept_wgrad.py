@@ -100,6 +100,7 @@ def test_tiles(sizes, M, N, ab, fmt):
     ([33, 64, 0, 31, 100], 1030, 700)])                        # one
 def test_every_tile(sizes, M, N, ab, fmt):
     wgrad(sizes, M, N, ab, fmt, "f32", seed=N, first=1, behind=1)
+    wgrad(sizes, M, N, ab, fmt, "f32", 1, seed=N, first=1)
     wgrad(sizes, M, N, ab, fmt, ab, 1, seed=N, extra=16, pad=8)
 
 

@@ -91,6 +91,14 @@ def test_many_rows(rows, E, k, fmt, d_fmt):
     run(rows, E, k, fmt, d_fmt, seed=E)
 
 
+@pytest.mark.parametrize("fmt", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("E", [7, 30, 62, 100, 250, 500, 1001])
+def test_every_width(E, fmt):
+    """Few rows, which one workgroup takes, and more of them."""
+    run(9, E, 2, fmt, seed=E)
+    run(40000 // E + 900, E, 2, fmt, seed=E)
+
+
 @pytest.mark.parametrize("k", [1, 3, 16, 70])
 def test_ids_a_row(k):
     run(100, 12, k, seed=k)

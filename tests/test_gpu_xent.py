@@ -41,6 +41,15 @@ def test_formats_accumulation_and_pieces(rows, N, K, ab):
         both(rows, N, K, ab, dx_fmt=dx, dw_fmt=dw, accum=accum, piece=piece, extra=1)
 
 
+@pytest.mark.parametrize("ab", ["bf16", "f16"])
+def test_float32_gradients_on_every_tile(ab):
+    """G in two terms, made on 32-row and on large tiles; a float32 weight gradient on large tiles, added to and not."""
+    both(24, 33000, 40, ab, dx_fmt="f32", dw_fmt="f32")
+    both(4096, 4100, 40, ab, dx_fmt="f32", dw_fmt="f32")
+    for accum in (0, 1):
+        both(1700, 4096, 4096, ab, want="w", dw_fmt="f32", accum=accum)
+
+
 def test_one_gradient_alone():
     """Of few rows, whose gradients otherwise share a launch, and of many."""
     for ab, f in (("bf16", "bf16"), ("f16", "f32")):

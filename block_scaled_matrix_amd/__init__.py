@@ -292,22 +292,32 @@ def _here(stream, *tensors):
     """The stream's handle, once every torch tensor given is known to live on the current device: the kernels
     take addresses, and one of the host or of another device would fault them. Work on another device goes
     under torch.cuda.device of that device."""
-    at = -1
+    at = -2
     for t in tensors:
         if t is None or type(t) is int:
             continue
         d = t.get_device()
+        if d == at:
+            continue
         if d < 0:
             raise BsmError(-13, f"a tensor on {t.device}: the library takes device memory")
-        if d != at:
-            import torch
-            if d != torch.cuda.current_device():
-                raise BsmError(-13, f"a tensor on {t.device} while the current device is cuda:{torch.cuda.current_device()}")
-            at = d
+        if _torch_c is None:
+            _fill_torch_c()
+        if d != _torch_c._cuda_getDevice():   # (current_device() without the check that CUDA is initialised: it holds t)
+            raise BsmError(-13, f"a tensor on {t.device} while the current device is cuda:{_torch_c._cuda_getDevice()}")
+        at = d
     if stream is None and at >= 0:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(at)   # (current_stream() without the object around it)
+        return _torch_c._cuda_getCurrentRawStream(at)   # (current_stream() without the object around it)
     return _stream(stream)
+
+
+_torch_c = None
+
+
+def _fill_torch_c():
+    global _torch_c
+    import torch
+    _torch_c = torch._C
 
 
 _dtypes = {}
@@ -320,13 +330,13 @@ def _array(t, dtype: str, what, least):
     if dtype not in _dtypes:
         import torch
         _dtypes[dtype] = getattr(torch, dtype)
+    if t.dtype is _dtypes[dtype] and t.is_contiguous() and t.numel() >= least:
+        return t.data_ptr()
     if t.dtype is not _dtypes[dtype]:
         raise BsmError(-8, f"{what} must be {dtype}, not {t.dtype}")
     if not t.is_contiguous():
         raise BsmError(-5, f"{what} must be contiguous")
-    if t.numel() < least:
-        raise BsmError(-9, f"{what} holds {t.numel()} elements, the call takes {least}")
-    return t.data_ptr()
+    raise BsmError(-9, f"{what} holds {t.numel()} elements, the call takes {least}")
 
 
 def _workspace(t, least):

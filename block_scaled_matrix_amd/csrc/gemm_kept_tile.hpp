@@ -262,8 +262,8 @@ __device__ __forceinline__ void product(const GemmArgs& a, int64_t m0, int64_t n
     for (int j = 0; j < 8; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   // Y: copy j of wave w holds k-rows 2w + 8j and the one behind (dense::dma_offsets); the swizzle differs between even
   // and odd j alone, so two offsets and a scalar step of 16 rows make all eight. Codes: copy j holds k-rows 4(w + 4j) ..
-  // + 3, 16 codes a lane. Scale words: lane l the word l%2 of the wave's row l/2 (a row's second word may lie past its
-  // end: the first again).
+  // + 3, 16 codes a lane. Scale words: lane l the word l%2 of the wave's row l/2 (a row's second word may lie past N's
+  // scales: the first again).
   uint32_t ao[2];
   // The short tile first: behind the loop, more matrix instructions on the same accumulators made the compiler move up to
   // 700 accumulators about in every turn of it. With one tile alone the copies, whose counts stay, read the first row
@@ -277,7 +277,7 @@ __device__ __forceinline__ void product(const GemmArgs& a, int64_t m0, int64_t n
   }
   const uint32_t bo = (uint32_t)((4 * w + (lane >> 4)) * ldb + min(n0 + 16 * (lane & 15), (a.N - 1) & ~int64_t(15)) - n0);
   const int r16 = (lane >> 1) & 15;
-  const uint32_t so = (uint32_t)((4 * (w + 4 * (r16 >> 2)) + (r16 & 3)) * lds_row + (n0 / 32 + 4 < a.ld_sfb ? 4 * (lane & 1) : 0));
+  const uint32_t so = (uint32_t)((4 * (w + 4 * (r16 >> 2)) + (r16 & 3)) * lds_row + (n0 + 128 < a.N ? 4 * (lane & 1) : 0));
   const uint32_t lds0 = gemm::lds_addr(lds);
   auto copy_a = [&](uint64_t base, int stage, int j) {
     gemm::dma16u(base + (uint64_t)((j >> 1) * 32 * lda), ao[j & 1], lds0 + stage * A_STAGE + 1024 * (w + 4 * j));

@@ -6,11 +6,11 @@
 //
 // The gradient needs the counts but not P, so each direction reads the logits once and nothing but the
 // counts passes between them. LPR lanes share a row (4 to 16, beyond 256 experts 64; four experts a lane and
-// vector, J vectors: lanes of 16 reduce without LDS, and more values a lane are more loads in flight), so a lane keeps the same experts for every row it sees: f stays in its registers, and P's
-// column sums are register sums, joined at the end across the wave's rows, the workgroup's waves (LDS)
-// and the workgroups (a second launch over at most 256 of them), all in a fixed order. A lane adds at
-// most 64 rows in float32, then into a double: a sum over any number of rows keeps its bits. Counts are
-// integers, so the LDS atomics that make them cannot change a result by their order.
+// vector, J vectors: lanes of 16 reduce without LDS, and more values a lane are more loads in flight), so a lane keeps
+// the same experts for every row it sees: f stays in its registers, and P's column sums are register sums, joined at the
+// end across the wave's rows, the workgroup's waves (LDS) and the workgroups (a second launch over at most 256 of them),
+// all in a fixed order. A lane adds at most 64 rows in float32, then into a double: a sum over any number of rows keeps
+// its bits. Counts are integers, so the LDS atomics that make them cannot change a result by their order.
 // Bound: for many rows the latency of a few loads and reductions behind one another, sixteen waves a CU in turn (32768
 // rows, 128 experts, bf16: 9 us for 8 MB, 4-8 us for the join, the gradient 9.5 us for 17 MB); for few rows launches, so
 // up to kOneGroup logits a single workgroup does everything in one (16 rows, 64 experts: 3.7 us).

@@ -204,7 +204,7 @@ struct GradTwo : Weights {
   }
 };
 
-// Sums as they are, or times a power of two on the device (f16).
+// Sums as they are, or times a power of two on the device (f16; NULL where there are no rows, whose sums are 0).
 template <bool BY>
 struct Times {
   static constexpr bool kStores = false;
@@ -212,7 +212,7 @@ struct Times {
   template <int MI, int NJ>
   __device__ __forceinline__ void operator()(int64_t, int64_t, f32x4 (&acc)[MI][NJ]) const {
     if constexpr (BY) {
-      const float f = *by;
+      const float f = by ? *by : 1.0f;
 #pragma unroll
       for (int m = 0; m < MI; m++)
 #pragma unroll

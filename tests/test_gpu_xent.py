@@ -77,6 +77,17 @@ def test_no_rows_and_no_width():
     assert (lse.cpu() - want).abs().max() < 1e-6 and (loss.cpu() - want * torch.tensor([1.0, 1, 0, 0, 1])).abs().max() < 1e-6
 
 
+@pytest.mark.parametrize("accum", [0, 1])
+@pytest.mark.parametrize("dw_fmt", ["f16", "f32"])
+def test_no_rows_in_f16(dw_fmt, accum):
+    """An empty micro-batch: no weights, so no power of two for them, and no workspace."""
+    N, K = 300, 200
+    dw = torch.full((N + 1, K), 3.0, dtype=DT[dw_fmt], device="cuda")
+    say("cross entropy grad of no rows", dw_fmt, accum)
+    bsm.bsm_gemm_cross_entropy_grad(0, N, K, "f16", None, K, None, K, None, None, None, 0, None, "f16", None, K, dw_fmt, dw, K, accum)
+    assert (dw[:N] == 3.0 * accum).all() and (dw[N] == 3.0).all()
+
+
 @pytest.mark.parametrize("rows,N", [(40, 300), (500, 20000)])
 def test_rows_without_a_label(rows, N):
     """No label at all; labels far outside; such a row's NaN stays in its row of logits."""

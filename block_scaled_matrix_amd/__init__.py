@@ -488,15 +488,18 @@ def bsm_block_scale_ewise_grad(rows, K, fmt: str, Q, ldq, SF, ld_sf, dy_fmt: str
 def bsm_gemm_grouped_wgrad_block_scale(rows, M, N, n_groups, offsets, ab: str, A, lda, b_fmt: str, B, ldb, SFB, ld_sfb, d_fmt: str,
                                        D, ldd, stride_d, accum=0, stream=None):
     _operand_fmt(ab)
+    _float_fmt(d_fmt, "d_fmt")
     # (a call without groups, rows of D or columns reads no offsets)
     some = n_groups > 0 and M > 0 and N > 0
     off = _array(offsets, "int32", "offsets", n_groups + 1 if some else 0)
     r = rows if some else 0
     x, c = _rows(A, ab, "A", r, M, lda, 8), _rows(B, "u8", "B", r, N, ldb, 16)
     f = _rows(SFB, "u8", "SFB", r, (N + 31) // 32, ld_sfb, 4)
+    need = (n_groups - 1) * stride_d + (M - 1) * ldd + N
+    d = _rows(D, d_fmt, "D", 1 if some else 0, need, need)
     s = _here(stream, offsets, A, B, SFB, D)
     _check(lib().bsm_gemm_grouped_wgrad_block_scale(rows, M, N, n_groups, off, DTYPE[ab], x, lda, DTYPE[b_fmt], c, ldb, f, ld_sfb,
-                                                    DTYPE[d_fmt], _ptr(D), ldd, stride_d, accum, s))
+                                                    DTYPE[d_fmt], d, ldd, stride_d, accum, s))
 
 
 def bsm_gemm_cross_entropy_workspace(rows, N) -> int:

@@ -210,3 +210,18 @@ def test_kept_weight_gradient_refusals():
         expect(name, kept_wgrad, **bad)
     for none in (dict(M=0), dict(N=0), dict(n_groups=0, offsets=0)):
         kept_wgrad(a=0, b=0, sf=0, d=0, **none)
+
+
+def test_kept_weight_gradient_output_refusals():
+    """D of another type than d_fmt says, and D that ends before the last group's last row does."""
+    z = lambda n, t=torch.float32: torch.zeros(n, dtype=t)
+    whole = 3 * 8192 + 63 * 104 + 100
+    for name, bad in (("BSM_E_DTYPE", dict(d=z(4 * 8192, torch.bfloat16))), ("BSM_E_DTYPE", dict(d_fmt="bf16", d=z(4 * 8192))),
+                      ("BSM_E_DTYPE", dict(d=z(4 * 8192, torch.int32))), ("BSM_E_DTYPE", dict(d_fmt="e4m3")),
+                      ("BSM_E_SHAPE", dict(d=z(whole - 1))), ("BSM_E_SHAPE", dict(d=z(whole + 3)[4:])),
+                      ("BSM_E_SHAPE", dict(n_groups=1, d=z(63 * 104 + 99))), ("BSM_E_SHAPE", dict(rows=0, d=z(whole - 1))),
+                      ("BSM_E_ALIGN", dict(d=z(2 * whole).view(-1, 2)[:, 0])),
+                      # long enough: refused for living on the host
+                      ("BSM_E_ARG", dict(d=z(whole))), ("BSM_E_ARG", dict(n_groups=1, d=z(63 * 104 + 100))),
+                      ("BSM_E_ARG", dict(d=z(whole + 4)[4:])), ("BSM_E_ARG", dict(d_fmt="bf16", d=z(whole, torch.bfloat16)))):
+        expect(name, kept_wgrad, **bad)

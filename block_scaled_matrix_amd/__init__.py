@@ -349,13 +349,31 @@ def _workspace(t, least):
     return t.data_ptr()
 
 
+_SIZE = {"f32": 4, "bf16": 2, "f16": 2}
+
+
+def _output(t, d_fmt: str, n, stride, rows, cols, ld):
+    """Address of the output D of n matrices of rows x cols elements, `stride` apart, which a torch tensor (of any type) has
+    to hold from its start on: the kernels write to its last row's end."""
+    if t is None or type(t) is int or n <= 0 or rows <= 0 or cols <= 0:
+        return _ptr(t)
+    need = ((n - 1) * stride + (rows - 1) * ld + cols) * _SIZE.get(d_fmt, 0)
+    size = t.element_size()
+    if not (t.is_contiguous() and t.numel() * size >= need):   # (as nearly every call has it)
+        have = t.untyped_storage().nbytes() - t.storage_offset() * size
+        if have < need:
+            raise BsmError(-9, f"D holds {have} bytes from its start on, the call writes to byte {need}")
+    return _ptr(t)
+
+
 def bsm_gemm_grouped(rows, N, K, n_groups, offsets, ab: str, A, lda, B, ldb, b_major: str, stride_b, d_fmt: str, D, ldd,
                      accum=0, ew: bsm_ewise | None = None, stream=None):
     # (a call without groups, rows or columns reads no offsets)
     off = _array(offsets, "int32", "offsets", n_groups + 1 if n_groups > 0 and rows > 0 and N > 0 else 0)
     s = _here(stream, offsets, A, B, D)
+    d = _output(D, d_fmt, min(n_groups, 1), 0, rows, N, ldd)
     _check(lib().bsm_gemm_grouped(rows, N, K, n_groups, off, DTYPE[ab], _ptr(A), lda, _ptr(B), ldb,
-                                  b_major.encode(), stride_b, DTYPE[d_fmt], _ptr(D), ldd, accum,
+                                  b_major.encode(), stride_b, DTYPE[d_fmt], d, ldd, accum,
                                   C.byref(ew) if ew is not None else None, s))
 
 
@@ -364,8 +382,9 @@ def bsm_gemm_grouped_wgrad(rows, M, N, n_groups, offsets, ab: str, A, lda, B, ld
     # (a call without groups, rows of D or columns reads no offsets)
     off = _array(offsets, "int32", "offsets", n_groups + 1 if n_groups > 0 and M > 0 and N > 0 else 0)
     s = _here(stream, offsets, A, B, D)
+    d = _output(D, d_fmt, n_groups, stride_d, M, N, ldd)
     _check(lib().bsm_gemm_grouped_wgrad(rows, M, N, n_groups, off, DTYPE[ab], _ptr(A), lda, _ptr(B), ldb,
-                                        DTYPE[d_fmt], _ptr(D), ldd, stride_d, accum, s))
+                                        DTYPE[d_fmt], d, ldd, stride_d, accum, s))
 
 
 def bsm_gemm_grouped_block_scale(rows, N, K, n_groups, offsets, a_fmt: str, A, lda, SFA, ld_sfa, b_fmt: str, B, ldb, stride_b,
@@ -374,9 +393,10 @@ def bsm_gemm_grouped_block_scale(rows, N, K, n_groups, offsets, a_fmt: str, A, l
     # (a call without groups, rows or columns reads no offsets)
     off = _array(offsets, "int32", "offsets", n_groups + 1 if n_groups > 0 and rows > 0 and N > 0 else 0)
     s = _here(stream, offsets, A, SFA, B, SFB, D)
+    d = _output(D, d_fmt, min(n_groups, 1), 0, rows, N, ldd)
     _check(lib().bsm_gemm_grouped_block_scale(rows, N, K, n_groups, off, DTYPE[a_fmt], _ptr(A), lda,
                                               _ptr(SFA), ld_sfa, DTYPE[b_fmt], _ptr(B), ldb, stride_b, _ptr(SFB), ld_sfb,
-                                              stride_sfb, fast, DTYPE[d_fmt], _ptr(D), ldd, accum,
+                                              stride_sfb, fast, DTYPE[d_fmt], d, ldd, accum,
                                               C.byref(ew) if ew is not None else None, s))
 
 
@@ -391,8 +411,9 @@ def bsm_gemm_lora(rows, N, K, R, n_adapters, adapter, ab: str, X, ldx, W, ldw, L
     scales = _array(scale, "float32", "scale", n_adapters if with_adapters else 0)
     work = _workspace(workspace, rows * ((R + 31) // 32 * 32) * 4 if with_adapters else 0)
     s = _here(stream, adapter, X, W, LA, LB, scale, workspace, D)
+    d = _output(D, d_fmt, 1, 0, rows, N, ldd)
     _check(lib().bsm_gemm_lora(rows, N, K, R, n_adapters, ids, DTYPE[ab], _ptr(X), ldx, _ptr(W), ldw, _ptr(LA), ld_la, stride_la,
-                               _ptr(LB), ld_lb, stride_lb, scales, work, DTYPE[d_fmt], _ptr(D), ldd, accum,
+                               _ptr(LB), ld_lb, stride_lb, scales, work, DTYPE[d_fmt], d, ldd, accum,
                                C.byref(ew) if ew is not None else None, s))
 
 

@@ -180,3 +180,18 @@ def test_short_arrays_are_refused():
         expect("BSM_E_ARG", lora, adapter=ints(1), **unused)             # (refused for its device alone)
         expect("BSM_E_ARG", lora, scale=torch.ones(1), **unused)
         expect("BSM_E_ARG", lora, ws=torch.zeros(1), **unused)
+
+
+def test_outputs_too_short_are_refused(monkeypatch):
+    """D that ends before the call's last row does, a bf16 one for float32 results among them. (Where the tensors live is
+    looked at before that.)"""
+    monkeypatch.setattr(bsm, "_here", lambda stream, *tensors: 0)
+    z = lambda n, t=torch.bfloat16: torch.zeros(n, dtype=t)
+    for fn, extra, whole in ((grouped, {}, 99 * 64 + 64), (wgrad, {}, 3 * 4096 + 64 * 64), (mx, {}, 99 * 64 + 64),
+                             (lora, {}, 99 * 64 + 64), (wgrad, dict(n_groups=1, stride_d=0), 64 * 64)):
+        for bad in (dict(d=z(whole - 1)), dict(d_fmt="f32", d=z(2 * whole - 1)), dict(d_fmt="f32", d=z(whole - 1, torch.float32)),
+                    dict(d=z(whole + 7)[8:]), dict(d=z(2 * whole - 2, torch.uint8))):
+            expect("BSM_E_SHAPE", fn, **extra, **bad)
+        # long enough: refused for what comes after it
+        for good in (dict(d=z(whole)), dict(d_fmt="f32", d=z(2 * whole)), dict(d=z(2 * whole, torch.uint8)), dict(d=z(whole + 8)[8:])):
+            expect("BSM_E_ARG", fn, accum=2, **extra, **good)

@@ -51,14 +51,14 @@ __device__ __forceinline__ void load8(const void* p, int64_t i, int left, float 
 }
 
 // Rounded to the format; finite values beyond f16's range become its largest (a value that fits f16 may be kept as a
-// code just past it: 65504 as 65536).
-template <int F>
+// code just past it: 65504 as 65536), and where BOUND says so those beyond bf16's (its own last ones are kept as 2^128).
+template <int F, bool BOUND>
 __device__ __forceinline__ uint16_t bits16(float v) {
-  if constexpr (F == BSM_BF16) return f32_to_bf16_bits(v);
+  if constexpr (F == BSM_BF16) return f32_to_bf16_bits(BOUND ? kept::clamp_bf16(v) : v);
   else return f32_to_f16_bits(kept::clamp_f16(v));
 }
 
-template <int F>
+template <int F, bool BOUND>
 __device__ __forceinline__ void store8(void* p, int64_t i, int left, const float (&v)[8]) {
   if constexpr (F == BSM_F32) {
     float* q = (float*)p + i;
@@ -78,12 +78,12 @@ __device__ __forceinline__ void store8(void* p, int64_t i, int left, const float
     if (left >= 8) {
       u32x4 x;
 #pragma unroll
-      for (int e = 0; e < 4; e++) x[e] = bits16<F>(v[2 * e]) | (uint32_t)bits16<F>(v[2 * e + 1]) << 16;
+      for (int e = 0; e < 4; e++) x[e] = bits16<F, BOUND>(v[2 * e]) | (uint32_t)bits16<F, BOUND>(v[2 * e + 1]) << 16;
       __builtin_nontemporal_store(x, (u32x4*)q);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; e++)
-        if (e < left) q[e] = bits16<F>(v[e]);
+        if (e < left) q[e] = bits16<F, BOUND>(v[e]);
     }
   }
 }
@@ -162,14 +162,24 @@ __global__ __launch_bounds__(256) void k_use(KeptArgs a, Divide per_row, uint32_
 #pragma unroll
   for (int u = 0; u < UNROLL; u++) {
     float v[8];
+    // A finite value is made a finite one in 16 bits, and f of it (-2^128, a mask's fill as it is kept, gives f's limit and
+    // not NaN). In float32 without f it is the value rounded: infinity from 2^128 on. The slope has the same limits at both.
+    constexpr bool BOUND = EW == 1 || (EW == 0 && F != BSM_F32);
 #pragma unroll
-    for (int h = 0; h < 2; h++) kept::decode4<FMT>(c[u][h], s[u], v + 4 * h);
+    for (int h = 0; h < 2; h++) kept::decode4<FMT, BOUND>(c[u][h], s[u], v + 4 * h);
 #pragma unroll
     for (int e = 0; e < 8; e++) {
-      if constexpr (EW == 1) v[e] = silu_affine(v[e], a.ew_scale, a.ew_bias);
+      if constexpr (EW == 1) {
+        const float x = v[e];
+        v[e] = silu_affine(x, a.ew_scale, a.ew_bias);
+        if constexpr (F != BSM_F32)   // (times a scale above 1 it may leave float32)
+          if (__builtin_fabsf(v[e]) == INFINITY && __builtin_fabsf(x) < INFINITY && __builtin_fabsf(a.ew_scale) < INFINITY &&
+              __builtin_fabsf(a.ew_bias) < INFINITY)
+            v[e] = __builtin_copysignf(kept::kMaxF32, v[e]);
+      }
       if constexpr (EW == 2) v[e] = dy[u][e] * (a.ew_op ? a.ew_scale * kept::silu_slope(v[e]) : 1.0f);
     }
-    store8<F>(a.D, p[u].row * a.ldd + p[u].col, p[u].left, v);
+    store8<F, EW != 2>(a.D, p[u].row * a.ldd + p[u].col, p[u].left, v);
   }
 }
 

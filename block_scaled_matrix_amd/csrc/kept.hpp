@@ -28,6 +28,8 @@ hipError_t launch_gemm_kept_wgrad(const GemmArgs& a, const GroupArgs& gr, hipStr
 
 namespace kept {
 
+constexpr float kMaxF32 = 0x1.fffffep127f, kMaxBf16 = 0x1.fep127f;
+
 // n / d for n < 2^31: the top of n times 2^(31+s) / d rounded up, 2^(s-1) < d <= 2^s. The excess of the
 // multiplier, less than d, moves the quotient by less than 1 / d.
 struct Divide {
@@ -68,9 +70,18 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
   return (uint32_t)r;
 }
 
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-// Four codes times the scale (exact: at most four significant bits).
+// From this scale code on a finite code may stand for 2^128 or more.
 template <int FMT>
+constexpr int kWideScale = FMT == BSM_E4M3 ? 247 : 240;
+// scale() for values that are taken in f16: above the scale before that every code but 0 lies past f16's range, and stays in
+// float32's.
+template <int FMT>
+__device__ __forceinline__ float scale_f16(int code) { return scale(code == 255 ? 255 : min(code, kWideScale<FMT> - 1)); }
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+// Four codes times the scale (exact: at most four significant bits). BOUND: finite codes beyond float32's range give its
+// largest value, not infinity.
+template <int FMT, bool BOUND = false>
 __device__ __forceinline__ void decode4(uint32_t c, float s, float* v) {
   f32x2 lo, hi;
   if constexpr (FMT == BSM_E4M3) {
@@ -80,12 +91,20 @@ __device__ __forceinline__ void decode4(uint32_t c, float s, float* v) {
     lo = __builtin_amdgcn_cvt_pk_f32_bf8((int)c, false);
     hi = __builtin_amdgcn_cvt_pk_f32_bf8((int)c, true);
   }
-  v[0] = lo[0] * s; v[1] = lo[1] * s; v[2] = hi[0] * s; v[3] = hi[1] * s;
+  const float u[4] = {lo[0], lo[1], hi[0], hi[1]};
+#pragma unroll
+  for (int e = 0; e < 4; e++) {
+    v[e] = u[e] * s;
+    if constexpr (BOUND) v[e] = __builtin_fabsf(v[e]) == INFINITY && __builtin_fabsf(u[e]) < INFINITY ? __builtin_copysignf(kMaxF32, u[e]) : v[e];
+  }
 }
 
-// Finite values to f16's range; infinities and NaN as they are.
+// Finite values to f16's and bf16's range; infinities and NaN as they are.
 __device__ __forceinline__ float clamp_f16(float v) {
   return __builtin_fabsf(v) < INFINITY ? __builtin_amdgcn_fmed3f(v, -65504.0f, 65504.0f) : v;
+}
+__device__ __forceinline__ float clamp_bf16(float v) {
+  return __builtin_fabsf(v) < INFINITY ? __builtin_amdgcn_fmed3f(v, -kMaxBf16, kMaxBf16) : v;
 }
 
 // d/dx x / (1 + e^-x) = s (1 + x (1 - s)), s = 1 / (1 + e^-x). With t = e^-|x| both s and 1 - s are quotients of

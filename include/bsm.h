@@ -453,8 +453,8 @@ int bsm_router_balance_grad(int64_t rows, int32_t n_experts, int32_t k, int32_t 
  *   SF[t*ld_sf + k/32] = e + 127, e the smallest integer with max |X| over the block's finite values <= max_fmt * 2^e
  *   (448 or 57344; e at least -127), Q[t*ldq + k] = X(t,k) * 2^-e rounded to nearest even.
  * No finite value saturates: normal codes are off by at most 2^-4 (E4M3) or 2^-3 (E5M2) of the value, smaller ones by at
- * most 2^(e-10) or 2^(e-17). NaN is kept as NaN, an infinity as the format's (E4M3 has none: NaN), without touching the
- * block's scale.
+ * most 2^(e-10) or 2^(e-17); from 1.9375 * 2^127 (1.875 * 2^127) on the code stands for 2^128. NaN is kept as NaN, an
+ * infinity as the format's (E4M3 has none: NaN), without touching the block's scale.
  *   x_fmt:     BSM_BF16, BSM_F16 or BSM_F32; X 16-byte aligned, ldx a multiple of 8 (16-bit) or 4 (F32);
  *   fmt:       BSM_E4M3 or BSM_E5M2; Q 16-byte aligned, ldq a multiple of 16;
  *   SF:        4-byte aligned, ld_sf >= ceil(K/32) and a multiple of 4;
@@ -464,10 +464,11 @@ int bsm_block_scale_save(int64_t rows, int64_t K, int32_t x_fmt, const void* X, 
                          uint8_t* SF, int64_t ld_sf, void* stream);
 
 /* The kept values back: D[t*ldd + k] = f(dec(Q[t*ldq + k]) * 2^(SF[t*ld_sf + k/32] - 127)), rounded to d_fmt (BSM_BF16,
- * BSM_F16 or BSM_F32); in F16 a finite value beyond the format's range becomes its largest. f as for bsm_gemm_ewise (an
- * activation made again from its kept input), or ew NULL for none. A scale code of 0xFF makes its block NaN. Q, ldq, SF
- * and ld_sf as above (Q spans whole rows); D 16-byte aligned, ldd a multiple of 8 (16-bit) or 4 (F32). Q and SF must not
- * overlap D. */
+ * BSM_F16 or BSM_F32); in F16 and BF16 a finite value beyond the format's range becomes its largest (the type's lowest value,
+ * a mask's fill, comes back as such), in F32 a value of 2^128 or more is infinite. f as for bsm_gemm_ewise (an activation made
+ * again from its kept input), or ew NULL for none; f takes values of 2^128 or more as float32's largest. A scale code of 0xFF
+ * makes its block NaN. Q, ldq, SF and ld_sf as above (Q spans whole rows); D 16-byte aligned, ldd a multiple of 8 (16-bit) or
+ * 4 (F32). Q and SF must not overlap D. */
 int bsm_block_scale_restore(int64_t rows, int64_t K, int32_t fmt, const uint8_t* Q, int64_t ldq, const uint8_t* SF, int64_t ld_sf,
                             int32_t d_fmt, void* D, int64_t ldd, const bsm_ewise* ew, void* stream);
 

@@ -241,6 +241,67 @@ def test_f16_at_the_end_of_its_range():
     check_restore(Q, S, v, s, "e4m3", "f16")
 
 
+def ends(v, s, K, d):
+    """values() in the format d, finite ones beyond its range its largest (codes and scales of any maker)."""
+    x = values(v, s, K)
+    m = torch.finfo(DT[d]).max
+    return torch.where(torch.isfinite(x), x.clamp(-m, m), x).to(DT[d])
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("d", ["bf16", "f16"])
+def test_every_code_under_every_scale_in_16_bits(d, fmt):
+    """Finite values beyond the range come back as its largest, infinite codes as infinity."""
+    codes = torch.arange(256, dtype=torch.uint8).view(8, 32).repeat(256, 1)
+    s = torch.arange(256, dtype=torch.uint8).repeat_interleave(8).view(-1, 1)
+    S = torch.zeros(2048, 4, dtype=torch.uint8)
+    S[:, :1] = s
+    want = ends(codes.view(F8[fmt]).double(), s, 32, d)
+    want[s[:, 0] == 255] = float("nan")
+    D = torch.empty(2048, 32, dtype=DT[d], device="cuda")
+    say("restore every code", d, fmt)
+    bsm.bsm_block_scale_restore(2048, 32, fmt, codes.cuda(), 32, S.cuda(), 4, d, D, 32)
+    assert same(D.cpu(), want)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("x_fmt", ["bf16", "f32"])
+def test_lowest_value_of_the_type(x_fmt, fmt):
+    """A mask's fill, kept as a code that stands for -2^128, comes back finite in 16 bits."""
+    low = torch.finfo(DT[x_fmt]).min
+    x = torch.randn(6, 64).to(DT[x_fmt])
+    x[1:, 5:40] = low
+    x[3] = low
+    x[4, 50] = -low
+    Q, S, v, s = check_save(x, x_fmt, fmt)
+    assert float(values(v, s, 64).min()) == -2.0 ** 128
+    for d in ("bf16", "f16"):
+        D = torch.empty(6, 64, dtype=DT[d], device="cuda")
+        bsm.bsm_block_scale_restore(6, 64, fmt, Q, Q.stride(0), S, S.stride(0), d, D, 64)
+        assert same(D.cpu(), ends(v, s, 64, d)) and torch.isfinite(D).all()
+
+
+@pytest.mark.parametrize("d", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_activation_of_values_beyond_float32(fmt, d):
+    """f of a code that stands for +-2^128 or more: f's limit below, the largest value (float32: infinity) above."""
+    big = 0x78                                          # 256 and 32768
+    codes = torch.full((4, 32), big, dtype=torch.uint8)
+    codes[1], codes[2], codes[3] = big | 0x80, 0x30, 0x7F
+    S = torch.full((4, 4), 127 + (120 if fmt == "e4m3" else 113), dtype=torch.uint8)
+    D = torch.empty(4, 32, dtype=DT[d], device="cuda")
+    say("activation beyond float32", d, fmt)
+    bsm.bsm_block_scale_restore(4, 32, fmt, codes.cuda(), 32, S.cuda(), 4, d, D, 32, bsm.ewise_desc("silu_affine", 1.5, -0.25))
+    m = float("inf") if d == "f32" else torch.finfo(DT[d]).max
+    got = D.cpu().float()
+    mid = float(codes[2, 0].view(F8[fmt]).float()) * 2.0 ** (120 if fmt == "e4m3" else 113) * 1.5
+    assert (got[0] == m).all() and (got[1] == -0.25).all() and torch.isnan(got[3]).all()
+    assert (got[2] == (m if d == "f16" else mid)).all()
+    bsm.bsm_block_scale_restore(4, 32, fmt, codes.cuda(), 32, S.cuda(), 4, d, D, 32, bsm.ewise_desc("silu_affine", 2.0 ** -10, 0.0))
+    if d == "bf16":      # 2^128 counts as float32's largest: 2^-10 of it is 2^118 in bf16
+        assert (D[0].float() == 2.0 ** 118).all() and not D[1].any()
+
+
 def test_long_rows_and_many_rows():
     """More than 2^31 elements: past 32-bit offsets."""
     rows, K = 1 << 16, 32800

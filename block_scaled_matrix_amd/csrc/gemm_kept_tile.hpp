@@ -23,8 +23,10 @@ namespace keptmm {
 
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 
-// Eight codes times 2^(code - 127) as the operand's 16-bit format.
-template <int DT, int FMT>
+// Eight codes times 2^(code - 127) as the operand's 16-bit format. Finite ones beyond its range are its largest value: in f16
+// by the scale, in bf16 where BOUND says so. (In bf16 that takes more operations than the conversion, and seldom a scale
+// asks for it: the small tiles convert again where a wave has met one; of the 256 x 256 tile see k_gemm_kept.hip.)
+template <int DT, int FMT, bool BOUND>
 __device__ __forceinline__ uint4 widen8(uint32_t c0, uint32_t c1, uint32_t code) {
   if constexpr (DT == BSM_BF16) {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -35,10 +37,19 @@ __device__ __forceinline__ uint4 widen8(uint32_t c0, uint32_t c1, uint32_t code)
       else v = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(c, s, decltype(hi)::value);
       return __builtin_bit_cast(uint32_t, v);
     };
-    return make_uint4(two(c0, std::false_type{}), two(c0, std::true_type{}), two(c1, std::false_type{}), two(c1, std::true_type{}));
+    uint32_t w[4] = {two(c0, std::false_type{}), two(c0, std::true_type{}), two(c1, std::false_type{}), two(c1, std::true_type{})};
+    if constexpr (BOUND) {
+      // infinities that are not the code's own: one less in their bits
+#pragma unroll
+      for (int e = 0; e < 8; e++) {
+        const uint32_t byte = (e < 4 ? c0 : c1) >> (8 * (e & 3)), half = w[e >> 1] >> (16 * (e & 1));
+        if ((half & 0x7FFFu) == 0x7F80u && !(FMT == BSM_E5M2 && (byte & 0x7Fu) == 0x7Cu)) w[e >> 1] -= 1u << (16 * (e & 1));
+      }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
   } else {
     float v[8];
-    const float s = kept::scale((int)code);
+    const float s = kept::scale_f16<FMT>((int)code);
     kept::decode4<FMT>(c0, s, v);
     kept::decode4<FMT>(c1, s, v + 4);
     uint32_t w[4];
@@ -134,9 +145,10 @@ __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, 
     gemm::dma16u(gb, bo, lds0 + RAW_AT + stage * RAW + 1024 * w);
     gemm::dma4u(gs, so, lds0 + SCALES_AT + stage * SCALES + 256 * w);
   };
-  auto put = [&](int h, uint32_t c0, uint32_t c1, uint32_t word) {
+  const uint32_t wide = n0 + 8 * uc < a.N ? kept::kWideScale<FMT> : 256;   // (past N the scales may be anything)
+  auto put = [&](int h, uint32_t c0, uint32_t c1, uint32_t code, auto bound) {
     const int kr = 8 * w + ur + h * (64 / GROUPS);
-    lds_write_b128(lds + WIDE_AT + kr * T::KROW + ((uc ^ T::swz(kr)) << 4), widen8<DT, FMT>(c0, c1, (word >> (8 * byte)) & 255));
+    lds_write_b128(lds + WIDE_AT + kr * T::KROW + ((uc ^ T::swz(kr)) << 4), widen8<DT, FMT, decltype(bound)::value>(c0, c1, code));
   };
   if (q == 0 && nt > 0) {
     const int64_t col = min(n0 + 8 * uc, (a.N - 1) & ~int64_t(7));
@@ -149,7 +161,7 @@ __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, 
         c = *(const uint2*)(B + row * a.ldb + col);
         word = *(const uint32_t*)(a.SFB + row * a.ld_sfb + word0);
       }
-      put(h, c.x, c.y, word);
+      put(h, c.x, c.y, (word >> (8 * byte)) & 255, std::true_type{});
     }
 #pragma unroll
     for (int j = 0; j < T::COPIES; j++) {
@@ -167,12 +179,20 @@ __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, 
     gemm::stage_barrier<(R - 2) * (T::COPIES + 2)>();
     issue(it + R - 1, R == 2 ? st ^ 1 : ring == 0 ? R - 1 : ring - 1);
     if (t > 0 && t < nt) {
+      u32x2 c[UNITS];
+      uint32_t code[UNITS], top = 0;
 #pragma unroll
       for (int h = 0; h < UNITS; h++) {
         const int row = ur + h * (64 / GROUPS);   // of the wave's eight
-        const u32x2 c = *(const BSM_LDS u32x2*)(lds + RAW_AT + st * RAW + 1024 * w + SIZE * row + 8 * uc);
-        put(h, c[0], c[1], *(const BSM_LDS uint32_t*)(lds + SCALES_AT + st * SCALES + 256 * w + 4 * row));
+        c[h] = *(const BSM_LDS u32x2*)(lds + RAW_AT + st * RAW + 1024 * w + SIZE * row + 8 * uc);
+        code[h] = (*(const BSM_LDS uint32_t*)(lds + SCALES_AT + st * SCALES + 256 * w + 4 * row) >> (8 * byte)) & 255;
+        put(h, c[h][0], c[h][1], code[h], std::false_type{});
+        top = max(top, code[h]);
       }
+      if constexpr (DT == BSM_BF16)
+        if (__builtin_expect(__any(top >= wide), 0))
+#pragma unroll
+          for (int h = 0; h < UNITS; h++) put(h, c[h][0], c[h][1], code[h], std::true_type{});
     }
     gemm::lds_barrier();
     if (t < nt) {
@@ -250,8 +270,9 @@ __device__ __forceinline__ void mfma_steps(const dense::Frags& f, f32x4 (&acc)[8
   (one(std::integral_constant<int, I>{}), ...);
 }
 
+// The lane's result: whether it has met a scale of kept::kWideScale or more (bf16 values beyond the range are infinite then).
 template <int DT, int FMT>
-__device__ __forceinline__ void product(const GemmArgs& a, int64_t m0, int64_t n0, uint8_t* lds, int lane, int w, f32x4 (&acc)[8][8]) {
+__device__ __forceinline__ bool product(const GemmArgs& a, int64_t m0, int64_t n0, uint8_t* lds, int lane, int w, f32x4 (&acc)[8][8]) {
   using namespace dense;
   const int wa = 128 * (w >> 1), wb = 128 * (w & 1);
   const uint16_t* A = (const uint16_t*)a.A;
@@ -302,11 +323,11 @@ __device__ __forceinline__ void product(const GemmArgs& a, int64_t m0, int64_t n
   const uint32_t from = lds0 + RAW_AT + 1024 * w + 8 * lane;
   const uint32_t from_scale = lds0 + SCALES_AT + 256 * w + 8 * (lane >> 5) + ((lane & 31) >> 2);
   auto put = [&](int u, uint32_t c0, uint32_t c1, uint32_t code) {
-    const uint4 x = widen8<DT, FMT>(c0, c1, code);
+    const uint4 x = widen8<DT, FMT, false>(c0, c1, code);
     *at_lds<u32x4>(to[u & 1] + 8192 * (u >> 1)) = u32x4{x.x, x.y, x.z, x.w};
   };
   u32x2 c;
-  uint32_t code;
+  uint32_t code, top = 0;
   auto take = [&](int u, int slot) {
     c = *at_lds<u32x2>(from + slot * X_RAW + 4096 * (u >> 1) + 512 * (u & 1));
     code = *at_lds<uint8_t>(from_scale + slot * X_SCALES + 32 * (u >> 1) + 16 * (u & 1));
@@ -353,6 +374,7 @@ __device__ __forceinline__ void product(const GemmArgs& a, int64_t m0, int64_t n
         sc = a.SFB[row * a.ld_sfb + col / 32];
       }
       put(u, x.x, x.y, sc);
+      top = max(top, sc);
     }
     fill_tile_masked<false>(A, a.lda, m0, a.M, 0, head, lds, w, lane);
     issue_codes(1, 1);
@@ -388,7 +410,10 @@ __device__ __forceinline__ void product(const GemmArgs& a, int64_t m0, int64_t n
       if constexpr (g == C0 - 1) gemm::lds_barrier();
       if constexpr (g >= C0 && (g - C0) % CPS == 0 && (g - C0) / CPS < COPIES) copy((g - C0) / CPS);
       if constexpr (g >= V0 && (g - V0) % VPS == 0 && (g - V0) / VPS < 8) take((g - V0) / VPS, next);
-      if constexpr (g >= V0 + LATER && (g - V0 - LATER) % VPS == 0 && (g - V0 - LATER) / VPS < 8) put((g - V0 - LATER) / VPS, c[0], c[1], code);
+      if constexpr (g >= V0 + LATER && (g - V0 - LATER) % VPS == 0 && (g - V0 - LATER) / VPS < 8) {
+        put((g - V0 - LATER) / VPS, c[0], c[1], code);
+        top = max(top, code);
+      }
       if constexpr (g == B2) gemm::stage_barrier<COPIES>();
       if constexpr (g >= G2 && g - G2 < 16) read(na, tb, 0, g - G2, f0);
     };
@@ -399,6 +424,7 @@ __device__ __forceinline__ void product(const GemmArgs& a, int64_t m0, int64_t n
     slot = next;
   }
   gemm::stage_barrier<0>();
+  return top >= (n0 + 8 * (lane & 31) < a.N ? kept::kWideScale<FMT> : 256);   // (past N the scales may be anything)
 }
 
 }  // namespace large

@@ -67,6 +67,33 @@ __global__ __launch_bounds__(256 * Q, 4) void k_kept_wgrad(GemmArgs a, GroupArgs
   keptmm::mid2::tile<DT, FMT, SIZE, R, Q>(a, SIZE * (int64_t)tm, SIZE * (int64_t)tn, lds + q * LDS, lds, lane, w, q);
 }
 
+// The 128 x 128 tile at (m0, n0) of the product whose arguments lie in LDS, for a workgroup of the large tiles. A function, not
+// inlined: the large tile's loop pays for what stands beside it in registers.
+constexpr int kArgsAt = 128 * 1024;
+static_assert(keptmm::mid2::lds_bytes<128, 2>() <= kArgsAt && kArgsAt + sizeof(GemmArgs) <= keptmm::large::LDS_BYTES, "the arguments in LDS");
+template <int DT, int FMT>
+__device__ __attribute__((noinline)) void small_tile(uint32_t lds0, int m0, int n0) {
+  // (the same in every lane, which the compiler does not know of a function's arguments)
+  auto same = [](auto x) {
+    if constexpr (sizeof(x) == 4) return (decltype(x))__builtin_amdgcn_readfirstlane(x);
+    else {
+      const uint64_t b = __builtin_bit_cast(uint64_t, x);
+      const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)b), hi = __builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
+      return __builtin_bit_cast(decltype(x), (uint64_t)hi << 32 | lo);
+    }
+  };
+  lds0 = same(lds0);
+  uint8_t* lds = (uint8_t*)(BSM_LDS uint8_t*)(uintptr_t)lds0;
+  const BSM_LDS GemmArgs* v = (const BSM_LDS GemmArgs*)(uintptr_t)(lds0 + kArgsAt);
+  GemmArgs a{};
+  a.M = same(v->M); a.N = same(v->N); a.K = same(v->K);
+  a.A = same(v->A); a.lda = same(v->lda); a.B = same(v->B); a.ldb = same(v->ldb);
+  a.SFB = same(v->SFB); a.ld_sfb = same(v->ld_sfb);
+  a.D = same(v->D); a.ldd = same(v->ldd); a.d_fmt = same(v->d_fmt); a.accum = same(v->accum);
+  const int t = threadIdx.x;
+  keptmm::mid2::tile<DT, FMT, 128, 2, 1>(a, same(m0), same(n0), lds, lds, t & 63, same(t >> 6), 0);
+}
+
 // Long groups first: a tile takes its group's rows, and a long one begun last keeps its CU while the others are done (16381
 // rows over 8 groups, the longest 8082 and the seventh in order: 335 us in order).
 template <int DT, int FMT, int OUT, dense::Add ADD>
@@ -76,7 +103,25 @@ __global__ __launch_bounds__(256, 1) void k_kept_wgrad_large(GemmArgs a, GroupAr
   int tm, tn;
   if (!enter(a, gr, tiles_m, tiles_n, [&](int turn) { return ranked_group(gr, turn, (int*)lds); }, tm, tn)) return;
   f32x4 acc[8][8];
-  keptmm::large::product<DT, FMT>(a, 256 * (int64_t)tm, 256 * (int64_t)tn, lds, lane, w, acc);
+  const bool wide = keptmm::large::product<DT, FMT>(a, 256 * (int64_t)tm, 256 * (int64_t)tn, lds, lane, w, acc);
+  if constexpr (DT == BSM_BF16) {
+    // A scale so wide that a finite code may lie beyond bf16's range: the tile again as small ones, which bound what they
+    // convert. (In the loop itself a bound in every conversion takes 16381 rows over 8 groups, 4096 x 2048 from 267 to 290 us, a
+    // branch round it 287, one branch a K tile 311; this 273.)
+    ((int*)lds)[w] = __any(wide);   // (every wave is done with LDS)
+    __syncthreads();
+    const int4 met = *(const int4*)lds;
+    __syncthreads();
+    if (__builtin_expect(__builtin_amdgcn_readfirstlane(met.x | met.y | met.z | met.w), 0)) {
+      if (threadIdx.x == 0) *(GemmArgs*)(lds + kArgsAt) = a;
+      for (int i = 0; i < 4; i++) {
+        const int64_t m = 256 * (int64_t)tm + 128 * (i >> 1), n = 256 * (int64_t)tn + 128 * (i & 1);
+        __syncthreads();
+        if (m < a.M && n < a.N) small_tile<DT, FMT>(gemm::lds_addr(lds), (int)m, (int)n);
+      }
+      return;
+    }
+  }
   const int64_t row0 = 256 * (int64_t)tm + 128 * (w >> 1), col0 = 256 * (int64_t)tn + 128 * (w & 1);
   dense::store_large<OUT, ADD>(a, row0, col0, lane, acc, lds + 32768 * w);
 }

@@ -70,13 +70,17 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) 
   return (uint32_t)r;
 }
 
+// scale() for values that are taken in f16, where it need not be larger than 2^119 (2^112 for E5M2: from there on every code
+// but 0 lies past f16's range, and none past float32's yet) nor smaller than 2^-126.
+template <int FMT>
+__device__ __forceinline__ float scale_f16(int code) {
+  constexpr int TOP = FMT == BSM_E4M3 ? 246 : 239;
+  return __uint_as_float(code == 255 ? 0x7FC00000u : (uint32_t)min(max(code, 1), TOP) << 23);
+}
+
 // From this scale code on a finite code may stand for 2^128 or more.
 template <int FMT>
-constexpr int kWideScale = FMT == BSM_E4M3 ? 247 : 240;
-// scale() for values that are taken in f16: above the scale before that every code but 0 lies past f16's range, and stays in
-// float32's.
-template <int FMT>
-__device__ __forceinline__ float scale_f16(int code) { return scale(code == 255 ? 255 : min(code, kWideScale<FMT> - 1)); }
+constexpr uint32_t kWideScale = FMT == BSM_E4M3 ? 247 : 240;
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 // Four codes times the scale (exact: at most four significant bits). BOUND: finite codes beyond float32's range give its

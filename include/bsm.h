@@ -485,7 +485,7 @@ int bsm_block_scale_ewise_grad(int64_t rows, int64_t K, int32_t fmt, const uint8
  *   A(r,m) = A[r*lda + m] (dY, F16 or BF16),  B(r,n) = dec(B[r*ldb + n]) * 2^(SFB[r*ld_sfb + n/32] - 127),
  * the result of bsm_gemm_grouped_wgrad on the restored activations, without them in memory: B(r,n) is taken in ab's format,
  * which is exact inside its range (F16: finite values beyond 65504 become it and values below 2^-14 round to f16's
- * subnormals; BF16: below 2^-126 likewise).
+ * subnormals; BF16: finite ones of 2^128 or more become its largest, below 2^-126 likewise).
  *   b_fmt:     BSM_E4M3 or BSM_E5M2; B 16-byte aligned, ldb >= N and a multiple of 16, at most 2^23;
  *   SFB:       4-byte aligned, ld_sfb >= ceil(N/32) and a multiple of 4, at most 2^23. Both span whole rows; any N.
  * Everything else as for bsm_gemm_grouped_wgrad; A, B, SFB and offsets must not overlap D. The same inputs give the same

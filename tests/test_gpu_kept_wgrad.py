@@ -172,6 +172,44 @@ def test_f16_at_the_end_of_its_range():
     assert (got[0, :, :40] == 32752.0).all()
 
 
+@pytest.mark.parametrize("rows,M,N", [(32, 128, 64), (800, 200, 200), (1600, 1032, 1200), (70, 1000, 2100), (800, 4096, 3600)])   # each tile
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("ab", ["bf16", "f16"])
+def test_values_beyond_the_range(ab, fmt, rows, M, N):
+    """Codes that stand for more than ab's range (2^128 and more in BF16) enter as its largest value, not as infinity, so that
+    rows of zeros in dY leave no NaN; infinite codes stay so."""
+    g = torch.Generator().manual_seed(rows)
+    c, _ = kept_rows(rows, N, fmt, g, 1)
+    s = torch.randint(236, 255, (rows, (N + 31) // 32), generator=g).to(torch.uint8)
+    if fmt == "e5m2":
+        c[5, 3] = 0xFC
+    y = torch.zeros(rows, M, dtype=DT[ab])
+    y[5::8, :M:3] = 2.0 ** -12                          # one term a sum and group: exact
+    groups = -(-rows // 8)
+    off = torch.tensor([min(8 * i, rows) for i in range(groups + 1)], dtype=torch.int32, device="cuda")
+    sd = torch.full((rows, up(s.shape[1], 4)), 255, dtype=torch.uint8)
+    sd[:, :s.shape[1]] = s
+    cd = torch.zeros(rows, up(N, 16), dtype=torch.uint8)
+    cd[:, :N] = c
+    if rows >= 800:                                     # (one long group, one row of dY that is not 0)
+        groups, off = 1, off[[0, -1]].contiguous()
+        y[6:] = 0
+    D = torch.full((groups, M, up(N, 4)), float("nan"), device="cuda")
+    say("kept wgrad beyond the range", ab, fmt, rows, M, N)
+    bsm.bsm_gemm_grouped_wgrad_block_scale(rows, M, N, groups, off, ab, y.cuda(), M, fmt, cd.cuda(), cd.stride(0), sd.cuda(),
+                                           sd.stride(0), "f32", D, D.stride(1), D.stride(0))
+    m = torch.finfo(DT[ab]).max
+    x = values(c.view(F8[fmt]).double(), s, N)
+    x = torch.where(torch.isfinite(x), x.clamp(-m, m), x).float()
+    got = D[:, :, :N].cpu()
+    for i in range(groups):
+        r = 8 * i + 5
+        want = x[r] * 2.0 ** -12 if r < rows else torch.zeros(N)
+        inf = torch.isinf(x[8 * i:8 * i + 8]).any(0) if fmt == "e5m2" else torch.zeros(N, dtype=torch.bool)
+        assert torch.equal(got[i, 0, ~inf], want[~inf])
+        assert not got[i, 1][~inf].any() and torch.isnan(got[i, 1][inf]).all() and (got[i, 0][inf] == -float("inf")).all()
+
+
 def test_offsets_outside_the_rows_stay_inside():
     rows, M, N = 20, 24, 40
     y = torch.randn(rows, M).bfloat16().cuda()

@@ -239,3 +239,46 @@ def test_gradient_against_differences():
                 t[i, k] = keep
                 # G is rounded to bf16: 2^-8 of sum |G| |operand|, weights 0.2, values to 3
                 assert abs((hi - lo) / (2 * h) - float(g[i, k])) < 2.0 ** -8 * 5
+
+
+@pytest.mark.parametrize("ab", ["bf16", "f16"])
+def test_gradient_against_differences_within_two_terms(ab):
+    """The same of float32 gradients, at what G's two terms leave: the bound of xent_util for each element (the differences
+    themselves are good to 1e-8: h^2 / 6 of a third derivative below 20, and 2^-52 of the loss over 2 h)."""
+    rows, N, K = 5, 9, 6
+    x, w, labels, dloss = inputs(rows, N, K, ab, 3)
+    _, lse = check_loss(x, w, labels, ab)
+    dx, dw = check_grad(x, w, labels, dloss, lse, ab, "f32", "f32")
+    X, W, d = x.double().cpu(), w.double().cpu(), dloss.double().cpu()
+    lab = labels.cpu().long()
+    has = (lab >= 0) & (lab < N)
+
+    def f(a, b):
+        z = a @ b.T
+        return float((torch.where(has, torch.logsumexp(z, 1) - z.gather(1, lab.clamp(0, N - 1)[:, None])[:, 0], 0.0) * d).sum())
+
+    def differences(t):
+        out, h = torch.empty_like(t), 1e-5
+        for i in range(t.shape[0]):
+            for k in range(t.shape[1]):
+                keep = float(t[i, k])
+                t[i, k] = keep + h
+                hi = f(X, W)
+                t[i, k] = keep - h
+                out[i, k] = (hi - f(X, W)) / (2 * h)
+                t[i, k] = keep
+        return out
+
+    z, ez, rl, el, _, _, at = (t.cpu() for t in reference(x, w, labels))
+    p = torch.exp(z - rl[:, None])
+    G = torch.where(has[:, None], (p - torch.nn.functional.one_hot(at, N)) * d[:, None], 0.0)
+    r = (ez + el)[:, None] + (4 * z.abs() + 4 * rl.abs()[:, None] + 8) * 2.0 ** -24
+    e = torch.where(has[:, None], d.abs()[:, None] * (p * r + 2.0 ** -23), 0.0) + (2.0 ** -16 if ab == "bf16" else 2.0 ** -22) * G.abs() * 1.01
+    if ab == "f16":
+        e = torch.where(has[:, None], e + 2.0 ** -39 * float(d.abs().max()), 0.0)
+    sums = (2 * N + 2 * rows + 68) * 2.0 ** -23 * G.abs()
+    for got, want, tol in ((dx, differences(X), (e + sums) @ W.abs()), (dw, differences(W), (e + sums).T @ X.abs())):
+        miss = (got[:, :K].double().cpu() - want).abs() - (tol + 2.0 ** -24 * want.abs() + 1e-8)
+        assert (miss <= 0).all(), float(miss.max())
+        # (a gradient of zeros, or of another sign, would not pass)
+        assert (want.abs() > 100 * (tol + 1e-8)).sum() > 0.7 * want.numel() and tol.max() < 1e-4

@@ -206,7 +206,7 @@ struct NoMore {
 // LDS of its own (part q's starts at part 0's + q * LDS); part 0 adds the sums in part order and
 // stores. All waves of the workgroup come here together.
 // first < the whole K tiles: the sum begins at that tile and wraps (the same for every call of the tile, so the bits stay).
-// TERMS 2: A is the sum of two operands, the second `second` elements behind the first; both products make one sum.
+// TERMS > 1: A is the sum of so many operands, each `second` elements behind the one before; their products make one sum.
 template <int DT, int BM, bool AK, bool BKM, int BK = 64, class MORE = NoMore, int LDS = LDS_BYTES, int Q = 1, int TERMS = 1>
 __device__ __forceinline__ void tile(const GemmArgs& a, int64_t m0, int64_t n0, uint8_t* lds, int lane, int w,
                                      const MORE& more = MORE(), int q = 0, int first = 0, int64_t second = 0) {

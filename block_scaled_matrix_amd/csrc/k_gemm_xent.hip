@@ -7,13 +7,16 @@
 // logits end there: rows x N / 64 pairs leave the chip instead of rows x N logits. A second launch joins a row's
 // pairs in a fixed order.
 // Gradient: the vocabulary is cut into pieces. A piece's logits are made again (2 rows N K operations more than an
-// implementation that had kept them; the alternative, float32 logits of a batch, is 1 GB for 8190 x 32001), become G
-// in the accumulators and leave as 16-bit values, which two products then read: dX += G W_piece and dW_piece = G^T X.
+// implementation that had kept them), become G in the accumulators and leave as 16-bit values, which two products then read:
+// dX += G W_piece and dW_piece = G^T X. So nothing of rows x N lives between the two calls, and how much lives in the second
+// is the piece's choice: of the default piece no less than float32 logits would be (8190 x 32001: 1.32 GB with room for every
+// format, the logits 1.05 GB), of one of 4096 columns an eighth.
 // G is rounded to the operands' format because the matrix unit takes it so: half a step (2^-8 in bf16, 2^-11 in f16) of
-// each term, independent from term to term, like the rounding of a 16-bit gradient. A gradient kept in float32 takes G as two
-// such terms, 2^-18 (2^-24) of each left, and twice the product's operations. In f16 the weights are brought to 2^15 at
-// most by a power of two found on the device, so a probability keeps all its bits down to 2^-29 of the largest weight, and
-// the products' sums are scaled back in float32.
+// each term, independent from term to term, like the rounding of a 16-bit gradient. A gradient kept in float32 takes G as a
+// sum of such values, three in bf16, which are all of a float's bits, and two in f16 (2^-23 left), and as often the product's
+// operations. (Two in bf16 leave 2^-17: 2.5e-6 of dW's norm where float32 products have 3e-7.) In f16 the weights are
+// brought to 2^15 at most by a power of two found on the device, so a probability keeps all its bits down to 2^-29 of the
+// largest weight, and the products' sums are scaled back in float32.
 // Tiles: gemm_dense_tile.hpp (256 x 256) where they fill the chip, gemm_mid_tile.hpp (32 / 64 / 128 x 128) otherwise, and
 // for the loss of few rows skinny.hpp. dX with few tiles is cut along the vocabulary into parts that are summed in a
 // fixed order; with few rows both gradients share a launch (k_xent_both).
@@ -30,10 +33,10 @@ namespace {
 using namespace dense;
 
 // A product's K cut into n parts side by side: part p takes K elements p * per .. and writes its own sums, stride_d
-// elements behind part p - 1's. With two terms of A, `second` elements apart, half of the parts take the second. Makes `a`
-// the part's product and pid the tile's number in it.
+// elements behind part p - 1's. With several terms of A, `second` elements apart, the first n / terms parts take the first, and
+// so on. Makes `a` the part's product and pid the tile's number in it.
 struct Parts {
-  int n;
+  int n, terms;
   int64_t per, stride_d, second;
   template <bool AK, bool BKM>
   __device__ __forceinline__ void enter(GemmArgs& a, int tiles, int& pid) const {
@@ -41,9 +44,10 @@ struct Parts {
     int p = pid / tiles;
     pid -= p * tiles;
     a.D += p * stride_d;
-    if (second) {
-      if (2 * p >= n) a.A = (const uint16_t*)a.A + second;
-      p = 2 * p >= n ? p - n / 2 : p;
+    if (terms > 1) {
+      const int of = n / terms, t = p / of;
+      a.A = (const uint16_t*)a.A + t * second;
+      p -= t * of;
     }
     const int64_t k0 = p * per;
     a.A = (const uint16_t*)a.A + (AK ? k0 : k0 * a.lda);
@@ -67,8 +71,7 @@ __global__ __launch_bounds__(256, 1) void k_xent_large(GemmArgs a, EP ep, int ti
   if constexpr (!EP::kStores) store_large<OUT, ADD>(a, row0, col0, lane, acc, lds + 32768 * w);
 }
 
-// Tiles of BM x 128 (128-row ones with a K-major A: of as few rows as hold the last ones). TERMS 2: A's two terms in one
-// sum.
+// Tiles of BM x 128 (128-row ones with a K-major A: of as few rows as hold the last ones). TERMS > 1: A's terms in one sum.
 template <int DT, bool AK, bool BKM, class EP, int BM = 128, int BK = 64, int PER_CU = 2, int Q = 1, int TERMS = 1>
 __global__ __launch_bounds__(256 * Q, PER_CU * Q) void k_xent_mid(GemmArgs a, EP ep, int tiles_m, int tiles_n, Parts parts) {
   constexpr int LDS = 160 * 1024 / PER_CU / Q;
@@ -258,7 +261,7 @@ template <int DT, class EP>
 void launch_logits(const GemmArgs& g, Tile tile, const EP& ep, hipStream_t st) {
   const int64_t t = tile == LARGE ? 256 : 128, tm = (g.M + t - 1) / t, tn = (g.N + t - 1) / t;   // (FEW: one row of tiles)
   const dim3 grid((uint32_t)(tm * tn));
-  const Parts one{1, 0, 0, 0};
+  const Parts one{1, 1, 0, 0, 0};
   if (tile == LARGE) hipLaunchKernelGGL((k_xent_large<DT, true, true, DT, NEVER, EP>), grid, dim3(256), 0, st, g, ep, (int)tm, (int)tn, one);
   else if (tile == FEW) hipLaunchKernelGGL((k_xent_mid<DT, true, true, EP, 32, 64, 3>), grid, dim3(256), 0, st, g, ep, (int)tm, (int)tn, one);
   else if (tile == MID) hipLaunchKernelGGL((k_xent_mid<DT, true, true, EP>), grid, dim3(256), 0, st, g, ep, (int)tm, (int)tn, one);
@@ -315,11 +318,15 @@ struct Plan {
   bool large;
   int parts;
   int64_t per;      // columns of a part
-  int64_t g_second;             // elements from G's first term to its second
+  int64_t g_second;             // elements from a term of G to the next
   int64_t g_bytes, f_bytes, bytes;
 };
 
-// One piece takes what 1 GiB of G holds: more pieces cost dX its sums' way through memory once a piece.
+// Terms of G for gradients kept in float32.
+constexpr int f32_terms(int dt) { return dt == BSM_BF16 ? 3 : 2; }
+
+// One piece takes what 1 GiB of G holds (two terms: 2 GiB; three: 1 GiB of them all, so that the workspace need not be larger
+// for them): more pieces cost dX its sums' way through memory once a piece.
 constexpr int64_t kPieceBytes = int64_t(1) << 30;
 
 // dX has rows x K outputs and a sum over the whole piece: few tiles, long sums. Its tiles and parts are those of the least
@@ -347,9 +354,9 @@ void plan_dx(int64_t rows, int64_t K, Plan& p) {
   }
 }
 
-Plan plan_of(int64_t rows, int64_t N, int64_t K, int64_t piece) {
+Plan plan_of(int64_t rows, int64_t N, int64_t K, int64_t piece, int terms) {
   Plan p{};
-  if (piece <= 0) piece = std::max<int64_t>(kPieceBytes / (2 * std::max<int64_t>(rows, 1)), 4096);
+  if (piece <= 0) piece = std::max<int64_t>(kPieceBytes / ((terms == 3 ? 6 : 2) * std::max<int64_t>(rows, 1)), 4096);
   piece = std::min(piece, int64_t(1) << 21);   // (G's rows: 32-bit offsets in a tile)
   p.pieces = (N + piece - 1) / piece;
   const int64_t even = (N + p.pieces - 1) / p.pieces;            // pieces of one length
@@ -358,12 +365,15 @@ Plan plan_of(int64_t rows, int64_t N, int64_t K, int64_t piece) {
   p.ldg = (p.piece + 63) / 64 * 64;
   plan_dx(std::max<int64_t>(rows, 1), std::max<int64_t>(K, 1), p);
   p.ldf = (K + 3) / 4 * 4;
-  // (The workspace does not know the gradients' formats: room for both terms, and for twice the parts.)
   p.g_second = (rows * p.ldg + 127) / 128 * 128;
-  p.g_bytes = p.g_second * 4;
-  p.f_bytes = (2 * p.parts * rows * p.ldf * 4 + 255) / 256 * 256;
+  p.g_bytes = terms * p.g_second * 2;
+  p.f_bytes = (terms * p.parts * rows * p.ldf * 4 + 255) / 256 * 256;
   p.bytes = 256 + p.g_bytes + p.f_bytes;
   return p;
+}
+
+int terms_of(const XentGradArgs& g, int dt) {
+  return (g.dX && g.dx_fmt == BSM_F32) || (g.dW && g.dw_fmt == BSM_F32) ? f32_terms(dt) : 1;
 }
 
 template <int DT>
@@ -379,10 +389,11 @@ hipError_t launch_grad(const XentArgs& a, const XentGradArgs& g, const Plan& p, 
     down = by + 1;
   }
   using Times = xent::Times<DT == BSM_F16>;
-  const Parts one{1, 0, 0, 0};
-  // float32 gradients take G as two terms: dX in twice the parts, dW's in one sum
-  const bool two = (g.dX && g.dx_fmt == BSM_F32) || (g.dW && g.dw_fmt == BSM_F32);
-  const int dx_terms = g.dx_fmt == BSM_F32 ? 2 : 1;
+  const Parts one{1, 1, 0, 0, 0};
+  // float32 gradients take G as several terms: dX in as many times the parts, dW's in one sum
+  constexpr int TERMS = f32_terms(DT);
+  const bool more = terms_of(g, DT) > 1;
+  const int dx_terms = g.dx_fmt == BSM_F32 ? TERMS : 1;
   const bool direct = dx_terms == 1 && p.parts == 1 && p.pieces == 1;
   for (int64_t c0 = 0, at = 0; c0 < a.N; c0 += p.piece, at++) {
     const int64_t cols = std::min(p.piece, a.N - c0);
@@ -394,14 +405,14 @@ hipError_t launch_grad(const XentArgs& a, const XentGradArgs& g, const Plan& p, 
       Tile tile = tile_for(a.rows, cols);
       if (tile == SKINNY) tile = SPLIT;   // (fewer than 128 tiles)
       const xent::Weights weights{a.labels, a.lse, g.dloss, up, a.rows, a.N, c0};
-      if (two) launch_logits<DT>(z, tile, xent::GradTwo<DT>{weights, G, p.ldg, p.g_second, cols}, st);
+      if (more) launch_logits<DT>(z, tile, xent::GradTerms<DT, TERMS>{weights, G, p.ldg, p.g_second, cols}, st);
       else launch_logits<DT>(z, tile, xent::Grad{weights}, st);
     }
     GemmArgs x{}, w{};
     const Times ep{down};
     // (the last piece may be short: parts past its columns have nothing to add)
-    const Parts parts{dx_terms * (int)((cols + p.per - 1) / p.per), p.per, a.rows * p.ldf, dx_terms == 2 ? p.g_second : 0};
-    const bool dw_large = a.rows >= 1600 && tile_for(cols, a.K) == LARGE, dw_two = g.dw_fmt == BSM_F32;
+    const Parts parts{dx_terms * (int)((cols + p.per - 1) / p.per), dx_terms, p.per, a.rows * p.ldf, p.g_second};
+    const bool dw_large = a.rows >= 1600 && tile_for(cols, a.K) == LARGE, dw_more = g.dw_fmt == BSM_F32;
     if (g.dX && a.rows > 0) {
       x.M = a.rows; x.N = a.K; x.K = cols; x.dtype = DT;
       x.A = G; x.lda = p.ldg; x.B = W; x.ldb = a.ldw;
@@ -418,7 +429,7 @@ hipError_t launch_grad(const XentArgs& a, const XentGradArgs& g, const Plan& p, 
       const int xm = (int)((x.M + 127) / 128), xn = (int)((x.N + 127) / 128), ym = (int)((w.M + 127) / 128), yn = (int)((w.N + 127) / 128);
       const int xg = (xm * xn * parts.n + 7) / 8 * 8;
       const dim3 grid((uint32_t)(xg + ym * yn));
-      if (dw_two) hipLaunchKernelGGL((k_xent_both<DT, 2, Times>), grid, dim3(256), 0, st, x, w, ep, parts, xm, xn, ym, yn, xg, p.g_second);
+      if (dw_more) hipLaunchKernelGGL((k_xent_both<DT, TERMS, Times>), grid, dim3(256), 0, st, x, w, ep, parts, xm, xn, ym, yn, xg, p.g_second);
       else hipLaunchKernelGGL((k_xent_both<DT, 1, Times>), grid, dim3(256), 0, st, x, w, ep, parts, xm, xn, ym, yn, xg, int64_t(0));
       continue;
     }
@@ -438,15 +449,15 @@ hipError_t launch_grad(const XentArgs& a, const XentGradArgs& g, const Plan& p, 
       const dim3 grid((uint32_t)(m128 * n128));
       if (dw_large) {
         launch_large<DT, false>(w, ep, one, st);
-        if (dw_two) {
-          // (the second term as a product of its own onto the first: its sums' way through memory is short beside 1600 rows)
-          w.A = G + p.g_second;
+        // (the other terms as products of their own onto the first: their sums' way through memory is short beside 1600 rows)
+        for (int t = 1; t < TERMS && dw_more; t++) {
+          w.A = G + t * p.g_second;
           w.accum = 1;
           launch_large<DT, false>(w, ep, one, st);
         }
-      } else if (dw_two) {
-        hipLaunchKernelGGL((k_xent_mid<DT, false, false, Times, 128, 32, 4, 1, 2>), grid, dim3(256), 0, st, w, ep, (int)m128, (int)n128,
-                           Parts{1, 0, 0, p.g_second});
+      } else if (dw_more) {
+        hipLaunchKernelGGL((k_xent_mid<DT, false, false, Times, 128, 32, 4, 1, TERMS>), grid, dim3(256), 0, st, w, ep, (int)m128, (int)n128,
+                           Parts{1, 1, 0, 0, p.g_second});
       } else {
         hipLaunchKernelGGL((k_xent_mid<DT, false, false, Times, 128, 32, 4>), grid, dim3(256), 0, st, w, ep, (int)m128, (int)n128, one);
       }
@@ -479,10 +490,15 @@ hipError_t launch_xent(const XentArgs& a, void* workspace, hipStream_t st) {
   return a.dtype == BSM_BF16 ? launch_loss<BSM_BF16>(a, part, at, st) : launch_loss<BSM_F16>(a, part, at, st);
 }
 
-int64_t xent_grad_workspace(int64_t rows, int64_t N, int64_t K, int64_t piece) { return plan_of(rows, N, K, piece).bytes; }
+// (What the gradients' formats will be is not known here.)
+int64_t xent_grad_workspace(int64_t rows, int64_t N, int64_t K, int64_t piece) {
+  int64_t most = 0;
+  for (int terms = 1; terms <= 3; terms++) most = std::max(most, plan_of(rows, N, K, piece, terms).bytes);
+  return most;
+}
 
 hipError_t launch_xent_grad(const XentArgs& a, const XentGradArgs& g, void* workspace, hipStream_t st) {
-  const Plan p = plan_of(a.rows, a.N, a.K, g.piece);
+  const Plan p = plan_of(a.rows, a.N, a.K, g.piece, terms_of(g, a.dtype));
   return a.dtype == BSM_BF16 ? launch_grad<BSM_BF16>(a, g, p, (uint8_t*)workspace, st)
                              : launch_grad<BSM_F16>(a, g, p, (uint8_t*)workspace, st);
 }

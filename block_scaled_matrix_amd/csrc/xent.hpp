@@ -1,6 +1,7 @@
 // xent.hpp - cross entropy of a projection (k_gemm_xent.hip): the calls' arguments, and what a tile of logits becomes
 // while it is still in the accumulators.
 #pragma once
+#include <type_traits>
 #include "bsm_internal.hpp"
 #include "store16.hpp"
 
@@ -160,10 +161,10 @@ struct Grad : Weights {
   }
 };
 
-// As the sum of two 16-bit terms, rounded and what the rounding dropped, rounded (2^-18 of the value is left in bf16, 2^-24
-// in f16), for gradients kept in float32: `to` and `second` elements behind it.
-template <int DT>
-struct GradTwo : Weights {
+// As the sum of T 16-bit terms, rounded and again what the rounding dropped, for gradients kept in float32: term t at `to` +
+// t * second. Three terms are all of a float's bits in bf16 (24, eight a term); two leave at most 2^-23 of the value in f16.
+template <int DT, int T>
+struct GradTerms : Weights {
   static constexpr bool kStores = true;
   uint16_t* to;
   int64_t ld, second, cols;
@@ -171,35 +172,45 @@ struct GradTwo : Weights {
   __device__ __forceinline__ void operator()(int64_t row0, int64_t col0, f32x4 (&acc)[MI][NJ]) const {
     const int lane = threadIdx.x & 63, G = lane >> 4;
     const float f = by ? *by : 1.0f;
+    if (col0 >= cols) return;
+    const bool whole = col0 + 16 * NJ <= cols;   // wave-uniform
 #pragma unroll
     for (int m = 0; m < MI; m++) {
       const int64_t row = row0 + 16 * m + (lane & 15);
       f32x4 v[NJ];
       take(acc[m], v);
       turn(row, col0, G, f, v);
-      if (row < rows)
+      // (taken anew for each row of blocks: kept, the comparisons' masks spilled scalar registers)
+      int left = (int)min(cols - col0, (int64_t)(16 * NJ)) - 4 * G;
+      asm volatile("" : "+v"(left));
+      uint16_t* q = to + row * ld + col0 + 4 * G;
+      auto store = [&](auto all) {
 #pragma unroll
         for (int n = 0; n < NJ; n++) {
-          const int64_t col = col0 + 16 * n + 4 * G;
-          uint16_t* p = to + row * ld + col;
-          uint16_t h[4], r[4];
+          uint16_t* p = q + 16 * n;
 #pragma unroll
-          for (int e = 0; e < 4; e++) {
-            h[e] = gemm::to_bits16<DT>(v[n][e]);
-            r[e] = gemm::to_bits16<DT>(v[n][e] - gemm::from_bits16<DT>(h[e]));
-          }
-          if (col + 4 <= cols) {
-            *(uint2*)p = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
-            *(uint2*)(p + second) = make_uint2(r[0] | (uint32_t)r[1] << 16, r[2] | (uint32_t)r[3] << 16);
-          } else {
+          for (int t = 0; t < T; t++) {
+            uint16_t h[4];
 #pragma unroll
-            for (int e = 0; e < 4; e++)
-              if (col + e < cols) {
-                p[e] = h[e];
-                p[second + e] = r[e];
-              }
+            for (int e = 0; e < 4; e++) {
+              h[e] = gemm::to_bits16<DT>(v[n][e]);
+              v[n][e] -= gemm::from_bits16<DT>(h[e]);
+            }
+            if (decltype(all)::value || 16 * n + 4 <= left) {
+              *(uint2*)p = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; e++)
+                if (16 * n + e < left) p[e] = h[e];
+            }
+            p += second;
           }
         }
+      };
+      if (row < rows) {
+        if (whole) store(std::true_type{});
+        else store(std::false_type{});
+      }
     }
   }
 };

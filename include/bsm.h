@@ -519,14 +519,17 @@ int64_t bsm_gemm_cross_entropy_workspace(int64_t rows, int64_t N);
  *   dX[t*lddx + k] = sum_n G(t,n) W(n,k),   dW[n*lddw + k] = (accum ? dW[n*lddw + k] : 0) + sum_t G(t,n) X(t,k),
  * sums in float32, rounded once to their formats. (dW adds 0 * X(t,k) for a row without a label: X must be finite there too.)
  * The vocabulary is taken in pieces: a piece's logits are made again, and its
- * part of G is kept in the workspace, rounded to ab's format for a gradient of that format, and as the sum of two such values
- * (off by at most 2^-18 in BF16, 2^-24 in F16) for one in F32 (in F16 times a power of two that brings the largest |dloss|
- * to 2^15, so that probabilities keep their bits).
+ * part of G is kept in the workspace, rounded to ab's format for a gradient of that format, and for one in F32 as the sum of
+ * such values, three in BF16 (all of a float's bits) or two in F16 (off by at most 2^-23 of the value) (in F16 times a power of
+ * two that brings the largest |dloss| to 2^15, so that probabilities keep their bits).
  *   lse:       what bsm_gemm_cross_entropy wrote (DEVICE, rows float32);
  *   dloss:     DEVICE, rows float32, 4-byte aligned;
- *   piece:     columns of the vocabulary at once, 0 for the library's choice (1 GiB of G's values); each piece more costs
- *              dX another way through memory. At most 2^21 are taken at once;
- *   workspace: DEVICE, 16-byte aligned, bsm_gemm_cross_entropy_grad_workspace(rows, N, K, piece) bytes; as above;
+ *   piece:     columns of the vocabulary at once, 0 for the library's choice (1 GiB of one term of G, or of all three); each
+ *              piece more costs dX another way through memory. At most 2^21 are taken at once;
+ *   workspace: DEVICE, 16-byte aligned, bsm_gemm_cross_entropy_grad_workspace(rows, N, K, piece) bytes; as above. It has room
+ *              for the terms of float32 gradients, whichever are asked for: with piece 0 up to 4 bytes a logit where one piece
+ *              holds the vocabulary (8190 rows, N 32001, K 4096: 1.32 GB, float32 logits would be 1.05 GB), with a piece of
+ *              the caller's 6 bytes a row and column of it, and the float32 parts of dX. A smaller piece takes less;
  *   dX, dx_fmt, lddx: BSM_F32 or ab; or dX NULL: not wanted;
  *   dW, dw_fmt, lddw: BSM_F32 or ab; or dW NULL: not wanted. Rows 0: dW = accum ? dW : 0;
  *   accum:     0 or 1 (dW alone).

@@ -282,3 +282,66 @@ def test_gradient_against_differences_within_two_terms(ab):
         assert (miss <= 0).all(), float(miss.max())
         # (a gradient of zeros, or of another sign, would not pass)
         assert (want.abs() > 100 * (tol + 1e-8)).sum() > 0.7 * want.numel() and tol.max() < 1e-4
+
+
+def float32_of_g(z, labels, lse, d):
+    """G in 64 bits, and its bound: with lse given, p is off by (4 |z| + 4 |lse| + 8) u of itself; G's terms, as one sum of
+    exact products, by 2^-22 of G at most (f16's two leave 2^-23, three additions 2^-23 each)."""
+    p = torch.exp(z - lse.double()[:, None])
+    G = p.clone()
+    G[torch.arange(z.shape[0], device="cuda"), labels.long()] -= 1.0
+    G *= d.double()[:, None]
+    r = (4 * z.abs() + 4 * lse.double().abs()[:, None] + 8) * 2.0 ** -24
+    return G, d.double()[:, None].abs() * (p * r + 2.0 ** -23) + (2.0 ** -23 + 3 * 2.0 ** -23) * G.abs() + 2.0 ** -39 * float(d.abs().max())
+
+
+@pytest.mark.parametrize("ab", ["bf16", "f16"])
+@pytest.mark.parametrize("rows,N,K,piece", [(40, 3000, 40, 0), (300, 5001, 304, 0), (300, 5001, 304, 1000), (1700, 4096, 4096, 0),
+                                            (1700, 4096, 4096, 2048)])
+def test_float32_weight_gradient_is_float32(rows, N, K, piece, ab):
+    """X of unit rows: dW is G transposed, every sum one product, so that what G's terms leave shows as it is."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = torch.eye(rows, K, device="cuda").to(DT[ab])
+    w = (torch.rand(N, K, device="cuda", generator=g) * 2 - 1).to(DT[ab])
+    labels = torch.randint(0, N, (rows,), device="cuda", generator=g, dtype=torch.int32)
+    d = torch.rand(rows, device="cuda", generator=g) * 0.9 + 0.1
+    z = w.double()[:, :rows].T.contiguous()
+    lse = torch.logsumexp(z, 1).float()
+    for accum in (0, 1):
+        dw = torch.full((N, up(K, 8)), -1.0 if accum else float("nan"), device="cuda")
+        work = torch.full((bsm.bsm_gemm_cross_entropy_grad_workspace(rows, N, K, piece),), 255, dtype=torch.uint8, device="cuda")
+        xp, wp = wide(x), wide(w)
+        say("float32 dW", rows, N, K, piece, ab, accum)
+        bsm.bsm_gemm_cross_entropy_grad(rows, N, K, ab, xp, xp.stride(0), wp, wp.stride(0), labels, lse, d, piece, work, ab, None, up(K, 8),
+                                        "f32", dw, dw.stride(0), accum)
+        G, tol = float32_of_g(z, labels, lse, d)
+        got = dw[:, :rows].double().T
+        if accum:
+            # (onto -1: each of up to three stores rounds at 1)
+            assert ((got - (G - 1)).abs() <= tol + 3 * 2.0 ** -24 * 2).all()
+        else:
+            assert ((got - G).abs() <= tol).all(), float(((got - G).abs() / tol).max())
+            small = G.abs() > 0
+            assert float(((got - G).abs() / G.abs())[small].mean()) < 2.0 ** -21     # (two bf16 terms: 2^-18.6 in the mean)
+            assert not dw[:, rows:K].any()
+
+
+@pytest.mark.parametrize("ab", ["bf16", "f16"])
+@pytest.mark.parametrize("rows,K,piece", [(40, 200, 0), (300, 1000, 0), (300, 1000, 300), (2300, 4096, 0)])
+def test_float32_input_gradient_is_float32(rows, K, piece, ab):
+    """W of unit rows: dX is G."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    N = K
+    x = (torch.rand(rows, K, device="cuda", generator=g) * 2 - 1).to(DT[ab])
+    w = torch.eye(N, device="cuda").to(DT[ab])
+    labels = torch.randint(0, N, (rows,), device="cuda", generator=g, dtype=torch.int32)
+    d = torch.rand(rows, device="cuda", generator=g) * 0.9 + 0.1
+    z = x.double()
+    lse = torch.logsumexp(z, 1).float()
+    dx = torch.full((rows, K), float("nan"), device="cuda")
+    work = torch.full((bsm.bsm_gemm_cross_entropy_grad_workspace(rows, N, K, piece),), 255, dtype=torch.uint8, device="cuda")
+    say("float32 dX", rows, K, piece, ab)
+    bsm.bsm_gemm_cross_entropy_grad(rows, N, K, ab, x, K, w, K, labels, lse, d, piece, work, "f32", dx, K, ab, None, K)
+    G, tol = float32_of_g(z, labels, lse, d)
+    assert ((dx.double() - G).abs() <= tol).all(), float(((dx.double() - G).abs() / tol).max())
+    assert float(((dx.double() - G).abs() / G.abs()).mean()) < 2.0 ** -21

@@ -107,13 +107,19 @@ __global__ __launch_bounds__(256, 1) void k_kept_wgrad_large(GemmArgs a, GroupAr
   if constexpr (DT == BSM_BF16) {
     // A scale so wide that a finite code may lie beyond bf16's range: the tile again as small ones, which bound what they
     // convert. (In the loop itself a bound in every conversion takes 16381 rows over 8 groups, 4096 x 2048 from 267 to 290 us, a
-    // branch round it 287, one branch a K tile 311; this 273.)
+    // branch round it 287, one branch a K tile 311; this 1%.)
     ((int*)lds)[w] = __any(wide);   // (every wave is done with LDS)
     __syncthreads();
     const int4 met = *(const int4*)lds;
     __syncthreads();
     if (__builtin_expect(__builtin_amdgcn_readfirstlane(met.x | met.y | met.z | met.w), 0)) {
-      if (threadIdx.x == 0) *(GemmArgs*)(lds + kArgsAt) = a;
+      BSM_LDS GemmArgs* v = (BSM_LDS GemmArgs*)(uintptr_t)(gemm::lds_addr(lds) + kArgsAt);
+      if (threadIdx.x == 0) {   // (one by one: a copy of the whole kept the arguments in memory)
+        v->M = a.M; v->N = a.N; v->K = a.K;
+        v->A = a.A; v->lda = a.lda; v->B = a.B; v->ldb = a.ldb;
+        v->SFB = a.SFB; v->ld_sfb = a.ld_sfb;
+        v->D = a.D; v->ldd = a.ldd; v->d_fmt = a.d_fmt; v->accum = a.accum;
+      }
       for (int i = 0; i < 4; i++) {
         const int64_t m = 256 * (int64_t)tm + 128 * (i >> 1), n = 256 * (int64_t)tn + 128 * (i & 1);
         __syncthreads();

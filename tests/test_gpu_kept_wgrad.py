@@ -242,3 +242,10 @@ def test_same_bits_on_every_call():
     a = wgrad([300, 77, 500], 520, 260, seed=2)[0]
     for _ in range(3):
         assert torch.equal(a, wgrad([300, 77, 500], 520, 260, seed=2)[0])
+
+
+@pytest.mark.parametrize("M,N", [(130, 200), (1030, 1200), (2056, 2400)])
+def test_one_long_group_among_empty_ones(M, N):
+    """The tile goes by the groups' mean length: one group with all of the rows on tiles for short ones."""
+    wgrad([0] * 5 + [2500] + [0] * 10, M, N, seed=M, first=1)
+    wgrad([0] * 3 + [2500, 1, 0, 0], M, N, "f16", "e5m2", "f16", 1, seed=M)

@@ -9,8 +9,8 @@
 // vector, J vectors: lanes of 16 reduce without LDS, and more values a lane are more loads in flight), so a lane keeps
 // the same experts for every row it sees: f stays in its registers, and P's column sums are register sums, joined at the
 // end across the wave's rows, the workgroup's waves (LDS) and the workgroups (a second launch over at most 256 of them),
-// all in a fixed order. A lane adds at most 64 rows in float32, then into a double: a sum over any number of rows keeps
-// its bits. Counts are integers, so the LDS atomics that make them cannot change a result by their order.
+// all in a fixed order. A lane adds at most 64 rows in float32, then into a double; a workgroup's sums go to the join as
+// float32, 2^-24 of each, and meet in double: the error does not grow with the rows. Counts are integers, so the LDS atomics that make them cannot change a result by their order.
 // Bound: for many rows the latency of a few loads and reductions behind one another, sixteen waves a CU in turn (32768
 // rows, 128 experts, bf16: 9 us for 8 MB, 4-8 us for the join, the gradient 9.5 us for 17 MB); for few rows launches, so
 // up to kOneGroup logits a single workgroup does everything in one (16 rows, 64 experts: 3.7 us).

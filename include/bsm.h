@@ -428,7 +428,8 @@ int64_t bsm_gemm_lora_workspace(int64_t rows, int64_t R);
  *   loss:      DEVICE, one float32 (0 where no row is kept);
  *   workspace: DEVICE, 16-byte aligned, bsm_router_balance_workspace(rows, n_experts) bytes (0 for few rows: may be NULL);
  *              holds nothing from one call to the next. Calls that may run at the same time need one each.
- * Probabilities are float32, their sums float64. A logit of -infinity has probability 0; a row kept whose logits are all
+ * Probabilities are float32; their sums over rows are float32 for up to 64 rows and float64 beyond (of many rows in parts,
+ * each rounded to float32 once). A logit of -infinity has probability 0; a row kept whose logits are all
  * -infinity has none at all (it counts among n). NaN and +infinity make the row's probabilities NaN. Every output is
  * written, for 0 rows too. The same inputs give the same bits. The inputs must not overlap the outputs. */
 int bsm_router_balance(int64_t rows, int32_t n_experts, int32_t k, int32_t l_fmt, const void* logits, int64_t ldl,
@@ -524,12 +525,13 @@ int64_t bsm_gemm_cross_entropy_workspace(int64_t rows, int64_t N);
  * two that brings the largest |dloss| to 2^15, so that probabilities keep their bits).
  *   lse:       what bsm_gemm_cross_entropy wrote (DEVICE, rows float32);
  *   dloss:     DEVICE, rows float32, 4-byte aligned;
- *   piece:     columns of the vocabulary at once, 0 for the library's choice (1 GiB of one term of G, or of all three); each
- *              piece more costs dX another way through memory. At most 2^21 are taken at once;
+ *   piece:     columns of the vocabulary at once, 0 for the library's choice (1 GiB of one term of G, or of all three, and at
+ *              least 4096 columns); each piece more costs dX another way through memory. At most 2^21 are taken at once;
  *   workspace: DEVICE, 16-byte aligned, bsm_gemm_cross_entropy_grad_workspace(rows, N, K, piece) bytes; as above. It has room
- *              for the terms of float32 gradients, whichever are asked for: with piece 0 up to 4 bytes a logit where one piece
- *              holds the vocabulary (8190 rows, N 32001, K 4096: 1.32 GB, float32 logits would be 1.05 GB), with a piece of
- *              the caller's 6 bytes a row and column of it, and the float32 parts of dX. A smaller piece takes less;
+ *              for the terms of float32 gradients, whichever are asked for: 6 bytes a row and column of the piece (with
+ *              piece 0 up to 1 GiB, then 4 bytes up to 2 GiB), and up to three times as many float32 dX as a piece is cut into
+ *              parts (few rows: up to 32). 8190 rows, N 32001, K 4096: 1.32 GB (float32 logits would be 1.05 GB); 200 rows, N
+ *              10007, K 1000: 67 MB (8 MB). A smaller piece takes less;
  *   dX, dx_fmt, lddx: BSM_F32 or ab; or dX NULL: not wanted;
  *   dW, dw_fmt, lddw: BSM_F32 or ab; or dW NULL: not wanted. Rows 0: dW = accum ? dW : 0;
  *   accum:     0 or 1 (dW alone).

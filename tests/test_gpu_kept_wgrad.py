@@ -249,3 +249,32 @@ def test_one_long_group_among_empty_ones(M, N):
     """The tile goes by the groups' mean length: one group with all of the rows on tiles for short ones."""
     wgrad([0] * 5 + [2500] + [0] * 10, M, N, seed=M, first=1)
     wgrad([0] * 3 + [2500, 1, 0, 0], M, N, "f16", "e5m2", "f16", 1, seed=M)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_large_tiles_beyond_the_range_added_to_in_16_bits(fmt):
+    """256 x 256 tiles whose scales reach past bf16's range, onto a bf16 D with rows and columns behind the tile's; one
+    group's scales are ordinary, and the bytes behind the scales hold wide ones."""
+    rows, M, N, ldd = 1500, 2050, 3610, 3624
+    g = torch.Generator().manual_seed(3)
+    off = [0, 740, 1500]
+    c, _ = kept_rows(rows, N, fmt, g, 1)
+    s = torch.randint(236, 255, (rows, (N + 31) // 32), generator=g).to(torch.uint8)
+    s[740:] = 127
+    y = torch.zeros(rows, up(M, 8), dtype=torch.bfloat16)
+    y[11, :M:3], y[745, 1:M:3] = 2.0 ** -12, 2.0 ** -12     # one term a sum: exact
+    sd = torch.full((rows, up(s.shape[1], 4) + 4), 250, dtype=torch.uint8)
+    sd[:, :s.shape[1]] = s
+    cd = torch.full((rows, up(N, 16)), 0x70, dtype=torch.uint8)
+    cd[:, :N] = c
+    D0 = torch.randn(2, M, ldd, generator=g).bfloat16()
+    D = D0.cuda()
+    say("kept wgrad beyond the range, added to", fmt)
+    bsm.bsm_gemm_grouped_wgrad_block_scale(rows, M, N, 2, torch.tensor(off, dtype=torch.int32, device="cuda"), "bf16", y.cuda(), y.shape[1],
+                                           fmt, cd.cuda(), cd.stride(0), sd.cuda(), sd.stride(0), "bf16", D, ldd, M * ldd, 1)
+    x = values(c.view(F8[fmt]).double(), s, N)
+    m = torch.finfo(torch.bfloat16).max
+    want = D0.clone()
+    for i, r in ((0, 11), (1, 745)):
+        want[i, i::3, :N] = (D0[i, i::3, :N].float() + x[r].clamp(-m, m).float() * 2.0 ** -12).bfloat16()
+    assert torch.equal(D.cpu(), want)
